@@ -79,7 +79,9 @@ typedef enum {
     SV_ERR_UNSUPPORTED = 4  /* a size or layout the library does not handle         */
 } sv_status_t;
 
-typedef enum { SV_DTYPE_BF16 = 0, SV_DTYPE_F32 = 1 } sv_dtype_t;
+/* SV_DTYPE_F16 is a type of the attention operators (sv_rotary, sv_kv_append,
+ * sv_paged_attention); logits are bf16 or fp32. */
+typedef enum { SV_DTYPE_BF16 = 0, SV_DTYPE_F32 = 1, SV_DTYPE_F16 = 2 } sv_dtype_t;
 
 /* Per-position / per-row status bits. */
 enum {
@@ -478,6 +480,121 @@ sv_status_t sv_verify_chain_shard_merge(const void* records, int n_shards, int n
                                         const int32_t* draft_tokens, const int32_t* verify_len, sv_sampling_t sp,
                                         uint64_t seed, int32_t* accept_len, int32_t* out_tokens, int32_t* num_emitted,
                                         int32_t* row_status, void* ws, size_t ws_bytes, sv_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The target model's attention over the windows that are verified.  The
+ * planner's qo_indptr lays the batch's tokens out; these three calls rotate
+ * queries and keys by their positions, append keys and values to a paged
+ * cache, and attend every window over its request's cache.
+ *
+ * Conventions they share:
+ *  - Tensors are bf16, fp16 or fp32 (one type per call), the last axis (the
+ *    head's elements) contiguous; every other stride is given, in elements.
+ *  - Request r's window is tokens qo_indptr[r] .. qo_indptr[r + 1] - 1 of the
+ *    packed token axis (n_r of them, possibly none); tokens past
+ *    qo_indptr[n_req] are padding: neither read nor written.  kv_len[r]
+ *    counts request r's cached tokens with the window appended, so token i of
+ *    the window has position p = kv_len[r] - n_r + i.
+ *  - status (device) int32 [n_req] or NULL: SV_ROW_* bits are OR-ed into it;
+ *    the caller clears it.  SV_ROW_BAD_LAYOUT: a window outside the token
+ *    axis or longer than promised, a kv_len outside what the page table
+ *    holds, a page number outside [0, n_pages).  Nothing outside the tensors
+ *    is ever read or written.
+ */
+
+/* Token rows of some heads: element (token, head, e) is
+ * data[token * stride_token + head * stride_head + e]. */
+typedef struct {
+    void* data;           /* (device) */
+    int64_t stride_token; /* elements */
+    int64_t stride_head;  /* elements */
+    int32_t heads;
+} sv_heads_t;
+
+/* A paged cache: token p of request r is slot p % page_size of page
+ * page_table[r * ld_table + p / page_size]. */
+typedef struct {
+    sv_heads_t k, v;             /* stride_token: from slot to slot of a page; both have the same heads */
+    int64_t stride_page_k;       /* elements */
+    int64_t stride_page_v;       /* elements */
+    const int32_t* page_table;   /* (device) [n_req, ld_table], the first max_pages columns are used */
+    int32_t ld_table, max_pages;
+    int32_t n_pages, page_size;
+} sv_paged_kv_t;
+
+enum { SV_ROTARY_INTERLEAVED = 1, SV_ROTARY_INVERSE = 2 };
+
+/* A rotation by position: pair m (m < rot_dim / 2) at position p turns by
+ * p (freq[m][0] + freq[m][1]) whole turns, and is scaled by mscale:
+ *   a' = mscale (a cos t - b sin t),  b' = mscale (b cos t + a sin t).
+ * Pairs are elements (m, m + rot_dim / 2) of a head, or (2m, 2m + 1) with
+ * SV_ROTARY_INTERLEAVED; elements from rot_dim on are copied.  With
+ * SV_ROTARY_INVERSE t is negated, which makes the call the gradient of the one
+ * without it.  The frequency is an unevaluated sum high + low of two fp32
+ * numbers and the whole turns are taken off before the sine, so the angle of
+ * any 31-bit position is good to a few 1e-7 turns. */
+typedef struct {
+    const float* freq; /* (device) [rot_dim / 2][2], or NULL: no rotation (rot_dim 0) */
+    int32_t rot_dim;   /* even, 0 <= rot_dim <= head_dim */
+    int32_t flags;     /* SV_ROTARY_* */
+    float mscale;
+} sv_rotary_t;
+
+/*
+ * y = x rotated by positions (device) int32 [tokens].  x and y hold tokens
+ * rows of x.heads heads of head_dim elements; y may be x itself (same strides)
+ * but must not overlap it otherwise.
+ *   Errors: SV_ERR_INVALID_ARG for null pointers, negative sizes, an odd
+ *   rot_dim or one above head_dim, y.heads != x.heads; SV_ERR_UNSUPPORTED for
+ *   head_dim > 256.
+ */
+sv_status_t sv_rotary(sv_heads_t x, sv_heads_t y, sv_dtype_t dt, int tokens, int head_dim, const int32_t* positions,
+                      sv_rotary_t rope, sv_stream_t stream);
+
+/*
+ * Append the windows' keys (rotated) and values to the cache, each token at
+ * its position.  k and v hold `tokens` rows of the cache's heads.  q, if
+ * q.data is not NULL, is rotated by the same positions into q_out (which may
+ * be q itself) in the same launch.  A token whose position lies outside the
+ * page table, or whose page number is out of range, is not appended (its
+ * query is still rotated).  Two tokens of a call must not share a slot.
+ *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, head counts that
+ *   differ, SV_ROTARY_INVERSE; SV_ERR_UNSUPPORTED for head_dim > 256.
+ */
+sv_status_t sv_kv_append(sv_heads_t k, sv_heads_t v, sv_paged_kv_t cache, sv_dtype_t dt, int tokens, int head_dim,
+                         int n_req, const int32_t* qo_indptr, const int32_t* kv_len, sv_rotary_t rope, sv_heads_t q,
+                         sv_heads_t q_out, int32_t* status, sv_stream_t stream);
+
+/* Workspace bytes of sv_paged_attention; 0 for sizes it does not handle. */
+size_t sv_attention_workspace_size(int max_window, int q_heads, int kv_heads, int head_dim);
+
+enum { SV_ATTN_FULL = 1 }; /* every row sees the whole cache (no causal limit), for windows drafted as a block */
+
+/*
+ * Attention of every window over its request's cache, which the window has
+ * been appended to.  Query head h reads key head h / (q.heads / cache heads).
+ * Row (token i, head h) at position p sees the keys j < kv_len[r] with j <= p
+ * (unless SV_ATTN_FULL) and, when window_keys > 0, j > p - window_keys:
+ *   s_j = scale q.k_j,  out = sum_j exp(s_j - m) v_j / l,  m = max_j s_j,
+ *   l = sum_j exp(s_j - m),  lse = m + ln l  (fp32).
+ * A row that sees no key, or only keys whose s_j is -inf, gets out = 0 and
+ * lse = -inf.  What a row does not see has no influence on it, be it NaN or
+ * infinite.  Sums and statistics are fp32; the weights exp(s_j - m) of bf16
+ * and fp16 calls are rounded to that type before they meet the values.
+ *   q and out: `tokens` rows; out must not overlap q.  lse (device) fp32
+ *   [tokens, q.heads] or NULL.  max_window: a promise (host) that no window is
+ *   longer; longer ones are refused (SV_ROW_BAD_LAYOUT, rows not written), and
+ *   so are requests with kv_len outside [0, max_pages * page_size].
+ *   Workspace: sv_attention_workspace_size(...).
+ *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, q.heads not a
+ *   multiple of the cache's heads, a scale that is not finite;
+ *   SV_ERR_UNSUPPORTED for head_dim > 256.
+ */
+sv_status_t sv_paged_attention(sv_heads_t q, sv_paged_kv_t cache, sv_dtype_t dt, int tokens, int head_dim, int n_req,
+                               const int32_t* qo_indptr, const int32_t* kv_len, int max_window, float scale,
+                               int window_keys, int flags, sv_heads_t out, float* lse, int32_t* status, void* ws,
+                               size_t ws_bytes, sv_stream_t stream);
 
 /*
  * Measurement aid (not part of the method): when both are non-NULL, every

@@ -8,6 +8,7 @@ fallback: if the library is missing or no GPU is present the calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -20,7 +21,7 @@ SV_OK, SV_ERR_INVALID_ARG, SV_ERR_WORKSPACE, SV_ERR_CUDA, SV_ERR_UNSUPPORTED = 0
 # per-position status bits (SV_ROW_* in sv.h)
 SV_ROW_NONFINITE, SV_ROW_EMPTY, SV_ROW_BAD_TOKEN, SV_ROW_BAD_PARAM, SV_ROW_BAD_LAYOUT = 1, 2, 4, 8, 16
 SV_ROW_Q_ZERO, SV_ROW_RESID_ZERO, SV_ROW_UNSUPPORTED, SV_ROW_TIMEOUT = 32, 64, 128, 256
-DTYPE_BF16, DTYPE_F32 = 0, 1
+DTYPE_BF16, DTYPE_F32, DTYPE_F16 = 0, 1, 2
 ROW_NONFINITE, ROW_EMPTY, ROW_BAD_TOKEN, ROW_BAD_PARAM, ROW_BAD_LAYOUT = 1, 2, 4, 8, 16
 ROW_Q_ZERO, ROW_RESID_ZERO, ROW_UNSUPPORTED, ROW_TIMEOUT = 32, 64, 128, 256
 ROW_ERROR_MASK = (ROW_NONFINITE | ROW_EMPTY | ROW_BAD_TOKEN | ROW_BAD_PARAM | ROW_BAD_LAYOUT | ROW_UNSUPPORTED
@@ -31,7 +32,8 @@ EXPORTED = ("sv_workspace_size", "sv_workspace_size_block", "sv_status_string", 
             "sv_set_hist_timing_events", "sv_verify_chain_noalloc", "sv_plan_budget_cost", "sv_verify_stats",
             "sv_verify_block", "sv_estimator_state_bytes", "sv_estimator_init", "sv_estimator_predict",
             "sv_estimator_observe", "sv_shard_record_bytes", "sv_verify_chain_shard_rows",
-            "sv_verify_chain_shard_merge", "sv_q_rows_bytes", "sv_estimator_predict_q", "sv_verify_chain_q")
+            "sv_verify_chain_shard_merge", "sv_q_rows_bytes", "sv_estimator_predict_q", "sv_verify_chain_q",
+            "sv_rotary", "sv_kv_append", "sv_attention_workspace_size", "sv_paged_attention")
 
 
 class SVError(RuntimeError):
@@ -54,6 +56,25 @@ class RowDesc(ctypes.Structure):
                 ("cutoff_ties", ctypes.c_int32), ("kept", ctypes.c_int32), ("argmax", ctypes.c_int32),
                 ("status", ctypes.c_int32), ("temperature", ctypes.c_float)]
 
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class PagedKV(ctypes.Structure):
+    _fields_ = [("k", Heads), ("v", Heads), ("stride_page_k", ctypes.c_int64), ("stride_page_v", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+
+ROTARY_INTERLEAVED, ROTARY_INVERSE = 1, 2   # sv_rotary_t.flags
+ATTN_FULL = 1                               # sv_paged_attention flags
 
 _lib = None
 
@@ -119,6 +140,14 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     L.sv_set_timing_events.restype = I
     L.sv_set_hist_timing_events.argtypes = [P, P]
     L.sv_set_hist_timing_events.restype = I
+    L.sv_rotary.argtypes = [Heads, Heads, I, I, I, P, RotaryArgs, P]
+    L.sv_rotary.restype = I
+    L.sv_kv_append.argtypes = [Heads, Heads, PagedKV, I, I, I, I, P, P, RotaryArgs, Heads, Heads, P, P]
+    L.sv_kv_append.restype = I
+    L.sv_attention_workspace_size.argtypes = [I, I, I, I]
+    L.sv_attention_workspace_size.restype = SZ
+    L.sv_paged_attention.argtypes = [Heads, PagedKV, I, I, I, I, P, P, I, ctypes.c_float, I, I, Heads, P, P, P, SZ, P]
+    L.sv_paged_attention.restype = I
     _lib = L
     return L
 
@@ -520,3 +549,207 @@ def verify_chain_q(target: torch.Tensor, draft: Optional[torch.Tensor], draft_to
                                     _ptr(o.accept_len), _ptr(o.out_tokens), _ptr(o.num_emitted), _ptr(o.row_status),
                                     _ptr(w), w.numel(), _stream(dev)))
     return o
+
+
+# ---------------------------------------------------------------------------
+# The target model's attention over the windows: rotary positions, append to
+# a paged cache, attention over it
+# ---------------------------------------------------------------------------
+_ATTN_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+
+
+def _attn_dtype(t: torch.Tensor) -> int:
+    code = _ATTN_DTYPES.get(t.dtype)
+    if code is None:
+        raise SVError(f"tensors must be bf16, fp16 or fp32, got {t.dtype}")
+    return code
+
+
+def _heads(t: torch.Tensor, like: Optional[torch.Tensor] = None) -> Heads:
+    """A [tokens, heads, head_dim] tensor whose last axis is contiguous."""
+    if not t.is_cuda:
+        raise SVError("tensors must live on the GPU (the library has no CPU path)")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise SVError(f"expected [tokens, heads, head_dim], got {tuple(shape)}")
+    if stride[2] != 1 and shape[2] != 1:
+        raise SVError("the elements of a head must be contiguous")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device or shape[2] != like.shape[2]):
+        raise SVError(f"expected {like.dtype} heads of {like.shape[2]} on {like.device}, "
+                      f"got {t.dtype} heads of {shape[2]} on {t.device}")
+    return Heads(t.data_ptr(), stride[0], stride[1], shape[1])
+
+
+def _paged(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, n_req: int,
+           like: torch.Tensor) -> PagedKV:
+    """A cache [n_pages, page_size, heads, head_dim] (any strides but the last) and its table [n_req, columns]."""
+    if not (k_pages.is_cuda and v_pages.is_cuda and page_table.is_cuda):
+        raise SVError("tensors must live on the GPU (the library has no CPU path)")
+    ks, vs = k_pages.stride(), v_pages.stride()
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise SVError("k_pages and v_pages must both be [n_pages, page_size, heads, head_dim]")
+    if (ks[3] != 1 or vs[3] != 1) and shape[3] != 1:
+        raise SVError("the elements of a head must be contiguous")
+    if k_pages.dtype != like.dtype or v_pages.dtype != like.dtype or shape[3] != like.shape[2]:
+        raise SVError(f"expected {like.dtype} pages with heads of {like.shape[2]}, "
+                      f"got {k_pages.dtype}, {v_pages.dtype} and {shape[3]}")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_req:
+        raise SVError("page_table must be int32 [requests, pages]")
+    ts = page_table.stride()
+    cols = page_table.shape[1]
+    if ts[1] != 1 and cols > 1:
+        raise SVError("the rows of page_table must be contiguous")
+    return PagedKV(Heads(k_pages.data_ptr(), ks[1], ks[2], shape[2]), Heads(v_pages.data_ptr(), vs[1], vs[2], shape[2]),
+                   ks[0], vs[0], page_table.data_ptr(), ts[0] if n_req > 1 else max(ts[0], cols), cols, shape[0],
+                   shape[1])
+
+
+def _vector(t: torch.Tensor, n: int, what: str) -> int:
+    """Address of a contiguous int32 [n] tensor on the GPU."""
+    if not t.is_cuda:
+        raise SVError("tensors must live on the GPU (the library has no CPU path)")
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise SVError(f"{what} must be a contiguous int32 [{n}]")
+    return t.data_ptr()
+
+
+def _rope(freq: Optional[torch.Tensor], flags: int, mscale: float) -> RotaryArgs:
+    if freq is None:
+        return RotaryArgs(None, 0, flags, mscale)
+    if not freq.is_cuda:
+        raise SVError("tensors must live on the GPU (the library has no CPU path)")
+    if freq.dtype != torch.float32 or freq.dim() != 2 or freq.shape[1] != 2 or not freq.is_contiguous():
+        raise SVError("freq must be a contiguous fp32 [rot_dim / 2, 2] (see rotary_frequencies)")
+    return RotaryArgs(freq.data_ptr(), 2 * freq.shape[0], flags, mscale)
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                       original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                       low_band: float = 1.0, high_band: float = 4.0, device="cuda"):
+    """(freq, mscale) of a rotation: fp32 [rot_dim / 2, 2], turns per position as high + low, for sv_rotary_t.
+
+    f_m = base ** (-2 m / rot_dim) radians per position, then for contexts `factor` times the original length:
+
+    * None       as it is;
+    * "linear"   f / factor (positions interpolated);
+    * "ntk"      base * factor ** (rot_dim / (rot_dim - 2)), so that the slowest pair slows down by factor;
+    * "yarn"     (Peng et al., "YaRN", 2023) pairs that turn more than beta_fast times over original_len are kept,
+                 those below beta_slow turns are divided by factor, a linear ramp over m in between, and
+                 mscale = 0.1 ln(factor) + 1;
+    * "bands"    pairs whose wavelength is below original_len / high_band are kept, above original_len / low_band
+                 divided by factor, in between blended by original_len / wavelength.
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise SVError("rot_dim must be even and positive")
+    if not (factor > 0.0 and math.isfinite(factor)) or not (base > 1.0 and math.isfinite(base)):
+        raise SVError("factor must be positive and base above 1")
+    if scaling in ("yarn", "bands") and original_len < 1:
+        raise SVError(f"{scaling} needs original_len")
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / max(rot_dim - 2, 1))
+    m = torch.arange(rot_dim // 2, dtype=torch.float64)
+    f = base ** (-2.0 * m / rot_dim)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        at = [rot_dim * math.log(original_len / (2.0 * math.pi * b)) / (2.0 * math.log(base))
+              for b in (beta_fast, beta_slow)]
+        low, high = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim - 1)
+        ramp = ((m - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        f = f * (1.0 - ramp) + f / factor * ramp
+        mscale = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+    elif scaling == "bands":
+        keep = ((original_len * f / (2.0 * math.pi) - low_band) / (high_band - low_band)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+    elif scaling not in (None, "ntk"):
+        raise SVError(f"unknown scaling {scaling!r}")
+    turns = f / (2.0 * math.pi)
+    high = turns.to(torch.float32)
+    freq = torch.stack([high, (turns - high.double()).to(torch.float32)], dim=1)
+    return freq.contiguous().to(device), mscale
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, interleaved: bool = False,
+           inverse: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """sv_rotary: x [tokens, heads, head_dim] rotated by positions int32 [tokens] (out may be x).  With
+    inverse=True it maps the gradient of the output to the gradient of the input."""
+    hx = _heads(x)
+    tokens, _, d = x.shape
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape:
+        raise SVError(f"out must be {tuple(x.shape)}")
+    flags = (ROTARY_INTERLEAVED if interleaved else 0) | (ROTARY_INVERSE if inverse else 0)
+    _check(load().sv_rotary(hx, _heads(out, x), _attn_dtype(x), tokens, d, _vector(positions, tokens, "positions"),
+                            _rope(freq, flags, mscale), _stream(x.device)))
+    return out
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              page_table: torch.Tensor, qo_indptr: torch.Tensor, kv_len: torch.Tensor,
+              freq: Optional[torch.Tensor] = None, interleaved: bool = False, mscale: float = 1.0,
+              q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """sv_kv_append: the windows' k (rotated, if freq is given) and v [tokens, heads, head_dim] into the cache
+    [n_pages, page_size, heads, head_dim] at the end of each request's kv_len tokens.  With q its rotation is
+    returned (into q_out if given, which may be q)."""
+    hk, hv = _heads(k), _heads(v, k)
+    tokens, _, d = k.shape
+    n = kv_len.numel()
+    if v.shape != k.shape:
+        raise SVError("k and v must have one shape")
+    hq, ho = Heads(None, 0, 0, 0), Heads(None, 0, 0, 0)
+    if q is not None:
+        if q.shape[0] != tokens:
+            raise SVError("q and k must have the same tokens")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise SVError(f"q_out must be {tuple(q.shape)}")
+        hq, ho = _heads(q, k), _heads(q_out, k)
+    _check(load().sv_kv_append(hk, hv, _paged(k_pages, v_pages, page_table, n, k), _attn_dtype(k), tokens, d, n,
+                               _vector(qo_indptr, n + 1, "qo_indptr"), _vector(kv_len, n, "kv_len"),
+                               _rope(freq, ROTARY_INTERLEAVED if interleaved else 0, mscale), hq, ho,
+                               None if status is None else _vector(status, n, "status"), _stream(k.device)))
+    return q_out
+
+
+@dataclass
+class AttentionOut:
+    out: torch.Tensor            # [tokens, heads, head_dim]
+    lse: Optional[torch.Tensor]  # [tokens, heads] fp32
+
+
+def attention_workspace_size(max_window: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    size = load().sv_attention_workspace_size(max_window, q_heads, kv_heads, head_dim)
+    if size == 0:
+        raise SVError("sizes beyond what the library supports")
+    return size
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                    qo_indptr: torch.Tensor, kv_len: torch.Tensor, max_window: int, scale: Optional[float] = None,
+                    window: int = 0, full: bool = False, out: Optional[torch.Tensor] = None, lse: bool = True,
+                    status: Optional[torch.Tensor] = None, ws: Optional[Workspace] = None) -> AttentionOut:
+    """sv_paged_attention: q [tokens, heads, head_dim], packed by qo_indptr, over the paged cache; no window is longer
+    than max_window.  scale defaults to head_dim ** -0.5; window > 0 limits every row to its last `window` keys;
+    full=True drops the causal limit."""
+    hq = _heads(q)
+    tokens, heads, d = q.shape
+    n = kv_len.numel()
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise SVError(f"out must be {tuple(q.shape)}")
+    norm = torch.empty((tokens, heads), dtype=torch.float32, device=q.device) if lse else None
+    cache = _paged(k_pages, v_pages, page_table, n, q)
+    w = _ws(ws, q.device, attention_workspace_size(max_window, heads, cache.k.heads, d))
+    _check(load().sv_paged_attention(hq, cache, _attn_dtype(q), tokens, d, n, _vector(qo_indptr, n + 1, "qo_indptr"),
+                                     _vector(kv_len, n, "kv_len"), max_window, d ** -0.5 if scale is None else scale,
+                                     window, ATTN_FULL if full else 0, _heads(out, q),
+                                     None if norm is None else norm.data_ptr(),
+                                     None if status is None else _vector(status, n, "status"), w.data_ptr(),
+                                     w.numel(), _stream(q.device)))
+    return AttentionOut(out, norm)
