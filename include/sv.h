@@ -499,8 +499,9 @@ sv_status_t sv_verify_chain_shard_merge(const void* records, int n_shards, int n
  *  - status (device) int32 [n_req] or NULL: SV_ROW_* bits are OR-ed into it;
  *    the caller clears it.  SV_ROW_BAD_LAYOUT: a window outside the token
  *    axis or longer than promised, a kv_len outside what the page table
- *    holds, a page number outside [0, n_pages).  Nothing outside the tensors
- *    is ever read or written.
+ *    holds, a page number outside [0, n_pages).  Results of that request are
+ *    then not to be used; other requests are not affected, and nothing
+ *    outside the tensors is ever read or written.
  */
 
 /* Token rows of some heads: element (token, head, e) is

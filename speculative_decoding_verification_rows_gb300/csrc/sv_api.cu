@@ -2,17 +2,12 @@
 // workspace carving and the launch sequence of each entry point.
 #include <stdint.h>
 
+#include "sv_attn.cuh"
 #include "sv_internal.cuh"
 
 using namespace sv;
 
-namespace {
-
-constexpr int kMaxVocab = kMaxCluster * kHistMaxSlice;   // 524,280: one cluster per row
-constexpr int kPlanMaxK = 4094;
-constexpr int kPlanMaxN = (1 << 20) - 1;
-
-int sm_count()
+int sv::sm_count()
 {
     static int cached[128] = {0};
     int dev = 0;
@@ -24,6 +19,12 @@ int sm_count()
     }
     return cached[dev];
 }
+
+namespace {
+
+constexpr int kMaxVocab = kMaxCluster * kHistMaxSlice;   // 524,280: one cluster per row
+constexpr int kPlanMaxK = 4094;
+constexpr int kPlanMaxN = (1 << 20) - 1;
 
 bool ws_ok(const void* ws, size_t bytes, size_t need)
 {

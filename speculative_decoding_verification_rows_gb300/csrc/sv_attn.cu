@@ -1,5 +1,6 @@
 // sv_attn.cu -- attention of ragged windows over a paged cache: the entry
-// point, and the kernel that takes every layout.
+// point, and the kernel that takes every layout (sv_attn_tc.cu has the one
+// for the usual ones).
 #include <math.h>
 
 #include "sv_attn.cuh"
@@ -119,7 +120,7 @@ extern "C" size_t sv_attention_workspace_size(int max_window, int q_heads, int k
     if (max_window < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || head_dim < 1 ||
         head_dim > kAttnMaxDim)
         return 0;
-    return 256;
+    return head_dim == 64 || head_dim == 128 ? attn_tc_workspace(max_window, q_heads / kv_heads, head_dim) : 256;
 }
 
 extern "C" sv_status_t sv_paged_attention(sv_heads_t q, sv_paged_kv_t cache, sv_dtype_t dt, int tokens, int head_dim,
@@ -154,5 +155,7 @@ extern "C" sv_status_t sv_paged_attention(sv_heads_t q, sv_paged_kv_t cache, sv_
     a.full = flags & SV_ATTN_FULL ? 1 : 0;
     a.group = q.heads / cache.k.heads;
     a.scale = scale;
-    return launch_attn_rows(a, dt, stream) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    const cudaError_t e = attn_tc_takes(a, dt) ? launch_attn_tc(a, dt, ws, sm_count(), stream)
+                                               : launch_attn_rows(a, dt, stream);
+    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

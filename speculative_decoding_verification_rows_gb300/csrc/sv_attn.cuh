@@ -67,6 +67,14 @@ struct AttnArgs {
     float scale;
 };
 
+// The kernel that takes every layout.
 cudaError_t launch_attn_rows(const AttnArgs& a, sv_dtype_t dt, cudaStream_t s);
+
+// The tensor-core kernels: which calls they take, and their workspace.
+bool attn_tc_takes(const AttnArgs& a, sv_dtype_t dt);
+size_t attn_tc_workspace(int max_window, int group, int head_dim);
+cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_sms, cudaStream_t s);
+
+int sm_count();   // of the current device
 
 }  // namespace sv

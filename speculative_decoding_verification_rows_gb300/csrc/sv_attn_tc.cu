@@ -1,0 +1,1073 @@
+// sv_attn_tc.cu -- paged attention of bf16 and fp16 heads of 64 or 128 on the
+// 5th-generation tensor cores.
+//
+// Rows.  The query heads of a key head share its keys, so a request's window
+// of n tokens and a group of G heads is one matrix of n G rows (row = token G
+// + head) per key head.  An item is up to 256 rows of it against the keys they
+// see, in tiles of 128 keys.  An item's tiles are its cost.
+//
+// Split.  The items of a call, one after the other, are a line of tiles; CTA b
+// of B takes tiles [b T / B, (b + 1) T / B) of it, wherever items begin and
+// end.  Every CTA so does the same work, for one request of a million keys as
+// for hundreds of short ones, with no host knowledge of the lengths.  An item
+// that lies in one CTA is written at once; the pieces of the others go to the
+// workspace in fp32 with their maximum and sum, and a second kernel joins them
+// in the order of the line.
+//
+// Inside a CTA (one per SM).  Warp 0 loads key and value tiles by TMA, page by
+// page, into a ring; one thread of warp 1 issues the matrix products; two
+// groups of four warps are two slots that turn scores into weights, a thread a
+// row.  A slot has its own rows of scores S and output O in TMEM.  An item of
+// more than 128 rows gives each slot half of the rows and both read every tile;
+// an item of up to 128 rows gives both slots all of its rows and every other
+// tile, and the slots' results are joined at its end.  Either way the tensor
+// core works for one slot while the other is at its weights.  The weights P
+// take the place of S in TMEM and are the left operand of P V from there, so
+// neither ever passes through shared memory.
+//
+// Statistics.  m and l are fp32, one row a thread.  O is rescaled only when a
+// row's maximum grows by more than 2^8: weights are then below 2^8 instead of
+// 1, which fp32 sums and bf16 weights take without loss; fp16 weights are kept
+// 2^7 times larger, away from fp16's subnormals.  Weights are rounded to the
+// type of the values because that is what the tensor core multiplies; l sums
+// them before the rounding.
+//
+// What is not seen.  Scores of hidden keys are replaced by -inf, whatever they
+// are.  A hidden key's value would still meet weight 0, and 0 times NaN is NaN:
+// in tiles with hidden keys the slots write zeros over the values that no row
+// of the item sees, and if a value that only some rows see is not finite they
+// do that tile's P V themselves, in fp32, leaving out weights of 0.
+#include <cuda.h>
+#include <float.h>
+#include <limits.h>
+
+#include "sv_attn.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kTile = 128;              // keys of a tile, rows of a slot
+constexpr int kTcThreads = 384;
+constexpr int kTcWarps = kTcThreads / 32;
+constexpr int kMinTiles = 2;            // fewest tiles worth a CTA of its own
+constexpr uint32_t kTmemCols = 512;
+
+// ---- PTX ---------------------------------------------------------------------
+__device__ __forceinline__ void tc_alloc(uint32_t* where)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tc_free(uint32_t base)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTmemCols));
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// The barrier's phase completes when every product issued so far has.
+__device__ __forceinline__ void tc_commit(unsigned long long* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+// D (TMEM) (+)= A B^T, A and B in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// The same with A in TMEM.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+#define SV_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), \
+                    "=r"(r[o + 6]), "=r"(r[o + 7])
+#define SV_W8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), \
+                    "r"(r[o + 6]), "r"(r[o + 7])
+// 32 columns of the warp's 32 lanes, a lane's columns to a thread.
+__device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24)
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st32(const uint32_t* r, uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::SV_W8(r, 0),
+        SV_W8(r, 8), SV_W8(r, 16), SV_W8(r, 24), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t tc_ld1(uint32_t addr)
+{
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    return r;
+}
+// One page's (or part of a page's) rows of 64 elements, 128-byte swizzled.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int e, int head, int token, int page,
+                                         unsigned long long* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(e), "r"(head), "r"(token), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Whether any of the 128 threads of a slot says so; also their barrier.
+__device__ __forceinline__ bool slot_any(int slot, bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(1 + slot)
+        : "memory");
+    return r != 0u;
+}
+
+// Shared-memory descriptor of 128-byte swizzled rows of 64 16-bit elements:
+// groups of 8 rows are 1,024 bytes apart; `lead` is the distance from one 64
+// element block of the row axis to the next where that axis is contiguous.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead)
+{
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)((lead >> 4) & 0x3fffu) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp32 accumulators, both operands of one 16-bit type.
+__device__ __forceinline__ constexpr uint32_t instr_desc(bool bf16, bool b_rows_contiguous, int n)
+{
+    return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_rows_contiguous ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+           (uint32_t)(kTile >> 4) << 24;
+}
+
+template <typename T>
+struct Kind;
+template <>
+struct Kind<__nv_bfloat16> {
+    static constexpr bool kBf16 = true;
+    static constexpr float kBias = 0.f;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t x)
+    {
+        return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    }
+    static constexpr uint32_t kExpMask = 0x7f80u;   // all ones: infinite or NaN
+};
+template <>
+struct Kind<__half> {
+    static constexpr bool kBf16 = false;
+    static constexpr float kBias = 7.f;             // log2 of what weights are multiplied by
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t x)
+    {
+        return __half22float2(*reinterpret_cast<const __half2*>(&x));
+    }
+    static constexpr uint32_t kExpMask = 0x7c00u;
+};
+
+// ---- the line of tiles -----------------------------------------------------------
+struct TcArgs {
+    AttnArgs a;
+    float* part;            // [2 grid][part_rows][D] pieces of items
+    float2* part_ml;        // [2 grid][part_rows] their maximum (log2) and sum
+    int4* rec;              // [grid][2] what each CTA left there
+    int part_rows;
+    int grid;
+    int page_shift;         // page_size = 1 << page_shift up to a tile, else a multiple of it
+    float scale_log2;       // |scale| log2 e
+    int negate;             // scale < 0
+};
+
+// A request's window as rows and items.
+struct Window {
+    int n, len, t0, rows, items;
+    __device__ __forceinline__ int row0(int item) const { return item * 2 * kTile; }
+    __device__ __forceinline__ int item_rows(int item) const { return min(rows - row0(item), 2 * kTile); }
+};
+__device__ __forceinline__ Window window_of(const AttnArgs& a, int r, bool report)
+{
+    Window w;
+    w.t0 = a.qo_indptr[r];
+    const int t1 = a.qo_indptr[r + 1];
+    w.len = a.kv_len[r];
+    w.n = t1 - w.t0;
+    const bool bad = w.t0 < 0 || t1 > a.tokens || w.n < 0 || w.n > a.max_window || w.len < 0 ||
+                     (long long)w.len > (long long)a.cache.max_pages * a.cache.page_size;
+    if (bad) {
+        if (report && a.status) atomicOr(&a.status[r], kBadLayout);
+        w.n = 0;
+    }
+    w.rows = w.n * a.group;
+    w.items = (w.rows + 2 * kTile - 1) / (2 * kTile);
+    return w;
+}
+// Keys [lo, hi) that the row of token i of a window sees.
+__device__ __forceinline__ int2 seen(const AttnArgs& a, const Window& w, int i)
+{
+    const int pos = w.len - w.n + i;
+    const int hi = a.full ? w.len : max(0, pos + 1);
+    const int lo = a.window_keys > 0 ? max(0, pos - a.window_keys + 1) : 0;
+    return make_int2(min(lo, hi), hi);
+}
+// Key tiles [x, y) of an item; at least one, so that an item without keys is
+// still somebody's to write.
+__device__ __forceinline__ int2 item_tiles(const AttnArgs& a, const Window& w, int item)
+{
+    const int first = w.row0(item) / a.group, last = (w.row0(item) + w.item_rows(item) - 1) / a.group;
+    const int lo = seen(a, w, first).x, hi = seen(a, w, last).y;
+    const int x = lo / kTile;
+    return make_int2(x, max((hi + kTile - 1) / kTile, x + 1));
+}
+__device__ __forceinline__ long long head_tiles(const AttnArgs& a, const Window& w)
+{
+    long long c = 0;
+    for (int i = 0; i < w.items; ++i) {
+        const int2 t = item_tiles(a, w, i);
+        c += t.y - t.x;
+    }
+    return c;
+}
+
+// A piece of an item: the part of the line one CTA has of it.
+struct Piece {
+    int r, head, item;
+    int kt0, nt;            // first key tile and their number
+    bool first, last;       // the item's first and last tile are in it
+    Window w;
+};
+
+// Walks over a CTA's part of the line.  Every role of the CTA has its own and
+// they all see the same pieces.
+struct Walk {
+    long long left;         // tiles still to come
+    int r, head, item, done;   // done: tiles of the item behind
+    Window w;
+    int2 tiles;
+
+    __device__ __forceinline__ bool next(const AttnArgs& a, Piece& p)
+    {
+        if (left <= 0) return false;
+        const int have = tiles.y - tiles.x;
+        p.r = r;
+        p.head = head;
+        p.item = item;
+        p.w = w;
+        p.kt0 = tiles.x + done;
+        p.nt = (int)min((long long)(have - done), left);
+        p.first = done == 0;
+        p.last = done + p.nt == have;
+        left -= p.nt;
+        done += p.nt;
+        if (p.last && left > 0) {
+            done = 0;
+            if (++item == w.items) {
+                item = 0;
+                if (++head == a.cache.k.heads) {
+                    head = 0;
+                    do {
+                        if (++r >= a.n_req) {                   // not reached: tiles are left
+                            left = 0;
+                            return true;
+                        }
+                        w = window_of(a, r, false);
+                    } while (w.items == 0);
+                }
+            }
+            tiles = item_tiles(a, w, item);
+        }
+        return true;
+    }
+};
+
+// ---- shared memory ----------------------------------------------------------------
+template <int D>
+struct TcSmem {
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kTileBytes = kTile * D * 2;
+    alignas(1024) unsigned char q[2][kTileBytes];
+    alignas(1024) unsigned char kv[kStages][kTileBytes];
+    unsigned long long full[kStages], empty[kStages];
+    unsigned long long q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2], ml_full, drain;
+    float2 ml[kTile];               // slot 1's statistics of an item both slots share
+    long long scan[kTcWarps + 1];
+    Walk start;
+    uint32_t tmem;
+    int aborted;                    // a wait gave up: every later wait gives up at once
+    int by_hand[2];                 // the slot has done this tile's P V itself
+};
+
+// A bounded wait; after one that gave up the kernel runs to its end without
+// waiting, with wrong results and SV_ROW_TIMEOUT.
+__device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t parity, int* aborted)
+{
+    for (long long i = 0; i < kWaitPolls; ++i) {
+        if (mbar_try_wait(bar, parity)) return;
+        if (*(volatile int*)aborted) return;
+    }
+    *(volatile int*)aborted = 1;
+}
+
+// Where the ring holds a piece's tiles: the keys of the first `ahead` tiles,
+// then values of tile j and keys of tile j + ahead, j = 0, 1, ...
+__device__ __forceinline__ int entry_v(int j, int nt, int ahead) { return min(ahead, nt) + j + max(0, min(j, nt - ahead)); }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_tc_kernel(const TcArgs t, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
+{
+    using S = TcSmem<D>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ unsigned char raw[];
+    S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const AttnArgs& a = t.a;
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.q_full[s], kTile);
+            mbar_init(&sm.s_full[s], 1);
+            mbar_init(&sm.p_full[s], kTile);
+            mbar_init(&sm.pv_done[s], 1);
+            mbar_init(&sm.o_free[s], kTile);
+            sm.by_hand[s] = 0;
+        }
+        mbar_init(&sm.ml_full, kTile);
+        mbar_init(&sm.drain, 1);
+        sm.aborted = 0;
+        sm.start.left = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) tc_alloc(&sm.tmem);
+    pdl_enter();
+
+    // The CTA's part of the line: the tiles of every request summed, then the
+    // request its part begins in.
+    long long total = 0, mine = 0, incl = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        long long begin = 0, end = 0;
+        if (pass == 1) {
+            const long long b = min((long long)t.grid, max(1ll, total / kMinTiles));
+            if ((int)blockIdx.x < b) {
+                begin = total * (int)blockIdx.x / b;
+                end = total * ((int)blockIdx.x + 1) / b;
+            }
+            if (end <= begin) break;
+        }
+        long long before = 0;
+        for (int r0 = 0; r0 < a.n_req; r0 += kTcThreads) {
+            const int r = r0 + tid;
+            if (pass == 0 || a.n_req > kTcThreads) {
+                mine = 0;
+                if (r < a.n_req) {
+                    const Window w = window_of(a, r, pass == 0 && blockIdx.x == 0);
+                    mine = head_tiles(a, w) * a.cache.k.heads;
+                }
+                incl = mine;
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, incl, x);
+                    if (lane >= x) incl += y;
+                }
+                __syncthreads();
+                if (lane == 31) sm.scan[warp] = incl;
+                __syncthreads();
+                long long chunk = 0;
+                for (int w = 0; w < kTcWarps; ++w) {
+                    if (w < warp) incl += sm.scan[w];
+                    chunk += sm.scan[w];
+                }
+                if (pass == 0) total += chunk;
+                if (pass == 1) incl += before;
+                before += chunk;
+            }
+            if (pass == 1 && incl > begin && incl - mine <= begin) {      // one thread of the CTA
+                Walk k;
+                k.left = end - begin;
+                k.r = r;
+                k.w = window_of(a, r, false);
+                const long long per_head = mine / a.cache.k.heads;
+                long long off = begin - (incl - mine);
+                k.head = (int)(off / per_head);
+                off -= k.head * per_head;
+                k.item = 0;
+                k.tiles = item_tiles(a, k.w, 0);
+                while (off >= k.tiles.y - k.tiles.x) {
+                    off -= k.tiles.y - k.tiles.x;
+                    k.tiles = item_tiles(a, k.w, ++k.item);
+                }
+                k.done = (int)off;
+                sm.start = k;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    Walk walk = sm.start;
+    Piece p;
+
+    if (warp == 0) {
+        // ---- loads: lane i has page i of a tile --------------------------------------
+        const int page_size = a.cache.page_size;
+        const int per_tile = page_size < kTile ? kTile >> t.page_shift : 1;
+        const int box_rows = page_size < kTile ? page_size : kTile;
+        int ring = 0;
+        uint32_t phase = 1;                       // the first round finds every stage empty
+        while (walk.next(a, p)) {
+            const int32_t* table = a.cache.page_table + (int64_t)p.r * a.cache.ld_table;
+            const int ahead = p.w.item_rows(p.item) > kTile ? 1 : 2;
+            const int2 keys = make_int2(seen(a, p.w, p.w.row0(p.item) / a.group).x,
+                                        seen(a, p.w, (p.w.row0(p.item) + p.w.item_rows(p.item) - 1) / a.group).y);
+            if (keys.y <= keys.x) continue;       // nobody sees anything
+            // This lane's page of tile kt (-1: none); bad numbers become a page past the end, which reads as zeros.
+            auto page_of = [&](int j) -> int {
+                if (j >= p.nt || lane >= per_tile) return -1;
+                const int key = (p.kt0 + j) * kTile + lane * box_rows;
+                if (key >= keys.y || key + box_rows <= keys.x) return -1;   // nobody sees them: not even their numbers count
+                int page = table[page_size < kTile ? key >> t.page_shift : key / page_size];
+                if (page < 0 || page >= a.cache.n_pages) {
+                    if (a.status) atomicOr(&a.status[p.r], kBadLayout);
+                    page = a.cache.n_pages;
+                }
+                return page;
+            };
+            auto load = [&](const CUtensorMap* map, int j, int page) {
+                wait_or_abort(&sm.empty[ring], phase, &sm.aborted);
+                const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+                if (lane == 0) mbar_expect_tx(&sm.full[ring], (uint32_t)(__popc(have) * box_rows * D * 2));
+                __syncwarp();
+                if (page >= 0) {
+                    const int token = page_size > kTile ? ((p.kt0 + j) * kTile) % page_size : 0;
+#pragma unroll
+                    for (int e = 0; e < D; e += 64)
+                        tma_rows(smem_u32(sm.kv[ring]) + (uint32_t)(e / 64 * kTile + lane * box_rows) * 128u, map, e,
+                                 p.head, token, page, &sm.full[ring]);
+                }
+                if (++ring == kStages) {
+                    ring = 0;
+                    phase ^= 1u;
+                }
+            };
+            int v0 = page_of(0), v1 = page_of(1), v2 = page_of(2);     // pages of tiles j, j + 1, j + 2
+            load(&map_k, 0, v0);
+            if (ahead == 2 && p.nt > 1) load(&map_k, 1, v1);
+            for (int j = 0; j < p.nt; ++j) {
+                const int v3 = page_of(j + 3);
+                load(&map_v, j, v0);
+                if (j + ahead < p.nt) load(&map_k, j + ahead, ahead == 1 ? v1 : v2);
+                v0 = v1;
+                v1 = v2;
+                v2 = v3;
+            }
+        }
+    } else if (warp == 1) {
+        // ---- matrix products: one thread ----------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t kQk = instr_desc(Kind<T>::kBf16, false, kTile);
+            constexpr uint32_t kPv = instr_desc(Kind<T>::kBf16, true, D);
+            int ring = 0;
+            uint32_t phase = 0;
+            uint32_t q_uses[2] = {0, 0}, steps[2] = {0, 0}, o_uses[2] = {0, 0};
+            auto ready = [&]() { wait_or_abort(&sm.full[ring], phase, &sm.aborted); };
+            auto advance = [&]() {
+                if (++ring == kStages) {
+                    ring = 0;
+                    phase ^= 1u;
+                }
+            };
+            auto qk = [&](int s) {
+                const uint32_t qa = smem_u32(sm.q[s]), ka = smem_u32(sm.kv[ring]);
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (uint32_t)(k / 4) * (kTile * 128) + (uint32_t)(k % 4) * 32;
+                    tc_mma_ss(tmem + s * kTile, smem_desc(qa + off, 16), smem_desc(ka + off, 16), kQk, k > 0);
+                }
+                tc_commit(&sm.s_full[s]);
+            };
+            auto pv = [&](int s, bool add) {
+                wait_or_abort(&sm.p_full[s], steps[s] & 1u, &sm.aborted);
+                ++steps[s];
+                if (!add) {
+                    if (o_uses[s]) wait_or_abort(&sm.o_free[s], (o_uses[s] - 1) & 1u, &sm.aborted);
+                    ++o_uses[s];
+                }
+                tc_fence_after();
+                if (*(volatile int*)&sm.by_hand[s]) {
+                    *(volatile int*)&sm.by_hand[s] = 0;
+                } else {
+                    const uint32_t va = smem_u32(sm.kv[ring]);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        tc_mma_ts(tmem + 256 + s * 128, tmem + s * kTile + k * 8, smem_desc(va + k * 2048, kTile * 128), kPv,
+                                  add || k > 0);
+                }
+                tc_commit(&sm.pv_done[s]);
+            };
+            auto q_ready = [&](int s) {
+                wait_or_abort(&sm.q_full[s], q_uses[s] & 1u, &sm.aborted);
+                ++q_uses[s];
+            };
+            while (walk.next(a, p)) {
+                const bool pair = p.w.item_rows(p.item) > kTile;
+                const int2 keys = make_int2(seen(a, p.w, p.w.row0(p.item) / a.group).x,
+                                            seen(a, p.w, (p.w.row0(p.item) + p.w.item_rows(p.item) - 1) / a.group).y);
+                if (keys.y <= keys.x) continue;
+                q_ready(0);
+                ready();
+                qk(0);
+                if (pair) {
+                    q_ready(1);
+                    qk(1);
+                }
+                tc_commit(&sm.empty[ring]);
+                advance();
+                if (!pair && p.nt > 1) {
+                    q_ready(1);
+                    ready();
+                    qk(1);
+                    tc_commit(&sm.empty[ring]);
+                    advance();
+                }
+                for (int j = 0; j < p.nt; ++j) {
+                    ready();                                     // values of tile j
+                    if (pair) {
+                        const int v_ring = ring;
+                        const uint32_t v_phase = phase;
+                        advance();
+                        const int k_ring = ring;
+                        const uint32_t k_phase = phase;
+                        const bool more = j + 1 < p.nt;
+                        for (int s = 0; s < 2; ++s) {
+                            ring = v_ring;
+                            phase = v_phase;
+                            pv(s, j > 0);
+                            if (s == 1) tc_commit(&sm.empty[ring]);
+                            ring = k_ring;
+                            phase = k_phase;
+                            if (more) {
+                                if (s == 0) ready();
+                                qk(s);
+                                if (s == 1) tc_commit(&sm.empty[ring]);
+                            }
+                        }
+                        if (more) advance();
+                    } else {
+                        const int s = j & 1;
+                        pv(s, j > 1);
+                        tc_commit(&sm.empty[ring]);
+                        advance();
+                        if (j + 2 < p.nt) {
+                            ready();
+                            qk(s);
+                            tc_commit(&sm.empty[ring]);
+                            advance();
+                        }
+                    }
+                }
+            }
+            if (*(volatile int*)&sm.aborted) {                   // nothing in flight when the kernel ends
+                tc_commit(&sm.drain);
+                for (long long i = 0; i < kWaitPolls && !mbar_try_wait(&sm.drain, 0); ++i) {}
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---- the slots: a thread a row ---------------------------------------------------
+        const int slot = (warp - 4) >> 2, sw = warp & 3, row = sw * 32 + lane;
+        const uint32_t lanes = (uint32_t)(sw * 32) << 16;
+        const uint32_t s_at = tmem + lanes + slot * kTile, o_at = tmem + lanes + 256 + slot * 128;
+        uint32_t steps[2] = {0, 0}, o_uses[2] = {0, 0}, ml_uses = 0;
+        long long ring_base = 0;
+        int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
+        while (walk.next(a, p)) {
+            const int row0 = p.w.row0(p.item), rows = p.w.item_rows(p.item);
+            const bool pair = rows > kTile;
+            const int2 first_sees = seen(a, p.w, row0 / a.group), last_sees = seen(a, p.w, (row0 + rows - 1) / a.group);
+            const int key_lo = first_sees.x, key_hi = last_sees.y;     // keys that some row sees
+            const int all_lo = last_sees.x, all_hi = first_sees.y;     // keys that every row sees
+            const int nt = key_hi > key_lo ? p.nt : 0;
+            int n_steps[2];
+            n_steps[0] = pair ? nt : (nt + 1) / 2;
+            n_steps[1] = pair ? nt : nt / 2;
+            const int my_steps = slot ? n_steps[1] : n_steps[0];
+            const int local = pair ? slot * kTile + row : row;         // row of the item
+            const int my_row = row0 + local;
+            const bool valid = local < rows;
+            const bool warp_valid = (pair ? slot * kTile : 0) + sw * 32 < rows;
+            int2 see = make_int2(0, INT_MAX);                          // rows of nobody: no masking
+            if (valid) see = seen(a, p.w, my_row / a.group);
+            if (my_steps > 0) {
+                // This slot's rows of Q; its last products with the rows before are done (their scores came).
+                constexpr int kVecs = D / 8;
+                const int base = row0 + (pair ? slot * kTile : 0);
+                for (int i = 0; i < kVecs; ++i) {
+                    const int c = i * kTile + (tid & 127), qr = c / kVecs, v = c % kVecs;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (base + qr < row0 + rows) {
+                        const int tok = (base + qr) / a.group, g = (base + qr) - tok * a.group;
+                        x = *reinterpret_cast<const uint4*>((const T*)a.q.data + (int64_t)(p.w.t0 + tok) * a.q.stride_token +
+                                                            (int64_t)(p.head * a.group + g) * a.q.stride_head + v * 8);
+                        if (t.negate) {
+                            x.x ^= 0x80008000u;
+                            x.y ^= 0x80008000u;
+                            x.z ^= 0x80008000u;
+                            x.w ^= 0x80008000u;
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(sm.q[slot] + (v / 8) * (kTile * 128) + qr * 128 + ((v ^ qr) & 7) * 16) = x;
+                }
+                fence_async_smem();
+                mbar_arrive(&sm.q_full[slot]);
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int st = 0; st < my_steps; ++st) {
+                const int j = pair ? st : 2 * st + slot;
+                const int k0 = (p.kt0 + j) * kTile;
+                wait_or_abort(&sm.s_full[slot], steps[slot] & 1u, &sm.aborted);
+                tc_fence_after();
+                if (warp_valid) {
+                    float s[kTile];
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 32) tc_ld32(reinterpret_cast<uint32_t*>(s + c), s_at + c);
+                    tc_wait_ld();
+                    if (__any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile)) {
+                        const int lo = see.x - k0, hi = see.y - k0;
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
+                    }
+                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 8) {
+                        mx0 = fmaxf(mx0, fmaxf(s[c], s[c + 1]));
+                        mx1 = fmaxf(mx1, fmaxf(s[c + 2], s[c + 3]));
+                        mx2 = fmaxf(mx2, fmaxf(s[c + 4], s[c + 5]));
+                        mx3 = fmaxf(mx3, fmaxf(s[c + 6], s[c + 7]));
+                    }
+                    const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+                    const bool grows = (mx - m) * t.scale_log2 > 8.f;   // from -inf: always, unless mx is -inf too
+                    if (__any_sync(0xffffffffu, grows)) {
+                        const float f = grows ? exp2_approx((m - mx) * t.scale_log2) : 1.f;
+                        if (grows) {
+                            m = mx;
+                            l *= f;
+                        }
+                        if (st > 0) {
+                            wait_or_abort(&sm.pv_done[slot], (steps[slot] - 1) & 1u, &sm.aborted);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tc_ld32(o, o_at + c);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tc_st32(o, o_at + c);
+                            }
+                        }
+                    }
+                    const float shift = Kind<T>::kBias - (m == -INFINITY ? 0.f : m * t.scale_log2);
+                    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 64) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float e0 = exp2_approx(fmaf(s[c + 2 * i], t.scale_log2, shift));
+                            const float e1 = exp2_approx(fmaf(s[c + 2 * i + 1], t.scale_log2, shift));
+                            const float e2 = exp2_approx(fmaf(s[c + 2 * i + 2], t.scale_log2, shift));
+                            const float e3 = exp2_approx(fmaf(s[c + 2 * i + 3], t.scale_log2, shift));
+                            l0 += e0;
+                            l1 += e1;
+                            l2 += e2;
+                            l3 += e3;
+                            w[i] = Kind<T>::pack(e0, e1);
+                            w[i + 1] = Kind<T>::pack(e2, e3);
+                        }
+                        tc_st32(w, s_at + c / 2);
+                    }
+                    l += (l0 + l1) + (l2 + l3);
+                    tc_wait_st();
+                }
+                if (k0 < all_lo || k0 + kTile > all_hi) {
+                    // A tile with hidden keys: its values as the products may read them.
+                    const int ahead = pair ? 1 : 2;
+                    const long long e = ring_base + entry_v(j, nt, ahead);
+                    const int stage = (int)(e % kStages);
+                    wait_or_abort(&sm.full[stage], (uint32_t)(e / kStages) & 1u, &sm.aborted);
+                    unsigned char* vt = sm.kv[stage];
+                    const int key = k0 + row;
+                    bool odd = false;
+                    if (key < key_lo || key >= key_hi) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    } else {
+                        uint32_t bad = 0;
+                        constexpr uint32_t m2 = Kind<T>::kExpMask | Kind<T>::kExpMask << 16;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 +
+                                                                            (c & 7) * 16);
+                            bad |= __vcmpeq2(x.x & m2, m2) | __vcmpeq2(x.y & m2, m2) | __vcmpeq2(x.z & m2, m2) |
+                                   __vcmpeq2(x.w & m2, m2);
+                        }
+                        odd = bad != 0;
+                    }
+                    fence_async_smem();
+                    if (slot_any(slot, odd)) {
+                        if (warp_valid) {
+                            if (st > 0) {
+                                wait_or_abort(&sm.pv_done[slot], (steps[slot] - 1) & 1u, &sm.aborted);
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                if (st > 0) {
+                                    tc_ld32(o, o_at + c);
+                                    tc_wait_ld();
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                                }
+#pragma unroll 1
+                                for (int kk = 0; kk < kTile; ++kk) {
+                                    const uint32_t w2 = tc_ld1(s_at + kk / 2);
+                                    tc_wait_ld();
+                                    const float2 wf = Kind<T>::unpack(w2);
+                                    const float wt = kk & 1 ? wf.y : wf.x;
+                                    if (wt == 0.f) continue;
+#pragma unroll
+                                    for (int i = 0; i < 32; i += 8) {
+                                        const int v = (c + i) / 8;
+                                        const uint4 x = *reinterpret_cast<const uint4*>(
+                                            vt + (v / 8) * (kTile * 128) + kk * 128 + ((v ^ kk) & 7) * 16);
+                                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                        for (int y = 0; y < 4; ++y) {
+                                            const float2 f = Kind<T>::unpack(xs[y]);
+                                            o[i + 2 * y] = __float_as_uint(fmaf(wt, f.x, __uint_as_float(o[i + 2 * y])));
+                                            o[i + 2 * y + 1] =
+                                                __float_as_uint(fmaf(wt, f.y, __uint_as_float(o[i + 2 * y + 1])));
+                                        }
+                                    }
+                                }
+                                __syncwarp();
+                                tc_st32(o, o_at + c);
+                            }
+                            tc_wait_st();
+                        }
+                        if (row == 0) *(volatile int*)&sm.by_hand[slot] = 1;
+                    }
+                }
+                ++steps[slot];
+                tc_fence_before();
+                mbar_arrive(&sm.p_full[slot]);
+            }
+            ring_base += 2 * nt;
+            steps[slot ^ 1] += slot ? n_steps[0] : n_steps[1];
+
+            // ---- the piece's end: the row's sums go out ------------------------------------
+            const bool both = !pair && n_steps[1] > 0;
+            const float m2 = m == -INFINITY ? 0.f : m * t.scale_log2;
+            if (my_steps > 0) {
+                wait_or_abort(&sm.pv_done[slot], (steps[slot] - 1) & 1u, &sm.aborted);
+                tc_fence_after();
+            }
+            if (both && slot == 1) {
+                if (o_uses[1]) wait_or_abort(&sm.o_free[1], (o_uses[1] - 1) & 1u, &sm.aborted);   // slot 0 has read the last ones
+                sm.ml[row] = make_float2(m2, l);
+                mbar_arrive(&sm.ml_full);
+            }
+            if (pair || slot == 0) {
+                float f0 = 1.f, f1 = 0.f, mt = m2, lt = l;
+                if (both) {
+                    wait_or_abort(&sm.ml_full, ml_uses & 1u, &sm.aborted);
+                    wait_or_abort(&sm.pv_done[1], (steps[1] - 1) & 1u, &sm.aborted);
+                    tc_fence_after();
+                    const float2 o = sm.ml[row];
+                    if (l == 0.f) {
+                        mt = o.x;
+                    } else if (o.y != 0.f) {
+                        mt = fmaxf(m2, o.x);
+                    }
+                    f0 = l == 0.f ? 0.f : exp2_approx(m2 - mt);
+                    f1 = o.y == 0.f ? 0.f : exp2_approx(o.x - mt);
+                    lt = l * f0 + o.y * f1;
+                }
+                const bool whole = p.first && p.last;
+                const int part = 2 * (int)blockIdx.x + (p.first ? 1 : 0);
+                const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
+                const float g0 = f0 * inv, g1 = f1 * inv;
+                const int tok = my_row / a.group, g = my_row - tok * a.group;
+                const int64_t token = p.w.t0 + tok;
+                const int head = p.head * a.group + g;
+                if (warp_valid) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        if (my_steps > 0) {
+                            tc_ld32(o, o_at + c);
+                            tc_wait_ld();
+                        }
+                        float x[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = my_steps > 0 && lt != 0.f ? __uint_as_float(o[i]) * g0 : 0.f;
+                        if (both) {
+                            tc_ld32(o, o_at + 128 + c);
+                            tc_wait_ld();
+                            if (f1 != 0.f) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) x[i] = fmaf(__uint_as_float(o[i]), g1, f0 == 0.f ? 0.f : x[i]);
+                            }
+                        }
+                        if (valid && whole) {
+                            T* dst = (T*)a.out.data + token * a.out.stride_token + (int64_t)head * a.out.stride_head + c;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8)
+                                *reinterpret_cast<uint4*>(dst + i) =
+                                    make_uint4(Kind<T>::pack(x[i], x[i + 1]), Kind<T>::pack(x[i + 2], x[i + 3]),
+                                               Kind<T>::pack(x[i + 4], x[i + 5]), Kind<T>::pack(x[i + 6], x[i + 7]));
+                        } else if (valid) {
+                            float* dst = t.part + ((int64_t)part * t.part_rows + local) * D + c;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        }
+                    }
+                    if (valid && whole) {
+                        if (a.lse)
+                            a.lse[token * a.q.heads + head] =
+                                lt == 0.f ? -INFINITY : (mt - Kind<T>::kBias) * 0.69314718055994531f + logf(lt);
+                    } else if (valid) {
+                        t.part_ml[(int64_t)part * t.part_rows + local] = make_float2(mt - Kind<T>::kBias, lt);
+                    }
+                }
+                tc_fence_before();
+                if (my_steps > 0) mbar_arrive(&sm.o_free[slot]);
+                if (both) mbar_arrive(&sm.o_free[1]);
+            }
+            if (n_steps[0] > 0) ++o_uses[0];
+            if (n_steps[1] > 0) ++o_uses[1];
+            if (both) ++ml_uses;
+            if (!p.first) rec0 = make_int4(p.last ? 1 : 2, 0, 0, 0);
+            if (p.first && !p.last) rec1 = make_int4(1, p.r, p.head, p.item);
+        }
+        if (slot == 0 && row == 0) {
+            t.rec[2 * blockIdx.x] = rec0;
+            t.rec[2 * blockIdx.x + 1] = rec1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (sm.aborted) {
+        if (warp == 0)                                    // loads in flight land before the kernel ends
+            for (int i = lane; i < kStages; i += 32)
+                for (int ph = 0; ph < 2; ++ph)
+                    for (long long x = 0; x < kWaitPolls / 16 && !mbar_try_wait(&sm.full[i], (uint32_t)ph); ++x) {}
+        if (a.status)
+            for (int r = tid; r < a.n_req; r += kTcThreads) atomicOr(&a.status[r], kTimeout);
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tc_free(tmem);
+    }
+}
+
+// Joins the pieces of an item: CTA x of the first kernel began it, the ones
+// after it have the rest.  A warp a row; pieces in the order of the line.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) attn_join_kernel(const TcArgs t)
+{
+    pdl_enter();
+    const AttnArgs& a = t.a;
+    const int c0 = (int)blockIdx.x;
+    const int4 rec = t.rec[2 * c0 + 1];
+    if (!rec.x) return;
+    const Window w = window_of(a, rec.y, false);
+    const int rows = w.item_rows(rec.w), row0 = w.row0(rec.w);
+    int last = c0 + 1;
+    while (last < t.grid - 1 && t.rec[2 * last].x == 2) ++last;
+    const int lane = (int)threadIdx.x & 31;
+    for (int row = (int)blockIdx.y * 4 + ((int)threadIdx.x >> 5); row < rows; row += (int)gridDim.y * 4) {
+        const int64_t at0 = (int64_t)(2 * c0 + 1) * t.part_rows + row;
+        auto at = [&](int c) { return c == c0 ? at0 : (int64_t)(2 * c) * t.part_rows + row; };
+        float mt = -INFINITY;
+        for (int c = c0; c <= last; ++c) {
+            const float2 ml = t.part_ml[at(c)];
+            if (ml.y != 0.f) mt = fmaxf(mt, ml.x);
+        }
+        constexpr int kE = D / 32;
+        float x[kE], lt = 0.f;
+#pragma unroll
+        for (int i = 0; i < kE; ++i) x[i] = 0.f;
+#pragma unroll 4
+        for (int c = c0; c <= last; ++c) {
+            const float2 ml = t.part_ml[at(c)];
+            const float* src = t.part + at(c) * D + lane * kE;
+            float y[kE];
+#pragma unroll
+            for (int i = 0; i < kE; ++i) y[i] = src[i];
+            if (ml.y == 0.f) continue;
+            const float f = exp2_approx(ml.x - mt);
+            lt = fmaf(ml.y, f, lt);
+#pragma unroll
+            for (int i = 0; i < kE; ++i) x[i] = fmaf(y[i], f, x[i]);
+        }
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const int tok = (row0 + row) / a.group, g = (row0 + row) - tok * a.group;
+        const int64_t token = w.t0 + tok;
+        const int head = rec.z * a.group + g;
+        T* dst = (T*)a.out.data + token * a.out.stride_token + (int64_t)head * a.out.stride_head + lane * kE;
+        uint32_t o[kE / 2];
+#pragma unroll
+        for (int i = 0; i < kE; i += 2) o[i / 2] = Kind<T>::pack(x[i] * inv, x[i + 1] * inv);
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) reinterpret_cast<uint32_t*>(dst)[i] = o[i];
+        if (a.lse && lane == 0)
+            a.lse[token * a.q.heads + head] = lt == 0.f ? -INFINITY : mt * 0.69314718055994531f + logf(lt);
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static const EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+bool make_map(CUtensorMap* m, const sv_heads_t& h, int64_t stride_page, const sv_paged_kv_t& c, int head_dim, bool bf16)
+{
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)h.heads, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages};
+    const cuuint64_t row = (cuuint64_t)head_dim * 2;     // stride of an axis of one
+    const cuuint64_t strides[3] = {h.heads > 1 ? (cuuint64_t)h.stride_head * 2 : row, (cuuint64_t)h.stride_token * 2,
+                                   c.n_pages > 1 ? (cuuint64_t)stride_page * 2 : row};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile), 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, h.data, dims, strides, box,
+              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int part_rows(int max_window, int group)
+{
+    const long long r = (long long)max_window * group;
+    return (int)(r > kTile ? 2 * kTile : r < 1 ? 1 : r);
+}
+
+template <typename T, int D>
+cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s)
+{
+    const size_t smem = sizeof(TcSmem<D>) + 1024;
+    static_assert(sizeof(TcSmem<D>) + 1024 <= 232448, "shared memory of one CTA");
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attn_tc_kernel<T, D>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv);
+    if (e != cudaSuccess) return e;
+    const int y = (t.part_rows + 3) / 4;
+    return launch_pdl(attn_join_kernel<T, D>, dim3(t.grid - 1, y > 16 ? 16 : y), dim3(128), 0, s, t);
+}
+
+}  // namespace
+
+constexpr int kTcMaxGrid = 152;   // CTAs the workspace has room for: one per SM
+
+size_t attn_tc_workspace(int max_window, int group, int head_dim)
+{
+    const size_t rows = 2 * (size_t)kTcMaxGrid * (size_t)part_rows(max_window, group);
+    return 256 + sizeof(int4) * 2 * kTcMaxGrid + rows * sizeof(float2) + rows * (size_t)head_dim * sizeof(float);
+}
+
+bool attn_tc_takes(const AttnArgs& a, sv_dtype_t dt)
+{
+    const sv_paged_kv_t& c = a.cache;
+    const int p = c.page_size;
+    return (dt == SV_DTYPE_BF16 || dt == SV_DTYPE_F16) && (a.head_dim == 64 || a.head_dim == 128) &&
+           ((p >= 8 && p <= kTile && kTile % p == 0) || p % kTile == 0) && c.n_pages > 0 &&
+           (long long)c.max_pages * p <= 1ll << 30 && heads_aligned(a.q, 8, 2) && heads_aligned(a.out, 8, 2) &&
+           heads_aligned(c.k, 8, 2) && heads_aligned(c.v, 8, 2) && c.stride_page_k % 8 == 0 && c.stride_page_v % 8 == 0 &&
+           c.k.stride_token > 0 && c.v.stride_token > 0 && c.k.stride_head > 0 && c.v.stride_head > 0 &&
+           c.stride_page_k > 0 && c.stride_page_v > 0;
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_sms, cudaStream_t s)
+{
+    TcArgs t{};
+    t.a = a;
+    t.part_rows = part_rows(a.max_window, a.group);
+    t.grid = num_sms < kTcMaxGrid ? (num_sms < 2 ? 2 : num_sms) : kTcMaxGrid;
+    char* w = static_cast<char*>(ws);
+    const size_t rows = 2 * (size_t)kTcMaxGrid * (size_t)t.part_rows;
+    t.rec = reinterpret_cast<int4*>(w);
+    t.part_ml = reinterpret_cast<float2*>(w + sizeof(int4) * 2 * kTcMaxGrid);
+    t.part = reinterpret_cast<float*>(w + (sizeof(int4) * 2 * kTcMaxGrid + rows * sizeof(float2) + 255) / 256 * 256);
+    t.page_shift = 0;
+    while (a.cache.page_size < kTile && (1 << t.page_shift) < a.cache.page_size) ++t.page_shift;
+    t.scale_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, FLT_MIN);   // above 0: hidden scores stay -inf
+    t.negate = a.scale < 0.f;
+    const bool bf16 = dt == SV_DTYPE_BF16;
+    CUtensorMap mk, mv;
+    if (!make_map(&mk, a.cache.k, a.cache.stride_page_k, a.cache, a.head_dim, bf16) ||
+        !make_map(&mv, a.cache.v, a.cache.stride_page_v, a.cache, a.head_dim, bf16))
+        return cudaErrorInvalidValue;
+    if (a.head_dim == 64)
+        return bf16 ? launch_tc<__nv_bfloat16, 64>(t, mk, mv, s) : launch_tc<__half, 64>(t, mk, mv, s);
+    return bf16 ? launch_tc<__nv_bfloat16, 128>(t, mk, mv, s) : launch_tc<__half, 128>(t, mk, mv, s);
+}
+
+}  // namespace sv
