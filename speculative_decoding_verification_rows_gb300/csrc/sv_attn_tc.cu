@@ -109,12 +109,29 @@ __device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr)
         : "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t* r, uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : SV_R8(r, 0), SV_R8(r, 8)
+        : "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tc_st32(const uint32_t* r, uint32_t addr)
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
         "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::SV_W8(r, 0),
         SV_W8(r, 8), SV_W8(r, 16), SV_W8(r, 24), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(const uint32_t* r, uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::SV_W8(r, 0),
+        SV_W8(r, 8), "r"(addr)
         : "memory");
 }
 __device__ __forceinline__ uint32_t tc_ld1(uint32_t addr)
@@ -324,8 +341,10 @@ struct TcSmem {
     unsigned long long full[kStages], empty[kStages];
     unsigned long long q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2], ml_full, drain;
     float2 ml[kTile];               // slot 1's statistics of an item both slots share
-    long long scan[kTcWarps + 1];
+    long long scan[kTcWarps];
     Walk start;
+    Walk walk[kTcWarps];            // a warp's place on the line and its piece: in registers they would cost the
+    Piece piece[kTcWarps];          // slots the room for their scores
     uint32_t tmem;
     int aborted;                    // a wait gave up: every later wait gives up at once
     int by_hand[2];                 // the slot has done this tile's P V itself
@@ -342,6 +361,17 @@ __device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t 
     *(volatile int*)aborted = 1;
 }
 
+// The warp's next piece, in shared memory.
+template <typename S>
+__device__ __forceinline__ bool next_piece(S& sm, const AttnArgs& a, int warp, int lane)
+{
+    uint32_t more = 0;
+    __syncwarp();
+    if (lane == 0) more = sm.walk[warp].next(a, sm.piece[warp]);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, more, 0) != 0u;
+}
+
 // Where the ring holds a piece's tiles: the keys of the first `ahead` tiles,
 // then values of tile j and keys of tile j + ahead, j = 0, 1, ...
 __device__ __forceinline__ int entry_v(int j, int nt, int ahead) { return min(ahead, nt) + j + max(0, min(j, nt - ahead)); }
@@ -352,8 +382,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 {
     using S = TcSmem<D>;
     constexpr int kStages = S::kStages;
-    extern __shared__ unsigned char raw[];
-    S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) unsigned char raw[];
+    S& sm = *reinterpret_cast<S*>(raw);
     const AttnArgs& a = t.a;
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -442,9 +472,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    Walk walk = sm.start;
-    Piece p;
-
+    // The slots hold a row of 128 scores a thread, the other warps little: of
+    // the 384 x 168 registers of the launch, 128 x 88 + 256 x 208.
+    if (lane == 0) sm.walk[warp] = sm.start;
+    const Piece& p = sm.piece[warp];
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
         // ---- loads: lane i has page i of a tile --------------------------------------
         const int page_size = a.cache.page_size;
@@ -452,7 +485,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int box_rows = page_size < kTile ? page_size : kTile;
         int ring = 0;
         uint32_t phase = 1;                       // the first round finds every stage empty
-        while (walk.next(a, p)) {
+        while (next_piece(sm, a, warp, lane)) {
             const int32_t* table = a.cache.page_table + (int64_t)p.r * a.cache.ld_table;
             const int ahead = p.w.item_rows(p.item) > kTile ? 1 : 2;
             const int2 keys = make_int2(seen(a, p.w, p.w.row0(p.item) / a.group).x,
@@ -501,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp == 1) {
         // ---- matrix products: one thread ----------------------------------------------
-        if (lane == 0) {
+        {
             constexpr uint32_t kQk = instr_desc(Kind<T>::kBf16, false, kTile);
             constexpr uint32_t kPv = instr_desc(Kind<T>::kBf16, true, D);
             int ring = 0;
@@ -528,7 +561,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 wait_or_abort(&sm.p_full[s], steps[s] & 1u, &sm.aborted);
                 ++steps[s];
                 if (!add) {
-                    if (o_uses[s]) wait_or_abort(&sm.o_free[s], (o_uses[s] - 1) & 1u, &sm.aborted);
+                    wait_or_abort(&sm.o_free[s], ~o_uses[s] & 1u, &sm.aborted);   // the first finds it free
                     ++o_uses[s];
                 }
                 tc_fence_after();
@@ -547,7 +580,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 wait_or_abort(&sm.q_full[s], q_uses[s] & 1u, &sm.aborted);
                 ++q_uses[s];
             };
-            while (walk.next(a, p)) {
+            while (next_piece(sm, a, warp, lane)) {
+                if (lane != 0) continue;
                 const bool pair = p.w.item_rows(p.item) > kTile;
                 const int2 keys = make_int2(seen(a, p.w, p.w.row0(p.item) / a.group).x,
                                             seen(a, p.w, (p.w.row0(p.item) + p.w.item_rows(p.item) - 1) / a.group).y);
@@ -605,21 +639,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
             }
-            if (*(volatile int*)&sm.aborted) {                   // nothing in flight when the kernel ends
+            if (lane == 0 && *(volatile int*)&sm.aborted) {      // nothing in flight when the kernel ends
                 tc_commit(&sm.drain);
                 for (long long i = 0; i < kWaitPolls && !mbar_try_wait(&sm.drain, 0); ++i) {}
             }
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- the slots: a thread a row ---------------------------------------------------
         const int slot = (warp - 4) >> 2, sw = warp & 3, row = sw * 32 + lane;
         const uint32_t lanes = (uint32_t)(sw * 32) << 16;
         const uint32_t s_at = tmem + lanes + slot * kTile, o_at = tmem + lanes + 256 + slot * 128;
-        uint32_t steps[2] = {0, 0}, o_uses[2] = {0, 0}, ml_uses = 0;
-        long long ring_base = 0;
-        int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
-        while (walk.next(a, p)) {
+        uint32_t steps[2] = {0, 0}, o_uses = 0, ml_uses = 0;   // o_uses: of slot 1
+        uint32_t ring_base = 0;
+        if (slot == 0 && row == 0) t.rec[2 * blockIdx.x] = t.rec[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        while (next_piece(sm, a, warp, lane)) {
             const int row0 = p.w.row0(p.item), rows = p.w.item_rows(p.item);
             const bool pair = rows > kTile;
             const int2 first_sees = seen(a, p.w, row0 / a.group), last_sees = seen(a, p.w, (row0 + rows - 1) / a.group);
@@ -660,9 +696,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_arrive(&sm.q_full[slot]);
             }
             float m = -INFINITY, l = 0.f;
+            const int key0 = p.kt0 * kTile;
             for (int st = 0; st < my_steps; ++st) {
                 const int j = pair ? st : 2 * st + slot;
-                const int k0 = (p.kt0 + j) * kTile;
+                const int k0 = key0 + j * kTile;
                 wait_or_abort(&sm.s_full[slot], steps[slot] & 1u, &sm.aborted);
                 tc_fence_after();
                 if (warp_valid) {
@@ -671,9 +708,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int c = 0; c < kTile; c += 32) tc_ld32(reinterpret_cast<uint32_t*>(s + c), s_at + c);
                     tc_wait_ld();
                     if (__any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile)) {
-                        const int lo = see.x - k0, hi = see.y - k0;
+                        const uint32_t lo = (uint32_t)(see.x - k0), count = (uint32_t)(see.y - see.x);
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
+                        for (int c = 0; c < kTile; ++c) s[c] = (uint32_t)c - lo < count ? s[c] : -INFINITY;
                     }
                     float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
@@ -695,23 +732,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             wait_or_abort(&sm.pv_done[slot], (steps[slot] - 1) & 1u, &sm.aborted);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tc_ld32(o, o_at + c);
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tc_ld16(o, o_at + c);
                                 tc_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tc_st32(o, o_at + c);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tc_st16(o, o_at + c);
                             }
                         }
                     }
                     const float shift = Kind<T>::kBias - (m == -INFINITY ? 0.f : m * t.scale_log2);
                     float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 64) {
-                        uint32_t w[32];
+                    for (int c = 0; c < kTile; c += 32) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < 16; i += 2) {
                             const float e0 = exp2_approx(fmaf(s[c + 2 * i], t.scale_log2, shift));
                             const float e1 = exp2_approx(fmaf(s[c + 2 * i + 1], t.scale_log2, shift));
                             const float e2 = exp2_approx(fmaf(s[c + 2 * i + 2], t.scale_log2, shift));
@@ -723,7 +760,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             w[i] = Kind<T>::pack(e0, e1);
                             w[i + 1] = Kind<T>::pack(e2, e3);
                         }
-                        tc_st32(w, s_at + c / 2);
+                        tc_st16(w, s_at + c / 2);
                     }
                     l += (l0 + l1) + (l2 + l3);
                     tc_wait_st();
@@ -731,9 +768,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (k0 < all_lo || k0 + kTile > all_hi) {
                     // A tile with hidden keys: its values as the products may read them.
                     const int ahead = pair ? 1 : 2;
-                    const long long e = ring_base + entry_v(j, nt, ahead);
-                    const int stage = (int)(e % kStages);
-                    wait_or_abort(&sm.full[stage], (uint32_t)(e / kStages) & 1u, &sm.aborted);
+                    const uint32_t e = ring_base + (uint32_t)entry_v(j, nt, ahead);
+                    const uint32_t stage = e % kStages;
+                    wait_or_abort(&sm.full[stage], e / kStages & 1u, &sm.aborted);
                     unsigned char* vt = sm.kv[stage];
                     const int key = k0 + row;
                     bool odd = false;
@@ -805,7 +842,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&sm.p_full[slot]);
             }
-            ring_base += 2 * nt;
+            ring_base = (ring_base + 2u * (uint32_t)nt) % (2 * kStages);   // what its stage and phase need
             steps[slot ^ 1] += slot ? n_steps[0] : n_steps[1];
 
             // ---- the piece's end: the row's sums go out ------------------------------------
@@ -816,7 +853,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after();
             }
             if (both && slot == 1) {
-                if (o_uses[1]) wait_or_abort(&sm.o_free[1], (o_uses[1] - 1) & 1u, &sm.aborted);   // slot 0 has read the last ones
+                wait_or_abort(&sm.o_free[1], ~o_uses & 1u, &sm.aborted);   // slot 0 has read the last ones
                 sm.ml[row] = make_float2(m2, l);
                 mbar_arrive(&sm.ml_full);
             }
@@ -888,15 +925,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (my_steps > 0) mbar_arrive(&sm.o_free[slot]);
                 if (both) mbar_arrive(&sm.o_free[1]);
             }
-            if (n_steps[0] > 0) ++o_uses[0];
-            if (n_steps[1] > 0) ++o_uses[1];
+            if (n_steps[1] > 0) ++o_uses;
             if (both) ++ml_uses;
-            if (!p.first) rec0 = make_int4(p.last ? 1 : 2, 0, 0, 0);
-            if (p.first && !p.last) rec1 = make_int4(1, p.r, p.head, p.item);
-        }
-        if (slot == 0 && row == 0) {
-            t.rec[2 * blockIdx.x] = rec0;
-            t.rec[2 * blockIdx.x + 1] = rec1;
+            if (slot == 0 && row == 0) {
+                if (!p.first) t.rec[2 * blockIdx.x].x = p.last ? 1 : 2;
+                if (p.first && !p.last) t.rec[2 * blockIdx.x + 1] = make_int4(1, p.r, p.head, p.item);
+            }
         }
     }
     tc_fence_before();
@@ -1013,8 +1047,8 @@ int part_rows(int max_window, int group)
 template <typename T, int D>
 cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s)
 {
-    const size_t smem = sizeof(TcSmem<D>) + 1024;
-    static_assert(sizeof(TcSmem<D>) + 1024 <= 232448, "shared memory of one CTA");
+    const size_t smem = sizeof(TcSmem<D>);
+    static_assert(sizeof(TcSmem<D>) <= 232448, "shared memory of one CTA");
     cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(attn_tc_kernel<T, D>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv);
