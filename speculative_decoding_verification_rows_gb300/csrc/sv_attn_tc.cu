@@ -218,14 +218,22 @@ struct Kind<__half> {
 };
 
 // ---- the line of tiles -----------------------------------------------------------
+// x / d for 0 <= x < 2^31 by a multiplication: m = ceil(2^(31 + L) / d) with
+// 2^L >= d is off by less than d in 2^(31 + L), so x m / 2^(31 + L) by less than
+// 1 / d, which does not reach the next whole number.
+struct Divisor {
+    uint32_t m, shift;
+    __device__ __forceinline__ int operator()(int x) const { return (int)((uint64_t)(uint32_t)x * m >> shift); }
+};
+
 struct TcArgs {
     AttnArgs a;
+    Divisor by_group, by_page;
     float* part;            // [2 grid][part_rows][D] pieces of items
     float2* part_ml;        // [2 grid][part_rows] their maximum (log2) and sum
     int4* rec;              // [grid][2] what each CTA left there
     int part_rows;
     int grid;
-    int page_shift;         // page_size = 1 << page_shift up to a tile, else a multiple of it
     float scale_log2;       // |scale| log2 e
     int negate;             // scale < 0
 };
@@ -254,7 +262,8 @@ __device__ __forceinline__ Window window_of(const AttnArgs& a, int r, bool repor
     return w;
 }
 // Keys [lo, hi) that the row of token i of a window sees.
-__device__ __forceinline__ int2 seen(const AttnArgs& a, const Window& w, int i)
+template <typename W>
+__device__ __forceinline__ int2 seen(const AttnArgs& a, const W& w, int i)
 {
     const int pos = w.len - w.n + i;
     const int hi = a.full ? w.len : max(0, pos + 1);
@@ -263,19 +272,20 @@ __device__ __forceinline__ int2 seen(const AttnArgs& a, const Window& w, int i)
 }
 // Key tiles [x, y) of an item; at least one, so that an item without keys is
 // still somebody's to write.
-__device__ __forceinline__ int2 item_tiles(const AttnArgs& a, const Window& w, int item)
+__device__ __forceinline__ int2 item_tiles(const TcArgs& t, const Window& w, int item)
 {
-    const int first = w.row0(item) / a.group, last = (w.row0(item) + w.item_rows(item) - 1) / a.group;
-    const int lo = seen(a, w, first).x, hi = seen(a, w, last).y;
+    const int first = t.by_group(w.row0(item)), last = t.by_group(w.row0(item) + w.item_rows(item) - 1);
+    const int lo = seen(t.a, w, first).x, hi = seen(t.a, w, last).y;
     const int x = lo / kTile;
     return make_int2(x, max((hi + kTile - 1) / kTile, x + 1));
 }
-__device__ __forceinline__ long long head_tiles(const AttnArgs& a, const Window& w)
+__device__ __forceinline__ long long head_tiles(const TcArgs& t, const Window& w)
 {
     long long c = 0;
+#pragma unroll 1
     for (int i = 0; i < w.items; ++i) {
-        const int2 t = item_tiles(a, w, i);
-        c += t.y - t.x;
+        const int2 x = item_tiles(t, w, i);
+        c += x.y - x.x;
     }
     return c;
 }
@@ -283,55 +293,80 @@ __device__ __forceinline__ long long head_tiles(const AttnArgs& a, const Window&
 // A piece of an item: the part of the line one CTA has of it.
 struct Piece {
     int r, head, item;
-    int kt0, nt;            // first key tile and their number
-    bool first, last;       // the item's first and last tile are in it
-    Window w;
+    int row0, rows;         // the item's rows among the window's
+    int kt0, nt;            // first key tile and their number; 0: no row sees a key, -1: no more pieces
+    int first, last;        // the item's first and last tile are in it
+    int t0, n, len;         // the window's first token, its length, the request's cached tokens
+    int key_lo, key_hi;     // keys that some row of the item sees
+    int all_lo, all_hi;     // keys that every row of it sees
+
+    // An item of more than 128 rows: each slot has rows of its own and every
+    // tile; otherwise both have all the rows and every other tile.  A unit is
+    // one slot's work on one tile; unit u is slot u & 1's.
+    __device__ __forceinline__ bool pair() const { return rows > kTile; }
+    __device__ __forceinline__ int steps(int slot) const { return pair() ? nt : (nt + 1 - slot) >> 1; }
 };
 
-// Walks over a CTA's part of the line.  Every role of the CTA has its own and
-// they all see the same pieces.
+// Walks over a CTA's part of the line.
 struct Walk {
-    long long left;         // tiles still to come
+    long long left;            // tiles still to come
     int r, head, item, done;   // done: tiles of the item behind
     Window w;
     int2 tiles;
 
-    __device__ __forceinline__ bool next(const AttnArgs& a, Piece& p)
+    __device__ __forceinline__ void next(const TcArgs& t, Piece& p)
     {
-        if (left <= 0) return false;
+        if (left <= 0) {
+            p.nt = -1;
+            return;
+        }
         const int have = tiles.y - tiles.x;
         p.r = r;
         p.head = head;
         p.item = item;
-        p.w = w;
+        p.row0 = w.row0(item);
+        p.rows = w.item_rows(item);
         p.kt0 = tiles.x + done;
-        p.nt = (int)min((long long)(have - done), left);
+        const int nt = (int)min((long long)(have - done), left);
         p.first = done == 0;
-        p.last = done + p.nt == have;
-        left -= p.nt;
-        done += p.nt;
-        if (p.last && left > 0) {
+        const bool last = done + nt == have;
+        p.last = last;
+        p.t0 = w.t0;
+        p.n = w.n;
+        p.len = w.len;
+        const int2 top = seen(t.a, w, t.by_group(p.row0)), bottom = seen(t.a, w, t.by_group(p.row0 + p.rows - 1));
+        p.key_lo = top.x;
+        p.key_hi = bottom.y;
+        p.all_lo = bottom.x;
+        p.all_hi = top.y;
+        p.nt = bottom.y > top.x ? nt : 0;
+        left -= nt;
+        done += nt;
+        if (last && left > 0) {
             done = 0;
             if (++item == w.items) {
                 item = 0;
-                if (++head == a.cache.k.heads) {
+                if (++head == t.a.cache.k.heads) {
                     head = 0;
+#pragma unroll 1
                     do {
-                        if (++r >= a.n_req) {                   // not reached: tiles are left
+                        if (++r >= t.a.n_req) {                 // not reached: tiles are left
                             left = 0;
-                            return true;
+                            return;
                         }
-                        w = window_of(a, r, false);
+                        w = window_of(t.a, r, false);
                     } while (w.items == 0);
                 }
             }
-            tiles = item_tiles(a, w, item);
+            tiles = item_tiles(t, w, item);
         }
-        return true;
     }
 };
 
 // ---- shared memory ----------------------------------------------------------------
+constexpr int kPieces = 4;
+constexpr int kPieceReaders = 10;   // warps: loads, products, two slots
+
 template <int D>
 struct TcSmem {
     static constexpr int kStages = D == 128 ? 5 : 10;
@@ -340,11 +375,11 @@ struct TcSmem {
     alignas(1024) unsigned char kv[kStages][kTileBytes];
     unsigned long long full[kStages], empty[kStages];
     unsigned long long q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2], ml_full, drain;
+    unsigned long long piece_full[kPieces], piece_empty[kPieces];
+    Piece pieces[kPieces];          // warp 2 walks ahead of the other roles
     float2 ml[kTile];               // slot 1's statistics of an item both slots share
     long long scan[kTcWarps];
     Walk start;
-    Walk walk[kTcWarps];            // a warp's place on the line and its piece: in registers they would cost the
-    Piece piece[kTcWarps];          // slots the room for their scores
     uint32_t tmem;
     int aborted;                    // a wait gave up: every later wait gives up at once
     int by_hand[2];                 // the slot has done this tile's P V itself
@@ -354,40 +389,71 @@ struct TcSmem {
 // waiting, with wrong results and SV_ROW_TIMEOUT.
 __device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t parity, int* aborted)
 {
-    for (long long i = 0; i < kWaitPolls; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < (int)kWaitPolls; ++i) {
         if (mbar_try_wait(bar, parity)) return;
         if (*(volatile int*)aborted) return;
     }
     *(volatile int*)aborted = 1;
 }
 
-// The warp's next piece, in shared memory.
-template <typename S>
-__device__ __forceinline__ bool next_piece(S& sm, const AttnArgs& a, int warp, int lane)
-{
-    uint32_t more = 0;
-    __syncwarp();
-    if (lane == 0) more = sm.walk[warp].next(a, sm.piece[warp]);
-    __syncwarp();
-    return __shfl_sync(0xffffffffu, more, 0) != 0u;
-}
-
 // Where the ring holds a piece's tiles: the keys of the first `ahead` tiles,
 // then values of tile j and keys of tile j + ahead, j = 0, 1, ...
-__device__ __forceinline__ int entry_v(int j, int nt, int ahead) { return min(ahead, nt) + j + max(0, min(j, nt - ahead)); }
+__device__ __forceinline__ uint32_t entry_v(int j, int nt, int ahead)
+{
+    return (uint32_t)(min(ahead, nt) + j + max(0, min(j, nt - ahead)));
+}
+__device__ __forceinline__ uint32_t entry_k(int j, int ahead) { return (uint32_t)(j < ahead ? j : 2 * j - ahead + 1); }
 
+__device__ __forceinline__ bool one_lane()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0u;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c)
+{
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b)
+{
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long pair_of(float lo, float hi)
+{
+    unsigned long long d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 halves(unsigned long long x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+
+// The code is kept small on purpose (one copy of every step, loops that are not
+// unrolled): the roles run different parts of it at the same time, and at
+// 195 KB, with the steps inlined wherever they occur, instruction misses took
+// most of the time of short items.
 template <typename T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    attn_tc_kernel(const TcArgs t, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
+    attn_tc_kernel(const __grid_constant__ TcArgs t, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v)
 {
     using S = TcSmem<D>;
-    constexpr int kStages = S::kStages;
+    constexpr uint32_t kStages = S::kStages;
     extern __shared__ __align__(1024) unsigned char raw[];
     S& sm = *reinterpret_cast<S*>(raw);
     const AttnArgs& a = t.a;
-    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = (int)threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < (int)kStages; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
         }
@@ -398,6 +464,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&sm.pv_done[s], 1);
             mbar_init(&sm.o_free[s], kTile);
             sm.by_hand[s] = 0;
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&sm.piece_full[i], 1);
+            mbar_init(&sm.piece_empty[i], kPieceReaders);
         }
         mbar_init(&sm.ml_full, kTile);
         mbar_init(&sm.drain, 1);
@@ -410,27 +480,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     // The CTA's part of the line: the tiles of every request summed, then the
     // request its part begins in.
-    long long total = 0, mine = 0, incl = 0;
+    long long total = 0, per_head = 0, incl = 0;
+#pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         long long begin = 0, end = 0;
         if (pass == 1) {
-            const long long b = min((long long)t.grid, max(1ll, total / kMinTiles));
-            if ((int)blockIdx.x < b) {
-                begin = total * (int)blockIdx.x / b;
-                end = total * ((int)blockIdx.x + 1) / b;
-            }
+            const int b = (int)min((long long)t.grid, max(1ll, total / kMinTiles)), x = (int)blockIdx.x;
+            if (x >= b) break;
+            const long long each = total / b;
+            const int more = (int)(total - each * b);          // the first CTAs have one tile more
+            begin = each * x + min(x, more);
+            end = begin + each + (x < more);
             if (end <= begin) break;
         }
         long long before = 0;
+#pragma unroll 1
         for (int r0 = 0; r0 < a.n_req; r0 += kTcThreads) {
             const int r = r0 + tid;
             if (pass == 0 || a.n_req > kTcThreads) {
-                mine = 0;
-                if (r < a.n_req) {
-                    const Window w = window_of(a, r, pass == 0 && blockIdx.x == 0);
-                    mine = head_tiles(a, w) * a.cache.k.heads;
-                }
-                incl = mine;
+                per_head = 0;
+                if (r < a.n_req) per_head = head_tiles(t, window_of(a, r, pass == 0 && blockIdx.x == 0));
+                incl = per_head * a.cache.k.heads;
 #pragma unroll
                 for (int x = 1; x < 32; x <<= 1) {
                     const long long y = __shfl_up_sync(0xffffffffu, incl, x);
@@ -440,6 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 31) sm.scan[warp] = incl;
                 __syncthreads();
                 long long chunk = 0;
+#pragma unroll 1
                 for (int w = 0; w < kTcWarps; ++w) {
                     if (w < warp) incl += sm.scan[w];
                     chunk += sm.scan[w];
@@ -448,20 +519,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (pass == 1) incl += before;
                 before += chunk;
             }
+            const long long mine = per_head * a.cache.k.heads;
             if (pass == 1 && incl > begin && incl - mine <= begin) {      // one thread of the CTA
                 Walk k;
                 k.left = end - begin;
                 k.r = r;
                 k.w = window_of(a, r, false);
-                const long long per_head = mine / a.cache.k.heads;
+                k.head = k.item = 0;
                 long long off = begin - (incl - mine);
-                k.head = (int)(off / per_head);
-                off -= k.head * per_head;
-                k.item = 0;
-                k.tiles = item_tiles(a, k.w, 0);
-                while (off >= k.tiles.y - k.tiles.x) {
+#pragma unroll 1
+                for (; off >= per_head; ++k.head) off -= per_head;
+#pragma unroll 1
+                for (;; ++k.item) {
+                    k.tiles = item_tiles(t, k.w, k.item);
+                    if (off < k.tiles.y - k.tiles.x) break;
                     off -= k.tiles.y - k.tiles.x;
-                    k.tiles = item_tiles(a, k.w, ++k.item);
                 }
                 k.done = (int)off;
                 sm.start = k;
@@ -474,472 +546,458 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tmem = sm.tmem;
     // The slots hold a row of 128 scores a thread, the other warps little: of
     // the 384 x 168 registers of the launch, 128 x 88 + 256 x 208.
-    if (lane == 0) sm.walk[warp] = sm.start;
-    const Piece& p = sm.piece[warp];
+    // Piece k of the CTA, for every lane of a reading warp; false after the last.
+    auto piece_ready = [&](uint32_t k) {
+        wait_or_abort(&sm.piece_full[k % kPieces], k / kPieces & 1u, &sm.aborted);
+        return sm.pieces[k % kPieces].nt >= 0 && !*(volatile int*)&sm.aborted;
+    };
+    auto piece_release = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.piece_empty[k % kPieces]);
+    };
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0) {
-        // ---- loads: lane i has page i of a tile --------------------------------------
-        const int page_size = a.cache.page_size;
-        const int per_tile = page_size < kTile ? kTile >> t.page_shift : 1;
-        const int box_rows = page_size < kTile ? page_size : kTile;
-        int ring = 0;
-        uint32_t phase = 1;                       // the first round finds every stage empty
-        while (next_piece(sm, a, warp, lane)) {
-            const int32_t* table = a.cache.page_table + (int64_t)p.r * a.cache.ld_table;
-            const int ahead = p.w.item_rows(p.item) > kTile ? 1 : 2;
-            const int2 keys = make_int2(seen(a, p.w, p.w.row0(p.item) / a.group).x,
-                                        seen(a, p.w, (p.w.row0(p.item) + p.w.item_rows(p.item) - 1) / a.group).y);
-            if (keys.y <= keys.x) continue;       // nobody sees anything
-            // This lane's page of tile kt (-1: none); bad numbers become a page past the end, which reads as zeros.
-            auto page_of = [&](int j) -> int {
-                if (j >= p.nt || lane >= per_tile) return -1;
-                const int key = (p.kt0 + j) * kTile + lane * box_rows;
-                if (key >= keys.y || key + box_rows <= keys.x) return -1;   // nobody sees them: not even their numbers count
-                int page = table[page_size < kTile ? key >> t.page_shift : key / page_size];
-                if (page < 0 || page >= a.cache.n_pages) {
-                    if (a.status) atomicOr(&a.status[p.r], kBadLayout);
-                    page = a.cache.n_pages;
-                }
-                return page;
-            };
-            auto load = [&](const CUtensorMap* map, int j, int page) {
-                wait_or_abort(&sm.empty[ring], phase, &sm.aborted);
-                const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-                if (lane == 0) mbar_expect_tx(&sm.full[ring], (uint32_t)(__popc(have) * box_rows * D * 2));
-                __syncwarp();
-                if (page >= 0) {
-                    const int token = page_size > kTile ? ((p.kt0 + j) * kTile) % page_size : 0;
-#pragma unroll
-                    for (int e = 0; e < D; e += 64)
-                        tma_rows(smem_u32(sm.kv[ring]) + (uint32_t)(e / 64 * kTile + lane * box_rows) * 128u, map, e,
-                                 p.head, token, page, &sm.full[ring]);
-                }
-                if (++ring == kStages) {
-                    ring = 0;
-                    phase ^= 1u;
-                }
-            };
-            int v0 = page_of(0), v1 = page_of(1), v2 = page_of(2);     // pages of tiles j, j + 1, j + 2
-            load(&map_k, 0, v0);
-            if (ahead == 2 && p.nt > 1) load(&map_k, 1, v1);
-            for (int j = 0; j < p.nt; ++j) {
-                const int v3 = page_of(j + 3);
-                load(&map_v, j, v0);
-                if (j + ahead < p.nt) load(&map_k, j + ahead, ahead == 1 ? v1 : v2);
-                v0 = v1;
-                v1 = v2;
-                v2 = v3;
-            }
-        }
-    } else if (warp == 1) {
-        // ---- matrix products: one thread ----------------------------------------------
-        {
-            constexpr uint32_t kQk = instr_desc(Kind<T>::kBf16, false, kTile);
-            constexpr uint32_t kPv = instr_desc(Kind<T>::kBf16, true, D);
-            int ring = 0;
-            uint32_t phase = 0;
-            uint32_t q_uses[2] = {0, 0}, steps[2] = {0, 0}, o_uses[2] = {0, 0};
-            auto ready = [&]() { wait_or_abort(&sm.full[ring], phase, &sm.aborted); };
-            auto advance = [&]() {
-                if (++ring == kStages) {
-                    ring = 0;
-                    phase ^= 1u;
-                }
-            };
-            auto qk = [&](int s) {
-                const uint32_t qa = smem_u32(sm.q[s]), ka = smem_u32(sm.kv[ring]);
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (uint32_t)(k / 4) * (kTile * 128) + (uint32_t)(k % 4) * 32;
-                    tc_mma_ss(tmem + s * kTile, smem_desc(qa + off, 16), smem_desc(ka + off, 16), kQk, k > 0);
-                }
-                tc_commit(&sm.s_full[s]);
-            };
-            auto pv = [&](int s, bool add) {
-                wait_or_abort(&sm.p_full[s], steps[s] & 1u, &sm.aborted);
-                ++steps[s];
-                if (!add) {
-                    wait_or_abort(&sm.o_free[s], ~o_uses[s] & 1u, &sm.aborted);   // the first finds it free
-                    ++o_uses[s];
-                }
-                tc_fence_after();
-                if (*(volatile int*)&sm.by_hand[s]) {
-                    *(volatile int*)&sm.by_hand[s] = 0;
-                } else {
-                    const uint32_t va = smem_u32(sm.kv[ring]);
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        tc_mma_ts(tmem + 256 + s * 128, tmem + s * kTile + k * 8, smem_desc(va + k * 2048, kTile * 128), kPv,
-                                  add || k > 0);
-                }
-                tc_commit(&sm.pv_done[s]);
-            };
-            auto q_ready = [&](int s) {
-                wait_or_abort(&sm.q_full[s], q_uses[s] & 1u, &sm.aborted);
-                ++q_uses[s];
-            };
-            while (next_piece(sm, a, warp, lane)) {
-                if (lane != 0) continue;
-                const bool pair = p.w.item_rows(p.item) > kTile;
-                const int2 keys = make_int2(seen(a, p.w, p.w.row0(p.item) / a.group).x,
-                                            seen(a, p.w, (p.w.row0(p.item) + p.w.item_rows(p.item) - 1) / a.group).y);
-                if (keys.y <= keys.x) continue;
-                q_ready(0);
-                ready();
-                qk(0);
-                if (pair) {
-                    q_ready(1);
-                    qk(1);
-                }
-                tc_commit(&sm.empty[ring]);
-                advance();
-                if (!pair && p.nt > 1) {
-                    q_ready(1);
-                    ready();
-                    qk(1);
-                    tc_commit(&sm.empty[ring]);
-                    advance();
-                }
-                for (int j = 0; j < p.nt; ++j) {
-                    ready();                                     // values of tile j
-                    if (pair) {
-                        const int v_ring = ring;
-                        const uint32_t v_phase = phase;
-                        advance();
-                        const int k_ring = ring;
-                        const uint32_t k_phase = phase;
-                        const bool more = j + 1 < p.nt;
-                        for (int s = 0; s < 2; ++s) {
-                            ring = v_ring;
-                            phase = v_phase;
-                            pv(s, j > 0);
-                            if (s == 1) tc_commit(&sm.empty[ring]);
-                            ring = k_ring;
-                            phase = k_phase;
-                            if (more) {
-                                if (s == 0) ready();
-                                qk(s);
-                                if (s == 1) tc_commit(&sm.empty[ring]);
-                            }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 0) {
+            // ---- loads: lane i has page i of a tile --------------------------------------
+            const int page_size = a.cache.page_size;
+            const int box_rows = min(page_size, kTile);
+            uint32_t base = 0;                        // ring entries of the pieces before
+#pragma unroll 1
+            for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
+                const Piece& p = sm.pieces[pk % kPieces];
+                const int nt = p.nt, key0 = p.kt0 * kTile, key_lo = p.key_lo, key_hi = p.key_hi, head = p.head;
+                const int32_t* table = a.cache.page_table + (int64_t)p.r * a.cache.ld_table;
+                const int ahead = p.pair() ? 1 : 2;
+                // Page numbers of tiles u .. u + 3; a tile's are read when they are needed three tiles later.
+                int p0 = -1, p1 = -1, p2 = -1, p3 = -1;
+#pragma unroll 1
+                for (int u = -3; u < nt; ++u) {
+                    p0 = p1;
+                    p1 = p2;
+                    p2 = p3;
+                    p3 = -1;
+                    const int key = key0 + (u + 3) * kTile + lane * box_rows;
+                    if (u + 3 < nt && lane * box_rows < kTile && key < key_hi && key + box_rows > key_lo)
+                        p3 = table[t.by_page(key)];   // pages that nobody sees are not looked at
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {     // values of tile u, keys of tile u + ahead
+                        const int j = half ? u + ahead : u;
+                        if (j < 0 || j >= nt || (half && u < -ahead)) continue;
+                        const uint32_t e = base + (half ? entry_k(j, ahead) : entry_v(j, nt, ahead)), stage = e % kStages;
+                        const int key_of_page = key0 + j * kTile + lane * box_rows;
+                        const bool mine = lane * box_rows < kTile && key_of_page < key_hi && key_of_page + box_rows > key_lo;
+                        int page = !half ? p0 : ahead == 1 ? p1 : p2;
+                        if (mine && (page < 0 || page >= a.cache.n_pages)) {
+                            if (a.status) atomicOr(&a.status[p.r], kBadLayout);
+                            page = a.cache.n_pages;            // past the end: reads as zeros
                         }
-                        if (more) advance();
-                    } else {
-                        const int s = j & 1;
-                        pv(s, j > 1);
-                        tc_commit(&sm.empty[ring]);
-                        advance();
-                        if (j + 2 < p.nt) {
-                            ready();
-                            qk(s);
-                            tc_commit(&sm.empty[ring]);
-                            advance();
+                        const uint32_t have = __ballot_sync(0xffffffffu, mine);
+                        wait_or_abort(&sm.empty[stage], ~(e / kStages) & 1u, &sm.aborted);   // the first round finds it empty
+                        if (lane == 0) mbar_expect_tx(&sm.full[stage], (uint32_t)(__popc(have) * box_rows * D * 2));
+                        __syncwarp();
+                        if (mine) {
+                            const int token = page_size > kTile ? key_of_page - t.by_page(key_of_page) * page_size : 0;
+                            const CUtensorMap* map = half ? &map_k : &map_v;
+#pragma unroll
+                            for (int x = 0; x < D; x += 64)
+                                tma_rows(smem_u32(sm.kv[stage]) + (uint32_t)(x / 64 * kTile + lane * box_rows) * 128u, map, x,
+                                         head, token, page, &sm.full[stage]);
                         }
                     }
                 }
+                base = (base + 2u * (uint32_t)nt) % (2 * kStages);   // what stage and phase need of it
             }
-            if (lane == 0 && *(volatile int*)&sm.aborted) {      // nothing in flight when the kernel ends
-                tc_commit(&sm.drain);
-                for (long long i = 0; i < kWaitPolls && !mbar_try_wait(&sm.drain, 0); ++i) {}
+        } else if (warp == 1) {
+            // ---- matrix products: one lane issues them ------------------------------------
+            constexpr uint32_t kQk = instr_desc(Kind<T>::kBf16, false, kTile);
+            constexpr uint32_t kPv = instr_desc(Kind<T>::kBf16, true, D);
+            const uint64_t q_desc = smem_desc(smem_u32(sm.q[0]), 16), k_desc = smem_desc(smem_u32(sm.kv[0]), 16),
+                           v_desc = smem_desc(smem_u32(sm.kv[0]), kTile * 128);
+            constexpr uint32_t kBytes = S::kTileBytes >> 4;    // a tile in a descriptor's units
+            uint32_t base = 0, q_uses[2] = {0, 0}, steps[2] = {0, 0}, o_uses[2] = {0, 0};
+#pragma unroll 1
+            for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
+                const Piece& p = sm.pieces[pk % kPieces];
+                const bool pair = p.pair();
+                const int nt = p.nt, ahead = pair ? 1 : 2, units = pair ? 2 * nt : nt;
+                // P V of unit u, then the scores of unit u + 2 in their place.
+#pragma unroll 1
+                for (int u = -2; u < units; ++u) {
+                    const int s = u & 1;
+                    if (u >= 0) {
+                        const int j = pair ? u >> 1 : u;
+                        const uint32_t e = base + entry_v(j, nt, ahead), stage = e % kStages;
+                        wait_or_abort(&sm.full[stage], e / kStages & 1u, &sm.aborted);
+                        wait_or_abort(&sm.p_full[s], (s ? steps[1] : steps[0]) & 1u, &sm.aborted);
+                        if (s) ++steps[1]; else ++steps[0];
+                        const bool add = u >= 2;
+                        if (!add) {
+                            wait_or_abort(&sm.o_free[s], ~(s ? o_uses[1] : o_uses[0]) & 1u, &sm.aborted);   // at first it is
+                            if (s) ++o_uses[1]; else ++o_uses[0];
+                        }
+                        tc_fence_after();
+                        const bool by_hand = *(volatile int*)&sm.by_hand[s];
+                        const uint32_t o_at = tmem + 256 + s * 128, p_at = tmem + s * kTile;
+                        const uint64_t vd = v_desc + stage * kBytes;
+                        if (one_lane()) {
+                            if (!by_hand) {
+#pragma unroll
+                                for (int k = 0; k < kTile / 16; ++k)
+                                    tc_mma_ts(o_at, p_at + k * 8, vd + k * (2048 >> 4), kPv, add || k > 0);
+                            }
+                            tc_commit(&sm.pv_done[s]);
+                            if (!pair || s) tc_commit(&sm.empty[stage]);       // its last reader
+                        }
+                        __syncwarp();
+                        if (by_hand && lane == 0) *(volatile int*)&sm.by_hand[s] = 0;
+                    }
+                    if (u + 2 < units) {
+                        const int j = pair ? (u + 2) >> 1 : u + 2;
+                        const uint32_t e = base + entry_k(j, ahead), stage = e % kStages;
+                        if (u < 0) {
+                            wait_or_abort(&sm.q_full[s], (s ? q_uses[1] : q_uses[0]) & 1u, &sm.aborted);
+                            if (s) ++q_uses[1]; else ++q_uses[0];
+                        }
+                        wait_or_abort(&sm.full[stage], e / kStages & 1u, &sm.aborted);
+                        tc_fence_after();
+                        const uint32_t s_at = tmem + s * kTile;
+                        const uint64_t qd = q_desc + s * kBytes, kd = k_desc + stage * kBytes;
+                        if (one_lane()) {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = ((uint32_t)(k / 4) * (kTile * 128) + (uint32_t)(k % 4) * 32) >> 4;
+                                tc_mma_ss(s_at, qd + off, kd + off, kQk, k > 0);
+                            }
+                            tc_commit(&sm.s_full[s]);
+                            if (!pair || s) tc_commit(&sm.empty[stage]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                base = (base + 2u * (uint32_t)nt) % (2 * kStages);
             }
+            if (*(volatile int*)&sm.aborted) {                   // nothing in flight when the kernel ends
+                if (one_lane()) tc_commit(&sm.drain);
+                __syncwarp();
+#pragma unroll 1
+                for (int i = 0; i < (int)kWaitPolls && !mbar_try_wait(&sm.drain, 0); ++i) {}
+            }
+        } else if (warp == 2) {
+            // ---- the walk over the CTA's pieces: one thread ----------------------------------
+            if (lane == 0) {
+                Walk walk = sm.start;
+#pragma unroll 1
+                for (uint32_t pk = 0;; ++pk) {
+                    wait_or_abort(&sm.piece_empty[pk % kPieces], ~(pk / kPieces) & 1u, &sm.aborted);
+                    Piece& p = sm.pieces[pk % kPieces];
+                    walk.next(t, p);
+                    const bool end = p.nt < 0 || *(volatile int*)&sm.aborted;
+                    mbar_arrive(&sm.piece_full[pk % kPieces]);
+                    if (end) break;
+                }
+            }
+            __syncwarp();
         }
-        __syncwarp();
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- the slots: a thread a row ---------------------------------------------------
         const int slot = (warp - 4) >> 2, sw = warp & 3, row = sw * 32 + lane;
         const uint32_t lanes = (uint32_t)(sw * 32) << 16;
         const uint32_t s_at = tmem + lanes + slot * kTile, o_at = tmem + lanes + 256 + slot * 128;
-        uint32_t steps[2] = {0, 0}, o_uses = 0, ml_uses = 0;   // o_uses: of slot 1
-        uint32_t ring_base = 0;
+        uint32_t my_steps_done = 0, other_steps_done = 0, o_uses = 0, ml_uses = 0, base = 0;   // o_uses: of slot 1
         if (slot == 0 && row == 0) t.rec[2 * blockIdx.x] = t.rec[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-        while (next_piece(sm, a, warp, lane)) {
-            const int row0 = p.w.row0(p.item), rows = p.w.item_rows(p.item);
-            const bool pair = rows > kTile;
-            const int2 first_sees = seen(a, p.w, row0 / a.group), last_sees = seen(a, p.w, (row0 + rows - 1) / a.group);
-            const int key_lo = first_sees.x, key_hi = last_sees.y;     // keys that some row sees
-            const int all_lo = last_sees.x, all_hi = first_sees.y;     // keys that every row sees
-            const int nt = key_hi > key_lo ? p.nt : 0;
-            int n_steps[2];
-            n_steps[0] = pair ? nt : (nt + 1) / 2;
-            n_steps[1] = pair ? nt : nt / 2;
-            const int my_steps = slot ? n_steps[1] : n_steps[0];
-            const int local = pair ? slot * kTile + row : row;         // row of the item
-            const int my_row = row0 + local;
-            const bool valid = local < rows;
-            const bool warp_valid = (pair ? slot * kTile : 0) + sw * 32 < rows;
-            int2 see = make_int2(0, INT_MAX);                          // rows of nobody: no masking
-            if (valid) see = seen(a, p.w, my_row / a.group);
-            if (my_steps > 0) {
-                // This slot's rows of Q; its last products with the rows before are done (their scores came).
-                constexpr int kVecs = D / 8;
-                const int base = row0 + (pair ? slot * kTile : 0);
-                for (int i = 0; i < kVecs; ++i) {
-                    const int c = i * kTile + (tid & 127), qr = c / kVecs, v = c % kVecs;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (base + qr < row0 + rows) {
-                        const int tok = (base + qr) / a.group, g = (base + qr) - tok * a.group;
-                        x = *reinterpret_cast<const uint4*>((const T*)a.q.data + (int64_t)(p.w.t0 + tok) * a.q.stride_token +
-                                                            (int64_t)(p.head * a.group + g) * a.q.stride_head + v * 8);
-                        if (t.negate) {
-                            x.x ^= 0x80008000u;
-                            x.y ^= 0x80008000u;
-                            x.z ^= 0x80008000u;
-                            x.w ^= 0x80008000u;
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(sm.q[slot] + (v / 8) * (kTile * 128) + qr * 128 + ((v ^ qr) & 7) * 16) = x;
-                }
-                fence_async_smem();
-                mbar_arrive(&sm.q_full[slot]);
-            }
+        uint32_t pk = 0;
+        bool have = false;          // piece pk is being worked on
+#pragma unroll 1
+        for (;;) {
+            const Piece& p = sm.pieces[pk % kPieces];
             float m = -INFINITY, l = 0.f;
-            const int key0 = p.kt0 * kTile;
-            for (int st = 0; st < my_steps; ++st) {
-                const int j = pair ? st : 2 * st + slot;
-                const int k0 = key0 + j * kTile;
-                wait_or_abort(&sm.s_full[slot], steps[slot] & 1u, &sm.aborted);
-                tc_fence_after();
-                if (warp_valid) {
-                    float s[kTile];
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 32) tc_ld32(reinterpret_cast<uint32_t*>(s + c), s_at + c);
-                    tc_wait_ld();
-                    if (__any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile)) {
-                        const uint32_t lo = (uint32_t)(see.x - k0), count = (uint32_t)(see.y - see.x);
-#pragma unroll
-                        for (int c = 0; c < kTile; ++c) s[c] = (uint32_t)c - lo < count ? s[c] : -INFINITY;
-                    }
-                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 8) {
-                        mx0 = fmaxf(mx0, fmaxf(s[c], s[c + 1]));
-                        mx1 = fmaxf(mx1, fmaxf(s[c + 2], s[c + 3]));
-                        mx2 = fmaxf(mx2, fmaxf(s[c + 4], s[c + 5]));
-                        mx3 = fmaxf(mx3, fmaxf(s[c + 6], s[c + 7]));
-                    }
-                    const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-                    const bool grows = (mx - m) * t.scale_log2 > 8.f;   // from -inf: always, unless mx is -inf too
-                    if (__any_sync(0xffffffffu, grows)) {
-                        const float f = grows ? exp2_approx((m - mx) * t.scale_log2) : 1.f;
-                        if (grows) {
-                            m = mx;
-                            l *= f;
-                        }
-                        if (st > 0) {
-                            wait_or_abort(&sm.pv_done[slot], (steps[slot] - 1) & 1u, &sm.aborted);
-                            tc_fence_after();
+            int my_steps = 0;
+            if (have) {
+                const bool pair = p.pair();
+                my_steps = p.steps(slot);
+                const int local = (pair ? slot * kTile : 0) + row;     // row of the item
+                const bool warp_valid = local - lane < p.rows;
+                int2 see = make_int2(0, INT_MAX);                      // rows of nobody: no masking
+                if (local < p.rows) see = seen(a, p, t.by_group(p.row0 + local));
+                int k0 = (p.kt0 + (pair ? 0 : slot)) * kTile;
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o[16];
-                                tc_ld16(o, o_at + c);
-                                tc_wait_ld();
+                for (int st = 0; st < my_steps; ++st, k0 += pair ? kTile : 2 * kTile) {
+                    wait_or_abort(&sm.s_full[slot], my_steps_done & 1u, &sm.aborted);
+                    tc_fence_after();
+                    if (warp_valid) {
+                        float s[kTile];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tc_st16(o, o_at + c);
+                        for (int c = 0; c < kTile; c += 32) tc_ld32(reinterpret_cast<uint32_t*>(s + c), s_at + c);
+                        tc_wait_ld();
+                        if (__any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile)) {
+                            const uint32_t lo = (uint32_t)(see.x - k0), count = (uint32_t)(see.y - see.x);
+#pragma unroll
+                            for (int c = 0; c < kTile; ++c) s[c] = (uint32_t)c - lo < count ? s[c] : -INFINITY;
+                        }
+                        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < kTile; c += 8) {
+                            mx0 = fmaxf(fmaxf(mx0, s[c]), s[c + 1]);
+                            mx1 = fmaxf(fmaxf(mx1, s[c + 2]), s[c + 3]);
+                            mx2 = fmaxf(fmaxf(mx2, s[c + 4]), s[c + 5]);
+                            mx3 = fmaxf(fmaxf(mx3, s[c + 6]), s[c + 7]);
+                        }
+                        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+                        const bool grows = (mx - m) * t.scale_log2 > 8.f;   // from -inf: always, unless mx is -inf too
+                        if (__any_sync(0xffffffffu, grows)) {
+                            const float f = grows ? exp2_approx((m - mx) * t.scale_log2) : 1.f;
+                            if (grows) {
+                                m = mx;
+                                l *= f;
                             }
-                        }
-                    }
-                    const float shift = Kind<T>::kBias - (m == -INFINITY ? 0.f : m * t.scale_log2);
-                    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 32) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float e0 = exp2_approx(fmaf(s[c + 2 * i], t.scale_log2, shift));
-                            const float e1 = exp2_approx(fmaf(s[c + 2 * i + 1], t.scale_log2, shift));
-                            const float e2 = exp2_approx(fmaf(s[c + 2 * i + 2], t.scale_log2, shift));
-                            const float e3 = exp2_approx(fmaf(s[c + 2 * i + 3], t.scale_log2, shift));
-                            l0 += e0;
-                            l1 += e1;
-                            l2 += e2;
-                            l3 += e3;
-                            w[i] = Kind<T>::pack(e0, e1);
-                            w[i + 1] = Kind<T>::pack(e2, e3);
-                        }
-                        tc_st16(w, s_at + c / 2);
-                    }
-                    l += (l0 + l1) + (l2 + l3);
-                    tc_wait_st();
-                }
-                if (k0 < all_lo || k0 + kTile > all_hi) {
-                    // A tile with hidden keys: its values as the products may read them.
-                    const int ahead = pair ? 1 : 2;
-                    const uint32_t e = ring_base + (uint32_t)entry_v(j, nt, ahead);
-                    const uint32_t stage = e % kStages;
-                    wait_or_abort(&sm.full[stage], e / kStages & 1u, &sm.aborted);
-                    unsigned char* vt = sm.kv[stage];
-                    const int key = k0 + row;
-                    bool odd = false;
-                    if (key < key_lo || key >= key_hi) {
-#pragma unroll
-                        for (int c = 0; c < D / 8; ++c)
-                            *reinterpret_cast<uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 + (c & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    } else {
-                        uint32_t bad = 0;
-                        constexpr uint32_t m2 = Kind<T>::kExpMask | Kind<T>::kExpMask << 16;
-#pragma unroll
-                        for (int c = 0; c < D / 8; ++c) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 +
-                                                                            (c & 7) * 16);
-                            bad |= __vcmpeq2(x.x & m2, m2) | __vcmpeq2(x.y & m2, m2) | __vcmpeq2(x.z & m2, m2) |
-                                   __vcmpeq2(x.w & m2, m2);
-                        }
-                        odd = bad != 0;
-                    }
-                    fence_async_smem();
-                    if (slot_any(slot, odd)) {
-                        if (warp_valid) {
                             if (st > 0) {
-                                wait_or_abort(&sm.pv_done[slot], (steps[slot] - 1) & 1u, &sm.aborted);
+                                wait_or_abort(&sm.pv_done[slot], (my_steps_done - 1) & 1u, &sm.aborted);
                                 tc_fence_after();
-                            }
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                if (st > 0) {
-                                    tc_ld32(o, o_at + c);
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t o[16];
+                                    tc_ld16(o, o_at + c);
                                     tc_wait_ld();
-                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tc_st16(o, o_at + c);
+                                }
+                            }
+                        }
+                        const float shift = Kind<T>::kBias - (m == -INFINITY ? 0.f : m * t.scale_log2);
+                        const unsigned long long scale2 = pair_of(t.scale_log2, t.scale_log2), shift2 = pair_of(shift, shift);
+                        unsigned long long l0 = 0, l1 = 0;
+#pragma unroll
+                        for (int c = 0; c < kTile; c += 32) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 x = halves(fma2(pair_of(s[c + 2 * i], s[c + 2 * i + 1]), scale2, shift2));
+                                const float2 y = halves(fma2(pair_of(s[c + 2 * i + 2], s[c + 2 * i + 3]), scale2, shift2));
+                                const float e0 = exp2_approx(x.x), e1 = exp2_approx(x.y);
+                                const float e2 = exp2_approx(y.x), e3 = exp2_approx(y.y);
+                                l0 = add2(l0, pair_of(e0, e1));
+                                l1 = add2(l1, pair_of(e2, e3));
+                                w[i] = Kind<T>::pack(e0, e1);
+                                w[i + 1] = Kind<T>::pack(e2, e3);
+                            }
+                            tc_st16(w, s_at + c / 2);
+                        }
+                        const float2 ls = halves(add2(l0, l1));
+                        l += ls.x + ls.y;
+                        tc_wait_st();
+                    }
+                    if (k0 < p.all_lo || k0 + kTile > p.all_hi) {
+                        // A tile with hidden keys: its values as the products may read them.
+                        const uint32_t e = base + entry_v(pair ? st : 2 * st + slot, p.nt, pair ? 1 : 2), stage = e % kStages;
+                        wait_or_abort(&sm.full[stage], e / kStages & 1u, &sm.aborted);
+                        unsigned char* vt = sm.kv[stage];
+                        const int key = k0 + row;
+                        const bool nobodys = key < p.key_lo || key >= p.key_hi;
+                        constexpr uint32_t m2 = Kind<T>::kExpMask | Kind<T>::kExpMask << 16;
+                        uint32_t bad = 0;
+#pragma unroll 4
+                        for (int c = 0; c < D / 8; ++c) {          // in the swizzle's order: no two lanes in one bank
+                            uint4* x = reinterpret_cast<uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 + ((c ^ row) & 7) * 16);
+                            if (nobodys) {
+                                *x = make_uint4(0, 0, 0, 0);
+                            } else {
+                                const uint4 y = *x;
+                                bad |= __vcmpeq2(y.x & m2, m2) | __vcmpeq2(y.y & m2, m2) | __vcmpeq2(y.z & m2, m2) |
+                                       __vcmpeq2(y.w & m2, m2);
+                            }
+                        }
+                        fence_async_smem();
+                        if (slot_any(slot, bad != 0)) {
+                            if (warp_valid) {
+                                if (st > 0) {
+                                    wait_or_abort(&sm.pv_done[slot], (my_steps_done - 1) & 1u, &sm.aborted);
+                                    tc_fence_after();
+                                }
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 32) {
+                                    uint32_t o[32];
 #pragma unroll
                                     for (int i = 0; i < 32; ++i) o[i] = 0u;
-                                }
-#pragma unroll 1
-                                for (int kk = 0; kk < kTile; ++kk) {
-                                    const uint32_t w2 = tc_ld1(s_at + kk / 2);
-                                    tc_wait_ld();
-                                    const float2 wf = Kind<T>::unpack(w2);
-                                    const float wt = kk & 1 ? wf.y : wf.x;
-                                    if (wt == 0.f) continue;
-#pragma unroll
-                                    for (int i = 0; i < 32; i += 8) {
-                                        const int v = (c + i) / 8;
-                                        const uint4 x = *reinterpret_cast<const uint4*>(
-                                            vt + (v / 8) * (kTile * 128) + kk * 128 + ((v ^ kk) & 7) * 16);
-                                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                        for (int y = 0; y < 4; ++y) {
-                                            const float2 f = Kind<T>::unpack(xs[y]);
-                                            o[i + 2 * y] = __float_as_uint(fmaf(wt, f.x, __uint_as_float(o[i + 2 * y])));
-                                            o[i + 2 * y + 1] =
-                                                __float_as_uint(fmaf(wt, f.y, __uint_as_float(o[i + 2 * y + 1])));
-                                        }
+                                    if (st > 0) {
+                                        tc_ld32(o, o_at + c);
+                                        tc_wait_ld();
                                     }
+#pragma unroll 1
+                                    for (int kk = 0; kk < kTile; ++kk) {
+                                        const uint32_t w2 = tc_ld1(s_at + kk / 2);
+                                        tc_wait_ld();
+                                        const float2 wf = Kind<T>::unpack(w2);
+                                        const float wt = kk & 1 ? wf.y : wf.x;
+                                        if (wt != 0.f) {
+#pragma unroll
+                                            for (int i = 0; i < 32; i += 8) {
+                                                const int v = (c + i) / 8;
+                                                const uint4 x = *reinterpret_cast<const uint4*>(
+                                                    vt + (v / 8) * (kTile * 128) + kk * 128 + ((v ^ kk) & 7) * 16);
+                                                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                                for (int y = 0; y < 4; ++y) {
+                                                    const float2 f = Kind<T>::unpack(xs[y]);
+                                                    uint32_t* q = o + i + 2 * y;
+                                                    q[0] = __float_as_uint(fmaf(wt, f.x, __uint_as_float(q[0])));
+                                                    q[1] = __float_as_uint(fmaf(wt, f.y, __uint_as_float(q[1])));
+                                                }
+                                            }
+                                        }
+                                        __syncwarp();
+                                    }
+                                    tc_st32(o, o_at + c);
                                 }
-                                __syncwarp();
-                                tc_st32(o, o_at + c);
+                                tc_wait_st();
                             }
-                            tc_wait_st();
+                            if (row == 0) *(volatile int*)&sm.by_hand[slot] = 1;
                         }
-                        if (row == 0) *(volatile int*)&sm.by_hand[slot] = 1;
                     }
+                    ++my_steps_done;
+                    tc_fence_before();
+                    mbar_arrive(&sm.p_full[slot]);
                 }
-                ++steps[slot];
-                tc_fence_before();
-                mbar_arrive(&sm.p_full[slot]);
+                base = (base + 2u * (uint32_t)p.nt) % (2 * kStages);
+                other_steps_done += p.steps(slot ^ 1);
             }
-            ring_base = (ring_base + 2u * (uint32_t)nt) % (2 * kStages);   // what its stage and phase need
-            steps[slot ^ 1] += slot ? n_steps[0] : n_steps[1];
+
+            // ---- the next piece's rows of Q; the products with the rows before are done (their scores came)
+            const uint32_t nk = have ? pk + 1 : 0;
+            const bool more = piece_ready(nk);
+            if (more) {
+                const Piece& n = sm.pieces[nk % kPieces];
+                if (n.steps(slot) > 0) {
+                    constexpr int kVecs = D / 8, kStep = kTile / kVecs;      // vectors of a row, rows of a pass
+                    const int v = tid % kVecs, top = n.row0 + (n.pair() ? slot * kTile : 0), end = n.row0 + n.rows;
+                    const T* src = (const T*)a.q.data + (int64_t)n.head * a.group * a.q.stride_head + v * 8;
+                    unsigned char* dst = sm.q[slot] + (v / 8) * (kTile * 128);
+                    uint4 x[kVecs];
+#pragma unroll
+                    for (int i = 0; i < kVecs; ++i) {
+                        const int r = top + (tid & 127) / kVecs + i * kStep;
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (r < end) {
+                            const int tok = t.by_group(r), g = r - tok * a.group;
+                            x[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(n.t0 + tok) * a.q.stride_token +
+                                                                   (int64_t)g * a.q.stride_head);
+                        }
+                    }
+                    const uint32_t sign = t.negate ? 0x80008000u : 0u;
+#pragma unroll
+                    for (int i = 0; i < kVecs; ++i) {
+                        const int qr = (tid & 127) / kVecs + i * kStep;
+                        *reinterpret_cast<uint4*>(dst + qr * 128 + ((v ^ qr) & 7) * 16) =
+                            make_uint4(x[i].x ^ sign, x[i].y ^ sign, x[i].z ^ sign, x[i].w ^ sign);
+                    }
+                    fence_async_smem();
+                    mbar_arrive(&sm.q_full[slot]);
+                }
+            }
 
             // ---- the piece's end: the row's sums go out ------------------------------------
-            const bool both = !pair && n_steps[1] > 0;
-            const float m2 = m == -INFINITY ? 0.f : m * t.scale_log2;
-            if (my_steps > 0) {
-                wait_or_abort(&sm.pv_done[slot], (steps[slot] - 1) & 1u, &sm.aborted);
-                tc_fence_after();
-            }
-            if (both && slot == 1) {
-                wait_or_abort(&sm.o_free[1], ~o_uses & 1u, &sm.aborted);   // slot 0 has read the last ones
-                sm.ml[row] = make_float2(m2, l);
-                mbar_arrive(&sm.ml_full);
-            }
-            if (pair || slot == 0) {
-                float f0 = 1.f, f1 = 0.f, mt = m2, lt = l;
-                if (both) {
-                    wait_or_abort(&sm.ml_full, ml_uses & 1u, &sm.aborted);
-                    wait_or_abort(&sm.pv_done[1], (steps[1] - 1) & 1u, &sm.aborted);
+            if (have) {
+                const bool pair = p.pair(), both = !pair && p.nt > 1;
+                const float m2 = m == -INFINITY ? 0.f : m * t.scale_log2;
+                if (my_steps > 0) {
+                    wait_or_abort(&sm.pv_done[slot], (my_steps_done - 1) & 1u, &sm.aborted);
                     tc_fence_after();
-                    const float2 o = sm.ml[row];
-                    if (l == 0.f) {
-                        mt = o.x;
-                    } else if (o.y != 0.f) {
-                        mt = fmaxf(m2, o.x);
-                    }
-                    f0 = l == 0.f ? 0.f : exp2_approx(m2 - mt);
-                    f1 = o.y == 0.f ? 0.f : exp2_approx(o.x - mt);
-                    lt = l * f0 + o.y * f1;
                 }
-                const bool whole = p.first && p.last;
-                const int part = 2 * (int)blockIdx.x + (p.first ? 1 : 0);
-                const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
-                const float g0 = f0 * inv, g1 = f1 * inv;
-                const int tok = my_row / a.group, g = my_row - tok * a.group;
-                const int64_t token = p.w.t0 + tok;
-                const int head = p.head * a.group + g;
-                if (warp_valid) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        if (my_steps > 0) {
-                            tc_ld32(o, o_at + c);
-                            tc_wait_ld();
+                if (both && slot == 1) {
+                    wait_or_abort(&sm.o_free[1], ~o_uses & 1u, &sm.aborted);   // slot 0 has read the last ones
+                    sm.ml[row] = make_float2(m2, l);
+                    mbar_arrive(&sm.ml_full);
+                }
+                if (pair || slot == 0) {
+                    float f0 = 1.f, f1 = 0.f, mt = m2, lt = l;
+                    if (both) {
+                        wait_or_abort(&sm.ml_full, ml_uses & 1u, &sm.aborted);
+                        wait_or_abort(&sm.pv_done[1], (other_steps_done - 1) & 1u, &sm.aborted);
+                        tc_fence_after();
+                        const float2 o = sm.ml[row];
+                        if (l == 0.f) {
+                            mt = o.x;
+                        } else if (o.y != 0.f) {
+                            mt = fmaxf(m2, o.x);
                         }
-                        float x[32];
+                        f0 = l == 0.f ? 0.f : exp2_approx(m2 - mt);
+                        f1 = o.y == 0.f ? 0.f : exp2_approx(o.x - mt);
+                        lt = l * f0 + o.y * f1;
+                    }
+                    const int local = (pair ? slot * kTile : 0) + row;
+                    const bool valid = local < p.rows, whole = p.first && p.last;
+                    if (whole) {
+                        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+                        f0 *= inv;
+                        f1 *= inv;
+                    }
+                    const int64_t part = (int64_t)(2 * (int)blockIdx.x + (p.first ? 1 : 0)) * t.part_rows + local;
+                    const int tok = t.by_group(p.row0 + local), head = p.head * a.group + p.row0 + local - tok * a.group;
+                    const int64_t token = p.t0 + tok;
+                    if (local - lane < p.rows) {
+                        T* out = (T*)a.out.data + token * a.out.stride_token + (int64_t)head * a.out.stride_head;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16], o1[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = my_steps > 0 && lt != 0.f ? __uint_as_float(o[i]) * g0 : 0.f;
-                        if (both) {
-                            tc_ld32(o, o_at + 128 + c);
+                            for (int i = 0; i < 16; ++i) o[i] = o1[i] = 0u;
+                            if (my_steps > 0) tc_ld16(o, o_at + c);
+                            if (both) tc_ld16(o1, o_at + 128 + c);
                             tc_wait_ld();
-                            if (f1 != 0.f) {
+                            float x[16];
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) x[i] = fmaf(__uint_as_float(o[i]), g1, f0 == 0.f ? 0.f : x[i]);
+                            for (int i = 0; i < 16; ++i) {             // a slot of weight 0 has no say, whatever it holds
+                                x[i] = f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
+                                x[i] = f1 == 0.f ? x[i] : fmaf(__uint_as_float(o1[i]), f1, x[i]);
+                            }
+                            if (valid && whole) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 8)
+                                    *reinterpret_cast<uint4*>(out + c + i) =
+                                        make_uint4(Kind<T>::pack(x[i], x[i + 1]), Kind<T>::pack(x[i + 2], x[i + 3]),
+                                                   Kind<T>::pack(x[i + 4], x[i + 5]), Kind<T>::pack(x[i + 6], x[i + 7]));
+                            } else if (valid) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4)
+                                    *reinterpret_cast<float4*>(t.part + part * D + c + i) =
+                                        make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                             }
                         }
                         if (valid && whole) {
-                            T* dst = (T*)a.out.data + token * a.out.stride_token + (int64_t)head * a.out.stride_head + c;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                *reinterpret_cast<uint4*>(dst + i) =
-                                    make_uint4(Kind<T>::pack(x[i], x[i + 1]), Kind<T>::pack(x[i + 2], x[i + 3]),
-                                               Kind<T>::pack(x[i + 4], x[i + 5]), Kind<T>::pack(x[i + 6], x[i + 7]));
+                            if (a.lse)
+                                a.lse[token * a.q.heads + head] =
+                                    lt == 0.f ? -INFINITY : (mt - Kind<T>::kBias) * 0.69314718055994531f + logf(lt);
                         } else if (valid) {
-                            float* dst = t.part + ((int64_t)part * t.part_rows + local) * D + c;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                            t.part_ml[part] = make_float2(mt - Kind<T>::kBias, lt);
                         }
                     }
-                    if (valid && whole) {
-                        if (a.lse)
-                            a.lse[token * a.q.heads + head] =
-                                lt == 0.f ? -INFINITY : (mt - Kind<T>::kBias) * 0.69314718055994531f + logf(lt);
-                    } else if (valid) {
-                        t.part_ml[(int64_t)part * t.part_rows + local] = make_float2(mt - Kind<T>::kBias, lt);
-                    }
+                    tc_fence_before();
+                    if (my_steps > 0) mbar_arrive(&sm.o_free[slot]);
+                    if (both) mbar_arrive(&sm.o_free[1]);
                 }
-                tc_fence_before();
-                if (my_steps > 0) mbar_arrive(&sm.o_free[slot]);
-                if (both) mbar_arrive(&sm.o_free[1]);
+                if (p.steps(1) > 0) ++o_uses;
+                if (both) ++ml_uses;
+                if (slot == 0 && row == 0) {
+                    if (!p.first) t.rec[2 * blockIdx.x].x = p.last ? 1 : 2;
+                    if (p.first && !p.last) t.rec[2 * blockIdx.x + 1] = make_int4(1, p.r, p.head, p.item);
+                }
+                piece_release(pk);
             }
-            if (n_steps[1] > 0) ++o_uses;
-            if (both) ++ml_uses;
-            if (slot == 0 && row == 0) {
-                if (!p.first) t.rec[2 * blockIdx.x].x = p.last ? 1 : 2;
-                if (p.first && !p.last) t.rec[2 * blockIdx.x + 1] = make_int4(1, p.r, p.head, p.item);
-            }
+            if (!more) break;
+            pk = nk;
+            have = true;
         }
     }
     tc_fence_before();
     __syncthreads();
     if (sm.aborted) {
-        if (warp == 0)                                    // loads in flight land before the kernel ends
-            for (int i = lane; i < kStages; i += 32)
-                for (int ph = 0; ph < 2; ++ph)
-                    for (long long x = 0; x < kWaitPolls / 16 && !mbar_try_wait(&sm.full[i], (uint32_t)ph); ++x) {}
+        if (warp == 0) {                                  // loads in flight land before the kernel ends
+#pragma unroll 1
+            for (int i = lane; i < 2 * (int)kStages; i += 32)
+#pragma unroll 1
+                for (int x = 0; x < (int)kWaitPolls / 16 && !mbar_try_wait(&sm.full[i >> 1], (uint32_t)i & 1u); ++x) {}
+        }
         if (a.status)
             for (int r = tid; r < a.n_req; r += kTcThreads) atomicOr(&a.status[r], kTimeout);
         __syncthreads();
@@ -991,7 +1049,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const TcArgs t)
             for (int i = 0; i < kE; ++i) x[i] = fmaf(y[i], f, x[i]);
         }
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        const int tok = (row0 + row) / a.group, g = (row0 + row) - tok * a.group;
+        const int tok = t.by_group(row0 + row), g = row0 + row - tok * a.group;
         const int64_t token = w.t0 + tok;
         const int head = rec.z * a.group + g;
         T* dst = (T*)a.out.data + token * a.out.stride_token + (int64_t)head * a.out.stride_head + lane * kE;
@@ -1044,6 +1102,13 @@ int part_rows(int max_window, int group)
     return (int)(r > kTile ? 2 * kTile : r < 1 ? 1 : r);
 }
 
+Divisor divisor(int d)
+{
+    uint32_t l = 0;
+    while ((1ull << l) < (uint64_t)d) ++l;
+    return Divisor{(uint32_t)(((1ull << (31 + l)) + (uint64_t)d - 1) / (uint64_t)d), 31 + l};
+}
+
 template <typename T, int D>
 cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s)
 {
@@ -1090,8 +1155,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
     t.rec = reinterpret_cast<int4*>(w);
     t.part_ml = reinterpret_cast<float2*>(w + sizeof(int4) * 2 * kTcMaxGrid);
     t.part = reinterpret_cast<float*>(w + (sizeof(int4) * 2 * kTcMaxGrid + rows * sizeof(float2) + 255) / 256 * 256);
-    t.page_shift = 0;
-    while (a.cache.page_size < kTile && (1 << t.page_shift) < a.cache.page_size) ++t.page_shift;
+    t.by_group = divisor(a.group);
+    t.by_page = divisor(a.cache.page_size);
     t.scale_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, FLT_MIN);   // above 0: hidden scores stay -inf
     t.negate = a.scale < 0.f;
     const bool bf16 = dt == SV_DTYPE_BF16;
