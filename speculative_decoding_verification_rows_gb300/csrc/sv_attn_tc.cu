@@ -47,7 +47,7 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 128;              // keys of a tile, rows of a slot
-constexpr int kTcThreads = 384;
+constexpr int kTcThreads = 512;
 constexpr int kTcWarps = kTcThreads / 32;
 constexpr int kMinTiles = 2;            // fewest tiles worth a CTA of its own
 constexpr uint32_t kTmemCols = 512;
@@ -109,6 +109,16 @@ __device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr)
         : "r"(addr)
         : "memory");
 }
+#define SV_P8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), \
+                    "+r"(r[o + 6]), "+r"(r[o + 7])
+// Waits for the thread's loads; the N registers are not to be read before.
+template <int N>
+__device__ __forceinline__ void tc_loaded(uint32_t* r)
+{
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; i += 8) asm volatile("" : SV_P8((r + i), 0));
+}
 __device__ __forceinline__ void tc_ld16(uint32_t* r, uint32_t addr)
 {
     asm volatile(
@@ -134,6 +144,18 @@ __device__ __forceinline__ void tc_st16(const uint32_t* r, uint32_t addr)
         SV_W8(r, 8), "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tc_ld8(uint32_t* r, uint32_t addr)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : SV_R8(r, 0)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st8(const uint32_t* r, uint32_t addr)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::SV_W8(r, 0), "r"(addr)
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t tc_ld1(uint32_t addr)
 {
     uint32_t r;
@@ -156,19 +178,6 @@ __device__ __forceinline__ float exp2_approx(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Whether any of the 128 threads of a slot says so; also their barrier.
-__device__ __forceinline__ bool slot_any(int slot, bool x)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x), "r"(1 + slot)
-        : "memory");
-    return r != 0u;
-}
-
 // Shared-memory descriptor of 128-byte swizzled rows of 64 16-bit elements:
 // groups of 8 rows are 1,024 bytes apart; `lead` is the distance from one 64
 // element block of the row axis to the next where that axis is contiguous.
@@ -234,8 +243,7 @@ struct TcArgs {
     int4* rec;              // [grid][2] what each CTA left there
     int part_rows;
     int grid;
-    float scale_log2;       // |scale| log2 e
-    int negate;             // scale < 0
+    float scale_log2;       // scale log2 e
 };
 
 // A request's window as rows and items.
@@ -365,7 +373,7 @@ struct Walk {
 
 // ---- shared memory ----------------------------------------------------------------
 constexpr int kPieces = 4;
-constexpr int kPieceReaders = 10;   // warps: loads, products, two slots
+constexpr int kPieceReaders = 15;   // warps: loads, two slots' products, two slots, output
 
 template <int D>
 struct TcSmem {
@@ -374,13 +382,17 @@ struct TcSmem {
     alignas(1024) unsigned char q[2][kTileBytes];
     alignas(1024) unsigned char kv[kStages][kTileBytes];
     unsigned long long full[kStages], empty[kStages];
-    unsigned long long q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2], ml_full, drain;
+    unsigned long long q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
     unsigned long long piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];          // warp 2 walks ahead of the other roles
-    float2 ml[kTile];               // slot 1's statistics of an item both slots share
+    float2 ml[2][kTile];            // the slots' statistics of a finished piece
     long long scan[kTcWarps];
     Walk start;
     uint32_t tmem;
+    uint32_t turns[2];              // units of shared tiles whose products each slot has issued
+    uint32_t issued;                // ring entries whose loads have begun
+    uint32_t q_loads[2];            // warps that have filled each buffer of Q, over all its loads
+    int odd[2][3];                  // a slot's votes, three by turns: some value is not finite
     int aborted;                    // a wait gave up: every later wait gives up at once
     int by_hand[2];                 // the slot has done this tile's P V itself
 };
@@ -455,23 +467,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < (int)kStages; ++i) {
             mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.empty[i], 2);                // 2: each slot's products, or twice the one slot's
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&sm.q_full[s], kTile);
+            mbar_init(&sm.q_empty[s], 2);
+            sm.q_loads[s] = 0;
             mbar_init(&sm.s_full[s], 1);
-            mbar_init(&sm.p_full[s], kTile);
+            mbar_init(&sm.p_half[s], 4);               // 4: a warp at a time
+            mbar_init(&sm.p_full[s], 4);
             mbar_init(&sm.pv_done[s], 1);
-            mbar_init(&sm.o_free[s], kTile);
+            mbar_init(&sm.o_free[s], 4);
+            mbar_init(&sm.ml_full[s], 4);
+            mbar_init(&sm.vote[s], 4);
+            sm.turns[s] = 0;
+            sm.odd[s][0] = sm.odd[s][1] = sm.odd[s][2] = 0;
             sm.by_hand[s] = 0;
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&sm.piece_full[i], 1);
             mbar_init(&sm.piece_empty[i], kPieceReaders);
         }
-        mbar_init(&sm.ml_full, kTile);
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.drain, 2);
         sm.aborted = 0;
+        sm.issued = 0;
         sm.start.left = 0;
         mbar_fence_init();
     }
@@ -544,19 +562,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    // The slots hold a row of 128 scores a thread, the other warps little: of
-    // the 384 x 168 registers of the launch, 128 x 88 + 256 x 208.
     // Piece k of the CTA, for every lane of a reading warp; false after the last.
     auto piece_ready = [&](uint32_t k) {
         wait_or_abort(&sm.piece_full[k % kPieces], k / kPieces & 1u, &sm.aborted);
         return sm.pieces[k % kPieces].nt >= 0 && !*(volatile int*)&sm.aborted;
     };
-    auto piece_release = [&](uint32_t k) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.piece_empty[k % kPieces]);
+    // A count in shared memory has reached n.
+    auto reached = [&](const uint32_t* count, uint32_t n) {
+#pragma unroll 1
+        for (int i = 0; (int)(*(const volatile uint32_t*)count - n) < 0; ++i) {
+            if (i == (int)kWaitPolls) *(volatile int*)&sm.aborted = 1;
+            if (*(volatile int*)&sm.aborted) break;
+        }
     };
+    // Entry e of the ring has landed.  A reader that skips entries cannot go by the stage's phase alone: with the
+    // entry before e on that stage still to come, the phase of the one before that would pass for e's.
+    auto landed = [&](uint32_t e) {
+        reached(&sm.issued, e + 1);
+        wait_or_abort(&sm.full[e % kStages], e / kStages & 1u, &sm.aborted);
+    };
+    auto warp_arrive = [&](unsigned long long* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    auto piece_release = [&](uint32_t k) { warp_arrive(&sm.piece_empty[k % kPieces]); };
+    // The slots hold a row of 128 scores a thread, the other warps little: of
+    // the 512 x 128 registers of the launch, 128 x 72 + 256 x 176 + 128 x 88.
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
             // ---- loads: lane i has page i of a tile --------------------------------------
             const int page_size = a.cache.page_size;
@@ -593,7 +626,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         const uint32_t have = __ballot_sync(0xffffffffu, mine);
                         wait_or_abort(&sm.empty[stage], ~(e / kStages) & 1u, &sm.aborted);   // the first round finds it empty
-                        if (lane == 0) mbar_expect_tx(&sm.full[stage], (uint32_t)(__popc(have) * box_rows * D * 2));
+                        if (lane == 0) {
+                            mbar_expect_tx(&sm.full[stage], (uint32_t)(__popc(have) * box_rows * D * 2));
+                            __threadfence_block();
+                            *(volatile uint32_t*)&sm.issued = e + 1;
+                        }
                         __syncwarp();
                         if (mine) {
                             const int token = page_size > kTile ? key_of_page - t.by_page(key_of_page) * page_size : 0;
@@ -605,63 +642,69 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                 }
-                base = (base + 2u * (uint32_t)nt) % (2 * kStages);   // what stage and phase need of it
+                base += 2u * (uint32_t)nt;
             }
-        } else if (warp == 1) {
-            // ---- matrix products: one lane issues them ------------------------------------
+        } else if (warp != 2) {
+            // ---- matrix products: warp 1 slot 0's, warp 3 slot 1's, one lane issues them -----
+            const int s = warp >> 1;
             constexpr uint32_t kQk = instr_desc(Kind<T>::kBf16, false, kTile);
             constexpr uint32_t kPv = instr_desc(Kind<T>::kBf16, true, D);
             const uint64_t q_desc = smem_desc(smem_u32(sm.q[0]), 16), k_desc = smem_desc(smem_u32(sm.kv[0]), 16),
                            v_desc = smem_desc(smem_u32(sm.kv[0]), kTile * 128);
             constexpr uint32_t kBytes = S::kTileBytes >> 4;    // a tile in a descriptor's units
-            uint32_t base = 0, q_uses[2] = {0, 0}, steps[2] = {0, 0}, o_uses[2] = {0, 0};
+            const uint32_t o_at = tmem + 256 + s * 128, s_at = tmem + s * kTile;
+            uint32_t base = 0, q_uses[2] = {0, 0}, done = 0, o_uses = 0, q_next = 0, turns = 0;
 #pragma unroll 1
             for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
                 const Piece& p = sm.pieces[pk % kPieces];
                 const bool pair = p.pair();
-                const int nt = p.nt, ahead = pair ? 1 : 2, units = pair ? 2 * nt : nt;
-                // P V of unit u, then the scores of unit u + 2 in their place.
+                const int nt = p.nt, ahead = pair ? 1 : 2, each = pair ? 1 : 2, steps = p.steps(s);
+                const uint32_t qb = pair ? (uint32_t)s : q_next;
+                if (!pair && nt > 0) q_next ^= 1u;
+                if (nt > 0) {
+                    if (pair || qb == 0) ++q_uses[0];
+                    if (pair || qb == 1) ++q_uses[1];
+                    reached(&sm.q_loads[qb], 4u * (qb ? q_uses[1] : q_uses[0]));
+                    __threadfence_block();
+                }
+                const uint64_t qd = q_desc + qb * kBytes;
+                int j = pair ? 0 : s;                            // tile of the next scores
+                uint32_t e = base + entry_k(j, ahead), k_stage = e % kStages, v_stage = 0;
 #pragma unroll 1
-                for (int u = -2; u < units; ++u) {
-                    const int s = u & 1;
-                    if (u >= 0) {
-                        const int j = pair ? u >> 1 : u;
-                        const uint32_t e = base + entry_v(j, nt, ahead), stage = e % kStages;
-                        wait_or_abort(&sm.full[stage], e / kStages & 1u, &sm.aborted);
-                        wait_or_abort(&sm.p_full[s], (s ? steps[1] : steps[0]) & 1u, &sm.aborted);
-                        if (s) ++steps[1]; else ++steps[0];
-                        const bool add = u >= 2;
-                        if (!add) {
-                            wait_or_abort(&sm.o_free[s], ~(s ? o_uses[1] : o_uses[0]) & 1u, &sm.aborted);   // at first it is
-                            if (s) ++o_uses[1]; else ++o_uses[0];
-                        }
-                        tc_fence_after();
+                for (int st = 0; st <= steps; ++st) {
+                    const uint64_t vd = v_desc + v_stage * kBytes, kd = k_desc + k_stage * kBytes;
+                    // Where the slots share the tiles, arithmetic bounds the piece: what can be waited for is, before
+                    // the weights, so that nothing stands between the products.  Elsewhere the keys may be far off.
+                    if (st < steps && (pair || st == 0)) landed(e);
+                    if (st > 0) {                                // P V of step st - 1
+                        if (st == 1) wait_or_abort(&sm.o_free[s], ~o_uses++ & 1u, &sm.aborted);   // at first it is
+                        wait_or_abort(&sm.p_half[s], done & 1u, &sm.aborted);
                         const bool by_hand = *(volatile int*)&sm.by_hand[s];
-                        const uint32_t o_at = tmem + 256 + s * 128, p_at = tmem + s * kTile;
-                        const uint64_t vd = v_desc + stage * kBytes;
+                        if (pair) reached(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
+                        tc_fence_after();
+                        if (one_lane() && !by_hand) {
+#pragma unroll
+                            for (int k = 0; k < kTile / 32; ++k)
+                                tc_mma_ts(o_at, s_at + k * 8, vd + k * (2048 >> 4), kPv, st > 1 || k > 0);
+                        }
+                        wait_or_abort(&sm.p_full[s], done & 1u, &sm.aborted);
+                        ++done;
+                        tc_fence_after();
                         if (one_lane()) {
                             if (!by_hand) {
 #pragma unroll
-                                for (int k = 0; k < kTile / 16; ++k)
-                                    tc_mma_ts(o_at, p_at + k * 8, vd + k * (2048 >> 4), kPv, add || k > 0);
+                                for (int k = kTile / 32; k < kTile / 16; ++k)
+                                    tc_mma_ts(o_at, s_at + k * 8, vd + k * (2048 >> 4), kPv, true);
                             }
                             tc_commit(&sm.pv_done[s]);
-                            if (!pair || s) tc_commit(&sm.empty[stage]);       // its last reader
+                            tc_commit(&sm.empty[v_stage]);
+                            if (!pair) tc_commit(&sm.empty[v_stage]);
+                            if (by_hand) *(volatile int*)&sm.by_hand[s] = 0;
                         }
                         __syncwarp();
-                        if (by_hand && lane == 0) *(volatile int*)&sm.by_hand[s] = 0;
+                        if (!pair && st < steps) landed(e);
                     }
-                    if (u + 2 < units) {
-                        const int j = pair ? (u + 2) >> 1 : u + 2;
-                        const uint32_t e = base + entry_k(j, ahead), stage = e % kStages;
-                        if (u < 0) {
-                            wait_or_abort(&sm.q_full[s], (s ? q_uses[1] : q_uses[0]) & 1u, &sm.aborted);
-                            if (s) ++q_uses[1]; else ++q_uses[0];
-                        }
-                        wait_or_abort(&sm.full[stage], e / kStages & 1u, &sm.aborted);
-                        tc_fence_after();
-                        const uint32_t s_at = tmem + s * kTile;
-                        const uint64_t qd = q_desc + s * kBytes, kd = k_desc + stage * kBytes;
+                    if (st < steps) {                            // scores of step st, in the place of the last weights
                         if (one_lane()) {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
@@ -669,12 +712,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 tc_mma_ss(s_at, qd + off, kd + off, kQk, k > 0);
                             }
                             tc_commit(&sm.s_full[s]);
-                            if (!pair || s) tc_commit(&sm.empty[stage]);
+                            tc_commit(&sm.empty[k_stage]);
+                            if (!pair) tc_commit(&sm.empty[k_stage]);
+                            if (st + 1 == steps) {               // Q's last use
+                                tc_commit(&sm.q_empty[qb]);
+                                if (pair || nt == 1) tc_commit(&sm.q_empty[qb]);
+                            }
                         }
                         __syncwarp();
                     }
+                    if (pair && st > 0 && lane == 0) *(volatile uint32_t*)&sm.turns[s] = turns;
+                    if (st < steps) {                            // the values that go with these scores, the next keys
+                        const uint32_t ev = base + entry_v(j, nt, ahead);
+                        v_stage = ev % kStages;
+                        j += each;
+                        e = base + entry_k(j, ahead);
+                        k_stage = e % kStages;
+                        landed(ev);
+                    }
                 }
-                base = (base + 2u * (uint32_t)nt) % (2 * kStages);
+                base += 2u * (uint32_t)nt;
             }
             if (*(volatile int*)&sm.aborted) {                   // nothing in flight when the kernel ends
                 if (one_lane()) tc_commit(&sm.drain);
@@ -682,7 +739,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int i = 0; i < (int)kWaitPolls && !mbar_try_wait(&sm.drain, 0); ++i) {}
             }
-        } else if (warp == 2) {
+        } else {
             // ---- the walk over the CTA's pieces: one thread ----------------------------------
             if (lane == 0) {
                 Walk walk = sm.start;
@@ -698,24 +755,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             __syncwarp();
         }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         // ---- the slots: a thread a row ---------------------------------------------------
         const int slot = (warp - 4) >> 2, sw = warp & 3, row = sw * 32 + lane;
         const uint32_t lanes = (uint32_t)(sw * 32) << 16;
         const uint32_t s_at = tmem + lanes + slot * kTile, o_at = tmem + lanes + 256 + slot * 128;
-        uint32_t my_steps_done = 0, other_steps_done = 0, o_uses = 0, ml_uses = 0, base = 0;   // o_uses: of slot 1
-        if (slot == 0 && row == 0) t.rec[2 * blockIdx.x] = t.rec[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-        uint32_t pk = 0;
-        bool have = false;          // piece pk is being worked on
+        uint32_t steps_done = 0, o_uses = 0, votes = 0, base = 0;
 #pragma unroll 1
-        for (;;) {
+        for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
             const Piece& p = sm.pieces[pk % kPieces];
             float m = -INFINITY, l = 0.f;
-            int my_steps = 0;
-            if (have) {
+            {
                 const bool pair = p.pair();
-                my_steps = p.steps(slot);
+                const int my_steps = p.steps(slot);
                 const int local = (pair ? slot * kTile : 0) + row;     // row of the item
                 const bool warp_valid = local - lane < p.rows;
                 int2 see = make_int2(0, INT_MAX);                      // rows of nobody: no masking
@@ -723,25 +776,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 int k0 = (p.kt0 + (pair ? 0 : slot)) * kTile;
 #pragma unroll 1
                 for (int st = 0; st < my_steps; ++st, k0 += pair ? kTile : 2 * kTile) {
-                    wait_or_abort(&sm.s_full[slot], my_steps_done & 1u, &sm.aborted);
+                    wait_or_abort(&sm.s_full[slot], steps_done & 1u, &sm.aborted);
                     tc_fence_after();
                     if (warp_valid) {
-                        float s[kTile];
+                        uint32_t s[kTile];                             // fp32 scores
 #pragma unroll
-                        for (int c = 0; c < kTile; c += 32) tc_ld32(reinterpret_cast<uint32_t*>(s + c), s_at + c);
-                        tc_wait_ld();
+                        for (int c = 0; c < kTile; c += 32) tc_ld32(s + c, s_at + c);
+                        tc_loaded<kTile>(s);
                         if (__any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile)) {
                             const uint32_t lo = (uint32_t)(see.x - k0), count = (uint32_t)(see.y - see.x);
 #pragma unroll
-                            for (int c = 0; c < kTile; ++c) s[c] = (uint32_t)c - lo < count ? s[c] : -INFINITY;
+                            for (int c = 0; c < kTile; ++c) s[c] = (uint32_t)c - lo < count ? s[c] : 0xff800000u;   // -inf
                         }
+                        // Weights of columns c .. c + 31 under the maximum m, and their sum.
+                        unsigned long long l0, l1;
+                        uint32_t w[16];
+                        auto weigh = [&](int c) {
+                            const float shift = Kind<T>::kBias - (m == -INFINITY ? 0.f : m * t.scale_log2);
+                            const unsigned long long scale2 = pair_of(t.scale_log2, t.scale_log2),
+                                                     shift2 = pair_of(shift, shift);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const uint32_t* q = s + c + 2 * i;
+                                const float2 x = halves(fma2(pair_of(__uint_as_float(q[0]), __uint_as_float(q[1])), scale2, shift2));
+                                const float2 y = halves(fma2(pair_of(__uint_as_float(q[2]), __uint_as_float(q[3])), scale2, shift2));
+                                const float e0 = exp2_approx(x.x), e1 = exp2_approx(x.y);
+                                const float e2 = exp2_approx(y.x), e3 = exp2_approx(y.y);
+                                l0 = add2(l0, pair_of(e0, e1));
+                                l1 = add2(l1, pair_of(e2, e3));
+                                w[i] = Kind<T>::pack(e0, e1);
+                                w[i + 1] = Kind<T>::pack(e2, e3);
+                            }
+                        };
+                        // The first weights are taken under the maximum so far while the tile's is found, and again
+                        // if that was too small: rare after a row's first tile, and the maximum costs no time of its own.
+                        l0 = l1 = 0;
+                        weigh(0);
                         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
                         for (int c = 0; c < kTile; c += 8) {
-                            mx0 = fmaxf(fmaxf(mx0, s[c]), s[c + 1]);
-                            mx1 = fmaxf(fmaxf(mx1, s[c + 2]), s[c + 3]);
-                            mx2 = fmaxf(fmaxf(mx2, s[c + 4]), s[c + 5]);
-                            mx3 = fmaxf(fmaxf(mx3, s[c + 6]), s[c + 7]);
+                            mx0 = fmaxf(fmaxf(mx0, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+                            mx1 = fmaxf(fmaxf(mx1, __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
+                            mx2 = fmaxf(fmaxf(mx2, __uint_as_float(s[c + 4])), __uint_as_float(s[c + 5]));
+                            mx3 = fmaxf(fmaxf(mx3, __uint_as_float(s[c + 6])), __uint_as_float(s[c + 7]));
                         }
                         const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
                         const bool grows = (mx - m) * t.scale_log2 > 8.f;   // from -inf: always, unless mx is -inf too
@@ -752,46 +829,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 l *= f;
                             }
                             if (st > 0) {
-                                wait_or_abort(&sm.pv_done[slot], (my_steps_done - 1) & 1u, &sm.aborted);
+                                wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
                                 tc_fence_after();
 #pragma unroll 1
-                                for (int c = 0; c < D; c += 16) {
-                                    uint32_t o[16];
-                                    tc_ld16(o, o_at + c);
-                                    tc_wait_ld();
+                                for (int c = 0; c < D; c += 8) {
+                                    uint32_t o[8];
+                                    tc_ld8(o, o_at + c);
+                                    tc_loaded<8>(o);
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                    tc_st16(o, o_at + c);
+                                    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tc_st8(o, o_at + c);
                                 }
                             }
+                            l0 = l1 = 0;
+                            weigh(0);
                         }
-                        const float shift = Kind<T>::kBias - (m == -INFINITY ? 0.f : m * t.scale_log2);
-                        const unsigned long long scale2 = pair_of(t.scale_log2, t.scale_log2), shift2 = pair_of(shift, shift);
-                        unsigned long long l0 = 0, l1 = 0;
-#pragma unroll
-                        for (int c = 0; c < kTile; c += 32) {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float2 x = halves(fma2(pair_of(s[c + 2 * i], s[c + 2 * i + 1]), scale2, shift2));
-                                const float2 y = halves(fma2(pair_of(s[c + 2 * i + 2], s[c + 2 * i + 3]), scale2, shift2));
-                                const float e0 = exp2_approx(x.x), e1 = exp2_approx(x.y);
-                                const float e2 = exp2_approx(y.x), e3 = exp2_approx(y.y);
-                                l0 = add2(l0, pair_of(e0, e1));
-                                l1 = add2(l1, pair_of(e2, e3));
-                                w[i] = Kind<T>::pack(e0, e1);
-                                w[i + 1] = Kind<T>::pack(e2, e3);
-                            }
-                            tc_st16(w, s_at + c / 2);
+                        const bool edge = k0 < p.all_lo || k0 + kTile > p.all_hi;
+                        tc_st16(w, s_at);
+                        weigh(32);
+                        tc_st16(w, s_at + 16);
+                        weigh(64);
+                        if (!edge) {                                   // the products of the first half may begin
+                            tc_wait_st();
+                            tc_fence_before();
+                            warp_arrive(&sm.p_half[slot]);
                         }
+                        tc_st16(w, s_at + 32);
+                        weigh(96);
+                        tc_st16(w, s_at + 48);
                         const float2 ls = halves(add2(l0, l1));
                         l += ls.x + ls.y;
                         tc_wait_st();
+                    } else if (!(k0 < p.all_lo || k0 + kTile > p.all_hi)) {
+                        warp_arrive(&sm.p_half[slot]);
                     }
                     if (k0 < p.all_lo || k0 + kTile > p.all_hi) {
                         // A tile with hidden keys: its values as the products may read them.
                         const uint32_t e = base + entry_v(pair ? st : 2 * st + slot, p.nt, pair ? 1 : 2), stage = e % kStages;
-                        wait_or_abort(&sm.full[stage], e / kStages & 1u, &sm.aborted);
+                        landed(e);
                         unsigned char* vt = sm.kv[stage];
                         const int key = k0 + row;
                         const bool nobodys = key < p.key_lo || key >= p.key_hi;
@@ -809,10 +884,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                         fence_async_smem();
-                        if (slot_any(slot, bad != 0)) {
+                        // The slot's warps vote and wait for one another (bounded, as every wait: no hardware barrier here).
+                        const bool any_bad = __any_sync(0xffffffffu, bad != 0);
+                        if (any_bad && lane == 0) *(volatile int*)&sm.odd[slot][votes % 3u] = 1;
+                        // The next vote's: all have read it two votes ago, nobody writes it before this vote is over.
+                        if (row == 0) *(volatile int*)&sm.odd[slot][(votes + 1u) % 3u] = 0;
+                        __threadfence_block();
+                        warp_arrive(&sm.vote[slot]);
+                        wait_or_abort(&sm.vote[slot], votes & 1u, &sm.aborted);
+                        const bool by_hand = *(volatile int*)&sm.odd[slot][votes % 3u] != 0;
+                        ++votes;
+                        if (by_hand) {
                             if (warp_valid) {
                                 if (st > 0) {
-                                    wait_or_abort(&sm.pv_done[slot], (my_steps_done - 1) & 1u, &sm.aborted);
+                                    wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
                                     tc_fence_after();
                                 }
 #pragma unroll 1
@@ -822,12 +907,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                                     if (st > 0) {
                                         tc_ld32(o, o_at + c);
-                                        tc_wait_ld();
+                                        tc_loaded<32>(o);
                                     }
 #pragma unroll 1
                                     for (int kk = 0; kk < kTile; ++kk) {
-                                        const uint32_t w2 = tc_ld1(s_at + kk / 2);
+                                        uint32_t w2 = tc_ld1(s_at + kk / 2);
                                         tc_wait_ld();
+                                        asm volatile("" : "+r"(w2));
                                         const float2 wf = Kind<T>::unpack(w2);
                                         const float wt = kk & 1 ? wf.y : wf.x;
                                         if (wt != 0.f) {
@@ -854,79 +940,108 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                             if (row == 0) *(volatile int*)&sm.by_hand[slot] = 1;
                         }
+                        tc_fence_before();
+                        warp_arrive(&sm.p_half[slot]);
                     }
-                    ++my_steps_done;
+                    ++steps_done;
                     tc_fence_before();
-                    mbar_arrive(&sm.p_full[slot]);
+                    warp_arrive(&sm.p_full[slot]);
                 }
-                base = (base + 2u * (uint32_t)p.nt) % (2 * kStages);
-                other_steps_done += p.steps(slot ^ 1);
+                base += 2u * (uint32_t)p.nt;
+                if (my_steps > 0) {
+                    wait_or_abort(&sm.o_free[slot], ~o_uses & 1u, &sm.aborted);   // the last piece's have been read
+                    ++o_uses;
+                    sm.ml[slot][row] = make_float2(m == -INFINITY ? 0.f : m * t.scale_log2, l);
+                    warp_arrive(&sm.ml_full[slot]);
+                }
             }
+        }
 
-            // ---- the next piece's rows of Q; the products with the rows before are done (their scores came)
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // ---- rows of Q in, rows of the output out ------------------------------------------
+        const int sw = warp & 3, row = sw * 32 + lane;
+        const uint32_t o_at = tmem + ((uint32_t)(sw * 32) << 16) + 256;
+        uint32_t q_uses[2] = {0, 0}, steps[2] = {0, 0}, uses[2] = {0, 0}, q_next = 0;
+        if (row == 0) t.rec[2 * blockIdx.x] = t.rec[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        uint32_t pk = 0;
+        bool have = false;          // piece pk's output is to come
+#pragma unroll 1
+        for (;;) {
+            // Q of the next piece: where slots share it, into the buffer the piece before does not use.
             const uint32_t nk = have ? pk + 1 : 0;
             const bool more = piece_ready(nk);
             if (more) {
                 const Piece& n = sm.pieces[nk % kPieces];
-                if (n.steps(slot) > 0) {
+                const bool pair = n.pair();
+                const int bufs = n.nt == 0 ? 0 : pair ? 2 : 1;
+#pragma unroll 1
+                for (int i = 0; i < bufs; ++i) {
+                    const uint32_t qb = pair ? (uint32_t)i : q_next;
+                    wait_or_abort(&sm.q_empty[qb], ~(qb ? q_uses[1] : q_uses[0]) & 1u, &sm.aborted);
+                    if (qb) ++q_uses[1]; else ++q_uses[0];
                     constexpr int kVecs = D / 8, kStep = kTile / kVecs;      // vectors of a row, rows of a pass
-                    const int v = tid % kVecs, top = n.row0 + (n.pair() ? slot * kTile : 0), end = n.row0 + n.rows;
+                    const int v = tid % kVecs, top = n.row0 + i * kTile, end = n.row0 + n.rows;
                     const T* src = (const T*)a.q.data + (int64_t)n.head * a.group * a.q.stride_head + v * 8;
-                    unsigned char* dst = sm.q[slot] + (v / 8) * (kTile * 128);
-                    uint4 x[kVecs];
+                    unsigned char* dst = sm.q[qb] + (v / 8) * (kTile * 128);
+#pragma unroll 1
+                    for (int x0 = 0; x0 < kVecs; x0 += 8) {
+                        uint4 x[8];
 #pragma unroll
-                    for (int i = 0; i < kVecs; ++i) {
-                        const int r = top + (tid & 127) / kVecs + i * kStep;
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (r < end) {
-                            const int tok = t.by_group(r), g = r - tok * a.group;
-                            x[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(n.t0 + tok) * a.q.stride_token +
-                                                                   (int64_t)g * a.q.stride_head);
+                        for (int y = 0; y < 8; ++y) {
+                            const int r = top + (tid & 127) / kVecs + (x0 + y) * kStep;
+                            x[y] = make_uint4(0, 0, 0, 0);
+                            if (r < end) {
+                                const int tok = t.by_group(r), g = r - tok * a.group;
+                                x[y] = *reinterpret_cast<const uint4*>(src + (int64_t)(n.t0 + tok) * a.q.stride_token +
+                                                                       (int64_t)g * a.q.stride_head);
+                            }
                         }
-                    }
-                    const uint32_t sign = t.negate ? 0x80008000u : 0u;
 #pragma unroll
-                    for (int i = 0; i < kVecs; ++i) {
-                        const int qr = (tid & 127) / kVecs + i * kStep;
-                        *reinterpret_cast<uint4*>(dst + qr * 128 + ((v ^ qr) & 7) * 16) =
-                            make_uint4(x[i].x ^ sign, x[i].y ^ sign, x[i].z ^ sign, x[i].w ^ sign);
+                        for (int y = 0; y < 8; ++y) {
+                            const int qr = (tid & 127) / kVecs + (x0 + y) * kStep;
+                            *reinterpret_cast<uint4*>(dst + qr * 128 + ((v ^ qr) & 7) * 16) = x[y];
+                        }
                     }
                     fence_async_smem();
-                    mbar_arrive(&sm.q_full[slot]);
+                    __syncwarp();
+                    if (lane == 0) {
+                        __threadfence_block();
+                        atomicAdd(&sm.q_loads[qb], 1u);
+                    }
                 }
+                if (!pair && bufs) q_next ^= 1u;
             }
 
-            // ---- the piece's end: the row's sums go out ------------------------------------
             if (have) {
-                const bool pair = p.pair(), both = !pair && p.nt > 1;
-                const float m2 = m == -INFINITY ? 0.f : m * t.scale_log2;
-                if (my_steps > 0) {
-                    wait_or_abort(&sm.pv_done[slot], (my_steps_done - 1) & 1u, &sm.aborted);
-                    tc_fence_after();
-                }
-                if (both && slot == 1) {
-                    wait_or_abort(&sm.o_free[1], ~o_uses & 1u, &sm.aborted);   // slot 0 has read the last ones
-                    sm.ml[row] = make_float2(m2, l);
-                    mbar_arrive(&sm.ml_full);
-                }
-                if (pair || slot == 0) {
-                    float f0 = 1.f, f1 = 0.f, mt = m2, lt = l;
+                const Piece& p = sm.pieces[pk % kPieces];
+                const bool pair = p.pair(), both = !pair && p.nt > 1, whole = p.first && p.last;
+#pragma unroll 1
+                for (int s = 0; s < (pair ? 2 : 1); ++s) {          // slots that have rows of their own
+                    float f0 = 1.f, f1 = 0.f, mt = 0.f, lt = 0.f;
+                    if (p.nt > 0) {
+                        wait_or_abort(&sm.ml_full[s], (s ? uses[1] : uses[0]) & 1u, &sm.aborted);
+                        wait_or_abort(&sm.pv_done[s], ((s ? steps[1] : steps[0]) + p.steps(s) - 1) & 1u, &sm.aborted);
+                        mt = sm.ml[s][row].x;
+                        lt = sm.ml[s][row].y;
+                    }
                     if (both) {
-                        wait_or_abort(&sm.ml_full, ml_uses & 1u, &sm.aborted);
-                        wait_or_abort(&sm.pv_done[1], (other_steps_done - 1) & 1u, &sm.aborted);
-                        tc_fence_after();
-                        const float2 o = sm.ml[row];
-                        if (l == 0.f) {
+                        wait_or_abort(&sm.ml_full[1], uses[1] & 1u, &sm.aborted);
+                        wait_or_abort(&sm.pv_done[1], (steps[1] + p.steps(1) - 1) & 1u, &sm.aborted);
+                        const float2 o = sm.ml[1][row];
+                        const float m0 = mt, l0 = lt;
+                        if (l0 == 0.f) {
                             mt = o.x;
                         } else if (o.y != 0.f) {
-                            mt = fmaxf(m2, o.x);
+                            mt = fmaxf(m0, o.x);
                         }
-                        f0 = l == 0.f ? 0.f : exp2_approx(m2 - mt);
+                        f0 = l0 == 0.f ? 0.f : exp2_approx(m0 - mt);
                         f1 = o.y == 0.f ? 0.f : exp2_approx(o.x - mt);
-                        lt = l * f0 + o.y * f1;
+                        lt = l0 * f0 + o.y * f1;
                     }
-                    const int local = (pair ? slot * kTile : 0) + row;
-                    const bool valid = local < p.rows, whole = p.first && p.last;
+                    tc_fence_after();
+                    const int local = s * kTile + row;
+                    const bool valid = local < p.rows;
                     if (whole) {
                         const float inv = lt == 0.f ? 0.f : 1.f / lt;
                         f0 *= inv;
@@ -942,9 +1057,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             uint32_t o[16], o1[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[i] = o1[i] = 0u;
-                            if (my_steps > 0) tc_ld16(o, o_at + c);
+                            if (p.nt > 0) tc_ld16(o, o_at + s * 128 + c);
                             if (both) tc_ld16(o1, o_at + 128 + c);
-                            tc_wait_ld();
+                            tc_loaded<16>(o);
+                            tc_loaded<16>(o1);
                             float x[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {             // a slot of weight 0 has no say, whatever it holds
@@ -973,12 +1089,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     tc_fence_before();
-                    if (my_steps > 0) mbar_arrive(&sm.o_free[slot]);
-                    if (both) mbar_arrive(&sm.o_free[1]);
+                    if (p.nt > 0) warp_arrive(&sm.o_free[s]);
+                    if (both) warp_arrive(&sm.o_free[1]);
                 }
-                if (p.steps(1) > 0) ++o_uses;
-                if (both) ++ml_uses;
-                if (slot == 0 && row == 0) {
+                steps[0] += p.steps(0);
+                steps[1] += p.steps(1);
+                if (p.steps(0) > 0) ++uses[0];
+                if (p.steps(1) > 0) ++uses[1];
+                if (row == 0) {
                     if (!p.first) t.rec[2 * blockIdx.x].x = p.last ? 1 : 2;
                     if (p.first && !p.last) t.rec[2 * blockIdx.x + 1] = make_int4(1, p.r, p.head, p.item);
                 }
@@ -1136,7 +1254,7 @@ bool attn_tc_takes(const AttnArgs& a, sv_dtype_t dt)
 {
     const sv_paged_kv_t& c = a.cache;
     const int p = c.page_size;
-    return (dt == SV_DTYPE_BF16 || dt == SV_DTYPE_F16) && (a.head_dim == 64 || a.head_dim == 128) &&
+    return (dt == SV_DTYPE_BF16 || dt == SV_DTYPE_F16) && a.scale >= 0.f && (a.head_dim == 64 || a.head_dim == 128) &&
            ((p >= 8 && p <= kTile && kTile % p == 0) || p % kTile == 0) && c.n_pages > 0 &&
            (long long)c.max_pages * p <= 1ll << 30 && heads_aligned(a.q, 8, 2) && heads_aligned(a.out, 8, 2) &&
            heads_aligned(c.k, 8, 2) && heads_aligned(c.v, 8, 2) && c.stride_page_k % 8 == 0 && c.stride_page_v % 8 == 0 &&
@@ -1157,8 +1275,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
     t.part = reinterpret_cast<float*>(w + (sizeof(int4) * 2 * kTcMaxGrid + rows * sizeof(float2) + 255) / 256 * 256);
     t.by_group = divisor(a.group);
     t.by_page = divisor(a.cache.page_size);
-    t.scale_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, FLT_MIN);   // above 0: hidden scores stay -inf
-    t.negate = a.scale < 0.f;
+    t.scale_log2 = fmaxf(a.scale * 1.4426950408889634f, FLT_MIN);   // above 0: hidden scores stay -inf
     const bool bf16 = dt == SV_DTYPE_BF16;
     CUtensorMap mk, mv;
     if (!make_map(&mk, a.cache.k, a.cache.stride_page_k, a.cache, a.head_dim, bf16) ||
