@@ -162,6 +162,16 @@ __device__ __forceinline__ uint32_t tc_ld1(uint32_t addr)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr) : "memory");
     return r;
 }
+// Some tokens' rows of 64 elements of a group's heads.
+__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int e, int head, int token,
+                                      unsigned long long* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"(map), "r"(e), "r"(head), "r"(token), "r"(smem_u32(bar))
+        : "memory");
+}
 // One page's (or part of a page's) rows of 64 elements, 128-byte swizzled.
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int e, int head, int token, int page,
                                          unsigned long long* bar)
@@ -243,6 +253,7 @@ struct TcArgs {
     int4* rec;              // [grid][2] what each CTA left there
     int part_rows;
     int grid;
+    int q_tokens;           // tokens of a box of Q's map, 0: the output warps load Q
     float scale_log2;       // scale log2 e
 };
 
@@ -307,12 +318,13 @@ struct Piece {
     int t0, n, len;         // the window's first token, its length, the request's cached tokens
     int key_lo, key_hi;     // keys that some row of the item sees
     int all_lo, all_hi;     // keys that every row of it sees
+    int lead;               // the slot that has the first tile where tiles alternate
 
     // An item of more than 128 rows: each slot has rows of its own and every
     // tile; otherwise both have all the rows and every other tile.  A unit is
     // one slot's work on one tile; unit u is slot u & 1's.
     __device__ __forceinline__ bool pair() const { return rows > kTile; }
-    __device__ __forceinline__ int steps(int slot) const { return pair() ? nt : (nt + 1 - slot) >> 1; }
+    __device__ __forceinline__ int steps(int slot) const { return pair() ? nt : (nt + 1 - (slot ^ lead)) >> 1; }
 };
 
 // Walks over a CTA's part of the line.
@@ -382,16 +394,17 @@ struct TcSmem {
     alignas(1024) unsigned char q[2][kTileBytes];
     alignas(1024) unsigned char kv[kStages][kTileBytes];
     unsigned long long full[kStages], empty[kStages];
-    unsigned long long q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
+    unsigned long long q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
     unsigned long long piece_full[kPieces], piece_empty[kPieces];
-    Piece pieces[kPieces];          // warp 2 walks ahead of the other roles
+    Piece pieces[kPieces];          // warp 0 walks ahead of the other roles
     float2 ml[2][kTile];            // the slots' statistics of a finished piece
     long long scan[kTcWarps];
     Walk start;
     uint32_t tmem;
     uint32_t turns[2];              // units of shared tiles whose products each slot has issued
     uint32_t issued;                // ring entries whose loads have begun
-    uint32_t q_loads[2];            // warps that have filled each buffer of Q, over all its loads
+    uint32_t q_issued[2];           // loads of each buffer of Q begun (TMA)
+    uint32_t q_loads[2];            // warps that have filled each buffer of Q, over all its loads (output warps)
     int odd[2][3];                  // a slot's votes, three by turns: some value is not finite
     int aborted;                    // a wait gave up: every later wait gives up at once
     int by_hand[2];                 // the slot has done this tile's P V itself
@@ -456,7 +469,7 @@ __device__ __forceinline__ float2 halves(unsigned long long x)
 template <typename T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcArgs t, const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v)
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q)
 {
     using S = TcSmem<D>;
     constexpr uint32_t kStages = S::kStages;
@@ -470,8 +483,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&sm.empty[i], 2);                // 2: each slot's products, or twice the one slot's
         }
         for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.q_full[s], 1);
             mbar_init(&sm.q_empty[s], 2);
-            sm.q_loads[s] = 0;
+            sm.q_loads[s] = sm.q_issued[s] = 0;
             mbar_init(&sm.s_full[s], 1);
             mbar_init(&sm.p_half[s], 4);               // 4: a warp at a time
             mbar_init(&sm.p_full[s], 4);
@@ -587,13 +601,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     auto piece_release = [&](uint32_t k) { warp_arrive(&sm.piece_empty[k % kPieces]); };
     // The slots hold a row of 128 scores a thread, the other warps little: of
-    // the 512 x 128 registers of the launch, 128 x 72 + 256 x 176 + 128 x 88.
+    // the 512 x 128 registers of the launch, 128 x 64 + 256 x 176 + 128 x 96.
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 2) {
             // ---- loads: lane i has page i of a tile --------------------------------------
             const int page_size = a.cache.page_size;
-            const int box_rows = min(page_size, kTile);
+            const int box_rows = min(page_size, kTile), per_tile = kTile / box_rows;   // pages of a tile, up to 16
             uint32_t base = 0;                        // ring entries of the pieces before
 #pragma unroll 1
             for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
@@ -601,25 +615,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int nt = p.nt, key0 = p.kt0 * kTile, key_lo = p.key_lo, key_hi = p.key_hi, head = p.head;
                 const int32_t* table = a.cache.page_table + (int64_t)p.r * a.cache.ld_table;
                 const int ahead = p.pair() ? 1 : 2;
-                // Page numbers of tiles u .. u + 3; a tile's are read when they are needed three tiles later.
-                int p0 = -1, p1 = -1, p2 = -1, p3 = -1;
+                // Page numbers, a lane a page: 32 of them from tile `first` on, the 32 after those, and the 32 after
+                // those on their way.  A lane's page of a tile is another lane's number.
+                const int span = 32 / per_tile;               // tiles that 32 pages hold
+                auto fetch = [&](int tile) -> int {
+                    const int key = key0 + tile * kTile + lane * box_rows;
+                    if (tile + lane / per_tile >= nt || key >= key_hi || key + box_rows <= key_lo) return -1;
+                    return table[t.by_page(key)];             // pages that nobody sees are not looked at
+                };
+                int first = 0, now = fetch(0), next = fetch(span), later = fetch(2 * span);
 #pragma unroll 1
-                for (int u = -3; u < nt; ++u) {
-                    p0 = p1;
-                    p1 = p2;
-                    p2 = p3;
-                    p3 = -1;
-                    const int key = key0 + (u + 3) * kTile + lane * box_rows;
-                    if (u + 3 < nt && lane * box_rows < kTile && key < key_hi && key + box_rows > key_lo)
-                        p3 = table[t.by_page(key)];   // pages that nobody sees are not looked at
+                for (int u = -ahead; u < nt; ++u) {
+                    if (u == first + span) {
+                        first += span;
+                        now = next;
+                        next = later;
+                        later = fetch(first + 2 * span);
+                    }
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {     // values of tile u, keys of tile u + ahead
                         const int j = half ? u + ahead : u;
-                        if (j < 0 || j >= nt || (half && u < -ahead)) continue;
+                        if (j < 0 || j >= nt) continue;
                         const uint32_t e = base + (half ? entry_k(j, ahead) : entry_v(j, nt, ahead)), stage = e % kStages;
                         const int key_of_page = key0 + j * kTile + lane * box_rows;
-                        const bool mine = lane * box_rows < kTile && key_of_page < key_hi && key_of_page + box_rows > key_lo;
-                        int page = !half ? p0 : ahead == 1 ? p1 : p2;
+                        const bool mine = lane < per_tile && key_of_page < key_hi && key_of_page + box_rows > key_lo;
+                        const int at = (j - first) * per_tile + lane;
+                        const int page0 = __shfl_sync(0xffffffffu, now, at & 31), page1 = __shfl_sync(0xffffffffu, next, at & 31);
+                        int page = at < 32 ? page0 : page1;
                         if (mine && (page < 0 || page >= a.cache.n_pages)) {
                             if (a.status) atomicOr(&a.status[p.r], kBadLayout);
                             page = a.cache.n_pages;            // past the end: reads as zeros
@@ -628,7 +650,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         wait_or_abort(&sm.empty[stage], ~(e / kStages) & 1u, &sm.aborted);   // the first round finds it empty
                         if (lane == 0) {
                             mbar_expect_tx(&sm.full[stage], (uint32_t)(__popc(have) * box_rows * D * 2));
-                            __threadfence_block();
                             *(volatile uint32_t*)&sm.issued = e + 1;
                         }
                         __syncwarp();
@@ -644,7 +665,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 base += 2u * (uint32_t)nt;
             }
-        } else if (warp != 2) {
+        } else if (warp != 0) {
             // ---- matrix products: warp 1 slot 0's, warp 3 slot 1's, one lane issues them -----
             const int s = warp >> 1;
             constexpr uint32_t kQk = instr_desc(Kind<T>::kBf16, false, kTile);
@@ -664,12 +685,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (nt > 0) {
                     if (pair || qb == 0) ++q_uses[0];
                     if (pair || qb == 1) ++q_uses[1];
-                    reached(&sm.q_loads[qb], 4u * (qb ? q_uses[1] : q_uses[0]));
-                    __threadfence_block();
+                    // A slot without steps does not wait: it would not hold the buffer, which may be two loads on.
+                    const uint32_t use = qb ? q_uses[1] : q_uses[0];
+                    if (steps == 0) {
+                    } else if (t.q_tokens) {
+                        reached(&sm.q_issued[qb], use);
+                        wait_or_abort(&sm.q_full[qb], (use - 1) & 1u, &sm.aborted);
+                    } else {
+                        reached(&sm.q_loads[qb], 4u * use);
+                        __threadfence_block();
+                    }
                 }
                 const uint64_t qd = q_desc + qb * kBytes;
-                int j = pair ? 0 : s;                            // tile of the next scores
+                int j = pair ? 0 : s ^ p.lead;                   // tile of the next scores
                 uint32_t e = base + entry_k(j, ahead), k_stage = e % kStages, v_stage = 0;
+                bool edge = false;                               // the values' tile has hidden keys
 #pragma unroll 1
                 for (int st = 0; st <= steps; ++st) {
                     const uint64_t vd = v_desc + v_stage * kBytes, kd = k_desc + k_stage * kBytes;
@@ -679,7 +709,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (st > 0) {                                // P V of step st - 1
                         if (st == 1) wait_or_abort(&sm.o_free[s], ~o_uses++ & 1u, &sm.aborted);   // at first it is
                         wait_or_abort(&sm.p_half[s], done & 1u, &sm.aborted);
-                        const bool by_hand = *(volatile int*)&sm.by_hand[s];
+                        const bool by_hand = edge && *(volatile int*)&sm.by_hand[s];
                         if (pair) reached(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
                         tc_fence_after();
                         if (one_lane() && !by_hand) {
@@ -723,6 +753,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     if (pair && st > 0 && lane == 0) *(volatile uint32_t*)&sm.turns[s] = turns;
                     if (st < steps) {                            // the values that go with these scores, the next keys
+                        edge = (p.kt0 + j) * kTile < p.all_lo || (p.kt0 + j + 1) * kTile > p.all_hi;
                         const uint32_t ev = base + entry_v(j, nt, ahead);
                         v_stage = ev % kStages;
                         j += each;
@@ -743,14 +774,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // ---- the walk over the CTA's pieces: one thread ----------------------------------
             if (lane == 0) {
                 Walk walk = sm.start;
+                uint32_t q_uses[2] = {0, 0}, q_next = 0;
+                int lead = 0;
 #pragma unroll 1
                 for (uint32_t pk = 0;; ++pk) {
                     wait_or_abort(&sm.piece_empty[pk % kPieces], ~(pk / kPieces) & 1u, &sm.aborted);
                     Piece& p = sm.pieces[pk % kPieces];
                     walk.next(t, p);
+                    p.lead = lead;                       // an odd tile is the one slot's, then the other's
+                    if (!p.pair() && (p.nt & 1)) lead ^= 1;
                     const bool end = p.nt < 0 || *(volatile int*)&sm.aborted;
+                    const bool pair = p.pair();
+                    const int bufs = p.nt <= 0 || !t.q_tokens ? 0 : pair ? 2 : 1;
+                    const int q_head = p.head * a.group, q_token = p.t0 + t.by_group(p.row0);
                     mbar_arrive(&sm.piece_full[pk % kPieces]);
                     if (end) break;
+                    // Its rows of Q; where slots share them, into the buffer the piece before does not use.  Rows past
+                    // the box or the window are whatever lies there: rows of the products are independent.
+#pragma unroll 1
+                    for (int i = 0; i < bufs; ++i) {
+                        const uint32_t qb = pair ? (uint32_t)i : q_next;
+                        wait_or_abort(&sm.q_empty[qb], ~(qb ? q_uses[1] : q_uses[0]) & 1u, &sm.aborted);
+                        if (qb) ++q_uses[1]; else ++q_uses[0];
+                        mbar_expect_tx(&sm.q_full[qb], (uint32_t)(t.q_tokens * a.group * D * 2));
+                        *(volatile uint32_t*)&sm.q_issued[qb] = qb ? q_uses[1] : q_uses[0];
+#pragma unroll
+                        for (int x = 0; x < D; x += 64)
+                            tma_q(smem_u32(sm.q[qb]) + (uint32_t)(x / 64 * kTile * 128), &map_q, x, q_head,
+                                  q_token + i * t.q_tokens, &sm.q_full[qb]);
+                    }
+                    if (!pair && bufs) q_next ^= 1u;
                 }
             }
             __syncwarp();
@@ -772,46 +825,71 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int local = (pair ? slot * kTile : 0) + row;     // row of the item
                 const bool warp_valid = local - lane < p.rows;
                 int2 see = make_int2(0, INT_MAX);                      // rows of nobody: no masking
-                if (local < p.rows) see = seen(a, p, t.by_group(p.row0 + local));
-                int k0 = (p.kt0 + (pair ? 0 : slot)) * kTile;
+                const bool valid = local < p.rows;
+                if (valid) see = seen(a, p, t.by_group(p.row0 + local));
+                int k0 = (p.kt0 + (pair ? 0 : slot ^ p.lead)) * kTile;
 #pragma unroll 1
                 for (int st = 0; st < my_steps; ++st, k0 += pair ? kTile : 2 * kTile) {
                     wait_or_abort(&sm.s_full[slot], steps_done & 1u, &sm.aborted);
                     tc_fence_after();
-                    if (warp_valid) {
+                    const bool edge = k0 < p.all_lo || k0 + kTile > p.all_hi;      // a tile with hidden keys
+                    const uint32_t lo = (uint32_t)(see.x - k0), count = (uint32_t)(see.y - see.x);
+                    const bool masked = __any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile);
+                    // A larger maximum: the sums so far under it.
+                    auto grow = [&](float mx) {
+                        const bool grows = valid && (mx - m) * t.scale_log2 > 8.f;   // from -inf: always, unless mx is -inf
+                        if (!__any_sync(0xffffffffu, grows)) return false;
+                        const float f = grows ? exp2_approx((m - mx) * t.scale_log2) : 1.f;
+                        if (grows) {
+                            m = mx;
+                            l *= f;
+                        }
+                        if (st > 0) {
+                            wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 8) {
+                                uint32_t o[8];
+                                tc_ld8(o, o_at + c);
+                                tc_loaded<8>(o);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tc_st8(o, o_at + c);
+                            }
+                        }
+                        return true;
+                    };
+                    // Weights of 32 scores under the maximum m; their sums are added to l0 and l1.
+                    unsigned long long l0 = 0, l1 = 0;
+                    uint32_t w[16];
+                    auto weigh = [&](const uint32_t* s) {
+                        const float shift = Kind<T>::kBias - (m == -INFINITY ? 0.f : m * t.scale_log2);
+                        const unsigned long long scale2 = pair_of(t.scale_log2, t.scale_log2), shift2 = pair_of(shift, shift);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const uint32_t* q = s + 2 * i;
+                            const float2 x = halves(fma2(pair_of(__uint_as_float(q[0]), __uint_as_float(q[1])), scale2, shift2));
+                            const float2 y = halves(fma2(pair_of(__uint_as_float(q[2]), __uint_as_float(q[3])), scale2, shift2));
+                            const float e0 = exp2_approx(x.x), e1 = exp2_approx(x.y);
+                            const float e2 = exp2_approx(y.x), e3 = exp2_approx(y.y);
+                            l0 = add2(l0, pair_of(e0, e1));
+                            l1 = add2(l1, pair_of(e2, e3));
+                            w[i] = Kind<T>::pack(e0, e1);
+                            w[i + 1] = Kind<T>::pack(e2, e3);
+                        }
+                    };
+                    if (warp_valid && pair) {
                         uint32_t s[kTile];                             // fp32 scores
 #pragma unroll
                         for (int c = 0; c < kTile; c += 32) tc_ld32(s + c, s_at + c);
                         tc_loaded<kTile>(s);
-                        if (__any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile)) {
-                            const uint32_t lo = (uint32_t)(see.x - k0), count = (uint32_t)(see.y - see.x);
+                        if (masked) {
 #pragma unroll
                             for (int c = 0; c < kTile; ++c) s[c] = (uint32_t)c - lo < count ? s[c] : 0xff800000u;   // -inf
                         }
-                        // Weights of columns c .. c + 31 under the maximum m, and their sum.
-                        unsigned long long l0, l1;
-                        uint32_t w[16];
-                        auto weigh = [&](int c) {
-                            const float shift = Kind<T>::kBias - (m == -INFINITY ? 0.f : m * t.scale_log2);
-                            const unsigned long long scale2 = pair_of(t.scale_log2, t.scale_log2),
-                                                     shift2 = pair_of(shift, shift);
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const uint32_t* q = s + c + 2 * i;
-                                const float2 x = halves(fma2(pair_of(__uint_as_float(q[0]), __uint_as_float(q[1])), scale2, shift2));
-                                const float2 y = halves(fma2(pair_of(__uint_as_float(q[2]), __uint_as_float(q[3])), scale2, shift2));
-                                const float e0 = exp2_approx(x.x), e1 = exp2_approx(x.y);
-                                const float e2 = exp2_approx(y.x), e3 = exp2_approx(y.y);
-                                l0 = add2(l0, pair_of(e0, e1));
-                                l1 = add2(l1, pair_of(e2, e3));
-                                w[i] = Kind<T>::pack(e0, e1);
-                                w[i + 1] = Kind<T>::pack(e2, e3);
-                            }
-                        };
                         // The first weights are taken under the maximum so far while the tile's is found, and again
                         // if that was too small: rare after a row's first tile, and the maximum costs no time of its own.
-                        l0 = l1 = 0;
-                        weigh(0);
+                        weigh(s);
                         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
                         for (int c = 0; c < kTile; c += 8) {
@@ -820,80 +898,103 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             mx2 = fmaxf(fmaxf(mx2, __uint_as_float(s[c + 4])), __uint_as_float(s[c + 5]));
                             mx3 = fmaxf(fmaxf(mx3, __uint_as_float(s[c + 6])), __uint_as_float(s[c + 7]));
                         }
-                        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-                        const bool grows = (mx - m) * t.scale_log2 > 8.f;   // from -inf: always, unless mx is -inf too
-                        if (__any_sync(0xffffffffu, grows)) {
-                            const float f = grows ? exp2_approx((m - mx) * t.scale_log2) : 1.f;
-                            if (grows) {
-                                m = mx;
-                                l *= f;
-                            }
-                            if (st > 0) {
-                                wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c = 0; c < D; c += 8) {
-                                    uint32_t o[8];
-                                    tc_ld8(o, o_at + c);
-                                    tc_loaded<8>(o);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                    tc_st8(o, o_at + c);
-                                }
-                            }
+                        if (grow(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)))) {
                             l0 = l1 = 0;
-                            weigh(0);
+                            weigh(s);
                         }
-                        const bool edge = k0 < p.all_lo || k0 + kTile > p.all_hi;
                         tc_st16(w, s_at);
-                        weigh(32);
+                        weigh(s + 32);
                         tc_st16(w, s_at + 16);
-                        weigh(64);
+                        weigh(s + 64);
                         if (!edge) {                                   // the products of the first half may begin
                             tc_wait_st();
                             tc_fence_before();
                             warp_arrive(&sm.p_half[slot]);
                         }
                         tc_st16(w, s_at + 32);
-                        weigh(96);
+                        weigh(s + 96);
                         tc_st16(w, s_at + 48);
+                    } else if (warp_valid) {
+                        // The same in less code, for items that memory bounds: twice over 64 columns at a time, the
+                        // maximum first.
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < 2 * kTile; c += 64) {
+                            uint32_t s[64];
+                            tc_ld32(s, s_at + c % kTile);
+                            tc_ld32(s + 32, s_at + c % kTile + 32);
+                            tc_loaded<64>(s);
+                            if (masked) {
+                                const uint32_t from = (uint32_t)(c % kTile) - lo;
+#pragma unroll
+                                for (int i = 0; i < 64; ++i) s[i] = from + (uint32_t)i < count ? s[i] : 0xff800000u;
+                            }
+                            if (c < kTile) {
+                                float mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+                                for (int i = 0; i < 64; i += 8) {
+                                    mx = fmaxf(fmaxf(mx, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+                                    mx1 = fmaxf(fmaxf(mx1, __uint_as_float(s[i + 2])), __uint_as_float(s[i + 3]));
+                                    mx2 = fmaxf(fmaxf(mx2, __uint_as_float(s[i + 4])), __uint_as_float(s[i + 5]));
+                                    mx3 = fmaxf(fmaxf(mx3, __uint_as_float(s[i + 6])), __uint_as_float(s[i + 7]));
+                                }
+                                mx = fmaxf(fmaxf(mx, mx1), fmaxf(mx2, mx3));
+                                if (c == kTile - 64) grow(mx);
+                            } else {
+                                weigh(s);
+                                tc_st16(w, s_at + (c - kTile) / 2);
+                                weigh(s + 32);
+                                tc_st16(w, s_at + (c - kTile) / 2 + 16);
+                            }
+                        }
+                    }
+                    if (warp_valid) {
                         const float2 ls = halves(add2(l0, l1));
                         l += ls.x + ls.y;
                         tc_wait_st();
-                    } else if (!(k0 < p.all_lo || k0 + kTile > p.all_hi)) {
+                    }
+                    if (!edge && !(warp_valid && pair)) {
+                        tc_fence_before();
                         warp_arrive(&sm.p_half[slot]);
                     }
-                    if (k0 < p.all_lo || k0 + kTile > p.all_hi) {
-                        // A tile with hidden keys: its values as the products may read them.
-                        const uint32_t e = base + entry_v(pair ? st : 2 * st + slot, p.nt, pair ? 1 : 2), stage = e % kStages;
+                    if (edge) {
+                        // Its values as the products may read them.
+                        const uint32_t e = base + entry_v(k0 / kTile - p.kt0, p.nt, pair ? 1 : 2), stage = e % kStages;
                         landed(e);
                         unsigned char* vt = sm.kv[stage];
                         const int key = k0 + row;
-                        const bool nobodys = key < p.key_lo || key >= p.key_hi;
-                        constexpr uint32_t m2 = Kind<T>::kExpMask | Kind<T>::kExpMask << 16;
-                        uint32_t bad = 0;
-#pragma unroll 4
-                        for (int c = 0; c < D / 8; ++c) {          // in the swizzle's order: no two lanes in one bank
-                            uint4* x = reinterpret_cast<uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 + ((c ^ row) & 7) * 16);
-                            if (nobodys) {
-                                *x = make_uint4(0, 0, 0, 0);
-                            } else {
-                                const uint4 y = *x;
-                                bad |= __vcmpeq2(y.x & m2, m2) | __vcmpeq2(y.y & m2, m2) | __vcmpeq2(y.z & m2, m2) |
-                                       __vcmpeq2(y.w & m2, m2);
-                            }
+                        if (key < p.key_lo || key >= p.key_hi) {
+#pragma unroll 2
+                            for (int c = 0; c < D / 8; ++c)        // in the swizzle's order: no two lanes in one bank
+                                *reinterpret_cast<uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 + ((c ^ row) & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
                         }
                         fence_async_smem();
-                        // The slot's warps vote and wait for one another (bounded, as every wait: no hardware barrier here).
-                        const bool any_bad = __any_sync(0xffffffffu, bad != 0);
-                        if (any_bad && lane == 0) *(volatile int*)&sm.odd[slot][votes % 3u] = 1;
-                        // The next vote's: all have read it two votes ago, nobody writes it before this vote is over.
-                        if (row == 0) *(volatile int*)&sm.odd[slot][(votes + 1u) % 3u] = 0;
-                        __threadfence_block();
-                        warp_arrive(&sm.vote[slot]);
-                        wait_or_abort(&sm.vote[slot], votes & 1u, &sm.aborted);
-                        const bool by_hand = *(volatile int*)&sm.odd[slot][votes % 3u] != 0;
-                        ++votes;
+                        bool by_hand = false;
+                        // Keys that only some rows see: [key_lo, all_lo) and [all_hi, key_hi).
+                        if (k0 < min(p.all_lo, p.key_hi) || (k0 < p.key_hi && k0 + kTile > p.all_hi && p.all_hi < p.key_hi)) {
+                            uint32_t top = 0;                      // the largest magnitudes, as bits
+                            if (key >= p.key_lo && key < p.key_hi && (key < p.all_lo || key >= p.all_hi)) {
+#pragma unroll 2
+                                for (int c = 0; c < D / 8; ++c) {
+                                    const uint4 y = *reinterpret_cast<const uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 +
+                                                                                    ((c ^ row) & 7) * 16);
+                                    top = __vmaxu2(__vmaxu2(top, y.x & 0x7fff7fffu), y.y & 0x7fff7fffu);
+                                    top = __vmaxu2(__vmaxu2(top, y.z & 0x7fff7fffu), y.w & 0x7fff7fffu);
+                                }
+                            }
+                            const bool bad = max(top & 0xffffu, top >> 16) >= Kind<T>::kExpMask;
+                            // The slot's warps vote and wait for one another (bounded, as every wait: no hardware barrier).
+                            const bool any_bad = __any_sync(0xffffffffu, bad);
+                            if (any_bad && lane == 0) *(volatile int*)&sm.odd[slot][votes % 3u] = 1;
+                            // The next vote's: all have read it two votes ago, nobody writes it before this vote is over.
+                            if (row == 0) *(volatile int*)&sm.odd[slot][(votes + 1u) % 3u] = 0;
+                            __threadfence_block();
+                            warp_arrive(&sm.vote[slot]);
+                            wait_or_abort(&sm.vote[slot], votes & 1u, &sm.aborted);
+                            by_hand = *(volatile int*)&sm.odd[slot][votes % 3u] != 0;
+                            ++votes;
+                        }
                         if (by_hand) {
                             if (warp_valid) {
                                 if (st > 0) {
@@ -958,7 +1059,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
 
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         // ---- rows of Q in, rows of the output out ------------------------------------------
         const int sw = warp & 3, row = sw * 32 + lane;
         const uint32_t o_at = tmem + ((uint32_t)(sw * 32) << 16) + 256;
@@ -968,13 +1069,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool have = false;          // piece pk's output is to come
 #pragma unroll 1
         for (;;) {
-            // Q of the next piece: where slots share it, into the buffer the piece before does not use.
+            // Q of the next piece, where TMA cannot take it: its boxes need groups that divide a tile's rows.
             const uint32_t nk = have ? pk + 1 : 0;
             const bool more = piece_ready(nk);
             if (more) {
                 const Piece& n = sm.pieces[nk % kPieces];
                 const bool pair = n.pair();
-                const int bufs = n.nt == 0 ? 0 : pair ? 2 : 1;
+                const int bufs = n.nt == 0 || t.q_tokens ? 0 : pair ? 2 : 1;
 #pragma unroll 1
                 for (int i = 0; i < bufs; ++i) {
                     const uint32_t qb = pair ? (uint32_t)i : q_next;
@@ -1016,8 +1117,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (have) {
                 const Piece& p = sm.pieces[pk % kPieces];
                 const bool pair = p.pair(), both = !pair && p.nt > 1, whole = p.first && p.last;
+                const int lead = p.lead;
 #pragma unroll 1
-                for (int s = 0; s < (pair ? 2 : 1); ++s) {          // slots that have rows of their own
+                for (int i = 0; i < (pair ? 2 : 1); ++i) {          // rows of one slot, or of both
+                    const int s = pair ? i : lead;
                     float f0 = 1.f, f1 = 0.f, mt = 0.f, lt = 0.f;
                     if (p.nt > 0) {
                         wait_or_abort(&sm.ml_full[s], (s ? uses[1] : uses[0]) & 1u, &sm.aborted);
@@ -1026,9 +1129,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         lt = sm.ml[s][row].y;
                     }
                     if (both) {
-                        wait_or_abort(&sm.ml_full[1], uses[1] & 1u, &sm.aborted);
-                        wait_or_abort(&sm.pv_done[1], (steps[1] + p.steps(1) - 1) & 1u, &sm.aborted);
-                        const float2 o = sm.ml[1][row];
+                        const int z = s ^ 1;
+                        wait_or_abort(&sm.ml_full[z], (z ? uses[1] : uses[0]) & 1u, &sm.aborted);
+                        wait_or_abort(&sm.pv_done[z], ((z ? steps[1] : steps[0]) + p.steps(z) - 1) & 1u, &sm.aborted);
+                        const float2 o = sm.ml[z][row];
                         const float m0 = mt, l0 = lt;
                         if (l0 == 0.f) {
                             mt = o.x;
@@ -1040,7 +1144,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         lt = l0 * f0 + o.y * f1;
                     }
                     tc_fence_after();
-                    const int local = s * kTile + row;
+                    const int local = i * kTile + row;
                     const bool valid = local < p.rows;
                     if (whole) {
                         const float inv = lt == 0.f ? 0.f : 1.f / lt;
@@ -1052,32 +1156,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int64_t token = p.t0 + tok;
                     if (local - lane < p.rows) {
                         T* out = (T*)a.out.data + token * a.out.stride_token + (int64_t)head * a.out.stride_head;
+                        // A slot of weight 0 has no say, whatever it holds: not even 0 times it.
+                        const bool drop0 = f0 == 0.f, drop1 = f1 == 0.f, some = __any_sync(0xffffffffu, drop0 || (both && drop1));
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16], o1[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = o1[i] = 0u;
                             if (p.nt > 0) tc_ld16(o, o_at + s * 128 + c);
-                            if (both) tc_ld16(o1, o_at + 128 + c);
+                            if (both) tc_ld16(o1, o_at + (s ^ 1) * 128 + c);
                             tc_loaded<16>(o);
                             tc_loaded<16>(o1);
-                            float x[16];
+                            if (some) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {             // a slot of weight 0 has no say, whatever it holds
-                                x[i] = f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
-                                x[i] = f1 == 0.f ? x[i] : fmaf(__uint_as_float(o1[i]), f1, x[i]);
+                                for (int i = 0; i < 16; ++i) {
+                                    o[i] = drop0 ? 0u : o[i];
+                                    o1[i] = drop1 ? 0u : o1[i];
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+                            if (both) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
                             }
                             if (valid && whole) {
+                                uint32_t x[8];
 #pragma unroll
-                                for (int i = 0; i < 16; i += 8)
-                                    *reinterpret_cast<uint4*>(out + c + i) =
-                                        make_uint4(Kind<T>::pack(x[i], x[i + 1]), Kind<T>::pack(x[i + 2], x[i + 3]),
-                                                   Kind<T>::pack(x[i + 4], x[i + 5]), Kind<T>::pack(x[i + 6], x[i + 7]));
+                                for (int i = 0; i < 8; ++i)
+                                    x[i] = Kind<T>::pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                                *reinterpret_cast<uint4*>(out + c) = make_uint4(x[0], x[1], x[2], x[3]);
+                                *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
                             } else if (valid) {
 #pragma unroll
                                 for (int i = 0; i < 16; i += 4)
-                                    *reinterpret_cast<float4*>(t.part + part * D + c + i) =
-                                        make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                                    *reinterpret_cast<uint4*>(t.part + part * D + c + i) =
+                                        make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                             }
                         }
                         if (valid && whole) {
@@ -1090,7 +1203,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     tc_fence_before();
                     if (p.nt > 0) warp_arrive(&sm.o_free[s]);
-                    if (both) warp_arrive(&sm.o_free[1]);
+                    if (both) warp_arrive(&sm.o_free[s ^ 1]);
                 }
                 steps[0] += p.steps(0);
                 steps[1] += p.steps(1);
@@ -1110,7 +1223,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (sm.aborted) {
-        if (warp == 0) {                                  // loads in flight land before the kernel ends
+        if (warp == 2) {                                  // loads in flight land before the kernel ends
 #pragma unroll 1
             for (int i = lane; i < 2 * (int)kStages; i += 32)
 #pragma unroll 1
@@ -1214,6 +1327,21 @@ bool make_map(CUtensorMap* m, const sv_heads_t& h, int64_t stride_page, const sv
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_q_map(CUtensorMap* m, const sv_heads_t& q, int tokens, int head_dim, int group, int box_tokens, bool bf16)
+{
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)q.heads, (cuuint64_t)tokens};
+    const cuuint64_t row = (cuuint64_t)head_dim * 2;     // stride of an axis of one
+    const cuuint64_t strides[2] = {q.heads > 1 ? (cuuint64_t)q.stride_head * 2 : row,
+                                   tokens > 1 ? (cuuint64_t)q.stride_token * 2 : row};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)box_tokens};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, q.data, dims, strides, box,
+              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int part_rows(int max_window, int group)
 {
     const long long r = (long long)max_window * group;
@@ -1228,13 +1356,13 @@ Divisor divisor(int d)
 }
 
 template <typename T, int D>
-cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s)
+cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, cudaStream_t s)
 {
     const size_t smem = sizeof(TcSmem<D>);
     static_assert(sizeof(TcSmem<D>) <= 232448, "shared memory of one CTA");
     cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_tc_kernel<T, D>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv);
+    e = launch_pdl(attn_tc_kernel<T, D>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv, mq);
     if (e != cudaSuccess) return e;
     const int y = (t.part_rows + 3) / 4;
     return launch_pdl(attn_join_kernel<T, D>, dim3(t.grid - 1, y > 16 ? 16 : y), dim3(128), 0, s, t);
@@ -1277,13 +1405,17 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
     t.by_page = divisor(a.cache.page_size);
     t.scale_log2 = fmaxf(a.scale * 1.4426950408889634f, FLT_MIN);   // above 0: hidden scores stay -inf
     const bool bf16 = dt == SV_DTYPE_BF16;
-    CUtensorMap mk, mv;
+    CUtensorMap mk, mv, mq{};
     if (!make_map(&mk, a.cache.k, a.cache.stride_page_k, a.cache, a.head_dim, bf16) ||
         !make_map(&mv, a.cache.v, a.cache.stride_page_v, a.cache, a.head_dim, bf16))
         return cudaErrorInvalidValue;
+    if (kTile % a.group == 0 && a.q.stride_head > 0 && a.q.stride_token > 0) {
+        t.q_tokens = kTile / a.group < a.max_window ? kTile / a.group : a.max_window;
+        if (!make_q_map(&mq, a.q, a.tokens, a.head_dim, a.group, t.q_tokens, bf16)) return cudaErrorInvalidValue;
+    }
     if (a.head_dim == 64)
-        return bf16 ? launch_tc<__nv_bfloat16, 64>(t, mk, mv, s) : launch_tc<__half, 64>(t, mk, mv, s);
-    return bf16 ? launch_tc<__nv_bfloat16, 128>(t, mk, mv, s) : launch_tc<__half, 128>(t, mk, mv, s);
+        return bf16 ? launch_tc<__nv_bfloat16, 64>(t, mk, mv, mq, s) : launch_tc<__half, 64>(t, mk, mv, mq, s);
+    return bf16 ? launch_tc<__nv_bfloat16, 128>(t, mk, mv, mq, s) : launch_tc<__half, 128>(t, mk, mv, mq, s);
 }
 
 }  // namespace sv
