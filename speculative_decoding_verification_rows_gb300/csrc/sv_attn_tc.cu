@@ -49,7 +49,6 @@ namespace {
 constexpr int kTile = 128;              // keys of a tile, rows of a slot
 constexpr int kTcThreads = 512;
 constexpr int kTcWarps = kTcThreads / 32;
-constexpr int kMinTiles = 2;            // fewest tiles worth a CTA of its own
 constexpr uint32_t kTmemCols = 512;
 
 // ---- PTX ---------------------------------------------------------------------
@@ -253,6 +252,7 @@ struct TcArgs {
     int4* rec;              // [grid][2] what each CTA left there
     int part_rows;
     int grid;
+    unsigned long long inv_grid;   // ceil(2^64 / grid)
     int q_tokens;           // tokens of a box of Q's map, 0: the output warps load Q
     float scale_log2;       // scale log2 e
 };
@@ -477,35 +477,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     S& sm = *reinterpret_cast<S*>(raw);
     const AttnArgs& a = t.a;
     const int tid = (int)threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    if (tid == 0) {
-        for (int i = 0; i < (int)kStages; ++i) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 2);                // 2: each slot's products, or twice the one slot's
+    if (warp == 3) {                               // a lane a barrier of every kind
+        if (lane < (int)kStages) {
+            mbar_init(&sm.full[lane], 1);
+            mbar_init(&sm.empty[lane], 2);         // 2: each slot's products, or twice the one slot's
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&sm.q_full[s], 1);
-            mbar_init(&sm.q_empty[s], 2);
-            sm.q_loads[s] = sm.q_issued[s] = 0;
-            mbar_init(&sm.s_full[s], 1);
-            mbar_init(&sm.p_half[s], 4);               // 4: a warp at a time
-            mbar_init(&sm.p_full[s], 4);
-            mbar_init(&sm.pv_done[s], 1);
-            mbar_init(&sm.o_free[s], 4);
-            mbar_init(&sm.ml_full[s], 4);
-            mbar_init(&sm.vote[s], 4);
-            sm.turns[s] = 0;
-            sm.odd[s][0] = sm.odd[s][1] = sm.odd[s][2] = 0;
-            sm.by_hand[s] = 0;
+        if (lane < kPieces) {
+            mbar_init(&sm.piece_full[lane], 1);
+            mbar_init(&sm.piece_empty[lane], kPieceReaders);
         }
-        for (int i = 0; i < kPieces; ++i) {
-            mbar_init(&sm.piece_full[i], 1);
-            mbar_init(&sm.piece_empty[i], kPieceReaders);
+        if (lane < 2) {
+            mbar_init(&sm.q_full[lane], 1);
+            mbar_init(&sm.q_empty[lane], 2);
+            mbar_init(&sm.s_full[lane], 1);
+            mbar_init(&sm.p_half[lane], 4);        // 4: a warp at a time
+            mbar_init(&sm.p_full[lane], 4);
+            mbar_init(&sm.pv_done[lane], 1);
+            mbar_init(&sm.o_free[lane], 4);
+            mbar_init(&sm.ml_full[lane], 4);
+            mbar_init(&sm.vote[lane], 4);
+            sm.q_loads[lane] = sm.q_issued[lane] = sm.turns[lane] = 0;
+            sm.by_hand[lane] = 0;
+            sm.odd[lane][0] = sm.odd[lane][1] = sm.odd[lane][2] = 0;
         }
-        mbar_init(&sm.drain, 2);
-        sm.aborted = 0;
-        sm.issued = 0;
-        sm.start.left = 0;
+        if (lane == 0) {
+            mbar_init(&sm.drain, 2);
+            sm.aborted = 0;
+            sm.issued = 0;
+            sm.start.left = 0;
+        }
         mbar_fence_init();
+    }
+    if (warp == 2 && lane < 3) {
+        const CUtensorMap* map = lane == 0 ? &map_k : lane == 1 ? &map_v : &map_q;
+        if (lane < 2 || t.q_tokens) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     }
     if (warp == 1) tc_alloc(&sm.tmem);
     pdl_enter();
@@ -517,9 +522,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int pass = 0; pass < 2; ++pass) {
         long long begin = 0, end = 0;
         if (pass == 1) {
-            const int b = (int)min((long long)t.grid, max(1ll, total / kMinTiles)), x = (int)blockIdx.x;
+            // Two tiles a CTA at least; otherwise total / grid by the high word of a product, no division.
+            const bool few = total < 2ll * t.grid;
+            const int b = few ? max(1, (int)total >> 1) : t.grid, x = (int)blockIdx.x;
             if (x >= b) break;
-            const long long each = total / b;
+            const long long each = few ? min(total, 2ll) : (long long)__umul64hi((unsigned long long)total, t.inv_grid);
             const int more = (int)(total - each * b);          // the first CTAs have one tile more
             begin = each * x + min(x, more);
             end = begin + each + (x < more);
@@ -541,12 +548,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncthreads();
                 if (lane == 31) sm.scan[warp] = incl;
                 __syncthreads();
-                long long chunk = 0;
-#pragma unroll 1
-                for (int w = 0; w < kTcWarps; ++w) {
-                    if (w < warp) incl += sm.scan[w];
-                    chunk += sm.scan[w];
+                long long upto = lane < kTcWarps ? sm.scan[lane] : 0;      // the warps' sums, every warp for itself
+#pragma unroll
+                for (int x = 1; x < kTcWarps; x <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, upto, x);
+                    if (lane >= x) upto += y;
                 }
+                const long long chunk = __shfl_sync(0xffffffffu, upto, kTcWarps - 1);
+                const long long below = __shfl_sync(0xffffffffu, upto, (warp - 1) & 31);
+                if (warp > 0) incl += below;
                 if (pass == 0) total += chunk;
                 if (pass == 1) incl += before;
                 before += chunk;
@@ -830,9 +840,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 int k0 = (p.kt0 + (pair ? 0 : slot ^ p.lead)) * kTile;
 #pragma unroll 1
                 for (int st = 0; st < my_steps; ++st, k0 += pair ? kTile : 2 * kTile) {
+                    const bool edge = k0 < p.all_lo || k0 + kTile > p.all_hi;      // a tile with hidden keys
+                    bool by_hand = false;
+                    if (edge) {
+                        // Its values as the products may read them, while the scores are on their way.
+                        const uint32_t e = base + entry_v(k0 / kTile - p.kt0, p.nt, pair ? 1 : 2), stage = e % kStages;
+                        landed(e);
+                        unsigned char* vt = sm.kv[stage];
+                        const int key = k0 + row;
+                        if (key < p.key_lo || key >= p.key_hi) {
+#pragma unroll 2
+                            for (int c = 0; c < D / 8; ++c)        // in the swizzle's order: no two lanes in one bank
+                                *reinterpret_cast<uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 + ((c ^ row) & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_smem();
+                        // Keys that only some rows see: [key_lo, all_lo) and [all_hi, key_hi).
+                        if (k0 < min(p.all_lo, p.key_hi) || (k0 < p.key_hi && k0 + kTile > p.all_hi && p.all_hi < p.key_hi)) {
+                            uint32_t top = 0;                      // the largest magnitudes, as bits
+                            if (key >= p.key_lo && key < p.key_hi && (key < p.all_lo || key >= p.all_hi)) {
+#pragma unroll 2
+                                for (int c = 0; c < D / 8; ++c) {
+                                    const uint4 y = *reinterpret_cast<const uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 +
+                                                                                    ((c ^ row) & 7) * 16);
+                                    top = __vmaxu2(__vmaxu2(top, y.x & 0x7fff7fffu), y.y & 0x7fff7fffu);
+                                    top = __vmaxu2(__vmaxu2(top, y.z & 0x7fff7fffu), y.w & 0x7fff7fffu);
+                                }
+                            }
+                            const bool bad = max(top & 0xffffu, top >> 16) >= Kind<T>::kExpMask;
+                            // The slot's warps vote and wait for one another (bounded, as every wait: no hardware barrier).
+                            const bool any_bad = __any_sync(0xffffffffu, bad);
+                            if (any_bad && lane == 0) *(volatile int*)&sm.odd[slot][votes % 3u] = 1;
+                            // The next vote's: all have read it two votes ago, nobody writes it before this vote is over.
+                            if (row == 0) *(volatile int*)&sm.odd[slot][(votes + 1u) % 3u] = 0;
+                            __threadfence_block();
+                            warp_arrive(&sm.vote[slot]);
+                            wait_or_abort(&sm.vote[slot], votes & 1u, &sm.aborted);
+                            by_hand = *(volatile int*)&sm.odd[slot][votes % 3u] != 0;
+                            ++votes;
+                        }
+                    }
                     wait_or_abort(&sm.s_full[slot], steps_done & 1u, &sm.aborted);
                     tc_fence_after();
-                    const bool edge = k0 < p.all_lo || k0 + kTile > p.all_hi;      // a tile with hidden keys
                     const uint32_t lo = (uint32_t)(see.x - k0), count = (uint32_t)(see.y - see.x);
                     const bool masked = __any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile);
                     // A larger maximum: the sums so far under it.
@@ -906,7 +955,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         weigh(s + 32);
                         tc_st16(w, s_at + 16);
                         weigh(s + 64);
-                        if (!edge) {                                   // the products of the first half may begin
+                        if (!by_hand) {                                // the products of the first half may begin
                             tc_wait_st();
                             tc_fence_before();
                             warp_arrive(&sm.p_half[slot]);
@@ -953,94 +1002,57 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         l += ls.x + ls.y;
                         tc_wait_st();
                     }
-                    if (!edge && !(warp_valid && pair)) {
+                    if (!by_hand && !(warp_valid && pair)) {
                         tc_fence_before();
                         warp_arrive(&sm.p_half[slot]);
                     }
-                    if (edge) {
-                        // Its values as the products may read them.
-                        const uint32_t e = base + entry_v(k0 / kTile - p.kt0, p.nt, pair ? 1 : 2), stage = e % kStages;
-                        landed(e);
-                        unsigned char* vt = sm.kv[stage];
-                        const int key = k0 + row;
-                        if (key < p.key_lo || key >= p.key_hi) {
-#pragma unroll 2
-                            for (int c = 0; c < D / 8; ++c)        // in the swizzle's order: no two lanes in one bank
-                                *reinterpret_cast<uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 + ((c ^ row) & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async_smem();
-                        bool by_hand = false;
-                        // Keys that only some rows see: [key_lo, all_lo) and [all_hi, key_hi).
-                        if (k0 < min(p.all_lo, p.key_hi) || (k0 < p.key_hi && k0 + kTile > p.all_hi && p.all_hi < p.key_hi)) {
-                            uint32_t top = 0;                      // the largest magnitudes, as bits
-                            if (key >= p.key_lo && key < p.key_hi && (key < p.all_lo || key >= p.all_hi)) {
-#pragma unroll 2
-                                for (int c = 0; c < D / 8; ++c) {
-                                    const uint4 y = *reinterpret_cast<const uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 +
-                                                                                    ((c ^ row) & 7) * 16);
-                                    top = __vmaxu2(__vmaxu2(top, y.x & 0x7fff7fffu), y.y & 0x7fff7fffu);
-                                    top = __vmaxu2(__vmaxu2(top, y.z & 0x7fff7fffu), y.w & 0x7fff7fffu);
-                                }
+                    if (by_hand) {
+                        const uint32_t e = base + entry_v(k0 / kTile - p.kt0, p.nt, pair ? 1 : 2);
+                        const unsigned char* vt = sm.kv[e % kStages];
+                        if (warp_valid) {
+                            if (st > 0) {
+                                wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
+                                tc_fence_after();
                             }
-                            const bool bad = max(top & 0xffffu, top >> 16) >= Kind<T>::kExpMask;
-                            // The slot's warps vote and wait for one another (bounded, as every wait: no hardware barrier).
-                            const bool any_bad = __any_sync(0xffffffffu, bad);
-                            if (any_bad && lane == 0) *(volatile int*)&sm.odd[slot][votes % 3u] = 1;
-                            // The next vote's: all have read it two votes ago, nobody writes it before this vote is over.
-                            if (row == 0) *(volatile int*)&sm.odd[slot][(votes + 1u) % 3u] = 0;
-                            __threadfence_block();
-                            warp_arrive(&sm.vote[slot]);
-                            wait_or_abort(&sm.vote[slot], votes & 1u, &sm.aborted);
-                            by_hand = *(volatile int*)&sm.odd[slot][votes % 3u] != 0;
-                            ++votes;
-                        }
-                        if (by_hand) {
-                            if (warp_valid) {
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = 0u;
                                 if (st > 0) {
-                                    wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
-                                    tc_fence_after();
+                                    tc_ld32(o, o_at + c);
+                                    tc_loaded<32>(o);
                                 }
 #pragma unroll 1
-                                for (int c = 0; c < D; c += 32) {
-                                    uint32_t o[32];
+                                for (int kk = 0; kk < kTile; ++kk) {
+                                    uint32_t w2 = tc_ld1(s_at + kk / 2);
+                                    tc_wait_ld();
+                                    asm volatile("" : "+r"(w2));
+                                    const float2 wf = Kind<T>::unpack(w2);
+                                    const float wt = kk & 1 ? wf.y : wf.x;
+                                    if (wt != 0.f) {
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                                    if (st > 0) {
-                                        tc_ld32(o, o_at + c);
-                                        tc_loaded<32>(o);
-                                    }
-#pragma unroll 1
-                                    for (int kk = 0; kk < kTile; ++kk) {
-                                        uint32_t w2 = tc_ld1(s_at + kk / 2);
-                                        tc_wait_ld();
-                                        asm volatile("" : "+r"(w2));
-                                        const float2 wf = Kind<T>::unpack(w2);
-                                        const float wt = kk & 1 ? wf.y : wf.x;
-                                        if (wt != 0.f) {
+                                        for (int i = 0; i < 32; i += 8) {
+                                            const int v = (c + i) / 8;
+                                            const uint4 x = *reinterpret_cast<const uint4*>(
+                                                vt + (v / 8) * (kTile * 128) + kk * 128 + ((v ^ kk) & 7) * 16);
+                                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                                            for (int i = 0; i < 32; i += 8) {
-                                                const int v = (c + i) / 8;
-                                                const uint4 x = *reinterpret_cast<const uint4*>(
-                                                    vt + (v / 8) * (kTile * 128) + kk * 128 + ((v ^ kk) & 7) * 16);
-                                                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                                for (int y = 0; y < 4; ++y) {
-                                                    const float2 f = Kind<T>::unpack(xs[y]);
-                                                    uint32_t* q = o + i + 2 * y;
-                                                    q[0] = __float_as_uint(fmaf(wt, f.x, __uint_as_float(q[0])));
-                                                    q[1] = __float_as_uint(fmaf(wt, f.y, __uint_as_float(q[1])));
-                                                }
+                                            for (int y = 0; y < 4; ++y) {
+                                                const float2 f = Kind<T>::unpack(xs[y]);
+                                                uint32_t* q = o + i + 2 * y;
+                                                q[0] = __float_as_uint(fmaf(wt, f.x, __uint_as_float(q[0])));
+                                                q[1] = __float_as_uint(fmaf(wt, f.y, __uint_as_float(q[1])));
                                             }
                                         }
-                                        __syncwarp();
                                     }
-                                    tc_st32(o, o_at + c);
+                                    __syncwarp();
                                 }
-                                tc_wait_st();
+                                tc_st32(o, o_at + c);
                             }
-                            if (row == 0) *(volatile int*)&sm.by_hand[slot] = 1;
+                            tc_wait_st();
                         }
+                        if (row == 0) *(volatile int*)&sm.by_hand[slot] = 1;
                         tc_fence_before();
                         warp_arrive(&sm.p_half[slot]);
                     }
@@ -1240,55 +1252,106 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // Joins the pieces of an item: CTA x of the first kernel began it, the ones
-// after it have the rest.  A warp a row; pieces in the order of the line.
+// after it have the rest.  A warp a row while pieces are few; the block's four
+// warps share a row's pieces when they are many, a quarter each, and join them
+// in the order of the line.
+constexpr int kFewPieces = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) attn_join_kernel(const TcArgs t)
+__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ TcArgs t)
 {
+    constexpr int kE = D / 32;
+    __shared__ float sum_sh[4][D];
+    __shared__ float2 ml_sh[4];
     pdl_enter();
     const AttnArgs& a = t.a;
-    const int c0 = (int)blockIdx.x;
+    const int c0 = (int)blockIdx.x, warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
     const int4 rec = t.rec[2 * c0 + 1];
     if (!rec.x) return;
-    const Window w = window_of(a, rec.y, false);
-    const int rows = w.item_rows(rec.w), row0 = w.row0(rec.w);
-    int last = c0 + 1;
-    while (last < t.grid - 1 && t.rec[2 * last].x == 2) ++last;
-    const int lane = (int)threadIdx.x & 31;
-    for (int row = (int)blockIdx.y * 4 + ((int)threadIdx.x >> 5); row < rows; row += (int)gridDim.y * 4) {
-        const int64_t at0 = (int64_t)(2 * c0 + 1) * t.part_rows + row;
-        auto at = [&](int c) { return c == c0 ? at0 : (int64_t)(2 * c) * t.part_rows + row; };
-        float mt = -INFINITY;
-        for (int c = c0; c <= last; ++c) {
-            const float2 ml = t.part_ml[at(c)];
-            if (ml.y != 0.f) mt = fmaxf(mt, ml.x);
+    int last = c0 + 1;                                       // the CTA with the item's last piece
+#pragma unroll 1
+    for (; last < t.grid - 1; last += 32) {
+        const int c = last + lane;
+        const uint32_t ends = __ballot_sync(0xffffffffu, c >= t.grid - 1 || t.rec[2 * c].x != 2);
+        if (ends) {
+            last += __ffs(ends) - 1;
+            break;
         }
-        constexpr int kE = D / 32;
-        float x[kE], lt = 0.f;
+    }
+    last = min(last, t.grid - 1);
+    const Window w = window_of(a, rec.y, false);
+    const int rows = w.item_rows(rec.w), row0 = w.row0(rec.w), n = last - c0 + 1;
+    const bool shared = n > kFewPieces;
+    const int each = shared ? (n + 3) / 4 : n;               // pieces of a warp
+    const int i0 = shared ? warp * each : 0, i1 = min(n, i0 + each);
+    const int stride = (int)gridDim.y * (shared ? 1 : 4);
+#pragma unroll 1
+    for (int row = (int)blockIdx.y * (shared ? 1 : 4) + (shared ? 0 : warp); row < rows; row += stride) {
+        // Piece i of the row: the first one is the second record of its CTA.
+        auto at = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0)) * t.part_rows + row; };
+        float mt = -INFINITY, lt = 0.f, x[kE];
 #pragma unroll
-        for (int i = 0; i < kE; ++i) x[i] = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= last; ++c) {
-            const float2 ml = t.part_ml[at(c)];
-            const float* src = t.part + at(c) * D + lane * kE;
-            float y[kE];
+        for (int e = 0; e < kE; ++e) x[e] = 0.f;
+#pragma unroll 1
+        for (int i = i0; i < i1; i += 8) {                   // eight pieces' loads in flight
+            float2 ml[8];
+            float y[8][kE];
 #pragma unroll
-            for (int i = 0; i < kE; ++i) y[i] = src[i];
-            if (ml.y == 0.f) continue;
-            const float f = exp2_approx(ml.x - mt);
-            lt = fmaf(ml.y, f, lt);
+            for (int z = 0; z < 8; ++z) {
+                const int64_t q = at(min(i + z, i1 - 1));
+                ml[z] = t.part_ml[q];
+                if (i + z >= i1) ml[z].y = 0.f;
 #pragma unroll
-            for (int i = 0; i < kE; ++i) x[i] = fmaf(y[i], f, x[i]);
+                for (int e = 0; e < kE; ++e) y[z][e] = t.part[q * D + lane * kE + e];
+            }
+            float top = mt;
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+                if (ml[z].y != 0.f) top = fmaxf(top, ml[z].x);
+            const float keep = lt == 0.f ? 0.f : exp2_approx(mt - top);
+            mt = top;
+            lt *= keep;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) x[e] = keep == 0.f ? 0.f : x[e] * keep;
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+                if (ml[z].y == 0.f) continue;
+                const float f = exp2_approx(ml[z].x - mt);
+                lt = fmaf(ml[z].y, f, lt);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) x[e] = fmaf(y[z][e], f, x[e]);
+            }
+        }
+        if (shared) {
+            __syncthreads();                                 // the row before has been read
+            if (lane == 0) ml_sh[warp] = make_float2(mt, lt);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) sum_sh[warp][lane * kE + e] = x[e];
+            __syncthreads();
+            if (warp != 0) continue;
+            float top = -INFINITY;
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                if (ml_sh[z].y != 0.f) top = fmaxf(top, ml_sh[z].x);
+            lt = 0.f;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) x[e] = 0.f;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                if (ml_sh[z].y == 0.f) continue;
+                const float f = exp2_approx(ml_sh[z].x - top);
+                lt = fmaf(ml_sh[z].y, f, lt);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) x[e] = fmaf(sum_sh[z][lane * kE + e], f, x[e]);
+            }
+            mt = top;
         }
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
         const int tok = t.by_group(row0 + row), g = row0 + row - tok * a.group;
         const int64_t token = w.t0 + tok;
         const int head = rec.z * a.group + g;
         T* dst = (T*)a.out.data + token * a.out.stride_token + (int64_t)head * a.out.stride_head + lane * kE;
-        uint32_t o[kE / 2];
 #pragma unroll
-        for (int i = 0; i < kE; i += 2) o[i / 2] = Kind<T>::pack(x[i] * inv, x[i + 1] * inv);
-#pragma unroll
-        for (int i = 0; i < kE / 2; ++i) reinterpret_cast<uint32_t*>(dst)[i] = o[i];
+        for (int e = 0; e < kE; e += 2) reinterpret_cast<uint32_t*>(dst)[e / 2] = Kind<T>::pack(x[e] * inv, x[e + 1] * inv);
         if (a.lse && lane == 0)
             a.lse[token * a.q.heads + head] = lt == 0.f ? -INFINITY : mt * 0.69314718055994531f + logf(lt);
     }
@@ -1365,7 +1428,7 @@ cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap&
     e = launch_pdl(attn_tc_kernel<T, D>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv, mq);
     if (e != cudaSuccess) return e;
     const int y = (t.part_rows + 3) / 4;
-    return launch_pdl(attn_join_kernel<T, D>, dim3(t.grid - 1, y > 16 ? 16 : y), dim3(128), 0, s, t);
+    return launch_pdl(attn_join_kernel<T, D>, dim3(t.grid - 1, y), dim3(128), 0, s, t);
 }
 
 }  // namespace
@@ -1396,6 +1459,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
     t.a = a;
     t.part_rows = part_rows(a.max_window, a.group);
     t.grid = num_sms < kTcMaxGrid ? (num_sms < 2 ? 2 : num_sms) : kTcMaxGrid;
+    t.inv_grid = ~0ull / (unsigned)t.grid + 1;
     char* w = static_cast<char*>(ws);
     const size_t rows = 2 * (size_t)kTcMaxGrid * (size_t)t.part_rows;
     t.rec = reinterpret_cast<int4*>(w);
