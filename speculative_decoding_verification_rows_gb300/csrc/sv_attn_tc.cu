@@ -50,6 +50,7 @@ constexpr int kTile = 128;              // keys of a tile, rows of a slot
 constexpr int kTcThreads = 512;
 constexpr int kTcWarps = kTcThreads / 32;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kLongPiece = 16;
 
 // ---- PTX ---------------------------------------------------------------------
 __device__ __forceinline__ void tc_alloc(uint32_t* where)
@@ -430,6 +431,12 @@ __device__ __forceinline__ uint32_t entry_v(int j, int nt, int ahead)
 }
 __device__ __forceinline__ uint32_t entry_k(int j, int ahead) { return (uint32_t)(j < ahead ? j : 2 * j - ahead + 1); }
 
+// Bits lo .. hi - 1 of 32.
+__device__ __forceinline__ uint32_t columns_seen(int lo, int hi)
+{
+    const uint32_t below_hi = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
+    return lo >= 32 ? 0u : lo <= 0 ? below_hi : below_hi & (0xffffffffu << lo);
+}
 __device__ __forceinline__ bool one_lane()
 {
     uint32_t r;
@@ -832,6 +839,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             {
                 const bool pair = p.pair();
                 const int my_steps = p.steps(slot);
+                const bool whole_rows = pair && p.nt >= kLongPiece;
                 const int local = (pair ? slot * kTile : 0) + row;     // row of the item
                 const bool warp_valid = local - lane < p.rows;
                 int2 see = make_int2(0, INT_MAX);                      // rows of nobody: no masking
@@ -882,18 +890,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     wait_or_abort(&sm.s_full[slot], steps_done & 1u, &sm.aborted);
                     tc_fence_after();
-                    const uint32_t lo = (uint32_t)(see.x - k0), count = (uint32_t)(see.y - see.x);
+                    const int lo = see.x - k0, hi = see.y - k0;                    // the row's columns
+                    const bool nothing = __all_sync(0xffffffffu, see.x >= k0 + kTile || see.y <= k0);
                     const bool masked = __any_sync(0xffffffffu, see.x > k0 || see.y < k0 + kTile);
                     // A larger maximum: the sums so far under it.
                     auto grow = [&](float mx) {
                         const bool grows = valid && (mx - m) * t.scale_log2 > 8.f;   // from -inf: always, unless mx is -inf
                         if (!__any_sync(0xffffffffu, grows)) return false;
                         const float f = grows ? exp2_approx((m - mx) * t.scale_log2) : 1.f;
+                        const bool some = __any_sync(0xffffffffu, grows && l != 0.f);   // a row without weights so far has O = 0
                         if (grows) {
                             m = mx;
                             l *= f;
                         }
-                        if (st > 0) {
+                        if (st > 0 && some) {
                             wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
                             tc_fence_after();
 #pragma unroll 1
@@ -927,14 +937,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             w[i + 1] = Kind<T>::pack(e2, e3);
                         }
                     };
-                    if (warp_valid && pair) {
+                    if (nothing) {                                     // no row of the warp sees the tile
+                        if (warp_valid) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[i] = 0u;
+#pragma unroll
+                            for (int c = 0; c < kTile / 2; c += 16) tc_st16(w, s_at + c);
+                        }
+                    } else if (warp_valid && whole_rows) {
                         uint32_t s[kTile];                             // fp32 scores
 #pragma unroll
                         for (int c = 0; c < kTile; c += 32) tc_ld32(s + c, s_at + c);
                         tc_loaded<kTile>(s);
                         if (masked) {
 #pragma unroll
-                            for (int c = 0; c < kTile; ++c) s[c] = (uint32_t)c - lo < count ? s[c] : 0xff800000u;   // -inf
+                            for (int c = 0; c < kTile; c += 32) {
+                                const uint32_t in = columns_seen(lo - c, hi - c);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) s[c + i] = in >> i & 1u ? s[c + i] : 0xff800000u;   // -inf
+                            }
                         }
                         // The first weights are taken under the maximum so far while the tile's is found, and again
                         // if that was too small: rare after a row's first tile, and the maximum costs no time of its own.
@@ -974,9 +995,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc_ld32(s + 32, s_at + c % kTile + 32);
                             tc_loaded<64>(s);
                             if (masked) {
-                                const uint32_t from = (uint32_t)(c % kTile) - lo;
+                                const int at = c % kTile;
+                                const uint32_t in0 = columns_seen(lo - at, hi - at), in1 = columns_seen(lo - at - 32, hi - at - 32);
 #pragma unroll
-                                for (int i = 0; i < 64; ++i) s[i] = from + (uint32_t)i < count ? s[i] : 0xff800000u;
+                                for (int i = 0; i < 32; ++i) {
+                                    s[i] = in0 >> i & 1u ? s[i] : 0xff800000u;
+                                    s[i + 32] = in1 >> i & 1u ? s[i + 32] : 0xff800000u;
+                                }
                             }
                             if (c < kTile) {
                                 float mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -1002,7 +1027,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         l += ls.x + ls.y;
                         tc_wait_st();
                     }
-                    if (!by_hand && !(warp_valid && pair)) {
+                    if (!by_hand && (nothing || !(warp_valid && whole_rows))) {
                         tc_fence_before();
                         warp_arrive(&sm.p_half[slot]);
                     }
