@@ -41,6 +41,8 @@
 #include <float.h>
 #include <limits.h>
 
+#include <atomic>
+
 #include "sv_attn.cuh"
 
 namespace sv {
@@ -50,7 +52,8 @@ constexpr int kTile = 128;              // keys of a tile, rows of a slot
 constexpr int kTcThreads = 512;
 constexpr int kTcWarps = kTcThreads / 32;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kLongPiece = 16;
+constexpr int kLongPiece = 16;          // tiles of a piece whose slots take the unrolled code
+constexpr int kWholeTiles = 4;          // items of caches up to this long are not split
 
 // ---- PTX ---------------------------------------------------------------------
 __device__ __forceinline__ void tc_alloc(uint32_t* where)
@@ -253,6 +256,7 @@ struct TcArgs {
     int4* rec;              // [grid][2] what each CTA left there
     int part_rows;
     int grid;
+    int whole;              // items are not split: each counts as one tile of the line
     unsigned long long inv_grid;   // ceil(2^64 / grid)
     int q_tokens;           // tokens of a box of Q's map, 0: the output warps load Q
     float scale_log2;       // scale log2 e
@@ -305,7 +309,7 @@ __device__ __forceinline__ long long head_tiles(const TcArgs& t, const Window& w
 #pragma unroll 1
     for (int i = 0; i < w.items; ++i) {
         const int2 x = item_tiles(t, w, i);
-        c += x.y - x.x;
+        c += t.whole ? 1 : x.y - x.x;
     }
     return c;
 }
@@ -341,7 +345,7 @@ struct Walk {
             p.nt = -1;
             return;
         }
-        const int have = tiles.y - tiles.x;
+        const int have = t.whole ? 1 : tiles.y - tiles.x;
         p.r = r;
         p.head = head;
         p.item = item;
@@ -360,7 +364,7 @@ struct Walk {
         p.key_hi = bottom.y;
         p.all_lo = bottom.x;
         p.all_hi = top.y;
-        p.nt = bottom.y > top.x ? nt : 0;
+        p.nt = bottom.y <= top.x ? 0 : t.whole ? tiles.y - tiles.x : nt;
         left -= nt;
         done += nt;
         if (last && left > 0) {
@@ -529,11 +533,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int pass = 0; pass < 2; ++pass) {
         long long begin = 0, end = 0;
         if (pass == 1) {
-            // Two tiles a CTA at least; otherwise total / grid by the high word of a product, no division.
-            const bool few = total < 2ll * t.grid;
-            const int b = few ? max(1, (int)total >> 1) : t.grid, x = (int)blockIdx.x;
+            // Two tiles (or one item) a CTA at least; else total / grid by the high word of a product, no division.
+            const int least = t.whole ? 1 : 2;
+            const bool few = total < (long long)least * t.grid;
+            const int b = few ? max(1, (int)total / least) : t.grid, x = (int)blockIdx.x;
             if (x >= b) break;
-            const long long each = few ? min(total, 2ll) : (long long)__umul64hi((unsigned long long)total, t.inv_grid);
+            const long long each = few ? min(total, (long long)least)
+                                       : (long long)__umul64hi((unsigned long long)total, t.inv_grid);
             const int more = (int)(total - each * b);          // the first CTAs have one tile more
             begin = each * x + min(x, more);
             end = begin + each + (x < more);
@@ -581,8 +587,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (;; ++k.item) {
                     k.tiles = item_tiles(t, k.w, k.item);
-                    if (off < k.tiles.y - k.tiles.x) break;
-                    off -= k.tiles.y - k.tiles.x;
+                    const int cost = t.whole ? 1 : k.tiles.y - k.tiles.x;
+                    if (off < cost) break;
+                    off -= cost;
                 }
                 k.done = (int)off;
                 sm.start = k;
@@ -1448,10 +1455,18 @@ cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap&
 {
     const size_t smem = sizeof(TcSmem<D>);
     static_assert(sizeof(TcSmem<D>) <= 232448, "shared memory of one CTA");
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> ready{0};                   // a bit a device: the kernel may use that much there
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
     e = launch_pdl(attn_tc_kernel<T, D>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv, mq);
     if (e != cudaSuccess) return e;
+    if (t.whole) return cudaSuccess;
     const int y = (t.part_rows + 3) / 4;
     return launch_pdl(attn_join_kernel<T, D>, dim3(t.grid - 1, y), dim3(128), 0, s, t);
 }
@@ -1493,6 +1508,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
     t.by_group = divisor(a.group);
     t.by_page = divisor(a.cache.page_size);
     t.scale_log2 = fmaxf(a.scale * 1.4426950408889634f, FLT_MIN);   // above 0: hidden scores stay -inf
+    // Short caches: an item of up to kWholeTiles tiles is not worth a second kernel.
+    t.whole = (long long)a.cache.max_pages * a.cache.page_size <= (long long)kWholeTiles * kTile;
     const bool bf16 = dt == SV_DTYPE_BF16;
     CUtensorMap mk, mv, mq{};
     if (!make_map(&mk, a.cache.k, a.cache.stride_page_k, a.cache, a.head_dim, bf16) ||

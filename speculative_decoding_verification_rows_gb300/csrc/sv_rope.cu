@@ -70,10 +70,11 @@ struct RopeArgs {
 
 // A head is a set of units: each rotated unit is two parts of VEC elements
 // whose pairs it turns (rot_dim / 2 apart, or adjacent in the interleaved
-// layout), then one part per unit for what is only copied.  A thread keeps one
+// layout), then two parts a unit (one where they are odd) for what is only
+// copied.  A thread keeps one
 // unit of the head and walks over the heads of the CTA's tokens.
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     extern __shared__ float2 cs[];                       // [per_cta][rot_dim / 2]
     __shared__ int64_t base_k[kRopeMaxTok], base_v[kRopeMaxTok];   // the tokens' slots
@@ -117,14 +118,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
     }
     __syncthreads();
     const int turned = half / VEC;                                  // rotated units of a head
-    const int units = turned + (a.head_dim - 2 * half) / VEC;
+    const int copied = (a.head_dim - 2 * half) / VEC;
+    const bool by_two = copied % 2 == 0;
+    const int units = turned + (by_two ? copied / 2 : copied);
     const int step = kRopeThreads / units;                          // heads a pass of the CTA covers
     const int unit = tid % units;
     int h = tid / units;
     if (h >= step) return;
     const bool is_turned = unit < turned;
-    const int e0 = is_turned ? (INTER ? 2 * unit * VEC : unit * VEC) : 2 * half + (unit - turned) * VEC;
-    const int e1 = INTER ? e0 + VEC : e0 + half;
+    const bool two = is_turned || by_two;
+    const int e0 = is_turned ? (INTER ? 2 * unit * VEC : unit * VEC) : 2 * half + (unit - turned) * VEC * (by_two ? 2 : 1);
+    const int e1 = INTER || !is_turned ? e0 + VEC : e0 + half;
     const int nq = a.q.data ? a.q.heads : 0, nk = a.k.data ? a.k.heads : 0;
     const int heads = nq + 2 * nk;
     int t = 0;
@@ -154,7 +158,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
         using R = typename Raw<(int)sizeof(T) * VEC>::type;
         Part<T, VEC> x0, x1;
         x0.raw = *reinterpret_cast<const R*>(src + e0);
-        if (is_turned) x1.raw = *reinterpret_cast<const R*>(src + e1);
+        if (two) x1.raw = *reinterpret_cast<const R*>(src + e1);
         if (turn) {
             const float2* c = cs + t * half + unit * VEC;
             if (INTER && VEC > 1) {
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a)
             }
         }
         *reinterpret_cast<R*>(dst + e0) = x0.raw;
-        if (is_turned) *reinterpret_cast<R*>(dst + e1) = x1.raw;
+        if (two) *reinterpret_cast<R*>(dst + e1) = x1.raw;
     }
 }
 

@@ -8,6 +8,7 @@ fallback: if the library is missing or no GPU is present the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -231,10 +232,17 @@ class Workspace:
         off = (-self.buf.data_ptr()) % 256
         return self.buf[off:off + nbytes]
 
+    def address(self, nbytes: int) -> int:
+        """Where get(nbytes) starts, without the tensor; valid while this workspace is not grown."""
+        buf = self.buf
+        if buf is None or buf.numel() < nbytes + 256:
+            buf = self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
+        return (buf.data_ptr() + 255) & ~255
+
 
 def _ws(ws: Optional[Workspace], device, nbytes) -> torch.Tensor:
     if ws is None:
-        ws = Workspace(device)
+        ws = Workspace(q.device)
     return ws.get(nbytes)
 
 
@@ -555,71 +563,91 @@ def verify_chain_q(target: torch.Tensor, draft: Optional[torch.Tensor], draft_to
 # The target model's attention over the windows: rotary positions, append to
 # a paged cache, attention over it
 # ---------------------------------------------------------------------------
+# These calls run once a layer on a few tokens, where the host's work is what counts: one pass over each tensor's
+# metadata, no intermediate tensors, the stream's handle without its Python object.
 _ATTN_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _attn_dtype(t: torch.Tensor) -> int:
-    code = _ATTN_DTYPES.get(t.dtype)
+def _stream_handle(device: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _attn_dtype(dtype: torch.dtype) -> int:
+    code = _ATTN_DTYPES.get(dtype)
     if code is None:
-        raise SVError(f"tensors must be bf16, fp16 or fp32, got {t.dtype}")
+        raise SVError(f"tensors must be bf16, fp16 or fp32, got {dtype}")
     return code
 
 
-def _heads(t: torch.Tensor, like: Optional[torch.Tensor] = None) -> Heads:
+def _not_on_gpu():
+    return SVError("tensors must live on the GPU (the library has no CPU path)")
+
+
+def _heads(t: torch.Tensor, dtype: torch.dtype, device: int, head_dim: int) -> Heads:
     """A [tokens, heads, head_dim] tensor whose last axis is contiguous."""
-    if not t.is_cuda:
-        raise SVError("tensors must live on the GPU (the library has no CPU path)")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3:
-        raise SVError(f"expected [tokens, heads, head_dim], got {tuple(shape)}")
-    if stride[2] != 1 and shape[2] != 1:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != head_dim or t.dtype is not dtype or t.get_device() != device:
+        raise SVError(f"expected {dtype} [tokens, heads, {head_dim}] on cuda:{device}, got {t.dtype} {tuple(shape)} on {t.device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and head_dim != 1:
         raise SVError("the elements of a head must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or shape[2] != like.shape[2]):
-        raise SVError(f"expected {like.dtype} heads of {like.shape[2]} on {like.device}, "
-                      f"got {t.dtype} heads of {shape[2]} on {t.device}")
-    return Heads(t.data_ptr(), stride[0], stride[1], shape[1])
+    return Heads(t.data_ptr(), s0, s1, shape[1])
 
 
-def _paged(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, n_req: int,
-           like: torch.Tensor) -> PagedKV:
+def _tokens_heads(t: torch.Tensor):
+    """(tokens, heads, head_dim, dtype, device) of a call's leading tensor."""
+    device = t.get_device()
+    if device < 0:
+        raise _not_on_gpu()
+    if t.dim() != 3:
+        raise SVError(f"expected [tokens, heads, head_dim], got {tuple(t.shape)}")
+    tokens, heads, d = t.shape
+    return tokens, heads, d, t.dtype, device
+
+
+def _paged(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, n_req: int, dtype: torch.dtype,
+           device: int, head_dim: int) -> PagedKV:
     """A cache [n_pages, page_size, heads, head_dim] (any strides but the last) and its table [n_req, columns]."""
-    if not (k_pages.is_cuda and v_pages.is_cuda and page_table.is_cuda):
-        raise SVError("tensors must live on the GPU (the library has no CPU path)")
-    ks, vs = k_pages.stride(), v_pages.stride()
     shape = k_pages.shape
     if len(shape) != 4 or v_pages.shape != shape:
         raise SVError("k_pages and v_pages must both be [n_pages, page_size, heads, head_dim]")
-    if (ks[3] != 1 or vs[3] != 1) and shape[3] != 1:
+    if (k_pages.dtype is not dtype or v_pages.dtype is not dtype or shape[3] != head_dim or k_pages.get_device() != device or
+            v_pages.get_device() != device):
+        raise SVError(f"expected {dtype} pages with heads of {head_dim} on cuda:{device}, got {k_pages.dtype}, {v_pages.dtype} "
+                      f"and {shape[3]} on {k_pages.device}, {v_pages.device}")
+    kp, kt, kh, ke = k_pages.stride()
+    vp, vt, vh, ve = v_pages.stride()
+    if (ke != 1 or ve != 1) and head_dim != 1:
         raise SVError("the elements of a head must be contiguous")
-    if k_pages.dtype != like.dtype or v_pages.dtype != like.dtype or shape[3] != like.shape[2]:
-        raise SVError(f"expected {like.dtype} pages with heads of {like.shape[2]}, "
-                      f"got {k_pages.dtype}, {v_pages.dtype} and {shape[3]}")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_req:
-        raise SVError("page_table must be int32 [requests, pages]")
-    ts = page_table.stride()
-    cols = page_table.shape[1]
-    if ts[1] != 1 and cols > 1:
-        raise SVError("the rows of page_table must be contiguous")
-    return PagedKV(Heads(k_pages.data_ptr(), ks[1], ks[2], shape[2]), Heads(v_pages.data_ptr(), vs[1], vs[2], shape[2]),
-                   ks[0], vs[0], page_table.data_ptr(), ts[0] if n_req > 1 else max(ts[0], cols), cols, shape[0],
-                   shape[1])
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.get_device() != device:
+        raise SVError(f"page_table must be int32 [requests, pages] on cuda:{device}")
+    rows, cols = page_table.shape
+    ld, one = page_table.stride()
+    if rows != n_req or (one != 1 and cols > 1):
+        raise SVError("page_table must have a row for each request, and its rows must be contiguous")
+    heads = shape[2]
+    return PagedKV(Heads(k_pages.data_ptr(), kt, kh, heads), Heads(v_pages.data_ptr(), vt, vh, heads), kp, vp,
+                   page_table.data_ptr(), ld if n_req > 1 else max(ld, cols), cols, shape[0], shape[1])
 
 
-def _vector(t: torch.Tensor, n: int, what: str) -> int:
+def _vector(t: torch.Tensor, n: int, device: int, what: str) -> int:
     """Address of a contiguous int32 [n] tensor on the GPU."""
-    if not t.is_cuda:
-        raise SVError("tensors must live on the GPU (the library has no CPU path)")
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+    if t.get_device() != device:
+        raise _not_on_gpu() if not t.is_cuda else SVError(f"{what} must live on cuda:{device}")
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
         raise SVError(f"{what} must be a contiguous int32 [{n}]")
     return t.data_ptr()
 
 
-def _rope(freq: Optional[torch.Tensor], flags: int, mscale: float) -> RotaryArgs:
+def _rope(freq: Optional[torch.Tensor], flags: int, mscale: float, device: int) -> RotaryArgs:
     if freq is None:
         return RotaryArgs(None, 0, flags, mscale)
-    if not freq.is_cuda:
-        raise SVError("tensors must live on the GPU (the library has no CPU path)")
-    if freq.dtype != torch.float32 or freq.dim() != 2 or freq.shape[1] != 2 or not freq.is_contiguous():
+    if freq.get_device() != device:
+        raise _not_on_gpu() if not freq.is_cuda else SVError(f"freq must live on cuda:{device}")
+    if freq.dtype is not torch.float32 or freq.dim() != 2 or freq.shape[1] != 2 or not freq.is_contiguous():
         raise SVError("freq must be a contiguous fp32 [rot_dim / 2, 2] (see rotary_frequencies)")
     return RotaryArgs(freq.data_ptr(), 2 * freq.shape[0], flags, mscale)
 
@@ -675,15 +703,15 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, interle
            inverse: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """sv_rotary: x [tokens, heads, head_dim] rotated by positions int32 [tokens] (out may be x).  With
     inverse=True it maps the gradient of the output to the gradient of the input."""
-    hx = _heads(x)
-    tokens, _, d = x.shape
+    tokens, _, d, dtype, device = _tokens_heads(x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x)
     elif out.shape != x.shape:
         raise SVError(f"out must be {tuple(x.shape)}")
     flags = (ROTARY_INTERLEAVED if interleaved else 0) | (ROTARY_INVERSE if inverse else 0)
-    _check(load().sv_rotary(hx, _heads(out, x), _attn_dtype(x), tokens, d, _vector(positions, tokens, "positions"),
-                            _rope(freq, flags, mscale), _stream(x.device)))
+    _check((_lib or load()).sv_rotary(_heads(x, dtype, device, d), _heads(out, dtype, device, d), _attn_dtype(dtype), tokens,
+                                      d, _vector(positions, tokens, device, "positions"),
+                                      _rope(freq, flags, mscale, device), _stream_handle(device)))
     return out
 
 
@@ -695,25 +723,30 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
     """sv_kv_append: the windows' k (rotated, if freq is given) and v [tokens, heads, head_dim] into the cache
     [n_pages, page_size, heads, head_dim] at the end of each request's kv_len tokens.  With q its rotation is
     returned (into q_out if given, which may be q)."""
-    hk, hv = _heads(k), _heads(v, k)
-    tokens, _, d = k.shape
+    tokens, _, d, dtype, device = _tokens_heads(k)
     n = kv_len.numel()
     if v.shape != k.shape:
         raise SVError("k and v must have one shape")
-    hq, ho = Heads(None, 0, 0, 0), Heads(None, 0, 0, 0)
-    if q is not None:
+    if q is None:
+        hq = ho = _NO_HEADS
+    else:
         if q.shape[0] != tokens:
             raise SVError("q and k must have the same tokens")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q)
         elif q_out.shape != q.shape:
             raise SVError(f"q_out must be {tuple(q.shape)}")
-        hq, ho = _heads(q, k), _heads(q_out, k)
-    _check(load().sv_kv_append(hk, hv, _paged(k_pages, v_pages, page_table, n, k), _attn_dtype(k), tokens, d, n,
-                               _vector(qo_indptr, n + 1, "qo_indptr"), _vector(kv_len, n, "kv_len"),
-                               _rope(freq, ROTARY_INTERLEAVED if interleaved else 0, mscale), hq, ho,
-                               None if status is None else _vector(status, n, "status"), _stream(k.device)))
+        hq, ho = _heads(q, dtype, device, d), _heads(q_out, dtype, device, d)
+    _check((_lib or load()).sv_kv_append(
+        _heads(k, dtype, device, d), _heads(v, dtype, device, d),
+        _paged(k_pages, v_pages, page_table, n, dtype, device, d), _attn_dtype(dtype), tokens, d, n,
+        _vector(qo_indptr, n + 1, device, "qo_indptr"), _vector(kv_len, n, device, "kv_len"),
+        _rope(freq, ROTARY_INTERLEAVED if interleaved else 0, mscale, device), hq, ho,
+        None if status is None else _vector(status, n, device, "status"), _stream_handle(device)))
     return q_out
+
+
+_NO_HEADS = Heads(None, 0, 0, 0)
 
 
 @dataclass
@@ -722,6 +755,7 @@ class AttentionOut:
     lse: Optional[torch.Tensor]  # [tokens, heads] fp32
 
 
+@functools.lru_cache(maxsize=256)
 def attention_workspace_size(max_window: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     size = load().sv_attention_workspace_size(max_window, q_heads, kv_heads, head_dim)
     if size == 0:
@@ -736,20 +770,21 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     """sv_paged_attention: q [tokens, heads, head_dim], packed by qo_indptr, over the paged cache; no window is longer
     than max_window.  scale defaults to head_dim ** -0.5; window > 0 limits every row to its last `window` keys;
     full=True drops the causal limit."""
-    hq = _heads(q)
-    tokens, heads, d = q.shape
+    tokens, heads, d, dtype, device = _tokens_heads(q)
     n = kv_len.numel()
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     elif out.shape != q.shape:
         raise SVError(f"out must be {tuple(q.shape)}")
     norm = torch.empty((tokens, heads), dtype=torch.float32, device=q.device) if lse else None
-    cache = _paged(k_pages, v_pages, page_table, n, q)
-    w = _ws(ws, q.device, attention_workspace_size(max_window, heads, cache.k.heads, d))
-    _check(load().sv_paged_attention(hq, cache, _attn_dtype(q), tokens, d, n, _vector(qo_indptr, n + 1, "qo_indptr"),
-                                     _vector(kv_len, n, "kv_len"), max_window, d ** -0.5 if scale is None else scale,
-                                     window, ATTN_FULL if full else 0, _heads(out, q),
-                                     None if norm is None else norm.data_ptr(),
-                                     None if status is None else _vector(status, n, "status"), w.data_ptr(),
-                                     w.numel(), _stream(q.device)))
+    cache = _paged(k_pages, v_pages, page_table, n, dtype, device, d)
+    nbytes = attention_workspace_size(max_window, heads, cache.k.heads, d)
+    if ws is None:
+        ws = Workspace(q.device)
+    _check((_lib or load()).sv_paged_attention(
+        _heads(q, dtype, device, d), cache, _attn_dtype(dtype), tokens, d, n,
+        _vector(qo_indptr, n + 1, device, "qo_indptr"), _vector(kv_len, n, device, "kv_len"), max_window,
+        d ** -0.5 if scale is None else scale, window, ATTN_FULL if full else 0, _heads(out, dtype, device, d),
+        None if norm is None else norm.data_ptr(), None if status is None else _vector(status, n, device, "status"),
+        ws.address(nbytes), nbytes, _stream_handle(device)))
     return AttentionOut(out, norm)
