@@ -175,14 +175,14 @@ __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int 
         "l"(map), "r"(e), "r"(head), "r"(token), "r"(smem_u32(bar))
         : "memory");
 }
-// One page's (or part of a page's) rows of 64 elements, 128-byte swizzled.
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int e, int head, int token, int page,
+// A page's rows of one head, or 128 of them, in one box (see make_map).
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int e, int group, int page,
                                          unsigned long long* bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %4, %5}], "
         "[%6];" ::"r"(dst),
-        "l"(map), "r"(e), "r"(head), "r"(token), "r"(page), "r"(smem_u32(bar))
+        "l"(map), "r"(e), "r"(0), "r"(group), "r"(page), "r"(smem_u32(bar))
         : "memory");
 }
 __device__ __forceinline__ float exp2_approx(float x)
@@ -191,12 +191,12 @@ __device__ __forceinline__ float exp2_approx(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Shared-memory descriptor of 128-byte swizzled rows of 64 16-bit elements:
-// groups of 8 rows are 1,024 bytes apart; `lead` is the distance from one 64
-// element block of the row axis to the next where that axis is contiguous.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead)
+// Shared-memory descriptor of 128-byte swizzled rows of 64 16-bit elements in
+// groups of 8 rows, `group` bytes apart; `next64` is the distance from one block
+// of 64 to the next where the operand's row axis is the contiguous one.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t group, uint32_t next64 = 16)
 {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)((lead >> 4) & 0x3fffu) << 16 | (uint64_t)(1024 >> 4) << 32 |
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(next64 >> 4) << 16 | (uint64_t)(group >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // fp32 accumulators, both operands of one 16-bit type.
@@ -396,8 +396,15 @@ template <int D>
 struct TcSmem {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kTileBytes = kTile * D * 2;
+    // Q: blocks of 64 elements one after the other, 128 rows each.  Keys and values: groups of 8 keys one after the
+    // other, each with its blocks of 64 elements (1 KB a block), so that one box of a map fills a page's place.
+    static constexpr int kGroup = 1024 * (D / 64);
     alignas(1024) unsigned char q[2][kTileBytes];
     alignas(1024) unsigned char kv[kStages][kTileBytes];
+    static __device__ __forceinline__ int kv_at(int key, int vec)   // of 8 elements
+    {
+        return (key >> 3) * kGroup + (vec >> 3) * 1024 + (key & 7) * 128 + ((vec ^ key) & 7) * 16;
+    }
     unsigned long long full[kStages], empty[kStages];
     unsigned long long q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
     unsigned long long piece_full[kPieces], piece_empty[kPieces];
@@ -680,10 +687,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (mine) {
                             const int token = page_size > kTile ? key_of_page - t.by_page(key_of_page) * page_size : 0;
                             const CUtensorMap* map = half ? &map_k : &map_v;
-#pragma unroll
-                            for (int x = 0; x < D; x += 64)
-                                tma_rows(smem_u32(sm.kv[stage]) + (uint32_t)(x / 64 * kTile + lane * box_rows) * 128u, map, x,
-                                         head, token, page, &sm.full[stage]);
+                            tma_page(smem_u32(sm.kv[stage]) + (uint32_t)(lane * box_rows / 8 * S::kGroup), map,
+                                     head * (int)(half ? a.cache.k.stride_head : a.cache.v.stride_head), token / 8, page,
+                                     &sm.full[stage]);
                         }
                     }
                 }
@@ -694,8 +700,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int s = warp >> 1;
             constexpr uint32_t kQk = instr_desc(Kind<T>::kBf16, false, kTile);
             constexpr uint32_t kPv = instr_desc(Kind<T>::kBf16, true, D);
-            const uint64_t q_desc = smem_desc(smem_u32(sm.q[0]), 16), k_desc = smem_desc(smem_u32(sm.kv[0]), 16),
-                           v_desc = smem_desc(smem_u32(sm.kv[0]), kTile * 128);
+            const uint64_t q_desc = smem_desc(smem_u32(sm.q[0]), 1024), k_desc = smem_desc(smem_u32(sm.kv[0]), S::kGroup),
+                           v_desc = smem_desc(smem_u32(sm.kv[0]), S::kGroup, 1024);
             constexpr uint32_t kBytes = S::kTileBytes >> 4;    // a tile in a descriptor's units
             const uint32_t o_at = tmem + 256 + s * 128, s_at = tmem + s * kTile;
             uint32_t base = 0, q_uses[2] = {0, 0}, done = 0, o_uses = 0, q_next = 0, turns = 0;
@@ -739,7 +745,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (one_lane() && !by_hand) {
 #pragma unroll
                             for (int k = 0; k < kTile / 32; ++k)
-                                tc_mma_ts(o_at, s_at + k * 8, vd + k * (2048 >> 4), kPv, st > 1 || k > 0);
+                                tc_mma_ts(o_at, s_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, st > 1 || k > 0);
                         }
                         wait_or_abort(&sm.p_full[s], done & 1u, &sm.aborted);
                         ++done;
@@ -748,7 +754,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             if (!by_hand) {
 #pragma unroll
                                 for (int k = kTile / 32; k < kTile / 16; ++k)
-                                    tc_mma_ts(o_at, s_at + k * 8, vd + k * (2048 >> 4), kPv, true);
+                                    tc_mma_ts(o_at, s_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, true);
                             }
                             tc_commit(&sm.pv_done[s]);
                             tc_commit(&sm.empty[v_stage]);
@@ -762,8 +768,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (one_lane()) {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = ((uint32_t)(k / 4) * (kTile * 128) + (uint32_t)(k % 4) * 32) >> 4;
-                                tc_mma_ss(s_at, qd + off, kd + off, kQk, k > 0);
+                                const uint32_t in = (uint32_t)(k % 4) * 32, block = (uint32_t)(k / 4);
+                                tc_mma_ss(s_at, qd + ((block * kTile * 128 + in) >> 4), kd + ((block * 1024 + in) >> 4), kQk, k > 0);
                             }
                             tc_commit(&sm.s_full[s]);
                             tc_commit(&sm.empty[k_stage]);
@@ -866,7 +872,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (key < p.key_lo || key >= p.key_hi) {
 #pragma unroll 2
                             for (int c = 0; c < D / 8; ++c)        // in the swizzle's order: no two lanes in one bank
-                                *reinterpret_cast<uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 + ((c ^ row) & 7) * 16) =
+                                *reinterpret_cast<uint4*>(vt + S::kv_at(row, c)) =
                                     make_uint4(0, 0, 0, 0);
                         }
                         fence_async_smem();
@@ -876,8 +882,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             if (key >= p.key_lo && key < p.key_hi && (key < p.all_lo || key >= p.all_hi)) {
 #pragma unroll 2
                                 for (int c = 0; c < D / 8; ++c) {
-                                    const uint4 y = *reinterpret_cast<const uint4*>(vt + (c / 8) * (kTile * 128) + row * 128 +
-                                                                                    ((c ^ row) & 7) * 16);
+                                    const uint4 y = *reinterpret_cast<const uint4*>(vt + S::kv_at(row, c));
                                     top = __vmaxu2(__vmaxu2(top, y.x & 0x7fff7fffu), y.y & 0x7fff7fffu);
                                     top = __vmaxu2(__vmaxu2(top, y.z & 0x7fff7fffu), y.w & 0x7fff7fffu);
                                 }
@@ -1066,8 +1071,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                                         for (int i = 0; i < 32; i += 8) {
                                             const int v = (c + i) / 8;
-                                            const uint4 x = *reinterpret_cast<const uint4*>(
-                                                vt + (v / 8) * (kTile * 128) + kk * 128 + ((v ^ kk) & 7) * 16);
+                                            const uint4 x = *reinterpret_cast<const uint4*>(vt + S::kv_at(kk, v));
                                             const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                                             for (int y = 0; y < 4; ++y) {
@@ -1407,17 +1411,21 @@ EncodeFn encode_fn()
     return fn;
 }
 
+// Keys or values for one box a page: x within a row of the cache (a head's
+// elements are at its offset, whatever lies between the heads), row of a group
+// of 8, block of 64 elements, group, page.  A box is a head's rows of a page (or
+// 128 of them), and lands group by group.
 bool make_map(CUtensorMap* m, const sv_heads_t& h, int64_t stride_page, const sv_paged_kv_t& c, int head_dim, bool bf16)
 {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)h.heads, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages};
-    const cuuint64_t row = (cuuint64_t)head_dim * 2;     // stride of an axis of one
-    const cuuint64_t strides[3] = {h.heads > 1 ? (cuuint64_t)h.stride_head * 2 : row, (cuuint64_t)h.stride_token * 2,
-                                   c.n_pages > 1 ? (cuuint64_t)stride_page * 2 : row};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile), 1};
-    const cuuint32_t step[4] = {1, 1, 1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, h.data, dims, strides, box,
+    const cuuint64_t token = (cuuint64_t)h.stride_token * 2, row = (cuuint64_t)head_dim * 2;
+    const cuuint64_t dims[5] = {(cuuint64_t)(h.heads - 1) * (cuuint64_t)(h.heads > 1 ? h.stride_head : 0) + (cuuint64_t)head_dim,
+                                8, (cuuint64_t)head_dim / 64, (cuuint64_t)c.page_size / 8, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[4] = {token, 128, 8 * token, c.n_pages > 1 ? (cuuint64_t)stride_page * 2 : row};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)head_dim / 64, (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile) / 8, 1};
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, h.data, dims, strides, box,
               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1489,6 +1497,7 @@ bool attn_tc_takes(const AttnArgs& a, sv_dtype_t dt)
            ((p >= 8 && p <= kTile && kTile % p == 0) || p % kTile == 0) && c.n_pages > 0 &&
            (long long)c.max_pages * p <= 1ll << 30 && heads_aligned(a.q, 8, 2) && heads_aligned(a.out, 8, 2) &&
            heads_aligned(c.k, 8, 2) && heads_aligned(c.v, 8, 2) && c.stride_page_k % 8 == 0 && c.stride_page_v % 8 == 0 &&
+           (long long)c.k.heads * c.k.stride_head < 1ll << 31 && (long long)c.k.heads * c.v.stride_head < 1ll << 31 &&
            c.k.stride_token > 0 && c.v.stride_token > 0 && c.k.stride_head > 0 && c.v.stride_head > 0 &&
            c.stride_page_k > 0 && c.stride_page_v > 0;
 }
