@@ -399,6 +399,8 @@ struct TcSmem {
     // Q: blocks of 64 elements one after the other, 128 rows each.  Keys and values: groups of 8 keys one after the
     // other, each with its blocks of 64 elements (1 KB a block), so that one box of a map fills a page's place.
     static constexpr int kGroup = 1024 * (D / 64);
+    static constexpr bool kApart = D == 64;   // TMEM has room for weights beside the scores, after the slot's output
+    static constexpr int kWeightsAt = kApart ? 256 + 64 : 0;   // their column, for slot 0
     alignas(1024) unsigned char q[2][kTileBytes];
     alignas(1024) unsigned char kv[kStages][kTileBytes];
     static __device__ __forceinline__ int kv_at(int key, int vec)   // of 8 elements
@@ -406,7 +408,7 @@ struct TcSmem {
         return (key >> 3) * kGroup + (vec >> 3) * 1024 + (key & 7) * 128 + ((vec ^ key) & 7) * 16;
     }
     unsigned long long full[kStages], empty[kStages];
-    unsigned long long q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
+    unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_half[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
     unsigned long long piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];          // warp 0 walks ahead of the other roles
     float2 ml[2][kTile];            // the slots' statistics of a finished piece
@@ -432,6 +434,19 @@ __device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t 
         if (*(volatile int*)aborted) return;
     }
     *(volatile int*)aborted = 1;
+}
+
+__device__ __forceinline__ uint32_t mbar_test(unsigned long long* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok;
 }
 
 // Where the ring holds a piece's tiles: the keys of the first `ahead` tiles,
@@ -508,6 +523,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&sm.q_full[lane], 1);
             mbar_init(&sm.q_empty[lane], 2);
             mbar_init(&sm.s_full[lane], 1);
+            mbar_init(&sm.s_free[lane], 4);
             mbar_init(&sm.p_half[lane], 4);        // 4: a warp at a time
             mbar_init(&sm.p_full[lane], 4);
             mbar_init(&sm.pv_done[lane], 1);
@@ -626,6 +642,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         reached(&sm.issued, e + 1);
         wait_or_abort(&sm.full[e % kStages], e / kStages & 1u, &sm.aborted);
     };
+    auto landed_by_now = [&](uint32_t e) {
+        const uint32_t ok = mbar_test(&sm.full[e % kStages], e / kStages & 1u);
+        return __all_sync(0xffffffffu, (int)(*(volatile uint32_t*)&sm.issued - e) > 0 && ok) != 0;
+    };
     auto warp_arrive = [&](unsigned long long* bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -639,61 +659,65 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // ---- loads: lane i has page i of a tile --------------------------------------
             const int page_size = a.cache.page_size;
             const int box_rows = min(page_size, kTile), per_tile = kTile / box_rows;   // pages of a tile, up to 16
-            uint32_t base = 0;                        // ring entries of the pieces before
+            const int head_k = (int)a.cache.k.stride_head, head_v = (int)a.cache.v.stride_head;   // of heads, in elements
+            const uint32_t lane_at = (uint32_t)(lane * box_rows / 8 * S::kGroup);                // of the lane's page
+            const uint32_t box_bytes = (uint32_t)(box_rows * D * 2);
+            uint32_t entry = 0, stage = 0, free_phase = 1;       // the ring; its first round finds it empty
 #pragma unroll 1
             for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
                 const Piece& p = sm.pieces[pk % kPieces];
-                const int nt = p.nt, key0 = p.kt0 * kTile, key_lo = p.key_lo, key_hi = p.key_hi, head = p.head;
+                const int nt = p.nt, key_lane = p.kt0 * kTile + lane * box_rows, key_lo = p.key_lo, key_hi = p.key_hi;
+                const int x_k = p.head * head_k, x_v = p.head * head_v;
                 const int32_t* table = a.cache.page_table + (int64_t)p.r * a.cache.ld_table;
                 const int ahead = p.pair() ? 1 : 2;
                 // Page numbers, a lane a page: 32 of them from tile `first` on, the 32 after those, and the 32 after
                 // those on their way.  A lane's page of a tile is another lane's number.
                 const int span = 32 / per_tile;               // tiles that 32 pages hold
                 auto fetch = [&](int tile) -> int {
-                    const int key = key0 + tile * kTile + lane * box_rows;
+                    const int key = key_lane + tile * kTile;
                     if (tile + lane / per_tile >= nt || key >= key_hi || key + box_rows <= key_lo) return -1;
                     return table[t.by_page(key)];             // pages that nobody sees are not looked at
                 };
                 int first = 0, now = fetch(0), next = fetch(span), later = fetch(2 * span);
+                // A tile's boxes.  `known`: its stage was seen to be free.  The barrier is told of the bytes by one lane
+                // while the others issue: it waits for that lane's arrival whichever comes first.
+                auto load = [&](const CUtensorMap* map, int j, int x, bool known) {
+                    const int key = key_lane + j * kTile;
+                    const bool mine = lane < per_tile && key < key_hi && key + box_rows > key_lo;
+                    int page = __shfl_sync(0xffffffffu, j - first < span ? now : next, ((j - first) * per_tile + lane) & 31);
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
+                    if (mine && (unsigned)page >= (unsigned)a.cache.n_pages) {
+                        if (a.status) atomicOr(&a.status[p.r], kBadLayout);
+                        page = a.cache.n_pages;                // past the end: reads as zeros
+                    }
+                    const int group = page_size > kTile ? (key - t.by_page(key) * page_size) >> 3 : 0;
+                    if (!known) wait_or_abort(&sm.empty[stage], free_phase, &sm.aborted);
+                    ++entry;
+                    if (mine) tma_page(smem_u32(sm.kv[stage]) + lane_at, map, x, group, page, &sm.full[stage]);
+                    if (lane == 0) {
+                        mbar_expect_tx(&sm.full[stage], bytes);
+                        *(volatile uint32_t*)&sm.issued = entry;
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        free_phase ^= 1u;
+                    }
+                };
 #pragma unroll 1
-                for (int u = -ahead; u < nt; ++u) {
+                for (int u = -ahead; u < nt; ++u) {            // values of tile u, keys of tile u + ahead
+                    const bool has_v = u >= 0;
+                    const uint32_t other = stage + 1 == kStages ? 0 : stage + 1;
+                    const uint32_t free0 = mbar_test(&sm.empty[stage], free_phase),
+                                   free1 = mbar_test(&sm.empty[other], other ? free_phase : free_phase ^ 1u);
                     if (u == first + span) {
                         first += span;
                         now = next;
                         next = later;
                         later = fetch(first + 2 * span);
                     }
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {     // values of tile u, keys of tile u + ahead
-                        const int j = half ? u + ahead : u;
-                        if (j < 0 || j >= nt) continue;
-                        const uint32_t e = base + (half ? entry_k(j, ahead) : entry_v(j, nt, ahead)), stage = e % kStages;
-                        const int key_of_page = key0 + j * kTile + lane * box_rows;
-                        const bool mine = lane < per_tile && key_of_page < key_hi && key_of_page + box_rows > key_lo;
-                        const int at = (j - first) * per_tile + lane;
-                        const int page0 = __shfl_sync(0xffffffffu, now, at & 31), page1 = __shfl_sync(0xffffffffu, next, at & 31);
-                        int page = at < 32 ? page0 : page1;
-                        if (mine && (page < 0 || page >= a.cache.n_pages)) {
-                            if (a.status) atomicOr(&a.status[p.r], kBadLayout);
-                            page = a.cache.n_pages;            // past the end: reads as zeros
-                        }
-                        const uint32_t have = __ballot_sync(0xffffffffu, mine);
-                        wait_or_abort(&sm.empty[stage], ~(e / kStages) & 1u, &sm.aborted);   // the first round finds it empty
-                        if (lane == 0) {
-                            mbar_expect_tx(&sm.full[stage], (uint32_t)(__popc(have) * box_rows * D * 2));
-                            *(volatile uint32_t*)&sm.issued = e + 1;
-                        }
-                        __syncwarp();
-                        if (mine) {
-                            const int token = page_size > kTile ? key_of_page - t.by_page(key_of_page) * page_size : 0;
-                            const CUtensorMap* map = half ? &map_k : &map_v;
-                            tma_page(smem_u32(sm.kv[stage]) + (uint32_t)(lane * box_rows / 8 * S::kGroup), map,
-                                     head * (int)(half ? a.cache.k.stride_head : a.cache.v.stride_head), token / 8, page,
-                                     &sm.full[stage]);
-                        }
-                    }
+                    if (has_v) load(&map_v, u, x_v, free0);
+                    if (u + ahead < nt) load(&map_k, u + ahead, x_k, has_v ? free1 : free0);
                 }
-                base += 2u * (uint32_t)nt;
             }
         } else if (warp != 0) {
             // ---- matrix products: warp 1 slot 0's, warp 3 slot 1's, one lane issues them -----
@@ -703,8 +727,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint64_t q_desc = smem_desc(smem_u32(sm.q[0]), 1024), k_desc = smem_desc(smem_u32(sm.kv[0]), S::kGroup),
                            v_desc = smem_desc(smem_u32(sm.kv[0]), S::kGroup, 1024);
             constexpr uint32_t kBytes = S::kTileBytes >> 4;    // a tile in a descriptor's units
-            const uint32_t o_at = tmem + 256 + s * 128, s_at = tmem + s * kTile;
-            uint32_t base = 0, q_uses[2] = {0, 0}, done = 0, o_uses = 0, q_next = 0, turns = 0;
+            const uint32_t o_at = tmem + 256 + s * 128, s_at = tmem + s * kTile, p_at = s_at + S::kWeightsAt;
+            uint32_t scores = 0, base = 0, q_uses[2] = {0, 0}, done = 0, o_uses = 0, q_next = 0, turns = 0;
 #pragma unroll 1
             for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
                 const Piece& p = sm.pieces[pk % kPieces];
@@ -733,38 +757,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int st = 0; st <= steps; ++st) {
                     const uint64_t vd = v_desc + v_stage * kBytes, kd = k_desc + k_stage * kBytes;
-                    // Where the slots share the tiles, arithmetic bounds the piece: what can be waited for is, before
-                    // the weights, so that nothing stands between the products.  Elsewhere the keys may be far off.
-                    if (st < steps && (pair || st == 0)) landed(e);
-                    if (st > 0) {                                // P V of step st - 1
-                        if (st == 1) wait_or_abort(&sm.o_free[s], ~o_uses++ & 1u, &sm.aborted);   // at first it is
-                        wait_or_abort(&sm.p_half[s], done & 1u, &sm.aborted);
-                        const bool by_hand = edge && *(volatile int*)&sm.by_hand[s];
-                        if (pair) reached(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
+                    auto score = [&]() {
+                        if (S::kApart) wait_or_abort(&sm.s_free[s], ~scores++ & 1u, &sm.aborted);   // at first they are
                         tc_fence_after();
-                        if (one_lane() && !by_hand) {
-#pragma unroll
-                            for (int k = 0; k < kTile / 32; ++k)
-                                tc_mma_ts(o_at, s_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, st > 1 || k > 0);
-                        }
-                        wait_or_abort(&sm.p_full[s], done & 1u, &sm.aborted);
-                        ++done;
-                        tc_fence_after();
-                        if (one_lane()) {
-                            if (!by_hand) {
-#pragma unroll
-                                for (int k = kTile / 32; k < kTile / 16; ++k)
-                                    tc_mma_ts(o_at, s_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, true);
-                            }
-                            tc_commit(&sm.pv_done[s]);
-                            tc_commit(&sm.empty[v_stage]);
-                            if (!pair) tc_commit(&sm.empty[v_stage]);
-                            if (by_hand) *(volatile int*)&sm.by_hand[s] = 0;
-                        }
-                        __syncwarp();
-                        if (!pair && st < steps) landed(e);
-                    }
-                    if (st < steps) {                            // scores of step st, in the place of the last weights
                         if (one_lane()) {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
@@ -780,8 +775,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                         __syncwarp();
+                    };
+                    // Where the slots share the tiles, arithmetic bounds the piece: what can be waited for is, before
+                    // the weights, so that nothing stands between the products.  Elsewhere the keys may be far off.
+                    bool keys = st < steps && (pair || st == 0 || (S::kApart && landed_by_now(e)));
+                    if (keys) landed(e);
+                    const bool scored = keys && S::kApart;       // weights apart: the next scores need not wait for them
+                    if (scored) score();
+                    if (st > 0) {                                // P V of step st - 1
+                        if (st == 1) wait_or_abort(&sm.o_free[s], ~o_uses++ & 1u, &sm.aborted);   // at first it is
+                        wait_or_abort(&sm.p_half[s], done & 1u, &sm.aborted);
+                        const bool by_hand = edge && *(volatile int*)&sm.by_hand[s];
+                        if (pair && !S::kApart) reached(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
+                        tc_fence_after();
+                        if (one_lane() && !by_hand) {
+#pragma unroll
+                            for (int k = 0; k < kTile / 32; ++k)
+                                tc_mma_ts(o_at, p_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, st > 1 || k > 0);
+                        }
+                        wait_or_abort(&sm.p_full[s], done & 1u, &sm.aborted);
+                        ++done;
+                        tc_fence_after();
+                        if (one_lane()) {
+                            if (!by_hand) {
+#pragma unroll
+                                for (int k = kTile / 32; k < kTile / 16; ++k)
+                                    tc_mma_ts(o_at, p_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, true);
+                            }
+                            tc_commit(&sm.pv_done[s]);
+                            tc_commit(&sm.empty[v_stage]);
+                            if (!pair) tc_commit(&sm.empty[v_stage]);
+                            if (by_hand) *(volatile int*)&sm.by_hand[s] = 0;
+                        }
+                        __syncwarp();
                     }
-                    if (pair && st > 0 && lane == 0) *(volatile uint32_t*)&sm.turns[s] = turns;
+                    if (st < steps && !scored) {                 // scores of step st, in the place of the last weights
+                        if (!keys) landed(e);
+                        score();
+                    }
+                    if (pair && !S::kApart && st > 0 && lane == 0) *(volatile uint32_t*)&sm.turns[s] = turns;
                     if (st < steps) {                            // the values that go with these scores, the next keys
                         edge = (p.kt0 + j) * kTile < p.all_lo || (p.kt0 + j + 1) * kTile > p.all_hi;
                         const uint32_t ev = base + entry_v(j, nt, ahead);
@@ -843,7 +875,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- the slots: a thread a row ---------------------------------------------------
         const int slot = (warp - 4) >> 2, sw = warp & 3, row = sw * 32 + lane;
         const uint32_t lanes = (uint32_t)(sw * 32) << 16;
-        const uint32_t s_at = tmem + lanes + slot * kTile, o_at = tmem + lanes + 256 + slot * 128;
+        const uint32_t s_at = tmem + lanes + slot * kTile, o_at = tmem + lanes + 256 + slot * 128, p_at = s_at + S::kWeightsAt;
         uint32_t steps_done = 0, o_uses = 0, votes = 0, base = 0;
 #pragma unroll 1
         for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
@@ -949,18 +981,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             w[i + 1] = Kind<T>::pack(e2, e3);
                         }
                     };
+                    // Weights apart from the scores: the next scores may come once these are read, and the last
+                    // weights have to be used before the next are written.  (In one place the order is given.)
+                    auto scores_read = [&]() {
+                        if (S::kApart) {
+                            tc_fence_before();
+                            warp_arrive(&sm.s_free[slot]);
+                        }
+                    };
+                    auto weights_used = [&]() {
+                        if (S::kApart && steps_done > 0) {
+                            wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
+                            tc_fence_after();
+                        }
+                    };
                     if (nothing) {                                     // no row of the warp sees the tile
+                        scores_read();
+                        weights_used();
                         if (warp_valid) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) w[i] = 0u;
 #pragma unroll
-                            for (int c = 0; c < kTile / 2; c += 16) tc_st16(w, s_at + c);
+                            for (int c = 0; c < kTile / 2; c += 16) tc_st16(w, p_at + c);
                         }
                     } else if (warp_valid && whole_rows) {
                         uint32_t s[kTile];                             // fp32 scores
 #pragma unroll
                         for (int c = 0; c < kTile; c += 32) tc_ld32(s + c, s_at + c);
                         tc_loaded<kTile>(s);
+                        scores_read();
                         if (masked) {
 #pragma unroll
                             for (int c = 0; c < kTile; c += 32) {
@@ -984,18 +1033,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             l0 = l1 = 0;
                             weigh(s);
                         }
-                        tc_st16(w, s_at);
+                        weights_used();
+                        tc_st16(w, p_at);
                         weigh(s + 32);
-                        tc_st16(w, s_at + 16);
+                        tc_st16(w, p_at + 16);
                         weigh(s + 64);
                         if (!by_hand) {                                // the products of the first half may begin
                             tc_wait_st();
                             tc_fence_before();
                             warp_arrive(&sm.p_half[slot]);
                         }
-                        tc_st16(w, s_at + 32);
+                        tc_st16(w, p_at + 32);
                         weigh(s + 96);
-                        tc_st16(w, s_at + 48);
+                        tc_st16(w, p_at + 48);
                     } else if (warp_valid) {
                         // The same in less code, for items that memory bounds: twice over 64 columns at a time, the
                         // maximum first.
@@ -1006,6 +1056,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc_ld32(s, s_at + c % kTile);
                             tc_ld32(s + 32, s_at + c % kTile + 32);
                             tc_loaded<64>(s);
+                            if (c == 2 * kTile - 64) scores_read();
                             if (masked) {
                                 const int at = c % kTile;
                                 const uint32_t in0 = columns_seen(lo - at, hi - at), in1 = columns_seen(lo - at - 32, hi - at - 32);
@@ -1028,11 +1079,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 if (c == kTile - 64) grow(mx);
                             } else {
                                 weigh(s);
-                                tc_st16(w, s_at + (c - kTile) / 2);
+                                if (c == kTile) weights_used();
+                                tc_st16(w, p_at + (c - kTile) / 2);
                                 weigh(s + 32);
-                                tc_st16(w, s_at + (c - kTile) / 2 + 16);
+                                tc_st16(w, p_at + (c - kTile) / 2 + 16);
                             }
                         }
+                    }
+                    if (!warp_valid && !nothing) {                     // every step is waited for, or a later wait's phase
+                        scores_read();                                 // could be taken for an earlier one's
+                        weights_used();
                     }
                     if (warp_valid) {
                         const float2 ls = halves(add2(l0, l1));
@@ -1062,7 +1118,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 }
 #pragma unroll 1
                                 for (int kk = 0; kk < kTile; ++kk) {
-                                    uint32_t w2 = tc_ld1(s_at + kk / 2);
+                                    uint32_t w2 = tc_ld1(p_at + kk / 2);
                                     tc_wait_ld();
                                     asm volatile("" : "+r"(w2));
                                     const float2 wf = Kind<T>::unpack(w2);
@@ -1426,7 +1482,7 @@ bool make_map(CUtensorMap* m, const sv_heads_t& h, int64_t stride_page, const sv
     const cuuint32_t box[5] = {64, 8, (cuuint32_t)head_dim / 64, (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile) / 8, 1};
     const cuuint32_t step[5] = {1, 1, 1, 1, 1};
     return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, h.data, dims, strides, box,
-              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, head_dim > 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
