@@ -499,7 +499,7 @@ __device__ __forceinline__ float2 halves(unsigned long long x)
 // unrolled): the roles run different parts of it at the same time, and at
 // 195 KB, with the steps inlined wherever they occur, instruction misses took
 // most of the time of short items.
-template <typename T, int D>
+template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcArgs t, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q)
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int nt = p.nt, key_lane = p.kt0 * kTile + lane * box_rows, key_lo = p.key_lo, key_hi = p.key_hi;
                 const int x_k = p.head * head_k, x_v = p.head * head_v;
                 const int32_t* table = a.cache.page_table + (int64_t)p.r * a.cache.ld_table;
-                const int ahead = p.pair() ? 1 : 2;
+                const int ahead = PAIRS && p.pair() ? 1 : 2;
                 // Page numbers, a lane a page: 32 of them from tile `first` on, the 32 after those, and the 32 after
                 // those on their way.  A lane's page of a tile is another lane's number.
                 const int span = 32 / per_tile;               // tiles that 32 pages hold
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
             for (uint32_t pk = 0; piece_ready(pk); piece_release(pk++)) {
                 const Piece& p = sm.pieces[pk % kPieces];
-                const bool pair = p.pair();
+                const bool pair = PAIRS && p.pair();
                 const int nt = p.nt, ahead = pair ? 1 : 2, each = pair ? 1 : 2, steps = p.steps(s);
                 const uint32_t qb = pair ? (uint32_t)s : q_next;
                 if (!pair && nt > 0) q_next ^= 1u;
@@ -844,9 +844,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     Piece& p = sm.pieces[pk % kPieces];
                     walk.next(t, p);
                     p.lead = lead;                       // an odd tile is the one slot's, then the other's
-                    if (!p.pair() && (p.nt & 1)) lead ^= 1;
+                    if (!(PAIRS && p.pair()) && (p.nt & 1)) lead ^= 1;
                     const bool end = p.nt < 0 || *(volatile int*)&sm.aborted;
-                    const bool pair = p.pair();
+                    const bool pair = PAIRS && p.pair();
                     const int bufs = p.nt <= 0 || !t.q_tokens ? 0 : pair ? 2 : 1;
                     const int q_head = p.head * a.group, q_token = p.t0 + t.by_group(p.row0);
                     mbar_arrive(&sm.piece_full[pk % kPieces]);
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const Piece& p = sm.pieces[pk % kPieces];
             float m = -INFINITY, l = 0.f;
             {
-                const bool pair = p.pair();
+                const bool pair = PAIRS && p.pair();
                 const int my_steps = p.steps(slot);
                 const bool whole_rows = pair && p.nt >= kLongPiece;
                 const int local = (pair ? slot * kTile : 0) + row;     // row of the item
@@ -1178,7 +1178,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool more = piece_ready(nk);
             if (more) {
                 const Piece& n = sm.pieces[nk % kPieces];
-                const bool pair = n.pair();
+                const bool pair = PAIRS && n.pair();
                 const int bufs = n.nt == 0 || t.q_tokens ? 0 : pair ? 2 : 1;
 #pragma unroll 1
                 for (int i = 0; i < bufs; ++i) {
@@ -1220,7 +1220,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
             if (have) {
                 const Piece& p = sm.pieces[pk % kPieces];
-                const bool pair = p.pair(), both = !pair && p.nt > 1, whole = p.first && p.last;
+                const bool pair = PAIRS && p.pair(), both = !pair && p.nt > 1, whole = p.first && p.last;
                 const int lead = p.lead;
 #pragma unroll 1
                 for (int i = 0; i < (pair ? 2 : 1); ++i) {          // rows of one slot, or of both
@@ -1514,8 +1514,8 @@ Divisor divisor(int d)
     return Divisor{(uint32_t)(((1ull << (31 + l)) + (uint64_t)d - 1) / (uint64_t)d), 31 + l};
 }
 
-template <typename T, int D>
-cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, cudaStream_t s)
+template <typename T, int D, bool PAIRS>
+cudaError_t launch_tc_as(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, cudaStream_t s)
 {
     const size_t smem = sizeof(TcSmem<D>);
     static_assert(sizeof(TcSmem<D>) <= 232448, "shared memory of one CTA");
@@ -1524,15 +1524,23 @@ cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap&
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(attn_tc_kernel<T, D, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
     }
-    e = launch_pdl(attn_tc_kernel<T, D>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv, mq);
+    e = launch_pdl(attn_tc_kernel<T, D, PAIRS>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv, mq);
     if (e != cudaSuccess) return e;
     if (t.whole) return cudaSuccess;
     const int y = (t.part_rows + 3) / 4;
     return launch_pdl(attn_join_kernel<T, D>, dim3(t.grid - 1, y), dim3(128), 0, s, t);
+}
+
+// Windows that fit a slot's rows take a kernel without the code for items that
+// do not: instruction misses are a good part of short items' time.
+template <typename T, int D>
+cudaError_t launch_tc(const TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, cudaStream_t s)
+{
+    return t.part_rows > kTile ? launch_tc_as<T, D, true>(t, mk, mv, mq, s) : launch_tc_as<T, D, false>(t, mk, mv, mq, s);
 }
 
 }  // namespace
