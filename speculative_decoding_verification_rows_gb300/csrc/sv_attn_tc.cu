@@ -428,12 +428,22 @@ struct TcSmem {
 // waiting, with wrong results and SV_ROW_TIMEOUT.
 __device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t parity, int* aborted)
 {
-#pragma unroll 1
-    for (int i = 0; i < (int)kWaitPolls; ++i) {
-        if (mbar_try_wait(bar, parity)) return;
-        if (*(volatile int*)aborted) return;
-    }
-    *(volatile int*)aborted = 1;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .u32 n, a;\n\tmov.u32 n, %3;\n"
+        "again_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+        "@p bra done_%=;\n\t"
+        "ld.volatile.shared.u32 a, [%2];\n\t"
+        "setp.ne.u32 p, a, 0;\n\t"
+        "@p bra done_%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 p, n, 0;\n\t"
+        "@p bra again_%=;\n\t"
+        "mov.u32 a, 1;\n\t"
+        "st.volatile.shared.u32 [%2], a;\n"
+        "done_%=:\n\t}" ::"r"(smem_u32(bar)),
+        "r"(parity), "r"(smem_u32(aborted)), "n"((int)kWaitPolls)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t mbar_test(unsigned long long* bar, uint32_t parity)
