@@ -408,7 +408,7 @@ struct TcSmem {
         return (key >> 3) * kGroup + (vec >> 3) * 1024 + (key & 7) * 128 + ((vec ^ key) & 7) * 16;
     }
     unsigned long long full[kStages], empty[kStages];
-    unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_half[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
+    unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
     unsigned long long piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];          // warp 0 walks ahead of the other roles
     float2 ml[2][kTile];            // the slots' statistics of a finished piece
@@ -534,8 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&sm.q_empty[lane], 2);
             mbar_init(&sm.s_full[lane], 1);
             mbar_init(&sm.s_free[lane], 4);
-            mbar_init(&sm.p_half[lane], 4);        // 4: a warp at a time
-            mbar_init(&sm.p_full[lane], 4);
+            mbar_init(&sm.p_full[lane], 4);        // 4: a warp at a time
             mbar_init(&sm.pv_done[lane], 1);
             mbar_init(&sm.o_free[lane], 4);
             mbar_init(&sm.ml_full[lane], 4);
@@ -794,23 +793,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (scored) score();
                     if (st > 0) {                                // P V of step st - 1
                         if (st == 1) wait_or_abort(&sm.o_free[s], ~o_uses++ & 1u, &sm.aborted);   // at first it is
-                        wait_or_abort(&sm.p_half[s], done & 1u, &sm.aborted);
-                        const bool by_hand = edge && *(volatile int*)&sm.by_hand[s];
-                        if (pair && !S::kApart) reached(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
-                        tc_fence_after();
-                        if (one_lane() && !by_hand) {
-#pragma unroll
-                            for (int k = 0; k < kTile / 32; ++k)
-                                tc_mma_ts(o_at, p_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, st > 1 || k > 0);
-                        }
                         wait_or_abort(&sm.p_full[s], done & 1u, &sm.aborted);
                         ++done;
+                        const bool by_hand = edge && *(volatile int*)&sm.by_hand[s];
+                        if (pair && !S::kApart) reached(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
                         tc_fence_after();
                         if (one_lane()) {
                             if (!by_hand) {
 #pragma unroll
-                                for (int k = kTile / 32; k < kTile / 16; ++k)
-                                    tc_mma_ts(o_at, p_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, true);
+                                for (int k = 0; k < kTile / 16; ++k)
+                                    tc_mma_ts(o_at, p_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, st > 1 || k > 0);
                             }
                             tc_commit(&sm.pv_done[s]);
                             tc_commit(&sm.empty[v_stage]);
@@ -1028,9 +1020,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 for (int i = 0; i < 32; ++i) s[c + i] = in >> i & 1u ? s[c + i] : 0xff800000u;   // -inf
                             }
                         }
-                        // The first weights are taken under the maximum so far while the tile's is found, and again
-                        // if that was too small: rare after a row's first tile, and the maximum costs no time of its own.
-                        weigh(s);
                         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
                         for (int c = 0; c < kTile; c += 8) {
@@ -1039,20 +1028,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             mx2 = fmaxf(fmaxf(mx2, __uint_as_float(s[c + 4])), __uint_as_float(s[c + 5]));
                             mx3 = fmaxf(fmaxf(mx3, __uint_as_float(s[c + 6])), __uint_as_float(s[c + 7]));
                         }
-                        if (grow(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)))) {
-                            l0 = l1 = 0;
-                            weigh(s);
-                        }
+                        grow(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)));
+                        weigh(s);
                         weights_used();
                         tc_st16(w, p_at);
                         weigh(s + 32);
                         tc_st16(w, p_at + 16);
                         weigh(s + 64);
-                        if (!by_hand) {                                // the products of the first half may begin
-                            tc_wait_st();
-                            tc_fence_before();
-                            warp_arrive(&sm.p_half[slot]);
-                        }
                         tc_st16(w, p_at + 32);
                         weigh(s + 96);
                         tc_st16(w, p_at + 48);
@@ -1105,10 +1087,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         l += ls.x + ls.y;
                         tc_wait_st();
                     }
-                    if (!by_hand && (nothing || !(warp_valid && whole_rows))) {
-                        tc_fence_before();
-                        warp_arrive(&sm.p_half[slot]);
-                    }
                     if (by_hand) {
                         const uint32_t e = base + entry_v(k0 / kTile - p.kt0, p.nt, pair ? 1 : 2);
                         const unsigned char* vt = sm.kv[e % kStages];
@@ -1155,8 +1133,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc_wait_st();
                         }
                         if (row == 0) *(volatile int*)&sm.by_hand[slot] = 1;
-                        tc_fence_before();
-                        warp_arrive(&sm.p_half[slot]);
                     }
                     ++steps_done;
                     tc_fence_before();
