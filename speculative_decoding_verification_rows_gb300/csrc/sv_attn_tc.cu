@@ -42,6 +42,7 @@
 #include <limits.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "sv_attn.cuh"
 
@@ -1369,36 +1370,43 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         float mt = -INFINITY, lt = 0.f, x[kE];
 #pragma unroll
         for (int e = 0; e < kE; ++e) x[e] = 0.f;
+        auto take = [&](auto width) {                        // so many pieces' loads in flight
+            constexpr int kW = decltype(width)::value;
 #pragma unroll 1
-        for (int i = i0; i < i1; i += 8) {                   // eight pieces' loads in flight
-            float2 ml[8];
-            float y[8][kE];
+            for (int i = i0; i < i1; i += kW) {
+                float2 ml[kW];
+                float y[kW][kE];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) {
-                const int64_t q = at(min(i + z, i1 - 1));
-                ml[z] = t.part_ml[q];
-                if (i + z >= i1) ml[z].y = 0.f;
+                for (int z = 0; z < kW; ++z) {
+                    const int64_t q = at(min(i + z, i1 - 1));
+                    ml[z] = t.part_ml[q];
+                    if (i + z >= i1) ml[z].y = 0.f;
 #pragma unroll
-                for (int e = 0; e < kE; ++e) y[z][e] = t.part[q * D + lane * kE + e];
+                    for (int e = 0; e < kE; ++e) y[z][e] = t.part[q * D + lane * kE + e];
+                }
+                float top = mt;
+#pragma unroll
+                for (int z = 0; z < kW; ++z)
+                    if (ml[z].y != 0.f) top = fmaxf(top, ml[z].x);
+                const float keep = lt == 0.f ? 0.f : exp2_approx(mt - top);
+                mt = top;
+                lt *= keep;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) x[e] = keep == 0.f ? 0.f : x[e] * keep;
+#pragma unroll
+                for (int z = 0; z < kW; ++z) {
+                    if (ml[z].y == 0.f) continue;
+                    const float f = exp2_approx(ml[z].x - mt);
+                    lt = fmaf(ml[z].y, f, lt);
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) x[e] = fmaf(y[z][e], f, x[e]);
+                }
             }
-            float top = mt;
-#pragma unroll
-            for (int z = 0; z < 8; ++z)
-                if (ml[z].y != 0.f) top = fmaxf(top, ml[z].x);
-            const float keep = lt == 0.f ? 0.f : exp2_approx(mt - top);
-            mt = top;
-            lt *= keep;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) x[e] = keep == 0.f ? 0.f : x[e] * keep;
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-                if (ml[z].y == 0.f) continue;
-                const float f = exp2_approx(ml[z].x - mt);
-                lt = fmaf(ml[z].y, f, lt);
-#pragma unroll
-                for (int e = 0; e < kE; ++e) x[e] = fmaf(y[z][e], f, x[e]);
-            }
-        }
+        };
+        if (shared)
+            take(std::integral_constant<int, 8>{});
+        else
+            take(std::integral_constant<int, 2>{});
         if (shared) {
             __syncthreads();                                 // the row before has been read
             if (lane == 0) ml_sh[warp] = make_float2(mt, lt);
