@@ -242,7 +242,7 @@ class Workspace:
 
 def _ws(ws: Optional[Workspace], device, nbytes) -> torch.Tensor:
     if ws is None:
-        ws = Workspace(q.device)
+        ws = Workspace(device)
     return ws.get(nbytes)
 
 
