@@ -18,7 +18,10 @@ constexpr int kRowElems = kAttnMaxDim / 32;   // head elements a lane can hold
 // values.  The warps' results are joined in warp order.  Every access is one
 // element wide, so that any stride, page size and head size is served; each
 // row reads its request's whole cache from L2, and the warp sum of every key
-// bounds it.
+// bounds it (64 single tokens x 32 heads over 256 to 8,192 keys: 2.8 ms, 25 times
+// the tensor-core kernel's 0.108).  fp32, heads other than 64 and 128, pages that
+// neither divide nor fill tiles of 128 keys, unaligned tensors and negative scales
+// come here.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) attn_rows_kernel(const AttnArgs a)
 {

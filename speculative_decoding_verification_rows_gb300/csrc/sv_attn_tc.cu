@@ -14,16 +14,30 @@
 // workspace in fp32 with their maximum and sum, and a second kernel joins them
 // in the order of the line.
 //
-// Inside a CTA (one per SM).  Warp 0 loads key and value tiles by TMA, page by
-// page, into a ring; one thread of warp 1 issues the matrix products; two
-// groups of four warps are two slots that turn scores into weights, a thread a
-// row.  A slot has its own rows of scores S and output O in TMEM.  An item of
-// more than 128 rows gives each slot half of the rows and both read every tile;
-// an item of up to 128 rows gives both slots all of its rows and every other
-// tile, and the slots' results are joined at its end.  Either way the tensor
-// core works for one slot while the other is at its weights.  The weights P
-// take the place of S in TMEM and are the left operand of P V from there, so
-// neither ever passes through shared memory.
+// Inside a CTA (one per SM, 16 warps).  Warp 0 walks over the CTA's part of the
+// line and loads Q; warp 2 loads key and value tiles by TMA, a box a page, into
+// a ring; warps 1 and 3 issue the matrix products of a slot each; two groups of
+// four warps are the slots, which turn scores into weights, a thread a row; the
+// last four warps write outputs.  A slot has its own scores S and output O in
+// TMEM.  An item of more than 128 rows gives each slot half of the rows and both
+// read every tile, taking turns at the tensor core, so that one slot makes its
+// weights during the other's products; an item of up to 128 rows gives both
+// slots all of its rows and every other tile, and the slots' results are joined
+// at its end.  The weights P are the left operand of P V from TMEM, so neither
+// S nor P ever passes through shared memory: heads of 128 leave room for P only
+// in the place of S, heads of 64 have it apart, and their next scores are made
+// while the weights are.
+//
+// What bounds it (one GB300).  Few rows: HBM.  4 requests x 8 tokens x 64 heads
+// over 65,536 to 131,072 keys read 1.64 GB in 243 us, 6.75 TB/s, the measured copy
+// bandwidth; 64 single tokens over 256 to 8,192 keys take 108 us for 0.61 GB (83%
+// of it: some 7 us of the call are its start and the join), 256 ragged windows
+// over 128 to 4,096 keys 220 us for 1.23 GB (82%).  Many rows: the chain scores,
+// weights, P V, scores of a slot.  Chunks of 2,048 tokens over 8,192 and 16,384
+// keys take 0.56 ms, 1,350 TFLOP/s, 70% of cuBLAS' burst rate at the card's
+// power limit; the tensor core is busy 55% of the cycles.  Short items (ragged
+// prompts under a sliding window of 512, 58 us) are bound by latencies: start, the first
+// instruction fetches, a turn of the chain a tile.
 //
 // Statistics.  m and l are fp32, one row a thread.  O is rescaled only when a
 // row's maximum grows by more than 2^8: weights are then below 2^8 instead of
@@ -53,8 +67,13 @@ constexpr int kTile = 128;              // keys of a tile, rows of a slot
 constexpr int kTcThreads = 512;
 constexpr int kTcWarps = kTcThreads / 32;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kLongPiece = 16;          // tiles of a piece whose slots take the unrolled code
-constexpr int kWholeTiles = 4;          // items of caches up to this long are not split
+// Tiles of a piece of shared tiles from which on the slots take the unrolled
+// code: prompt chunks 633 us without it, 582 with; short items (6 tiles) 71 us with it, 66
+// without, for its instructions have to be fetched first.
+constexpr int kLongPiece = 16;
+// Caches of up to so many tiles (by the width of the page table) are not split:
+// a second kernel costs 3 us of the host and as much of the GPU, a tile 1.5.
+constexpr int kWholeTiles = 4;
 
 // ---- PTX ---------------------------------------------------------------------
 __device__ __forceinline__ void tc_alloc(uint32_t* where)
@@ -509,7 +528,9 @@ __device__ __forceinline__ float2 halves(unsigned long long x)
 // The code is kept small on purpose (one copy of every step, loops that are not
 // unrolled): the roles run different parts of it at the same time, and at
 // 195 KB, with the steps inlined wherever they occur, instruction misses took
-// most of the time of short items.
+// most of the time of short items (256 ragged windows: 523 us, 272 at 68 KB).
+// PAIRS: items of more than 128 rows may come; without their code the same took
+// 223 us instead of 242.
 template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcArgs t, const __grid_constant__ CUtensorMap map_k,
@@ -1525,7 +1546,8 @@ cudaError_t launch_tc_as(const TcArgs& t, const CUtensorMap& mk, const CUtensorM
     e = launch_pdl(attn_tc_kernel<T, D, PAIRS>, dim3(t.grid), dim3(kTcThreads), smem, s, t, mk, mv, mq);
     if (e != cudaSuccess) return e;
     if (t.whole) return cudaSuccess;
-    const int y = (t.part_rows + 3) / 4;
+    // A few rows a warp rather than one: 18 blocks an item took 57.5 us of ragged prompts of 256-row items, 64 blocks 60.5.
+    const int y = t.part_rows < 72 ? (t.part_rows + 3) / 4 : 18;
     return launch_pdl(attn_join_kernel<T, D>, dim3(t.grid - 1, y), dim3(128), 0, s, t);
 }
 
