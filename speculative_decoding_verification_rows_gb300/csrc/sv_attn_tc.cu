@@ -772,11 +772,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (pair || qb == 1) ++q_uses[1];
                     // A slot without steps does not wait: it would not hold the buffer, which may be two loads on.
                     const uint32_t use = qb ? q_uses[1] : q_uses[0];
-                    if (steps == 0) {
-                    } else if (t.q_tokens) {
+                    if (steps > 0 && t.q_tokens) {
                         reached(&sm.q_issued[qb], use);
                         wait_or_abort(&sm.q_full[qb], (use - 1) & 1u, &sm.aborted);
-                    } else {
+                    } else if (steps > 0) {
                         reached(&sm.q_loads[qb], 4u * use);
                         __threadfence_block();
                     }
@@ -821,7 +820,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (pair && !S::kApart) reached(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
                         tc_fence_after();
                         if (one_lane()) {
-                            if (!by_hand) {
+                            if (by_hand) {
+                                *(volatile int*)&sm.by_hand[s] = 0;   // before the commit that lets the slot set it again
+                                __threadfence_block();
+                            } else {
 #pragma unroll
                                 for (int k = 0; k < kTile / 16; ++k)
                                     tc_mma_ts(o_at, p_at + k * 8, vd + k * (2 * S::kGroup >> 4), kPv, st > 1 || k > 0);
@@ -829,7 +831,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc_commit(&sm.pv_done[s]);
                             tc_commit(&sm.empty[v_stage]);
                             if (!pair) tc_commit(&sm.empty[v_stage]);
-                            if (by_hand) *(volatile int*)&sm.by_hand[s] = 0;
                         }
                         __syncwarp();
                     }
@@ -973,6 +974,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         if (st > 0 && some) {
                             wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
+                            __syncwarp();                    // tensor memory is a whole warp's business
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D; c += 8) {
@@ -1016,6 +1018,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     auto weights_used = [&]() {
                         if (S::kApart && steps_done > 0) {
                             wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
+                            __syncwarp();
                             tc_fence_after();
                         }
                     };
@@ -1115,6 +1118,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (warp_valid) {
                             if (st > 0) {
                                 wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
+                                __syncwarp();
                                 tc_fence_after();
                             }
 #pragma unroll 1
@@ -1337,9 +1341,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (sm.aborted) {
         if (warp == 2) {                                  // loads in flight land before the kernel ends
 #pragma unroll 1
-            for (int i = lane; i < 2 * (int)kStages; i += 32)
+            for (int i = lane; i < 2 * (int)kStages + 4; i += 32) {
+                unsigned long long* bar = i < 2 * (int)kStages ? &sm.full[i >> 1] : &sm.q_full[(i - 2 * (int)kStages) >> 1];
 #pragma unroll 1
-                for (int x = 0; x < (int)kWaitPolls / 16 && !mbar_try_wait(&sm.full[i >> 1], (uint32_t)i & 1u); ++x) {}
+                for (int x = 0; x < (int)kWaitPolls / 16 && !mbar_try_wait(bar, (uint32_t)i & 1u); ++x) {}
+            }
         }
         if (a.status)
             for (int r = tid; r < a.n_req; r += kTcThreads) atomicOr(&a.status[r], kTimeout);
