@@ -4,7 +4,8 @@
 // Rows.  The query heads of a key head share its keys, so a request's window
 // of n tokens and a group of G heads is one matrix of n G rows (row = token G
 // + head) per key head.  An item is up to 256 rows of it against the keys they
-// see, in tiles of 128 keys.  An item's tiles are its cost.
+// see (128 rows where few keys are seen, kNarrowWindow), in tiles of 128 keys.
+// An item's tiles are its cost.
 //
 // Split.  The items of a call, one after the other, are a line of tiles; CTA b
 // of B takes tiles [b T / B, (b + 1) T / B) of it, wherever items begin and
@@ -34,10 +35,10 @@
 // of it: some 7 us of the call are its start and the join), 256 ragged windows
 // over 128 to 4,096 keys 220 us for 1.23 GB (82%).  Many rows: the chain scores,
 // weights, P V, scores of a slot.  Chunks of 2,048 tokens over 8,192 and 16,384
-// keys take 0.56 ms, 1,350 TFLOP/s, 70% of cuBLAS' burst rate at the card's
-// power limit; the tensor core is busy 55% of the cycles.  Short items (ragged
-// prompts under a sliding window of 512, 58 us) are bound by latencies: start, the first
-// instruction fetches, a turn of the chain a tile.
+// keys take 0.52 ms, 1,450 TFLOP/s, 76% of cuBLAS' burst rate, near the card's
+// power limit.  Short items (ragged prompts under a sliding window of 512, 54 us)
+// are bound by latencies: start, the first instruction fetches, a turn of the
+// chain a tile.
 //
 // Statistics.  m and l are fp32, one row a thread.  O is rescaled only when a
 // row's maximum grows by more than 2^8: weights are then below 2^8 instead of
@@ -67,13 +68,21 @@ constexpr int kTile = 128;              // keys of a tile, rows of a slot
 constexpr int kTcThreads = 512;
 constexpr int kTcWarps = kTcThreads / 32;
 constexpr uint32_t kTmemCols = 512;
-// Tiles of a piece of shared tiles from which on the slots take the unrolled
-// code: prompt chunks 633 us without it, 582 with; short items (6 tiles) 71 us with it, 66
-// without, for its instructions have to be fetched first.
-constexpr int kLongPiece = 16;
 // Caches of up to so many tiles (by the width of the page table) are not split:
 // a second kernel costs 3 us of the host and as much of the GPU, a tile 1.5.
 constexpr int kWholeTiles = 4;
+
+// Without shared heads an item's rows are as many tokens, each with keys of its
+// own: where few tiles are seen, items of 128 rows (slots take tiles by turns)
+// spare a good part of them against 256 (a slot's rows its own, every tile both
+// slots').  So it is up to these windows or, without one, caches of more than
+// one item.  us with 128 and 256 rows, 16 heads of 64: 64 prompts of 200-600
+// tokens, window 64 133 and 170, window 512 174 and 198; one of 8,000, window
+// 640 77 and 83, window 1,024 94 and 95; 32 whole prompts of 640 108 and 133,
+// 8 of 1,000 62 and 71; but 64 of 200 67 and 58.  With two query heads a key
+// head the same long prompts were slower with 128 rows (60 to 50, window 128).
+constexpr int kNarrowWindow = 640;
+constexpr int kNarrowCache = 1024;
 
 // ---- PTX ---------------------------------------------------------------------
 __device__ __forceinline__ void tc_alloc(uint32_t* where)
@@ -275,6 +284,7 @@ struct TcArgs {
     float2* part_ml;        // [2 grid][part_rows] their maximum (log2) and sum
     int4* rec;              // [grid][2] what each CTA left there
     int part_rows;
+    int item_shift;         // log2 of an item's rows: 8, or 7 where few keys are seen (kNarrowWindow)
     int grid;
     int whole;              // items are not split: each counts as one tile of the line
     unsigned long long inv_grid;   // ceil(2^64 / grid)
@@ -284,12 +294,13 @@ struct TcArgs {
 
 // A request's window as rows and items.
 struct Window {
-    int n, len, t0, rows, items;
-    __device__ __forceinline__ int row0(int item) const { return item * 2 * kTile; }
-    __device__ __forceinline__ int item_rows(int item) const { return min(rows - row0(item), 2 * kTile); }
+    int n, len, t0, rows, items, shift;
+    __device__ __forceinline__ int row0(int item) const { return item << shift; }
+    __device__ __forceinline__ int item_rows(int item) const { return min(rows - row0(item), 1 << shift); }
 };
-__device__ __forceinline__ Window window_of(const AttnArgs& a, int r, bool report)
+__device__ __forceinline__ Window window_of(const TcArgs& t, int r, bool report)
 {
+    const AttnArgs& a = t.a;
     Window w;
     w.t0 = a.qo_indptr[r];
     const int t1 = a.qo_indptr[r + 1];
@@ -302,7 +313,8 @@ __device__ __forceinline__ Window window_of(const AttnArgs& a, int r, bool repor
         w.n = 0;
     }
     w.rows = w.n * a.group;
-    w.items = (w.rows + 2 * kTile - 1) / (2 * kTile);
+    w.shift = t.item_shift;
+    w.items = (w.rows + (1 << w.shift) - 1) >> w.shift;
     return w;
 }
 // Keys [lo, hi) that the row of token i of a window sees.
@@ -399,7 +411,7 @@ struct Walk {
                             left = 0;
                             return;
                         }
-                        w = window_of(t.a, r, false);
+                        w = window_of(t, r, false);
                     } while (w.items == 0);
                 }
             }
@@ -530,7 +542,11 @@ __device__ __forceinline__ float2 halves(unsigned long long x)
 // 195 KB, with the steps inlined wherever they occur, instruction misses took
 // most of the time of short items (256 ragged windows: 523 us, 272 at 68 KB).
 // PAIRS: items of more than 128 rows may come; without their code the same took
-// 223 us instead of 242.
+// 223 us instead of 242.  Each variant has one way through the scores: with them
+// a row is held in registers whole (prompt chunks 582 us for 633), without them
+// 64 columns at a time in less code.  A kernel with both, by the length of the
+// piece, took 557 us of the same chunks, now 520; 132 of 32 prompts of 513
+// tokens, one head a key head, now 110.
 template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcArgs t, const __grid_constant__ CUtensorMap map_k,
@@ -605,7 +621,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int r = r0 + tid;
             if (pass == 0 || a.n_req > kTcThreads) {
                 per_head = 0;
-                if (r < a.n_req) per_head = head_tiles(t, window_of(a, r, pass == 0 && blockIdx.x == 0));
+                if (r < a.n_req) per_head = head_tiles(t, window_of(t, r, pass == 0 && blockIdx.x == 0));
                 incl = per_head * a.cache.k.heads;
 #pragma unroll
                 for (int x = 1; x < 32; x <<= 1) {
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 Walk k;
                 k.left = end - begin;
                 k.r = r;
-                k.w = window_of(a, r, false);
+                k.w = window_of(t, r, false);
                 k.head = k.item = 0;
                 long long off = begin - (incl - mine);
 #pragma unroll 1
@@ -909,7 +925,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             {
                 const bool pair = PAIRS && p.pair();
                 const int my_steps = p.steps(slot);
-                const bool whole_rows = pair && p.nt >= kLongPiece;
                 const int local = (pair ? slot * kTile : 0) + row;     // row of the item
                 const bool warp_valid = local - lane < p.rows;
                 int2 see = make_int2(0, INT_MAX);                      // rows of nobody: no masking
@@ -1031,7 +1046,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                             for (int c = 0; c < kTile / 2; c += 16) tc_st16(w, p_at + c);
                         }
-                    } else if (warp_valid && whole_rows) {
+                    } else if (PAIRS && warp_valid) {
                         uint32_t s[kTile];                             // fp32 scores
 #pragma unroll
                         for (int c = 0; c < kTile; c += 32) tc_ld32(s + c, s_at + c);
@@ -1063,8 +1078,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc_st16(w, p_at + 32);
                         weigh(s + 96);
                         tc_st16(w, p_at + 48);
-                    } else if (warp_valid) {
-                        // The same in less code, for items that memory bounds: twice over 64 columns at a time, the
+                    } else if (!PAIRS && warp_valid) {
+                        // The same in less code, where memory bounds the items: twice over 64 columns at a time, the
                         // maximum first.
                         float mx = -INFINITY;
 #pragma unroll 1
@@ -1384,7 +1399,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         }
     }
     last = min(last, t.grid - 1);
-    const Window w = window_of(a, rec.y, false);
+    const Window w = window_of(t, rec.y, false);
     const int rows = w.item_rows(rec.w), row0 = w.row0(rec.w), n = last - c0 + 1;
     const bool shared = n > kFewPieces;
     const int each = shared ? (n + 3) / 4 : n;               // pieces of a warp
@@ -1593,6 +1608,13 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
     TcArgs t{};
     t.a = a;
     t.part_rows = part_rows(a.max_window, a.group);
+    t.item_shift = 8;
+    const long long cached = (long long)a.cache.max_pages * a.cache.page_size;
+    const bool narrow = cached <= kNarrowCache || (a.window_keys > 0 && a.window_keys <= kNarrowWindow);
+    if (a.group == 1 && !a.full && cached > 2 * kTile && narrow) {
+        t.item_shift = 7;
+        t.part_rows = t.part_rows < kTile ? t.part_rows : kTile;
+    }
     t.grid = num_sms < kTcMaxGrid ? (num_sms < 2 ? 2 : num_sms) : kTcMaxGrid;
     t.inv_grid = ~0ull / (unsigned)t.grid + 1;
     char* w = static_cast<char*>(ws);
@@ -1604,7 +1626,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
     t.by_page = divisor(a.cache.page_size);
     t.scale_log2 = fmaxf(a.scale * 1.4426950408889634f, FLT_MIN);   // above 0: hidden scores stay -inf
     // Short caches: an item of up to kWholeTiles tiles is not worth a second kernel.
-    t.whole = (long long)a.cache.max_pages * a.cache.page_size <= (long long)kWholeTiles * kTile;
+    t.whole = cached <= (long long)kWholeTiles * kTile;
     const bool bf16 = dt == SV_DTYPE_BF16;
     CUtensorMap mk, mv, mq{};
     if (!make_map(&mk, a.cache.k, a.cache.stride_page_k, a.cache, a.head_dim, bf16) ||

@@ -162,3 +162,47 @@ def test_windows_of_a_whole_batch_without_tokens(ws):
     out = torch.full_like(q, 2.0)
     sv.paged_attention(q, kp, vp, table, qo, kv_len, 4, out=out, ws=ws)
     assert (out == 2.0).all()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64)])
+@pytest.mark.parametrize("windows,lens,window", [
+    ([257, 1, 0, 128, 300, 129], [257, 40, 9, 513, 700, 131], 0),       # caches of up to 1,024 keys
+    ([256, 129, 200, 3], [256, 200, 215, 0], 0),                        # of just over 256
+    ([140, 256, 7], [140, 256, 7], 0),                                  # of no more than that
+    ([500, 130, 1], [1100, 2000, 1500], 640),
+    ([500, 130, 1], [1100, 2000, 1500], 641),
+    ([400, 300], [1500, 300], 1),
+    ([129, 260], [400, 2500], 130),
+])
+def test_prompts_with_a_key_head_for_every_query_head(ws, dtype, d, windows, lens, window):
+    b = Batch(windows, lens, 2, 2, d, 16, dtype, seed=31)
+    close(attend(b, ws, repeats=20, window=window), b, attend64(b, window=window))
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64)])
+def test_prompts_that_see_every_key_of_a_short_cache(ws, dtype, d):
+    b = Batch([257, 130, 5], [600, 130, 700], 2, 2, d, 16, dtype, seed=32)
+    close(attend(b, ws, repeats=5, full=True), b, attend64(b, full=True))
+    close(attend(b, ws, repeats=5, full=True, window=200), b, attend64(b, full=True, window=200))
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64)])
+def test_poison_beyond_a_prompts_rows(ws, dtype, d):
+    # a key that slid out of some rows' window and one that others do not see yet, in tiles that both slots read
+    b = Batch([400, 300], [400, 1300], 2, 2, d, 16, dtype, seed=33)
+    clean = attend64(b, window=150)
+    spoiled = [(0, 200), (1, 1100)]
+    for r, p in spoiled:
+        b.v_pages[b.table[r, p // 16].item(), p % 16] = float("nan")
+    q, kp, vp, table, qo, kv_len = b.gpu()
+    got = sv.paged_attention(q, kp, vp, table, qo, kv_len, 400, window=150, ws=ws)
+    out, _, tol, _ = clean
+    diff = (got.out.double().cpu() - out).abs()
+    for r, p in spoiled:
+        first = b.lens[r] - b.windows[r]
+        for i in range(b.windows[r]):
+            row = b.qo[r] + i
+            if first + i - 149 <= p <= first + i:
+                assert got.out[row].isnan().all()
+            else:
+                assert (diff[row] <= tol[row]).all(), (r, i)
