@@ -284,6 +284,7 @@ struct TcArgs {
     float2* part_ml;        // [2 grid][part_rows] their maximum (log2) and sum
     int4* rec;              // [grid][2] what each CTA left there
     int part_rows;
+    int lanes_shift;        // log2 of the lanes that count a request's tiles
     int item_shift;         // log2 of an item's rows: 8, or 7 where few keys are seen (kNarrowWindow)
     int grid;
     int whole;              // items are not split: each counts as one tile of the line
@@ -335,15 +336,10 @@ __device__ __forceinline__ int2 item_tiles(const TcArgs& t, const Window& w, int
     const int x = lo / kTile;
     return make_int2(x, max((hi + kTile - 1) / kTile, x + 1));
 }
-__device__ __forceinline__ long long head_tiles(const TcArgs& t, const Window& w)
+__device__ __forceinline__ int item_cost(const TcArgs& t, const Window& w, int item)
 {
-    long long c = 0;
-#pragma unroll 1
-    for (int i = 0; i < w.items; ++i) {
-        const int2 x = item_tiles(t, w, i);
-        c += t.whole ? 1 : x.y - x.x;
-    }
-    return c;
+    const int2 x = item_tiles(t, w, item);
+    return t.whole ? 1 : x.y - x.x;
 }
 
 // A piece of an item: the part of the line one CTA has of it.
@@ -596,8 +592,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == 1) tc_alloc(&sm.tmem);
     pdl_enter();
 
-    // The CTA's part of the line: the tiles of every request summed, then the
-    // request its part begins in.
+    // The CTA's part of the line: the tiles of every request summed, a few
+    // lanes a request where there are few, then the request its part begins in.
     long long total = 0, per_head = 0, incl = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -617,11 +613,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         long long before = 0;
 #pragma unroll 1
-        for (int r0 = 0; r0 < a.n_req; r0 += kTcThreads) {
-            const int r = r0 + tid;
+        for (int r0 = 0; r0 < a.n_req; r0 += kTcThreads >> t.lanes_shift) {
+            const int r = r0 + (tid >> t.lanes_shift), lanes = 1 << t.lanes_shift, sub = tid & (lanes - 1);
             if (pass == 0 || a.n_req > kTcThreads) {
                 per_head = 0;
-                if (r < a.n_req) per_head = head_tiles(t, window_of(t, r, pass == 0 && blockIdx.x == 0));
+                if (r < a.n_req) {
+                    const Window w = window_of(t, r, pass == 0 && blockIdx.x == 0);
+#pragma unroll 1
+                    for (int i = sub; i < w.items; i += lanes) per_head += item_cost(t, w, i);
+                }
+#pragma unroll 1
+                for (int x = 1; x < lanes; x <<= 1) per_head += __shfl_xor_sync(0xffffffffu, per_head, x);
+                if (sub != 0) per_head = 0;              // counted once
                 incl = per_head * a.cache.k.heads;
 #pragma unroll
                 for (int x = 1; x < 32; x <<= 1) {
@@ -645,24 +648,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 before += chunk;
             }
             const long long mine = per_head * a.cache.k.heads;
-            if (pass == 1 && incl > begin && incl - mine <= begin) {      // one thread of the CTA
+            const uint32_t hit = __ballot_sync(0xffffffffu, pass == 1 && incl > begin && incl - mine <= begin);
+            if (hit) {                                   // one lane of the CTA; its warp looks for the item
+                const int src = __ffs((int)hit) - 1;
+                const long long of_head = __shfl_sync(0xffffffffu, per_head, src);
+                long long off = __shfl_sync(0xffffffffu, begin - (incl - mine), src);
                 Walk k;
                 k.left = end - begin;
-                k.r = r;
-                k.w = window_of(t, r, false);
-                k.head = k.item = 0;
-                long long off = begin - (incl - mine);
+                k.r = __shfl_sync(0xffffffffu, r, src);
+                k.w = window_of(t, k.r, false);
+                k.head = 0;
 #pragma unroll 1
-                for (; off >= per_head; ++k.head) off -= per_head;
+                for (; off >= of_head; ++k.head) off -= of_head;
 #pragma unroll 1
-                for (;; ++k.item) {
-                    k.tiles = item_tiles(t, k.w, k.item);
-                    const int cost = t.whole ? 1 : k.tiles.y - k.tiles.x;
-                    if (off < cost) break;
-                    off -= cost;
+                for (int i0 = 0; i0 < k.w.items; i0 += 32) {
+                    k.item = i0 + lane;
+                    const int cost = k.item < k.w.items ? item_cost(t, k.w, k.item) : 0;
+                    int upto = cost;
+#pragma unroll
+                    for (int x = 1; x < 32; x <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, upto, x);
+                        if (lane >= x) upto += y;
+                    }
+                    const uint32_t past = __ballot_sync(0xffffffffu, off < upto);
+                    if (past) {
+                        if (lane == __ffs((int)past) - 1) {
+                            k.tiles = item_tiles(t, k.w, k.item);
+                            k.done = (int)off - (upto - cost);
+                            sm.start = k;
+                        }
+                        break;
+                    }
+                    off -= __shfl_sync(0xffffffffu, upto, 31);
                 }
-                k.done = (int)off;
-                sm.start = k;
             }
         }
     }
@@ -1608,6 +1626,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
     TcArgs t{};
     t.a = a;
     t.part_rows = part_rows(a.max_window, a.group);
+    t.lanes_shift = 0;
+    while (t.lanes_shift < 5 && a.n_req <= kTcThreads >> (t.lanes_shift + 1)) ++t.lanes_shift;
     t.item_shift = 8;
     const long long cached = (long long)a.cache.max_pages * a.cache.page_size;
     const bool narrow = cached <= kNarrowCache || (a.window_keys > 0 && a.window_keys <= kNarrowWindow);

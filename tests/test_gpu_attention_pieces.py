@@ -206,3 +206,10 @@ def test_poison_beyond_a_prompts_rows(ws, dtype, d):
                 assert got.out[row].isnan().all()
             else:
                 assert (diff[row] <= tol[row]).all(), (r, i)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64)])
+@pytest.mark.parametrize("others", [0, 40])
+def test_a_prompt_of_more_items_than_a_warp_has_lanes(ws, dtype, d, others):
+    b = Batch([2] * others + [4500, 3, 0], [70] * others + [4600, 900, 5], 2, 1, d, 64, dtype, seed=34)
+    close(attend(b, ws, repeats=10, window=100), b, attend64(b, window=100))
