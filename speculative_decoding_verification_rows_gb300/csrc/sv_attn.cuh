@@ -70,8 +70,8 @@ struct AttnArgs {
 // The kernel that takes every layout.
 cudaError_t launch_attn_rows(const AttnArgs& a, sv_dtype_t dt, cudaStream_t s);
 
-// The tensor-core kernels: which calls they take (25 times as fast on single
-// tokens, 190 times on prompt chunks), and their workspace.
+// The tensor-core kernels: which calls they take (four times as fast on single
+// tokens, over a hundred times on prompt chunks), and their workspace.
 bool attn_tc_takes(const AttnArgs& a, sv_dtype_t dt);
 size_t attn_tc_workspace(int max_window, int group, int head_dim);
 cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_sms, cudaStream_t s);

@@ -213,3 +213,28 @@ def test_poison_beyond_a_prompts_rows(ws, dtype, d):
 def test_a_prompt_of_more_items_than_a_warp_has_lanes(ws, dtype, d, others):
     b = Batch([2] * others + [4500, 3, 0], [70] * others + [4600, 900, 5], 2, 1, d, 64, dtype, seed=34)
     close(attend(b, ws, repeats=10, window=100), b, attend64(b, window=100))
+
+
+@pytest.mark.parametrize("hq,hkv,d,page,dtype", [
+    (5, 1, 256, 10, BF16), (6, 2, 80, 16, F16), (3, 3, 33, 7, torch.float32), (2, 2, 256, 64, torch.float32),
+    (8, 1, 128, 24, BF16), (9, 3, 64, 16, torch.float32),
+])
+@pytest.mark.parametrize("windows,lens", [([1], [9000]), ([1, 3], [1, 4100]), ([2, 0, 1], [1030, 0, 130]),
+                                          ([150, 90], [700, 90])])
+def test_layouts_of_the_row_kernel(ws, hq, hkv, d, page, dtype, windows, lens):
+    # heads that four rows do not divide, single rows; a CTA a unit of work, and clusters of them over long caches
+    b = Batch(windows, lens, hq, hkv, d, page, dtype, seed=35)
+    close(attend(b, ws, repeats=3), b, attend64(b))
+    close(attend(b, ws, repeats=3, window=70), b, attend64(b, window=70))
+
+
+def test_a_page_number_out_of_range_where_ctas_share_the_keys(ws):
+    b = Batch([1, 2], [5000, 4000], 4, 1, 96, 16, BF16, seed=36)
+    ref = attend64(b)
+    q, kp, vp, table, qo, kv_len = b.gpu()
+    table[0, 200] = b.n_pages
+    table[0, 3] = -1
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    got = sv.paged_attention(q, kp, vp, table, qo, kv_len, 2, ws=ws, status=status)
+    assert status.tolist() == [sv.ROW_BAD_LAYOUT, 0]
+    close(got, b, ref, rows=slice(1, 3))
