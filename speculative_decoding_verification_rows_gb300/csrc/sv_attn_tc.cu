@@ -35,10 +35,10 @@
 // of it: some 7 us of the call are its start and the join), 256 ragged windows
 // over 128 to 4,096 keys 220 us for 1.23 GB (82%).  Many rows: the chain scores,
 // weights, P V, scores of a slot.  Chunks of 2,048 tokens over 8,192 and 16,384
-// keys take 0.52 ms, 1,450 TFLOP/s, 76% of cuBLAS' burst rate, near the card's
-// power limit.  Short items (ragged prompts under a sliding window of 512, 54 us)
-// are bound by latencies: start, the first instruction fetches, a turn of the
-// chain a tile.
+// keys take 0.52 ms (1,450 TFLOP/s, 76% of cuBLAS' burst rate) in a burst and
+// 0.56 ms at the card's power limit.  Short items (ragged prompts under a sliding
+// window of 512, 52 us) are bound by latencies: start, the first instruction
+// fetches, a turn of the chain a tile.
 //
 // Statistics.  m and l are fp32, one row a thread.  O is rescaled only when a
 // row's maximum grows by more than 2^8: weights are then below 2^8 instead of
@@ -540,9 +540,10 @@ __device__ __forceinline__ float2 halves(unsigned long long x)
 // PAIRS: items of more than 128 rows may come; without their code the same took
 // 223 us instead of 242.  Each variant has one way through the scores: with them
 // a row is held in registers whole (prompt chunks 582 us for 633), without them
-// 64 columns at a time in less code.  A kernel with both, by the length of the
-// piece, took 557 us of the same chunks, now 520; 132 of 32 prompts of 513
-// tokens, one head a key head, now 110.
+// 64 columns at a time in less code.  A kernel with both, whole rows for pieces of
+// 16 tiles or more, took 75 us of a prompt of 3,000 tokens x 16 heads of 64 (4 a
+// key head), now 66; 102 of four of 300-2,000 under a window of 2,048, now 88;
+// prompt chunks the same.
 template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcArgs t, const __grid_constant__ CUtensorMap map_k,
