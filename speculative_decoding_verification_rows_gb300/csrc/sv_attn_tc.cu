@@ -1150,11 +1150,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const uint32_t e = base + entry_v(k0 / kTile - p.kt0, p.nt, pair ? 1 : 2);
                         const unsigned char* vt = sm.kv[e % kStages];
                         if (warp_valid) {
-                            if (st > 0) {
+                            // O is free: the step before has been added to it, or, at a piece's first step, the
+                            // output warps have read the last piece's.
+                            if (st > 0)
                                 wait_or_abort(&sm.pv_done[slot], (steps_done - 1) & 1u, &sm.aborted);
-                                __syncwarp();
-                                tc_fence_after();
-                            }
+                            else
+                                wait_or_abort(&sm.o_free[slot], ~o_uses & 1u, &sm.aborted);
+                            __syncwarp();
+                            tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D; c += 32) {
                                 uint32_t o[32];
