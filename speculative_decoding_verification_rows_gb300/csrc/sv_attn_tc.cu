@@ -436,7 +436,7 @@ struct TcSmem {
         return (key >> 3) * kGroup + (vec >> 3) * 1024 + (key & 7) * 128 + ((vec ^ key) & 7) * 16;
     }
     unsigned long long full[kStages], empty[kStages];
-    unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain;
+    unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2], ml_full[2], vote[2], drain[2];
     unsigned long long piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];          // warp 0 walks ahead of the other roles
     float2 ml[2][kTile];            // the slots' statistics of a finished piece
@@ -452,14 +452,26 @@ struct TcSmem {
     int by_hand[2];                 // the slot has done this tile's P V itself
 };
 
-// A bounded wait; after one that gave up the kernel runs to its end without
-// waiting, with wrong results and SV_ROW_TIMEOUT.
+// Polls of a wait before it gives up.  A build that sets it low, for tests, does
+// not sleep between them.
+#ifdef SV_ATTN_WAIT_POLLS
+constexpr int kPolls = SV_ATTN_WAIT_POLLS;
+#define SV_POLL "mbarrier.test_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+#else
+constexpr int kPolls = (int)kWaitPolls;
+#define SV_POLL "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+#endif
+
+// A bounded wait.  After one that gave up the kernel runs to its end without
+// waiting, with wrong results and SV_ROW_TIMEOUT.  From then on nothing that is
+// in use may change hands: no piece is written and no load begun (a stage or a
+// piece that seems free may not be).
 __device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t parity, int* aborted)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .u32 n, a;\n\tmov.u32 n, %3;\n"
         "again_%=:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+        SV_POLL
         "@p bra done_%=;\n\t"
         "ld.volatile.shared.u32 a, [%2];\n\t"
         "setp.ne.u32 p, a, 0;\n\t"
@@ -470,7 +482,7 @@ __device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t 
         "mov.u32 a, 1;\n\t"
         "st.volatile.shared.u32 [%2], a;\n"
         "done_%=:\n\t}" ::"r"(smem_u32(bar)),
-        "r"(parity), "r"(smem_u32(aborted)), "n"((int)kWaitPolls)
+        "r"(parity), "r"(smem_u32(aborted)), "n"(kPolls)
         : "memory");
 }
 
@@ -507,6 +519,13 @@ __device__ __forceinline__ bool one_lane()
     asm volatile(
         "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0u;
+}
+// threadIdx.x read anew, where keeping it would cost a register all along.
+__device__ __forceinline__ int thread_now()
+{
+    int x;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
+    return x;
 }
 __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c)
 {
@@ -574,12 +593,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&sm.o_free[lane], 4);
             mbar_init(&sm.ml_full[lane], 4);
             mbar_init(&sm.vote[lane], 4);
+            mbar_init(&sm.drain[lane], 1);
             sm.q_loads[lane] = sm.q_issued[lane] = sm.turns[lane] = 0;
             sm.by_hand[lane] = 0;
             sm.odd[lane][0] = sm.odd[lane][1] = sm.odd[lane][2] = 0;
         }
         if (lane == 0) {
-            mbar_init(&sm.drain, 2);
             sm.aborted = 0;
             sm.issued = 0;
             sm.start.left = 0;
@@ -698,7 +717,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto reached = [&](const uint32_t* count, uint32_t n) {
 #pragma unroll 1
         for (int i = 0; (int)(*(const volatile uint32_t*)count - n) < 0; ++i) {
-            if (i == (int)kWaitPolls) *(volatile int*)&sm.aborted = 1;
+            if (i == kPolls) *(volatile int*)&sm.aborted = 1;
             if (*(volatile int*)&sm.aborted) break;
         }
     };
@@ -758,6 +777,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     const int group = page_size > kTile ? (key - t.by_page(key) * page_size) >> 3 : 0;
                     if (!known) wait_or_abort(&sm.empty[stage], free_phase, &sm.aborted);
+                    if (__any_sync(0xffffffffu, *(volatile int*)&sm.aborted)) return;
                     ++entry;
                     if (mine) tma_page(smem_u32(sm.kv[stage]) + lane_at, map, x, group, page, &sm.full[stage]);
                     if (lane == 0) {
@@ -886,12 +906,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 base += 2u * (uint32_t)nt;
             }
-            if (*(volatile int*)&sm.aborted) {                   // nothing in flight when the kernel ends
-                if (one_lane()) tc_commit(&sm.drain);
-                __syncwarp();
-#pragma unroll 1
-                for (int i = 0; i < (int)kWaitPolls && !mbar_try_wait(&sm.drain, 0); ++i) {}
-            }
         } else {
             // ---- the walk over the CTA's pieces: one thread ----------------------------------
             if (lane == 0) {
@@ -901,11 +915,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (uint32_t pk = 0;; ++pk) {
                     wait_or_abort(&sm.piece_empty[pk % kPieces], ~(pk / kPieces) & 1u, &sm.aborted);
+                    if (*(volatile int*)&sm.aborted) break;            // its readers may not be through with it
                     Piece& p = sm.pieces[pk % kPieces];
                     walk.next(t, p);
                     p.lead = lead;                       // an odd tile is the one slot's, then the other's
                     if (!(PAIRS && p.pair()) && (p.nt & 1)) lead ^= 1;
-                    const bool end = p.nt < 0 || *(volatile int*)&sm.aborted;
+                    const bool end = p.nt < 0;
                     const bool pair = PAIRS && p.pair();
                     const int bufs = p.nt <= 0 || !t.q_tokens ? 0 : pair ? 2 : 1;
                     const int q_head = p.head * a.group, q_token = p.t0 + t.by_group(p.row0);
@@ -917,6 +932,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int i = 0; i < bufs; ++i) {
                         const uint32_t qb = pair ? (uint32_t)i : q_next;
                         wait_or_abort(&sm.q_empty[qb], ~(qb ? q_uses[1] : q_uses[0]) & 1u, &sm.aborted);
+                        if (*(volatile int*)&sm.aborted) break;
                         if (qb) ++q_uses[1]; else ++q_uses[0];
                         mbar_expect_tx(&sm.q_full[qb], (uint32_t)(t.q_tokens * a.group * D * 2));
                         *(volatile uint32_t*)&sm.q_issued[qb] = qb ? q_uses[1] : q_uses[0];
@@ -1376,16 +1392,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (sm.aborted) {
-        if (warp == 2) {                                  // loads in flight land before the kernel ends
-#pragma unroll 1
-            for (int i = lane; i < 2 * (int)kStages + 4; i += 32) {
-                unsigned long long* bar = i < 2 * (int)kStages ? &sm.full[i >> 1] : &sm.q_full[(i - 2 * (int)kStages) >> 1];
-#pragma unroll 1
-                for (int x = 0; x < (int)kWaitPolls / 16 && !mbar_try_wait(bar, (uint32_t)i & 1u); ++x) {}
-            }
+        // What is in flight ends before the kernel does: either issuing warp's products, and every buffer's last load.
+        const int at = thread_now(), w = at >> 5, i = at & 31;
+        unsigned long long* bar = nullptr;
+        uint32_t phases = 0;
+        if (w == 1 || w == 3) {
+            bar = &sm.drain[w >> 1];
+            phases = 1;
+            if (one_lane()) tc_commit(bar);
+            __syncwarp();
+        } else if (w == 2 && i < (int)kStages) {
+            bar = &sm.full[i];
+            phases = (sm.issued + kStages - 1 - (uint32_t)i) / kStages;
+        } else if (w == 2 && i < (int)kStages + 2) {
+            bar = &sm.q_full[i - (int)kStages];
+            phases = sm.q_issued[i - (int)kStages];
         }
+#pragma unroll 1
+        for (int x = 0; phases > 0 && x < (int)kWaitPolls && !mbar_try_wait(bar, (phases - 1) & 1u); ++x) {}
+        __syncwarp();
         if (a.status)
-            for (int r = tid; r < a.n_req; r += kTcThreads) atomicOr(&a.status[r], kTimeout);
+            for (int r = at; r < a.n_req; r += kTcThreads) atomicOr(&a.status[r], kTimeout);
         __syncthreads();
     }
     if (warp == 1) {
