@@ -94,7 +94,8 @@ enum {
     SV_ROW_RESID_ZERO = 64,  /* informational: empty residual, sampled from p      */
     SV_ROW_UNSUPPORTED = 128, /* combination the library refuses (sv_verify_*)  */
     SV_ROW_TIMEOUT = 256      /* a bounded wait on a bulk copy gave up: rows of the
-                                 call were not processed (never seen in practice) */
+                                 call were not processed (never seen in practice);
+                                 of sv_paged_attention: results are right or NaN  */
 };
 #define SV_ROW_ERROR_MASK (SV_ROW_NONFINITE | SV_ROW_EMPTY | SV_ROW_BAD_TOKEN | SV_ROW_BAD_PARAM | \
                            SV_ROW_BAD_LAYOUT | SV_ROW_UNSUPPORTED | SV_ROW_TIMEOUT)
@@ -501,7 +502,9 @@ sv_status_t sv_verify_chain_shard_merge(const void* records, int n_shards, int n
  *    axis or longer than promised, a kv_len outside what the page table
  *    holds, a page number outside [0, n_pages).  Results of that request are
  *    then not to be used; other requests are not affected, and nothing
- *    outside the tensors is ever read or written.
+ *    outside the tensors is ever read or written.  SV_ROW_TIMEOUT
+ *    (sv_paged_attention): every request of the call gets it when a bounded
+ *    wait inside the kernel gave up.
  */
 
 /* Token rows of some heads: element (token, head, e) is
@@ -587,6 +590,8 @@ enum { SV_ATTN_FULL = 1 }; /* every row sees the whole cache (no causal limit), 
  *   [tokens, q.heads] or NULL.  max_window: a promise (host) that no window is
  *   longer; longer ones are refused (SV_ROW_BAD_LAYOUT, rows not written), and
  *   so are requests with kv_len outside [0, max_pages * page_size].
+ *   A call that gives up on a bounded wait (SV_ROW_TIMEOUT) leaves NaN in every
+ *   row, out and lse, that is not right, also where status is NULL.
  *   Workspace: sv_attention_workspace_size(...).
  *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, q.heads not a
  *   multiple of the cache's heads, a scale that is not finite;

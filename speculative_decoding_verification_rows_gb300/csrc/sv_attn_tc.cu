@@ -282,7 +282,7 @@ struct TcArgs {
     Divisor by_group, by_page;
     float* part;            // [2 grid][part_rows][D] pieces of items
     float2* part_ml;        // [2 grid][part_rows] their maximum (log2) and sum
-    int4* rec;              // [grid][2] what each CTA left there
+    int4* rec;              // [grid][2] what each CTA left there; y of the first: a wait of it gave up
     int part_rows;
     int lanes_shift;        // log2 of the lanes that count a request's tiles
     int item_shift;         // log2 of an item's rows: 8, or 7 where few keys are seen (kNarrowWindow)
@@ -462,8 +462,10 @@ constexpr int kPolls = (int)kWaitPolls;
 #define SV_POLL "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
 #endif
 
-// A bounded wait.  After one that gave up the kernel runs to its end without
-// waiting, with wrong results and SV_ROW_TIMEOUT.  From then on nothing that is
+// A bounded wait.  After one that gave up the CTA runs to its end without
+// waiting; every row of the call is then written with NaN by it (other CTAs may
+// write theirs over that), items that it has a piece of are NaN after the join,
+// and every request's status gets SV_ROW_TIMEOUT.  From then on nothing that is
 // in use may change hands: no piece is written and no load begun (a stage or a
 // piece that seems free may not be).
 __device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t parity, int* aborted)
@@ -1413,6 +1415,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (a.status)
             for (int r = at; r < a.n_req; r += kTcThreads) atomicOr(&a.status[r], kTimeout);
+        __syncthreads();                                  // what the CTA has written is written
+        if (at == 0) t.rec[2 * blockIdx.x].y = 1;
+#pragma unroll 1
+        for (int r = 0; r < a.n_req; ++r) {
+            const Window w = window_of(t, r, false);
+#pragma unroll 1
+            for (int i = at; i < w.rows * a.cache.k.heads; i += kTcThreads) {
+                const int64_t token = w.t0 + i / a.q.heads, head = i % a.q.heads;
+                T* out = (T*)a.out.data + token * a.out.stride_token + head * a.out.stride_head;
+#pragma unroll 1
+                for (int e = 0; e < D; ++e) out[e] = from_f32<T>(NAN);
+                if (a.lse) a.lse[token * a.q.heads + head] = NAN;
+            }
+        }
         __syncthreads();
     }
     if (warp == 1) {
@@ -1438,16 +1454,19 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const int4 rec = t.rec[2 * c0 + 1];
     if (!rec.x) return;
     int last = c0 + 1;                                       // the CTA with the item's last piece
+    bool lost = t.rec[2 * c0].y != 0;                        // a CTA with a piece gave up
 #pragma unroll 1
-    for (; last < t.grid - 1; last += 32) {
+    for (;; last += 32) {
         const int c = last + lane;
-        const uint32_t ends = __ballot_sync(0xffffffffu, c >= t.grid - 1 || t.rec[2 * c].x != 2);
+        const int4 left = t.rec[2 * min(c, t.grid - 1)];
+        const uint32_t ends = __ballot_sync(0xffffffffu, c >= t.grid - 1 || left.x != 2);
+        const uint32_t gone = __ballot_sync(0xffffffffu, left.y != 0);
+        lost = lost || (gone & (ends ? ends ^ (ends - 1) : 0xffffffffu)) != 0;   // up to the first end
         if (ends) {
-            last += __ffs(ends) - 1;
+            last += __ffs((int)ends) - 1;
             break;
         }
     }
-    last = min(last, t.grid - 1);
     const Window w = window_of(t, rec.y, false);
     const int rows = w.item_rows(rec.w), row0 = w.row0(rec.w), n = last - c0 + 1;
     const bool shared = n > kFewPieces;
@@ -1522,6 +1541,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
             }
             mt = top;
         }
+        if (lost) lt = NAN;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
         const int tok = t.by_group(row0 + row), g = row0 + row - tok * a.group;
         const int64_t token = w.t0 + tok;

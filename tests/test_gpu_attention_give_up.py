@@ -106,3 +106,24 @@ def test_the_next_call_is_right(libraries, monkeypatch):
     status = torch.zeros(b.n, dtype=torch.int32, device="cuda")
     got = sv.paged_attention(*args, 200, ws=ws, status=status)          # the same workspace, on the same stream
     assert status.tolist() == [0] * b.n and ((got.out.double().cpu() - out).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_results_of_a_call_that_gives_up_are_right_or_nan(impatient, name):
+    b = Batch(*SHAPES[name], seed=53, pad_tokens=2)
+    want, lse, tol, tol_l = attend64(b)
+    args = b.gpu()
+    ws, live, missing = sv.Workspace("cuda"), b.qo[-1], 0
+    for _ in range(12):
+        out = torch.full(args[0].shape, 3.0, dtype=b.dtype, device="cuda")
+        status = torch.zeros(b.n, dtype=torch.int32, device="cuda")
+        got = sv.paged_attention(*args, max(b.windows), out=out, status=status, ws=ws)
+        o, m = got.out[:live].double().cpu(), got.lse[:live].double().cpu()
+        assert (o.isnan() | ((o - want[:live]).abs() <= tol[:live])).all()
+        assert (m.isnan() | (m == lse[:live]) | ((m - lse[:live]).abs() <= tol_l[:live])).all()
+        missing += int(o.isnan().sum())
+        assert status[0].item() == sv.ROW_TIMEOUT or not (o.isnan().any() or m.isnan().any())
+        quiet = sv.paged_attention(*args, max(b.windows), ws=ws)             # and without a status
+        o = quiet.out[:live].double().cpu()
+        assert (o.isnan() | ((o - want[:live]).abs() <= tol[:live])).all()
+    assert impatient > 1 or missing
