@@ -488,6 +488,19 @@ __device__ __forceinline__ void wait_or_abort(unsigned long long* bar, uint32_t 
         : "memory");
 }
 
+// A count in shared memory that is given with what was done before it, and read
+// before what relies on that.
+__device__ __forceinline__ void give_count(uint32_t* count, uint32_t n)
+{
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(count)), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint32_t take_count(const uint32_t* count)
+{
+    uint32_t n;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(smem_u32(count)) : "memory");
+    return n;
+}
+
 __device__ __forceinline__ uint32_t mbar_test(unsigned long long* bar, uint32_t parity)
 {
     uint32_t ok;
@@ -715,23 +728,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wait_or_abort(&sm.piece_full[k % kPieces], k / kPieces & 1u, &sm.aborted);
         return sm.pieces[k % kPieces].nt >= 0 && !*(volatile int*)&sm.aborted;
     };
-    // A count in shared memory has reached n.
+    // A count in shared memory has reached n: the count.
     auto reached = [&](const uint32_t* count, uint32_t n) {
+        uint32_t x = take_count(count);
 #pragma unroll 1
-        for (int i = 0; (int)(*(const volatile uint32_t*)count - n) < 0; ++i) {
+        for (int i = 0; (int)(x - n) < 0; ++i) {
+            if (i == kPolls) *(volatile int*)&sm.aborted = 1;
+            if (*(volatile int*)&sm.aborted) break;
+            x = take_count(count);
+        }
+        return x;
+    };
+    // The other slot has had so many turns: an order of the products, which hand nothing over.
+    auto my_turn = [&](const uint32_t* turns, uint32_t n) {
+#pragma unroll 1
+        for (int i = 0; (int)(*(const volatile uint32_t*)turns - n) < 0; ++i) {
             if (i == kPolls) *(volatile int*)&sm.aborted = 1;
             if (*(volatile int*)&sm.aborted) break;
         }
     };
     // Entry e of the ring has landed.  A reader that skips entries cannot go by the stage's phase alone: with the
     // entry before e on that stage still to come, the phase of the one before that would pass for e's.
+    uint32_t begun = 0;                             // entries known to have begun
     auto landed = [&](uint32_t e) {
-        reached(&sm.issued, e + 1);
+        if ((int)(begun - e) <= 0) begun = reached(&sm.issued, e + 1);
         wait_or_abort(&sm.full[e % kStages], e / kStages & 1u, &sm.aborted);
     };
     auto landed_by_now = [&](uint32_t e) {
-        const uint32_t ok = mbar_test(&sm.full[e % kStages], e / kStages & 1u);
-        return __all_sync(0xffffffffu, (int)(*(volatile uint32_t*)&sm.issued - e) > 0 && ok) != 0;
+        begun = take_count(&sm.issued);             // first: before e has begun its stage's phase says nothing
+        return __all_sync(0xffffffffu, (int)(begun - e) > 0 && mbar_test(&sm.full[e % kStages], e / kStages & 1u)) != 0;
     };
     auto warp_arrive = [&](unsigned long long* bar) {
         __syncwarp();
@@ -784,7 +809,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (mine) tma_page(smem_u32(sm.kv[stage]) + lane_at, map, x, group, page, &sm.full[stage]);
                     if (lane == 0) {
                         mbar_expect_tx(&sm.full[stage], bytes);
-                        *(volatile uint32_t*)&sm.issued = entry;
+                        give_count(&sm.issued, entry);
                     }
                     if (++stage == kStages) {
                         stage = 0;
@@ -874,7 +899,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         wait_or_abort(&sm.p_full[s], done & 1u, &sm.aborted);
                         ++done;
                         const bool by_hand = edge && *(volatile int*)&sm.by_hand[s];
-                        if (pair && !S::kApart) reached(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
+                        if (pair && !S::kApart) my_turn(&sm.turns[s ^ 1], turns++ + (uint32_t)s);
                         tc_fence_after();
                         if (one_lane()) {
                             if (by_hand) {
@@ -937,7 +962,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (*(volatile int*)&sm.aborted) break;
                         if (qb) ++q_uses[1]; else ++q_uses[0];
                         mbar_expect_tx(&sm.q_full[qb], (uint32_t)(t.q_tokens * a.group * D * 2));
-                        *(volatile uint32_t*)&sm.q_issued[qb] = qb ? q_uses[1] : q_uses[0];
+                        give_count(&sm.q_issued[qb], qb ? q_uses[1] : q_uses[0]);
 #pragma unroll
                         for (int x = 0; x < D; x += 64)
                             tma_q(smem_u32(sm.q[qb]) + (uint32_t)(x / 64 * kTile * 128), &map_q, x, q_head,
