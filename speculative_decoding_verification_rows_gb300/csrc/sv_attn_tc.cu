@@ -318,13 +318,15 @@ __device__ __forceinline__ Window window_of(const TcArgs& t, int r, bool report)
     w.items = (w.rows + (1 << w.shift) - 1) >> w.shift;
     return w;
 }
-// Keys [lo, hi) that the row of token i of a window sees.
+// Keys [lo, hi) that the row of token i of a window sees.  A position may be
+// negative and a limit as large as an int: their difference is formed only where
+// the limit hides something.
 template <typename W>
 __device__ __forceinline__ int2 seen(const AttnArgs& a, const W& w, int i)
 {
     const int pos = w.len - w.n + i;
     const int hi = a.full ? w.len : max(0, pos + 1);
-    const int lo = a.window_keys > 0 ? max(0, pos - a.window_keys + 1) : 0;
+    const int lo = a.window_keys > 0 && pos >= a.window_keys ? pos - a.window_keys + 1 : 0;
     return make_int2(min(lo, hi), hi);
 }
 // Key tiles [x, y) of an item; at least one, so that an item without keys is
