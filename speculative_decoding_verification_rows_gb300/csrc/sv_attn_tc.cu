@@ -306,8 +306,9 @@ __device__ __forceinline__ Window window_of(const TcArgs& t, int r, bool report)
     w.t0 = a.qo_indptr[r];
     const int t1 = a.qo_indptr[r + 1];
     w.len = a.kv_len[r];
-    w.n = t1 - w.t0;
-    const bool bad = w.t0 < 0 || t1 > a.tokens || w.n < 0 || w.n > a.max_window || w.len < 0 ||
+    const bool on_axis = w.t0 >= 0 && t1 >= w.t0 && t1 <= a.tokens;
+    w.n = on_axis ? t1 - w.t0 : 0;
+    const bool bad = !on_axis || w.n > a.max_window || w.len < 0 ||
                      (long long)w.len > (long long)a.cache.max_pages * a.cache.page_size;
     if (bad) {
         if (report && a.status) atomicOr(&a.status[r], kBadLayout);

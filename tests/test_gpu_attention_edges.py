@@ -35,3 +35,17 @@ def test_a_window_of_any_size_over_rows_before_the_cache(ws, dtype, d, window):
         assert ((got.out.double().cpu() - want).abs() <= tol).all()
         m = got.lse.double().cpu()
         assert ((m == lse) | ((m - lse).abs() <= tol_l)).all()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64)])
+def test_windows_that_end_before_they_begin(ws, dtype, d):
+    # lengths that do not fit an int, under a promise that limits nothing
+    b = Batch([5, 4, 3], [50, 33, 130], 4, 2, d, 16, dtype, seed=64)
+    want, _, tol, _ = attend64(b)
+    q, kp, vp, table, qo, kv_len = b.gpu()
+    qo[2] = -2 ** 31
+    out = torch.full_like(q, 2.0)
+    status = torch.zeros(3, dtype=torch.int32, device="cuda")
+    sv.paged_attention(q, kp, vp, table, qo, kv_len, 2 ** 31 - 1, out=out, status=status, ws=ws)
+    assert status.tolist() == [0, sv.ROW_BAD_LAYOUT, sv.ROW_BAD_LAYOUT]
+    assert ((out.double().cpu() - want).abs() <= tol)[:5].all() and (out[5:] == 2.0).all()
