@@ -1732,7 +1732,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, sv_dtype_t dt, void* ws, int num_s
         !make_map(&mv, a.cache.v, a.cache.stride_page_v, a.cache, a.head_dim, bf16))
         return cudaErrorInvalidValue;
     if (kTile % a.group == 0 && a.q.stride_head > 0 && a.q.stride_token > 0) {
-        t.q_tokens = kTile / a.group < a.max_window ? kTile / a.group : a.max_window;
+        const int longest = a.max_window > 1 ? a.max_window : 1;         // a box has a token, needed or not
+        t.q_tokens = kTile / a.group < longest ? kTile / a.group : longest;
         if (!make_q_map(&mq, a.q, a.tokens, a.head_dim, a.group, t.q_tokens, bf16)) return cudaErrorInvalidValue;
     }
     if (a.head_dim == 64)

@@ -1,4 +1,5 @@
-"""The attention operators at the edges of their promises: limits that do not limit."""
+"""The attention operators at the edges of their promises: windows of no tokens, limits that do not
+limit."""
 import pytest
 import torch
 
@@ -21,6 +22,27 @@ def _lib():
 @pytest.fixture(scope="module")
 def ws():
     return sv.Workspace("cuda")
+
+
+@pytest.mark.parametrize("dtype,d", KERNELS)
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (10, 2)])
+def test_no_window_is_longer_than_nothing(ws, dtype, d, hq, hkv):
+    b = Batch([0, 0, 0], [40, 0, 300], hq, hkv, d, 16, dtype, pad_tokens=5)
+    q, kp, vp, table, qo, kv_len = b.gpu()
+    out = torch.full_like(q, 2.0)
+    status = torch.zeros(3, dtype=torch.int32, device="cuda")
+    sv.paged_attention(q, kp, vp, table, qo, kv_len, max(b.windows), out=out, status=status, ws=ws)
+    assert (out == 2.0).all() and status.tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype,d", KERNELS)
+def test_windows_longer_than_nothing_are_refused(ws, dtype, d):
+    b = Batch([0, 3, 1], [40, 9, 30], 4, 2, d, 16, dtype)
+    q, kp, vp, table, qo, kv_len = b.gpu()
+    out = torch.full_like(q, 2.0)
+    status = torch.zeros(3, dtype=torch.int32, device="cuda")
+    sv.paged_attention(q, kp, vp, table, qo, kv_len, 0, out=out, status=status, ws=ws)
+    assert (out == 2.0).all() and status.tolist() == [0, sv.ROW_BAD_LAYOUT, sv.ROW_BAD_LAYOUT]
 
 
 @pytest.mark.parametrize("dtype,d", KERNELS)
