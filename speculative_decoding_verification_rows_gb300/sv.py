@@ -575,6 +575,15 @@ def _stream_handle(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _launch(device: int, entry, *args):
+    """A call of the library on the device that its tensors live on."""
+    if torch.cuda.current_device() == device:
+        _check(entry(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args))
+
+
 def _attn_dtype(dtype: torch.dtype) -> int:
     code = _ATTN_DTYPES.get(dtype)
     if code is None:
@@ -709,9 +718,9 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, interle
     elif out.shape != x.shape:
         raise SVError(f"out must be {tuple(x.shape)}")
     flags = (ROTARY_INTERLEAVED if interleaved else 0) | (ROTARY_INVERSE if inverse else 0)
-    _check((_lib or load()).sv_rotary(_heads(x, dtype, device, d), _heads(out, dtype, device, d), _attn_dtype(dtype), tokens,
-                                      d, _vector(positions, tokens, device, "positions"),
-                                      _rope(freq, flags, mscale, device), _stream_handle(device)))
+    _launch(device, (_lib or load()).sv_rotary, _heads(x, dtype, device, d), _heads(out, dtype, device, d),
+            _attn_dtype(dtype), tokens, d, _vector(positions, tokens, device, "positions"),
+            _rope(freq, flags, mscale, device), _stream_handle(device))
     return out
 
 
@@ -737,12 +746,12 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
         elif q_out.shape != q.shape:
             raise SVError(f"q_out must be {tuple(q.shape)}")
         hq, ho = _heads(q, dtype, device, d), _heads(q_out, dtype, device, d)
-    _check((_lib or load()).sv_kv_append(
-        _heads(k, dtype, device, d), _heads(v, dtype, device, d),
+    _launch(
+        device, (_lib or load()).sv_kv_append, _heads(k, dtype, device, d), _heads(v, dtype, device, d),
         _paged(k_pages, v_pages, page_table, n, dtype, device, d), _attn_dtype(dtype), tokens, d, n,
         _vector(qo_indptr, n + 1, device, "qo_indptr"), _vector(kv_len, n, device, "kv_len"),
         _rope(freq, ROTARY_INTERLEAVED if interleaved else 0, mscale, device), hq, ho,
-        None if status is None else _vector(status, n, device, "status"), _stream_handle(device)))
+        None if status is None else _vector(status, n, device, "status"), _stream_handle(device))
     return q_out
 
 
@@ -781,10 +790,13 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     nbytes = attention_workspace_size(max_window, heads, cache.k.heads, d)
     if ws is None:
         ws = Workspace(q.device)
-    _check((_lib or load()).sv_paged_attention(
-        _heads(q, dtype, device, d), cache, _attn_dtype(dtype), tokens, d, n,
+    scratch = ws.address(nbytes)
+    if ws.buf.get_device() != device:
+        raise SVError(f"the workspace must live on cuda:{device}")
+    _launch(
+        device, (_lib or load()).sv_paged_attention, _heads(q, dtype, device, d), cache, _attn_dtype(dtype), tokens, d, n,
         _vector(qo_indptr, n + 1, device, "qo_indptr"), _vector(kv_len, n, device, "kv_len"), max_window,
         d ** -0.5 if scale is None else scale, window, ATTN_FULL if full else 0, _heads(out, dtype, device, d),
         None if norm is None else norm.data_ptr(), None if status is None else _vector(status, n, device, "status"),
-        ws.address(nbytes), nbytes, _stream_handle(device)))
+        scratch, nbytes, _stream_handle(device))
     return AttentionOut(out, norm)
