@@ -43,6 +43,24 @@ struct RowShape {
     };
 };
 
+// Where the count of windows that end before a token does not lead to the one
+// that holds it (tokens before the first window, broken windows): the first
+// request that is in order and holds token t, or n_req.  Says which are not.
+__device__ __noinline__ int look_through(const AttnArgs& a, int t)
+{
+    const long long room = (long long)a.cache.max_pages * a.cache.page_size;
+    int r = a.n_req;
+    for (int i = a.n_req - 1; i >= 0; --i) {
+        const int q0 = a.qo_indptr[i], q1 = a.qo_indptr[i + 1], n = a.kv_len[i];
+        if (q0 < 0 || q1 < q0 || q1 > a.tokens || q1 - q0 > a.max_window || n < 0 || n > room) {
+            if (a.status && threadIdx.x == 0) atomicOr(&a.status[i], kBadLayout);
+        } else if (q0 <= t && t < q1) {
+            r = i;
+        }
+    }
+    return r;
+}
+
 template <typename T, int kElems, int kRows>
 __global__ void __launch_bounds__(RowShape<T, kElems, kRows>::kWarps * 32, 1)
     attn_rows_kernel(const AttnArgs a)
@@ -60,14 +78,15 @@ __global__ void __launch_bounds__(RowShape<T, kElems, kRows>::kWarps * 32, 1)
     const int t = (int)(unit / per_token), g = (int)(unit % per_token / chunks);
     const int in_group = (int)(unit % chunks) * kRows, h0 = g * a.group + in_group;
     const int rows = min(kRows, a.group - in_group);
-    const int r = request_of_token(a.qo_indptr, a.n_req, t);
-    if (r >= a.n_req) return;                             // padding
-    const int q0 = a.qo_indptr[r], q1 = a.qo_indptr[r + 1], n = a.kv_len[r];
-    const bool bad = q0 < 0 || q0 > t || q1 > a.tokens || q1 - q0 > a.max_window || n < 0 ||
-                     (long long)n > (long long)a.cache.max_pages * a.cache.page_size;
-    if (bad) {
-        if (a.status && threadIdx.x == 0) atomicOr(&a.status[r], kBadLayout);
-        return;
+    const long long room = (long long)a.cache.max_pages * a.cache.page_size;
+    const int before = windows_before(a.qo_indptr, a.n_req, t);
+    if (before >= a.n_req) return;                        // padding
+    int r = before, n = a.kv_len[r], q1 = a.qo_indptr[r + 1];
+    if (!window_holds(a.qo_indptr, r, t, a.tokens, a.max_window) || n < 0 || n > room) {
+        r = look_through(a, t);
+        if (r >= a.n_req) return;                         // nobody's, or refused
+        n = a.kv_len[r];
+        q1 = a.qo_indptr[r + 1];
     }
     const long long pos = (long long)n - q1 + t;
     const int end = a.full ? n : (int)max(0ll, min((long long)n, pos + 1));

@@ -33,10 +33,18 @@ __device__ __forceinline__ __half from_f32<__half>(float x)
     return __float2half_rn(x);
 }
 
-// The number of windows that end at or before token t: the request that holds t, or n_req for
-// padding.  Called by every thread of the block (it holds block barriers), so
-// that the bounds are read side by side instead of one after the other.
-__device__ __forceinline__ int request_of_token(const int32_t* qo_indptr, int n_req, int t)
+// Request r's window, on the token axis and of up to `longest` tokens, holds token t.
+__device__ __forceinline__ bool window_holds(const int32_t* qo_indptr, int r, int t, int tokens, int longest)
+{
+    const int q0 = qo_indptr[r], q1 = qo_indptr[r + 1];
+    return q0 >= 0 && q0 <= t && t < q1 && q1 <= tokens && q1 - q0 <= longest;
+}
+
+// The number of windows that end at or before token t, which is the request that
+// holds it, if one does and the bounds only grow.  Called by every thread of the
+// block (it holds block barriers), so that the bounds are read side by side
+// instead of one after the other.
+__device__ __forceinline__ int windows_before(const int32_t* qo_indptr, int n_req, int t)
 {
     int r = 0;
     for (int i0 = 0; i0 < n_req; i0 += (int)blockDim.x) {
