@@ -495,8 +495,8 @@ sv_status_t sv_verify_chain_shard_merge(const void* records, int n_shards, int n
  *  - Request r's window is tokens qo_indptr[r] .. qo_indptr[r + 1] - 1 of the
  *    packed token axis (n_r of them, possibly none); tokens of no window
  *    (before qo_indptr[0], past qo_indptr[n_req]) are padding: neither read
- *    nor written.  kv_len[r] counts request r's cached tokens with the window appended, so token i of
- *    the window has position p = kv_len[r] - n_r + i.
+ *    nor written.  kv_len[r] counts request r's cached tokens with the window
+ *    appended, so token i of the window has position p = kv_len[r] - n_r + i.
  *  - status (device) int32 [n_req] or NULL: SV_ROW_* bits are OR-ed into it;
  *    the caller clears it.  SV_ROW_BAD_LAYOUT: a window outside the token
  *    axis or longer than promised, a kv_len outside what the page table

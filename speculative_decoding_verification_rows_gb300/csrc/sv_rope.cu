@@ -36,9 +36,9 @@ __device__ __forceinline__ float2 rotary_cs(int p, const float* freq, int m, flo
     const float hi = freq[2 * m], lo = freq[2 * m + 1];
     const float pf = (float)p;
     const float rest = (float)(int)((long long)p - (long long)pf);   // positions past 2^24: what the conversion lost
-    const float prod = pf * hi;
+    const float prod = __fmul_rn(pf, hi);   // rounded, here and where it is used: not to be fused with what follows
     const float err = __fmaf_rn(pf, hi, -prod);
-    float turns = (prod - rintf(prod)) + __fmaf_rn(pf, lo, __fmaf_rn(rest, hi, err));
+    float turns = __fsub_rn(prod, rintf(prod)) + __fmaf_rn(pf, lo, __fmaf_rn(rest, hi, err));
     if (inverse) turns = -turns;
     float s, c;
     sincospif(2.f * turns, &s, &c);
