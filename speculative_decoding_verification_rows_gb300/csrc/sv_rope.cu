@@ -18,7 +18,9 @@
 // off by p f 2^-24 turns (at p = 131,072 and f = 0.16: 1e-3).  With f = hi +
 // lo, p hi is split into its rounded product and the exact rest of it by an
 // fma, the whole turns of the product are taken off exactly, and the rest
-// terms are added to the fraction.
+// terms are added to the fraction.  Past 2^24 the rest terms reach tens of turns
+// and are split in the same way: four sums of numbers below 2, rounded to 2^-24
+// or less, are off by 2.4e-7 turns.
 #include <limits.h>
 
 #include "sv_attn.cuh"
@@ -35,10 +37,16 @@ __device__ __forceinline__ float2 rotary_cs(int p, const float* freq, int m, flo
 {
     const float hi = freq[2 * m], lo = freq[2 * m + 1];
     const float pf = (float)p;
-    const float rest = (float)(int)((long long)p - (long long)pf);   // positions past 2^24: what the conversion lost
     const float prod = __fmul_rn(pf, hi);   // rounded, here and where it is used: not to be fused with what follows
     const float err = __fmaf_rn(pf, hi, -prod);
-    float turns = __fsub_rn(prod, rintf(prod)) + __fmaf_rn(pf, lo, __fmaf_rn(rest, hi, err));
+    float rest = __fmaf_rn(pf, lo, err);
+    if (fabsf(pf) >= 16777216.f) {          // what was small is not: every part of the rest has whole turns of its own
+        const float lost = (float)(int)((long long)p - (long long)pf);   // by the conversion of p
+        const float a = __fmul_rn(lost, hi), b = __fmul_rn(pf, lo);
+        rest = __fsub_rn(err, rintf(err)) + __fsub_rn(a, rintf(a)) + __fsub_rn(b, rintf(b)) +
+               (__fmaf_rn(lost, hi, -a) + __fmaf_rn(pf, lo, -b) + lost * lo);
+    }
+    float turns = __fsub_rn(prod, rintf(prod)) + rest;
     if (inverse) turns = -turns;
     float s, c;
     sincospif(2.f * turns, &s, &c);
