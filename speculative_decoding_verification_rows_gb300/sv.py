@@ -711,7 +711,12 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
 def rotary(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, interleaved: bool = False,
            inverse: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """sv_rotary: x [tokens, heads, head_dim] rotated by positions int32 [tokens] (out may be x).  With
-    inverse=True it maps the gradient of the output to the gradient of the input."""
+    inverse=True it maps the gradient of the output to the gradient of the input.
+
+    The gradient reaches x through autograd where the call allocates its result; a call with out= records
+    nothing, and freq and mscale get no gradient."""
+    if out is None and x.requires_grad and torch.is_grad_enabled():
+        return _Rotary.apply(x, positions, freq, interleaved, inverse, mscale)
     tokens, _, d, dtype, device = _tokens_heads(x)
     if out is None:
         out = torch.empty_like(x)
@@ -724,6 +729,24 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, interle
     return out
 
 
+class _Rotary(torch.autograd.Function):
+    """The rotation in a graph: linear in x, its transpose is the inverse rotation with the same scale."""
+
+    @staticmethod
+    def forward(ctx, x, positions, freq, interleaved, inverse, mscale):
+        ctx.save_for_backward(positions, freq)
+        ctx.how = interleaved, inverse, mscale
+        return rotary(x, positions, freq, interleaved, inverse, mscale)
+
+    @staticmethod
+    def backward(ctx, dy):
+        positions, freq = ctx.saved_tensors
+        interleaved, inverse, mscale = ctx.how
+        if dy.stride(2) != 1:                       # a broadcast or transposed gradient
+            dy = dy.contiguous()
+        return rotary(dy, positions, freq, interleaved, not inverse, mscale), None, None, None, None, None
+
+
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
               page_table: torch.Tensor, qo_indptr: torch.Tensor, kv_len: torch.Tensor,
               freq: Optional[torch.Tensor] = None, interleaved: bool = False, mscale: float = 1.0,
@@ -731,7 +754,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
               status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """sv_kv_append: the windows' k (rotated, if freq is given) and v [tokens, heads, head_dim] into the cache
     [n_pages, page_size, heads, head_dim] at the end of each request's kv_len tokens.  With q its rotation is
-    returned (into q_out if given, which may be q)."""
+    returned (into q_out if given, which may be q).  Autograd records nothing of it."""
     tokens, _, d, dtype, device = _tokens_heads(k)
     n = kv_len.numel()
     if v.shape != k.shape:
@@ -778,7 +801,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                     status: Optional[torch.Tensor] = None, ws: Optional[Workspace] = None) -> AttentionOut:
     """sv_paged_attention: q [tokens, heads, head_dim], packed by qo_indptr, over the paged cache; no window is longer
     than max_window.  scale defaults to head_dim ** -0.5; window > 0 limits every row to its last `window` keys;
-    full=True drops the causal limit."""
+    full=True drops the causal limit.  Autograd records nothing of it: it has no gradient."""
     tokens, heads, d, dtype, device = _tokens_heads(q)
     n = kv_len.numel()
     if out is None:
