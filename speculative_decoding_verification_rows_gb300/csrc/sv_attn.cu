@@ -25,7 +25,7 @@ namespace {
 // Every access is one element wide, so that any stride, page size and head size
 // is served; instructions bound it.  64 single tokens over 4,224 keys, 32 heads
 // (4 a key head): fp32 heads of 128 0.48 ms (4.6 TB/s; 2.22 with a CTA a row and
-// a warp sum a key), bf16 heads of 96 0.50 (2.54), of 256 1.19 (5.1).  One token
+// a warp sum a key), bf16 heads of 96 0.48 (2.54), of 256 1.17 (5.1).  One token
 // over 131,072 keys, 8 heads of 256: 1.1 ms, 80 without the cluster and the
 // shared sums.  1,024 tokens over 2,048 keys, 16 fp32 heads of 64: 1.2 ms (4.9),
 // 6 TFLOP/s: prompts are the tensor-core kernel's business.

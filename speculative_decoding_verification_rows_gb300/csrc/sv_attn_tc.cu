@@ -30,12 +30,12 @@
 // while the weights are.
 //
 // What bounds it (one GB300).  Few rows: HBM.  4 requests x 8 tokens x 64 heads
-// over 65,536 to 131,072 keys read 1.64 GB in 243 us, 6.75 TB/s, the measured copy
+// over 65,536 to 131,072 keys read 1.64 GB in 242 us, 6.78 TB/s, the measured copy
 // bandwidth; 64 single tokens over 256 to 8,192 keys take 108 us for 0.61 GB (83%
 // of it: some 7 us of the call are its start and the join), 256 ragged windows
-// over 128 to 4,096 keys 220 us for 1.23 GB (82%).  Many rows: the chain scores,
+// over 128 to 4,096 keys 219 us for 1.23 GB (83%).  Many rows: the chain scores,
 // weights, P V, scores of a slot.  Chunks of 2,048 tokens over 8,192 and 16,384
-// keys take 0.52 ms (1,450 TFLOP/s, 76% of cuBLAS' burst rate) in a burst and
+// keys take 0.53 ms (1,430 TFLOP/s, 75% of cuBLAS' burst rate) in a burst and
 // 0.56 ms at the card's power limit.  Short items (ragged prompts under a sliding
 // window of 512, 52 us) are bound by latencies: start, the first instruction
 // fetches, a turn of the chain a tile.

@@ -7,9 +7,9 @@
 // a token has rot_dim / 2 angles but heads * rot_dim / 2 pairs, so a CTA takes
 // whole tokens, computes each angle of its tokens once into shared memory and
 // uses it for every head.  Measured on a GB300: 16,384 tokens x 40 heads x 128
-// bf16 rotated in 56 us (6.0 TB/s, 89% of the copy bandwidth); 12,200 tokens'
-// keys, values and queries (48 heads x 128, half of each rotated) placed in 52 us
-// (5.8 TB/s, 85%); a window of 8 tokens 2.8 us a call back to back.  Many small
+// bf16 rotated in 56 us (6.0 TB/s, 88% of the copy bandwidth); 12,200 tokens'
+// keys, values and queries (48 heads x 128, half of each rotated) placed in 53 us
+// (5.7 TB/s, 84%); a window of 8 tokens 2.8 us of GPU time.  Many small
 // CTAs hide their lookups and sines behind one another: reading ahead of them
 // within a thread cost registers, so occupancy, and was slower (65 us for 55 of
 // an earlier state), and so were 2 or 8 tokens a CTA.
