@@ -595,7 +595,8 @@ enum { SV_ATTN_FULL = 1 }; /* every row sees the whole cache (no causal limit), 
  *   Workspace: sv_attention_workspace_size(...).
  *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, q.heads not a
  *   multiple of the cache's heads, a scale that is not finite;
- *   SV_ERR_UNSUPPORTED for head_dim > 256.
+ *   SV_ERR_UNSUPPORTED for head_dim > 256 or more than 2^30 rows
+ *   (tokens x q.heads).
  */
 sv_status_t sv_paged_attention(sv_heads_t q, sv_paged_kv_t cache, sv_dtype_t dt, int tokens, int head_dim, int n_req,
                                const int32_t* qo_indptr, const int32_t* kv_len, int max_window, float scale,
