@@ -290,10 +290,9 @@ def _plain_select(state, case):
     n, beams, vocab, m = case["n"], case["beams"], case["vocab"], case["n_out"]
     x, c = state["logits"].double(), state["scores"].double()
     top = x.amax(-1, keepdim=True)
-    top = torch.where(top == -math.inf, 0.0, top)
-    lse = (top + (x - top).exp_().sum(-1, keepdim=True).log()).squeeze(-1)
-    base = torch.where(lse == -math.inf, -math.inf, c - lse)
-    x += base[..., None]
+    x -= torch.where(top == -math.inf, 0.0, top)
+    norm = x.exp().sum(-1).log()
+    x += torch.where(norm == -math.inf, -math.inf, c - norm)[..., None]
     if state["finished"] is not None:
         x.masked_fill_(state["finished"][..., None], -math.inf)
         x[..., state["end"]] = torch.where(state["finished"], c, x[..., state["end"]])
@@ -433,8 +432,9 @@ def _select64(state, case):
                 row[state["end"]] = c
             else:
                 l = state["logits"][i, b].double()
-                norm = float(torch.logsumexp(l, 0))
-                row = torch.full_like(l, -math.inf) if norm == -math.inf or c == -math.inf else l + (c - norm)
+                row = torch.full_like(l, -math.inf)
+                if c > -math.inf and float(l.max()) > -math.inf:
+                    row = torch.log_softmax(l, 0) + c
             rows.append(row)
         best, at = torch.cat(rows).sort(dim=-1, descending=True, stable=True)
         scores.append(best[:m])
