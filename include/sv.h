@@ -79,8 +79,9 @@ typedef enum {
     SV_ERR_UNSUPPORTED = 4  /* a size or layout the library does not handle         */
 } sv_status_t;
 
-/* SV_DTYPE_F16 is a type of the attention operators (sv_rotary, sv_kv_append,
- * sv_paged_attention); logits are bf16 or fp32. */
+/* SV_DTYPE_F16 is a type of the attention operators and the cache's pages
+ * (sv_rotary, sv_kv_append, sv_paged_attention, sv_kv_copy, sv_kv_compact); logits are
+ * bf16 or fp32. */
 typedef enum { SV_DTYPE_BF16 = 0, SV_DTYPE_F32 = 1, SV_DTYPE_F16 = 2 } sv_dtype_t;
 
 /* Per-position / per-row status bits. */
@@ -93,9 +94,10 @@ enum {
     SV_ROW_Q_ZERO = 32,      /* informational: q(d) == 0 at a tested position      */
     SV_ROW_RESID_ZERO = 64,  /* informational: empty residual, sampled from p      */
     SV_ROW_UNSUPPORTED = 128, /* combination the library refuses (sv_verify_*)  */
-    SV_ROW_TIMEOUT = 256      /* a bounded wait on a bulk copy gave up: rows of the
+    SV_ROW_TIMEOUT = 256,     /* a bounded wait on a bulk copy gave up: rows of the
                                  call were not processed (never seen in practice);
                                  of sv_paged_attention: results are right or NaN  */
+    SV_ROW_NO_PAGES = 512     /* sv_kv_fork: the pool has no pages for the request     */
 };
 #define SV_ROW_ERROR_MASK (SV_ROW_NONFINITE | SV_ROW_EMPTY | SV_ROW_BAD_TOKEN | SV_ROW_BAD_PARAM | \
                            SV_ROW_BAD_LAYOUT | SV_ROW_UNSUPPORTED | SV_ROW_TIMEOUT)
@@ -602,6 +604,160 @@ sv_status_t sv_paged_attention(sv_heads_t q, sv_paged_kv_t cache, sv_dtype_t dt,
                                const int32_t* qo_indptr, const int32_t* kv_len, int max_window, float scale,
                                int window_keys, int flags, sv_heads_t out, float* lse, int32_t* status, void* ws,
                                size_t ws_bytes, sv_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Beam search, and the cache's pages.  A search step scores every beam's
+ * continuations, selects the best of a request (sv_beam_select), and its
+ * beams' states and caches follow their parents (sv_beam_reorder, sv_kv_fork,
+ * sv_kv_copy).  Requests without beams use the page calls alone: room for the
+ * next window, pages of rejected tokens given back, accepted tokens moved
+ * together (sv_kv_compact).
+ */
+
+/* Workspace bytes of sv_beam_select; 0 for sizes it does not handle. */
+size_t sv_beam_workspace_size(int n, int beams, int vocab, int n_out);
+
+/*
+ * The n_out best continuations of every item (request) over its beams and the
+ * vocabulary.
+ *   logits   (device) bf16 or fp32; element (item, beam, token) at item *
+ *            stride_item + beam * stride_beam + token (strides in elements,
+ *            any alignment of the rows).
+ *   scores   (device) fp32 [n, beams]: the beams' scores c (log probabilities
+ *            so far).  -inf: the beam is dead, its row is not read.
+ *   finished (device) bytes [n, beams] or NULL: a beam that is marked has one
+ *            continuation, end_token with its score unchanged; its row is not
+ *            read.
+ *   A continuation's score is c - ln Z + (l - m), m = max l, Z = sum exp(l - m),
+ *   in 64 bits; -inf for tokens at -inf, for dead beams and for rows of nothing
+ *   but -inf.  The order is by score, descending, equal scores by beam and then
+ *   by token, ascending; it is that of the scores in 64 bits (errors of 1e-12),
+ *   and does not depend on timing.
+ *   out_tokens, out_parents (device) int32 [n, n_out]: the continuations' tokens
+ *   and beams, best first; out_scores (device) fp32 [n, n_out].
+ *   status   (device) int32 [n] or NULL, SV_ROW_* bits OR-ed in (the caller
+ *            clears it): SV_ROW_NONFINITE: NaN or +inf logit in a row that is
+ *            read; SV_ROW_BAD_PARAM: NaN or +inf score.  Such an item gets
+ *            tokens and parents of -1 and scores of NaN.
+ *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, n_out > beams * vocab,
+ *   an end_token outside the vocabulary where finished is given;
+ *   SV_ERR_UNSUPPORTED for more than 128 beams, n_out > 256, a vocabulary above
+ *   524,288, more than 2^22 rows.  Workspace: sv_beam_workspace_size(...).
+ */
+sv_status_t sv_beam_select(const void* logits, sv_dtype_t dt, int64_t stride_item, int64_t stride_beam, int n, int beams,
+                           int vocab, const float* scores, const uint8_t* finished, int end_token, int n_out,
+                           int32_t* out_tokens, int32_t* out_parents, float* out_scores, int32_t* status, void* ws,
+                           size_t ws_bytes, sv_stream_t stream);
+
+/*
+ * Rows follow their parents: row j of item i of dst becomes row parents[i][j]
+ * of item i of src.  Rows are row_bytes bytes, strides are in bytes.  dst may
+ * be src itself (the same strides, beams_in == beams_out): every row then
+ * becomes its parent's as it was before the call; otherwise the two must not
+ * overlap.
+ *   parents (device) int32 [n, beams_out]; one outside [0, beams_in) leaves its
+ *   row of dst as it is and sets SV_ROW_BAD_LAYOUT in status (device) int32 [n]
+ *   or NULL.
+ *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, different strides or
+ *   beams in place; SV_ERR_UNSUPPORTED for more than 65,535 items, 128 beams or
+ *   rows above 2^36 bytes.
+ */
+sv_status_t sv_beam_reorder(const void* src, int64_t src_stride_item, int64_t src_stride_beam, void* dst,
+                            int64_t dst_stride_item, int64_t dst_stride_beam, int64_t row_bytes, int n, int beams_in,
+                            int beams_out, const int32_t* parents, int32_t* status, sv_stream_t stream);
+
+/*
+ * Who holds which pages of a paged cache.  All of it is the caller's device
+ * memory; layers share one table.  Request r holds held[r] pages, the first
+ * columns of its row of page_table; ref_count[p] counts the holders of page p
+ * (those of the table, and whatever else the caller counts, such as a cache of
+ * prefixes).  A page without holders is free.
+ */
+typedef struct {
+    int32_t* page_table; /* [n_req, ld_table] */
+    int32_t* held;       /* [n_req]           */
+    int32_t* ref_count;  /* [n_pages]         */
+    int32_t ld_table, max_pages;
+    int32_t n_req, n_pages, page_size;
+} sv_page_pool_t;
+
+/* Workspace bytes of sv_kv_fork; 0 for sizes it does not handle. */
+size_t sv_kv_fork_workspace_size(int n_req, int max_pages, int n_pages);
+
+/*
+ * One step of every request's pages: request r takes the pages of the first
+ * keep_len[r] tokens of request parent[r], and gets room for new_len[r] tokens.
+ * With parent NULL requests keep their own: new_len = keep_len gives the rest
+ * back, new_len = 0 everything.  All requests move at once: parents are as they
+ * were before the call.
+ *   parent (device) int32 [n_req] or NULL; with group > 0 it numbers requests
+ *   within r's group of `group` consecutive ones (the beams of one search).
+ *   Whole pages that are kept are shared with whoever else holds them.  A begun
+ *   page (keep_len inside it) that is written on, as new_len > keep_len says,
+ *   must have one holder: where all of its holders after the call are requests
+ *   of the call that write on it, the one with the largest keep_len (the lowest
+ *   of equals) keeps it; every other writer gets a new page instead, and
+ *   copies[r] = {page, new page, tokens}, which sv_kv_copy carries out, for
+ *   every layer before anything is appended.  Requests without such a copy get
+ *   {-1, -1, -1}.
+ *   New pages are the lowest free numbers, in order of request and of column (a
+ *   copy's first); pages given back by the call are free for it.  A request
+ *   whose pages, counted after those of all requests before it, exceed the free
+ *   ones gets none: it holds the pages of keep_len tokens, nothing is copied for
+ *   it, and status gets SV_ROW_NO_PAGES.
+ *   A request with keep_len outside [0, held[parent] * page_size], new_len
+ *   outside [keep_len, max_pages * page_size], a parent outside its range or a
+ *   held count outside [0, max_pages] keeps what it holds and gets
+ *   SV_ROW_BAD_LAYOUT; so does a request with a page number outside the pool
+ *   among the pages it takes or gives back (such numbers are passed on, and not
+ *   counted).
+ *   Written: page_table (the columns that change; those past what a request
+ *   holds are left as they are), held, ref_count, copies (device) int32
+ *   [n_req][3]; status (device) int32 [n_req] or NULL, bits OR-ed in.
+ *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes; SV_ERR_UNSUPPORTED for
+ *   n_req > 65,536, n_pages or n_req * max_pages > 2^30.  Workspace:
+ *   sv_kv_fork_workspace_size(...).
+ */
+sv_status_t sv_kv_fork(sv_page_pool_t pool, const int32_t* parent, int group, const int32_t* keep_len,
+                       const int32_t* new_len, int32_t* copies, int32_t* status, void* ws, size_t ws_bytes,
+                       sv_stream_t stream);
+
+/*
+ * Copies of pages: the first copies[i][2] tokens of page copies[i][0] to page
+ * copies[i][1], keys and values, in every layer.  copies (device) int32
+ * [n_copies][3]; an entry with a negative page is left out.  A page that is
+ * copied to must not stand in another entry.  Of `cache` the page table is not
+ * used.  Layer y of the cache lies y * stride_layer elements after the first.
+ *   status (device) int32 [1] or NULL: SV_ROW_BAD_LAYOUT where an entry has a
+ *   page outside the cache, or tokens outside [0, page_size] (nothing is copied
+ *   for it).
+ *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, head counts that
+ *   differ; SV_ERR_UNSUPPORTED for more than 32,767 layers, tokens of more than
+ *   2^19 elements or pages of more than 2^30.
+ */
+sv_status_t sv_kv_copy(sv_paged_kv_t cache, sv_dtype_t dt, int head_dim, int layers, int64_t stride_layer_k,
+                       int64_t stride_layer_v, const int32_t* copies, int n_copies, int32_t* status,
+                       sv_stream_t stream);
+
+/*
+ * Kept tokens move together: token first[r] + keep[r][j] of request r becomes
+ * token first[r] + j, for j < n_keep[r], keys and values in every layer, in
+ * place.  The accepted path of a tree of drafts moves to the front of its
+ * window; a context from which tokens are evicted closes its gaps.  Keys keep
+ * the rotation they were appended with.
+ *   keep (device) int32 [n_req, ld_keep], ascending in each row; n_keep (device)
+ *   int32 [n_req]; first (device) int32 [n_req] or NULL (0).  The pages that
+ *   tokens move to must be the request's own (sv_kv_fork gives the rest back:
+ *   keep_len = first + n_keep).
+ *   status (device) int32 [n_req] or NULL: SV_ROW_BAD_LAYOUT for n_keep outside
+ *   [0, max_keep], a first below 0, an order that does not ascend, a token past
+ *   the page table, a page outside the cache.
+ *   Errors: as sv_kv_copy; SV_ERR_UNSUPPORTED for n_req > 65,536 too.
+ */
+sv_status_t sv_kv_compact(sv_paged_kv_t cache, sv_dtype_t dt, int head_dim, int layers, int64_t stride_layer_k,
+                          int64_t stride_layer_v, int n_req, const int32_t* first, const int32_t* keep, int ld_keep,
+                          int max_keep, const int32_t* n_keep, int32_t* status, sv_stream_t stream);
 
 /*
  * Measurement aid (not part of the method): when both are non-NULL, every

@@ -1,0 +1,1017 @@
+// sv_beam.cu -- beam search: the best continuations over beams and vocabulary,
+// and state rows that follow their beams' parents.
+//
+// Selection.  score(b, v) = base_b + (l_{b,v} - m_b), m_b the row's maximum,
+// base_b = c_b - ln sum exp(l - m_b).  What a call has to read is every live row
+// once; the rest is small.  So one kernel streams the rows (scan_kernel): a warp takes 4 KB
+// chunks, sums exp(l - ref) in fp32 against a running reference and leaves the
+// maximum of every 512-byte group.  The n_out best candidates lie in the n_out
+// best groups: a group that n_out others stand before (by maximum, then by
+// place) has n_out elements before each of its own.  A second kernel
+// (pick_kernel, a CTA an item) bounds the n_out-th best group's score from
+// below, reads again the few groups that reach the bound and sorts the
+// elements that do.
+//
+// Order.  Within a beam it is the logits' and exact.  Between beams it hangs on
+// the difference of two normalisers, and fp32 sums are off by up to kSumEps
+// (derived below), while candidates of a batch come nearer than that now and
+// then.  Where two neighbours of different beams do, at or before the last
+// selected place, the rows of both are summed again (refine_kernel), terms
+// in double-float arithmetic, the sum in whole numbers, and the item's saved
+// candidates are sorted once more: the order is then that of scores in 64 bits,
+// rows of the same values have the same sum in whatever order, and ties go to
+// the lowest place.
+#include <float.h>
+#include <math.h>
+
+#include "sv_attn.cuh"
+#include "sv_internal.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kMaxBeams = 128;
+constexpr int kMaxOut = 256;
+constexpr int kBeamMaxVocab = 1 << 19;
+constexpr int kScanThreads = 256;
+constexpr int kVecs = 8;                     // 16-byte vectors a lane takes of a chunk: a group each
+constexpr int kMaxSegChunks = 8;             // chunks a warp sums up before it leaves a partial sum
+constexpr int kPickThreads = 512;
+constexpr int kListCap = 2048;               // groups, and elements, that an item may have at its bound
+constexpr int kRefineElems = 4096;           // elements of a row a CTA of refine_kernel sums
+
+// |ln sum exp(l - m) - computed| of one row, V <= 2^19.  With p the row's probabilities, sum
+// p |l - m| = H - ln Z <= ln V <= 13.2, so an argument's relative error r costs
+// 13.2 r.  Differences to the reference and their product with log2 e: 2^-24 +
+// 2^-24 + 2^-26 -> 1.8e-6; ex2.approx 2^-22 for the term, for up to kMaxSegChunks
+// moves of the reference and for joining the partial sums: 10 (2^-22 + 2^-24) ->
+// 3.0e-6; sums by trees of 8 levels in a chunk, 8 chunks, 5 shuffles, 8 + 5
+// levels of partial sums: 34 2^-24 -> 2.0e-6; logf: an ulp of 13.2, 9.6e-7.
+constexpr double kSumEps = 8e-6;
+
+enum { kDead = 0, kLive = 1, kFinished = 2 };
+
+struct BeamArgs {
+    const void* logits;
+    int64_t stride_item, stride_beam;
+    int n, beams, vocab, n_out, end_token;
+    const float* scores;
+    const uint8_t* finished;
+    int32_t* out_tokens;
+    int32_t* out_parents;
+    float* out_scores;
+    int32_t* status;
+    // workspace
+    int32_t* n_flagged;      // rows to be summed again
+    int32_t* item_units;     // refine units of an item
+    int32_t* item_done;
+    int32_t* item_list;      // candidates saved, or -1: more than a list holds
+    uint32_t* item_mask;     // [n][4] beams that are summed again
+    int32_t* flagged;        // [rows]
+    float* row_max;          // [rows]
+    double* base;            // [rows]
+    float2* sums;            // [rows][segs] reference, sum
+    float* group_max;        // [rows][groups]
+    float* list_logit;       // [n][kListCap]
+    int32_t* list_flat;
+    ulonglong2* refined;     // [rows][refine segments] sums in units of 2^-26 and of 2^-58
+    int chunks, seg_chunks, segs, groups, refine_segs;
+};
+
+// What the rows' element type says about their layout in 16-byte vectors.
+template <int DT>
+struct Elem {
+    static constexpr int kSize = DT == 0 ? 2 : 4;
+    static constexpr int kPerVec = 16 / kSize;
+    static constexpr int kGroup = 32 * kPerVec;
+    static constexpr int kChunk = kVecs * kGroup;
+};
+
+// A row as vectors that start on 16-byte boundaries: element e is slot e + off.
+template <int DT>
+struct Row {
+    const char* base;
+    int off;
+    int vocab;
+    __device__ Row(const BeamArgs& a, int item, int beam)
+    {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(a.logits) +
+                            (uintptr_t)((item * a.stride_item + beam * a.stride_beam) * Elem<DT>::kSize);
+        off = (int)(p & 15u) / Elem<DT>::kSize;
+        base = reinterpret_cast<const char*>(p & ~(uintptr_t)15u);
+        vocab = a.vocab;
+    }
+    __device__ __forceinline__ uint4 whole(int vec) const
+    {
+        uint4 r;
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                     : "l"(base + (size_t)vec * 16));
+        return r;
+    }
+    // Element e as raw bits, -inf outside the row.
+    __device__ __forceinline__ uint32_t bits(int e) const
+    {
+        if (e < 0 || e >= vocab) return DT == 0 ? 0xFF80u : 0xFF800000u;
+        if (DT == 0) return reinterpret_cast<const uint16_t*>(base)[e + off];
+        return reinterpret_cast<const uint32_t*>(base)[e + off];
+    }
+    __device__ __forceinline__ uint4 vec(int v) const
+    {
+        const int e0 = v * Elem<DT>::kPerVec - off;
+        if (e0 >= 0 && e0 + Elem<DT>::kPerVec <= vocab) return whole(v);
+        if (DT == 0)
+            return make_uint4(bits(e0) | bits(e0 + 1) << 16, bits(e0 + 2) | bits(e0 + 3) << 16,
+                              bits(e0 + 4) | bits(e0 + 5) << 16, bits(e0 + 6) | bits(e0 + 7) << 16);
+        return make_uint4(bits(e0), bits(e0 + 1), bits(e0 + 2), bits(e0 + 3));
+    }
+    __device__ __forceinline__ float elem(int e) const
+    {
+        return __uint_as_float(DT == 0 ? bits(e) << 16 : bits(e));
+    }
+};
+
+// Element q of a vector, q known at compile time.
+template <int DT>
+__device__ __forceinline__ float vec_at(const uint4& v, int q)
+{
+    const int j = DT == 0 ? q >> 1 : q;
+    const uint32_t w = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+    if (DT == 0) return __uint_as_float((q & 1) ? (w & 0xFFFF0000u) : (w << 16));
+    return __uint_as_float(w);
+}
+
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float warp_max_nan(float x)
+{
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ float vec_max(const uint4& v)
+{
+    if (DT == 0) {
+        const uint32_t w = max2_nan(max2_nan(v.x, v.y), max2_nan(v.z, v.w));
+        return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+
+using pair_t = unsigned long long;   // two fp32 numbers, for the packed instructions
+__device__ __forceinline__ pair_t pack(float lo, float hi)
+{
+    pair_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack(pair_t p, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// exp(x - ref) of two elements.
+__device__ __forceinline__ pair_t exp_pair(float x0, float x1, pair_t minus_ref)
+{
+    const pair_t y = mul2(add2(pack(x0, x1), minus_ref), pack(kLog2e, kLog2e));
+    float y0, y1;
+    unpack(y, y0, y1);
+    return pack(exp2_approx(y0), exp2_approx(y1));
+}
+template <int DT>
+__device__ __forceinline__ pair_t vec_exp_sum(const uint4& v, pair_t minus_ref)
+{
+    const pair_t s = add2(exp_pair(vec_at<DT>(v, 0), vec_at<DT>(v, 1), minus_ref),
+                          exp_pair(vec_at<DT>(v, 2), vec_at<DT>(v, 3), minus_ref));
+    if (DT != 0) return s;
+    return add2(s, add2(exp_pair(vec_at<DT>(v, 4 % Elem<DT>::kPerVec), vec_at<DT>(v, 5 % Elem<DT>::kPerVec), minus_ref),
+                        exp_pair(vec_at<DT>(v, 6 % Elem<DT>::kPerVec), vec_at<DT>(v, 7 % Elem<DT>::kPerVec), minus_ref)));
+}
+
+__device__ __forceinline__ int beam_kind(const BeamArgs& a, int row, float* score)
+{
+    *score = a.scores[row];
+    if (*score == -INFINITY) return kDead;
+    return a.finished && a.finished[row] ? kFinished : kLive;
+}
+
+// Rows as streams: the unit is a segment of a row, a warp each.
+template <int DT>
+__global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_constant__ BeamArgs a)
+{
+    using E = Elem<DT>;
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *a.n_flagged = 0;
+        for (int i = threadIdx.x; i < a.n; i += kScanThreads) a.item_done[i] = 0;
+    }
+    const long long units = (long long)a.n * a.beams * a.segs;
+    const long long warps = (long long)gridDim.x * (kScanThreads / 32);
+    for (long long u = (long long)blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+        const int row_no = (int)(u / a.segs), seg = (int)(u - (long long)row_no * a.segs);
+        float score;
+        if (beam_kind(a, row_no, &score) != kLive) continue;
+        const Row<DT> row(a, row_no / a.beams, row_no % a.beams);
+        const int c1 = min((seg + 1) * a.seg_chunks, a.chunks);
+        float ref = -FLT_MAX, s_hi = 0.f, s_lo = 0.f;
+        for (int c = seg * a.seg_chunks; c < c1; ++c) {
+            uint4 v[kVecs];
+            const int v0 = c * (kVecs * 32) + lane;
+            if (c * E::kChunk - row.off >= 0 && (c + 1) * E::kChunk - row.off <= a.vocab) {
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) v[i] = row.whole(v0 + i * 32);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) v[i] = row.vec(v0 + i * 32);
+            }
+            float top = -INFINITY, mine = 0.f;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const float m = warp_max_nan(vec_max<DT>(v[i]));
+                top = max_nan(top, m);
+                if (lane == i) mine = m;
+            }
+            if (lane < kVecs) a.group_max[(size_t)row_no * a.groups + c * kVecs + lane] = mine;
+            if (top > ref) {
+                const float f = exp2_approx((ref - top) * kLog2e);
+                s_hi *= f;
+                s_lo *= f;
+                ref = top;
+            }
+            const pair_t minus_ref = pack(-ref, -ref);
+            pair_t t0 = vec_exp_sum<DT>(v[0], minus_ref), t1 = vec_exp_sum<DT>(v[1], minus_ref);
+#pragma unroll
+            for (int i = 2; i < kVecs; i += 2) {
+                t0 = add2(t0, vec_exp_sum<DT>(v[i], minus_ref));
+                t1 = add2(t1, vec_exp_sum<DT>(v[i + 1], minus_ref));
+            }
+            float x0, x1;
+            unpack(add2(t0, t1), x0, x1);
+            const dfloat s = df_two_sum(s_hi, x0 + x1);
+            s_hi = s.hi;
+            s_lo += s.lo;
+        }
+        float s = s_hi + s_lo;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (lane == 0) a.sums[(size_t)row_no * a.segs + seg] = make_float2(ref, s);
+    }
+}
+
+// The order of scores in 64 bits as that of unsigned numbers; -0 and +0 are one.
+__device__ __forceinline__ unsigned long long key_of_f64(double x)
+{
+    const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
+    return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double f64_of_key(unsigned long long k)
+{
+    return __longlong_as_double((long long)((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
+}
+
+// Candidates of an item in shared memory.
+struct Entries {
+    unsigned long long* key;
+    uint32_t* flat;     // beam * vocab + token
+    float* logit;
+};
+
+// Descending by score, ascending by place among equals (bitonic; the places are distinct).
+__device__ void sort_entries(const Entries& e, int n)
+{
+    int p = 1;
+    while (p < n) p <<= 1;
+    for (int i = n + threadIdx.x; i < p; i += blockDim.x) {
+        e.key[i] = 0ull;
+        e.flat[i] = 0xFFFFFFFFu;
+        e.logit[i] = -INFINITY;
+    }
+    __syncthreads();
+    for (int size = 2; size <= p; size <<= 1) {
+        for (int stride = size >> 1; stride; stride >>= 1) {
+            for (int t = threadIdx.x; t < (p >> 1); t += blockDim.x) {
+                const int i = 2 * t - (t & (stride - 1)), j = i + stride;
+                const bool down = (i & size) == 0;
+                const unsigned long long ki = e.key[i], kj = e.key[j];
+                const uint32_t fi = e.flat[i], fj = e.flat[j];
+                const bool before = ki > kj || (ki == kj && fi < fj);   // i stands before j
+                if (before != down) {
+                    const float li = e.logit[i];
+                    e.key[i] = kj;
+                    e.key[j] = ki;
+                    e.flat[i] = fj;
+                    e.flat[j] = fi;
+                    e.logit[i] = e.logit[j];
+                    e.logit[j] = li;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// The item's outputs from its sorted finite candidates.  Where they are fewer
+// than n_out, the places of score -inf follow from the lowest on; they are
+// among the first n_out places, since fewer than n_out are not -inf.
+template <int DT>
+__device__ void write_item(const BeamArgs& a, int item, const Entries& e, int n, const int* kind, int* scratch)
+{
+    const int tid = threadIdx.x;
+    if (tid < a.n_out && tid < n) {
+        const size_t o = (size_t)item * a.n_out + tid;
+        const int b = (int)(e.flat[tid] / (uint32_t)a.vocab);
+        a.out_tokens[o] = (int)(e.flat[tid] - (uint32_t)b * (uint32_t)a.vocab);
+        a.out_parents[o] = b;
+        a.out_scores[o] = (float)f64_of_key(e.key[tid]);
+    }
+    if (n >= a.n_out) return;
+    int empty = 0, b = 0, t = 0;
+    if (tid < a.n_out) {
+        b = tid / a.vocab;
+        t = tid - b * a.vocab;
+        if (kind[b] == kDead) empty = 1;
+        else if (kind[b] == kFinished) empty = t != a.end_token;
+        else empty = Row<DT>(a, item, b).elem(t) == -INFINITY;
+        scratch[tid] = empty;
+    }
+    __syncthreads();
+    if (empty) {
+        int at = n;
+        for (int i = 0; i < tid; ++i) at += scratch[i];
+        if (at < a.n_out) {
+            const size_t o = (size_t)item * a.n_out + at;
+            a.out_tokens[o] = t;
+            a.out_parents[o] = b;
+            a.out_scores[o] = -INFINITY;
+        }
+    }
+}
+
+struct PickShared {
+    unsigned long long key[kListCap];
+    uint32_t flat[kListCap];
+    float logit[kListCap];
+    int group[kListCap];
+    double base[kMaxBeams];
+    float base32[kMaxBeams];
+    float top[kMaxBeams];
+    int kind[kMaxBeams];
+    int scratch[kMaxOut];
+    uint32_t mask[4];
+    int n_groups, n_elems, bad, flag_at;
+};
+
+// A score in fp32 (a finite one stays finite), and how far it may be from the
+// one in 64 bits with the row's true sum.
+__device__ __forceinline__ float score32(const PickShared& sh, int b, float l)
+{
+    return l == -INFINITY ? l : fmaxf(sh.base32[b] + (l - sh.top[b]), -FLT_MAX);
+}
+__device__ __forceinline__ float slack32(const PickShared& sh, int b, float l)
+{
+    return (float)kSumEps + 0x1p-22f * (fabsf(sh.base32[b]) + fabsf(l - sh.top[b]));
+}
+__device__ __forceinline__ unsigned long long score_key(const PickShared& sh, int b, float l)
+{
+    return key_of_f64(sh.base[b] + ((double)l - (double)sh.top[b]));
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ BeamArgs a)
+{
+    __shared__ PickShared sh;
+    pdl_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int item = blockIdx.x, row0 = item * a.beams;
+    if (tid == 0) sh.n_groups = sh.n_elems = sh.bad = 0;
+    if (tid < 4) sh.mask[tid] = 0u;
+    __syncthreads();
+    // normalisers, a warp a beam
+    for (int b = warp; b < a.beams; b += kPickThreads / 32) {
+        float score;
+        int kind = beam_kind(a, row0 + b, &score);
+        double base = (double)score;
+        float top = 0.f;
+        if (!(score < INFINITY)) {
+            if (lane == 0) atomicOr(&sh.bad, kBadParam);
+            kind = kDead;
+        }
+        if (kind == kLive) {
+            const float2* sums = a.sums + (size_t)(row0 + b) * a.segs;
+            float m = -FLT_MAX;
+            for (int i = lane; i < a.segs; i += 32) m = fmaxf(m, sums[i].x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            float s = 0.f;
+            for (int i = lane; i < a.segs; i += 32) s += sums[i].y * exp2_approx((sums[i].x - m) * kLog2e);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            if (s == 0.f) kind = kDead;                           // nothing but -inf: every score is -inf
+            base = (double)score - (double)logf(s);
+            top = m;
+        }
+        if (lane == 0) {
+            sh.kind[b] = kind;
+            sh.base[b] = base;
+            sh.base32[b] = (float)base;
+            sh.top[b] = top;
+            a.base[row0 + b] = base;
+            a.row_max[row0 + b] = top;
+        }
+    }
+    __syncthreads();
+    // A lower bound on the n_out-th best group's score: the n_out-th largest of the threads' best.
+    float best = -INFINITY;
+    const int total = a.beams * a.groups;
+    for (int i = tid; i < total; i += kPickThreads) {
+        const int b = i / a.groups;
+        if (sh.kind[b] != kLive) continue;
+        const float m = a.group_max[(size_t)row0 * a.groups + i];
+        if (!(m < INFINITY)) atomicOr(&sh.bad, kNonfinite);
+        const float s = score32(sh, b, m);
+        if (s > -INFINITY) best = fmaxf(best, s - slack32(sh, b, m));
+    }
+    if (tid < a.beams && sh.kind[tid] == kFinished) best = fmaxf(best, sh.base32[tid]);
+    const uint32_t mine = key_of_f32_bits(__float_as_uint(best));
+    uint32_t bound_key = 0u;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t tv = bound_key | (1u << bit);
+        if (__syncthreads_count(mine >= tv) >= a.n_out) bound_key = tv;
+    }
+    const float bound = bound_key <= key_of_f32_bits(0xFF800000u) ? -FLT_MAX : f32_of_key(bound_key);
+    if (sh.bad) {                                                 // (its last write is before the barriers above)
+        if (tid < a.n_out) {
+            const size_t o = (size_t)item * a.n_out + tid;
+            a.out_tokens[o] = a.out_parents[o] = -1;
+            a.out_scores[o] = __int_as_float(0x7FC00000);
+        }
+        if (tid == 0 && a.status) atomicOr(&a.status[item], sh.bad);
+        return;
+    }
+    // the groups that may reach it
+    for (int i = tid; i < total; i += kPickThreads) {
+        const int b = i / a.groups;
+        if (sh.kind[b] != kLive) continue;
+        const float m = a.group_max[(size_t)row0 * a.groups + i];
+        const float s = score32(sh, b, m);
+        if (s > -INFINITY && s + slack32(sh, b, m) >= bound) {
+            const int at = atomicAdd(&sh.n_groups, 1);
+            if (at < kListCap) sh.group[at] = i;
+        }
+    }
+    if (tid < a.beams && sh.kind[tid] == kFinished && sh.base32[tid] >= bound) {   // one candidate: base alone
+        const int at = atomicAdd(&sh.n_elems, 1);
+        sh.flat[at] = (uint32_t)tid * (uint32_t)a.vocab + (uint32_t)a.end_token;
+        sh.logit[at] = 0.f;
+    }
+    __syncthreads();
+    bool hard = sh.n_groups > kListCap;
+    if (!hard) {
+        for (int g = warp; g < sh.n_groups; g += kPickThreads / 32) {
+            const int b = sh.group[g] / a.groups, vec = (sh.group[g] - b * a.groups) * 32 + lane;
+            const Row<DT> row(a, item, b);
+            const uint4 v = row.vec(vec);
+#pragma unroll
+            for (int q = 0; q < Elem<DT>::kPerVec; ++q) {
+                const float l = vec_at<DT>(v, q);
+                const float s = score32(sh, b, l);
+                if (s > -INFINITY && s + slack32(sh, b, l) >= bound) {
+                    const int at = atomicAdd(&sh.n_elems, 1);
+                    if (at < kListCap) {
+                        sh.flat[at] = (uint32_t)b * (uint32_t)a.vocab + (uint32_t)(vec * Elem<DT>::kPerVec + q - row.off);
+                        sh.logit[at] = l;
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int n = sh.n_elems;
+    hard = hard || n > kListCap;
+    const Entries e{sh.key, sh.flat, sh.logit};
+    if (!hard) {
+        for (int i = tid; i < n; i += kPickThreads)
+            sh.key[i] = score_key(sh, (int)(sh.flat[i] / (uint32_t)a.vocab), sh.logit[i]);
+        sort_entries(e, n);
+        // neighbours of two beams that the normalisers' errors may have put the wrong way round
+        for (int i = tid; i + 1 < n && i < a.n_out; i += kPickThreads) {
+            const int b0 = (int)(sh.flat[i] / (uint32_t)a.vocab), b1 = (int)(sh.flat[i + 1] / (uint32_t)a.vocab);
+            if (b0 == b1) continue;
+            const double e0 = sh.kind[b0] == kLive ? kSumEps : 0.0, e1 = sh.kind[b1] == kLive ? kSumEps : 0.0;
+            const double l0 = (double)sh.logit[i] - (double)sh.top[b0], l1 = (double)sh.logit[i + 1] - (double)sh.top[b1];
+            const double lo0 = (sh.base[b0] - e0) + l0, hi0 = (sh.base[b0] + e0) + l0;
+            const double lo1 = (sh.base[b1] - e1) + l1, hi1 = (sh.base[b1] + e1) + l1;
+            if (hi1 < lo0 || (lo0 == hi0 && lo1 == hi1)) continue;
+            if (sh.kind[b0] == kLive) atomicOr(&sh.mask[b0 >> 5], 1u << (b0 & 31));
+            if (sh.kind[b1] == kLive) atomicOr(&sh.mask[b1 >> 5], 1u << (b1 & 31));
+        }
+    } else if (tid < a.beams && sh.kind[tid] == kLive) {
+        atomicOr(&sh.mask[tid >> 5], 1u << (tid & 31));
+    }
+    __syncthreads();
+    const int again = __popc(sh.mask[0]) + __popc(sh.mask[1]) + __popc(sh.mask[2]) + __popc(sh.mask[3]);
+    if (again == 0) {
+        write_item<DT>(a, item, e, n, sh.kind, sh.scratch);
+        return;
+    }
+    // refine_kernel finishes the item
+    if (!hard)
+        for (int i = tid; i < n; i += kPickThreads) {
+            a.list_flat[(size_t)item * kListCap + i] = (int32_t)sh.flat[i];
+            a.list_logit[(size_t)item * kListCap + i] = sh.logit[i];
+        }
+    if (tid < 4) a.item_mask[item * 4 + tid] = sh.mask[tid];
+    if (tid == 0) {
+        a.item_list[item] = hard ? -1 : n;
+        a.item_units[item] = again * a.refine_segs;
+        sh.flag_at = atomicAdd(a.n_flagged, again);
+    }
+    __syncthreads();
+    if (tid < a.beams && (sh.mask[tid >> 5] >> (tid & 31) & 1u)) {
+        int at = sh.flag_at;
+        for (int w = 0; w < tid >> 5; ++w) at += __popc(sh.mask[w]);
+        at += __popc(sh.mask[tid >> 5] & ((1u << (tid & 31)) - 1u));
+        a.flagged[at] = row0 + tid;
+    }
+}
+
+// The best candidate below `key`, `place` (the previous one's) over the block: every thread brings its own best.
+__device__ void block_best(unsigned long long& key, uint32_t& place, unsigned long long* s_key, uint32_t* s_place)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto take = [&](unsigned long long k, uint32_t p) {
+        if (k > key || (k == key && p < place)) {
+            key = k;
+            place = p;
+        }
+    };
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const unsigned long long k = __shfl_xor_sync(0xFFFFFFFFu, key, o);
+        const uint32_t p = __shfl_xor_sync(0xFFFFFFFFu, place, o);
+        take(k, p);
+    }
+    __syncthreads();
+    if (lane == 0) {
+        s_key[warp] = key;
+        s_place[warp] = place;
+    }
+    __syncthreads();
+    for (int w = 0; w < kPickThreads / 32; ++w) take(s_key[w], s_place[w]);
+}
+
+// An item with more candidates at its bound than a list holds (rows of few
+// distinct values): its n_out best groups one after the other, then the n_out
+// best of their elements.  Returns how many there are.
+template <int DT>
+__device__ int pick_by_turns(const BeamArgs& a, int item, PickShared& sh)
+{
+    __shared__ unsigned long long s_key[kPickThreads / 32];
+    __shared__ uint32_t s_place[kPickThreads / 32];
+    const int tid = threadIdx.x, row0 = item * a.beams;
+    unsigned long long last_key = ~0ull;
+    uint32_t last = 0u;
+    int n_groups = 0;
+    const int total = a.beams * a.groups;
+    for (; n_groups < a.n_out; ++n_groups) {
+        unsigned long long key = 0ull;
+        uint32_t place = 0xFFFFFFFFu;
+        for (int i = tid; i < total; i += kPickThreads) {
+            const int b = i / a.groups;
+            float m;
+            if (sh.kind[b] == kLive) m = a.group_max[(size_t)row0 * a.groups + i];
+            else if (sh.kind[b] == kFinished && i == b * a.groups) m = 0.f;
+            else continue;
+            if (m == -INFINITY) continue;
+            const unsigned long long k = score_key(sh, b, m);
+            if (!(k < last_key || (k == last_key && (uint32_t)i > last))) continue;
+            if (k > key || (k == key && (uint32_t)i < place)) {
+                key = k;
+                place = (uint32_t)i;
+            }
+        }
+        block_best(key, place, s_key, s_place);
+        if (place == 0xFFFFFFFFu) break;
+        if (tid == 0) sh.group[n_groups] = (int)place;
+        last_key = key;
+        last = place;
+    }
+    __syncthreads();
+    last_key = ~0ull;
+    last = 0u;
+    int n = 0;
+    for (; n < a.n_out; ++n) {
+        unsigned long long key = 0ull;
+        uint32_t place = 0xFFFFFFFFu;
+        for (int i = tid; i < n_groups * 32; i += kPickThreads) {
+            const int b = sh.group[i >> 5] / a.groups;
+            const int vec = (sh.group[i >> 5] - b * a.groups) * 32 + (i & 31);
+            auto look = [&](float l, int token) {
+                if (l == -INFINITY) return;
+                const unsigned long long k = score_key(sh, b, l);
+                const uint32_t p = (uint32_t)b * (uint32_t)a.vocab + (uint32_t)token;
+                if (!(k < last_key || (k == last_key && p > last))) return;
+                if (k > key || (k == key && p < place)) {
+                    key = k;
+                    place = p;
+                }
+            };
+            if (sh.kind[b] == kFinished) {
+                if ((i & 31) == 0) look(0.f, a.end_token);
+                continue;
+            }
+            const Row<DT> row(a, item, b);
+            const uint4 v = row.vec(vec);
+#pragma unroll
+            for (int q = 0; q < Elem<DT>::kPerVec; ++q) look(vec_at<DT>(v, q), vec * Elem<DT>::kPerVec + q - row.off);
+        }
+        block_best(key, place, s_key, s_place);
+        if (place == 0xFFFFFFFFu) break;
+        if (tid == 0) {
+            sh.key[n] = key;
+            sh.flat[n] = place;
+        }
+        last_key = key;
+        last = place;
+    }
+    __syncthreads();
+    return n;
+}
+
+// Normalisers of the flagged rows again, then their items' order.  A term is a
+// double-float (2^-46 of itself) cut to units of 2^-58, so the sum of 2^19 is
+// good to 2^-39 of itself, and scores to 2e-12.
+template <int DT>
+__global__ void __launch_bounds__(kPickThreads) refine_kernel(const __grid_constant__ BeamArgs a)
+{
+    __shared__ PickShared sh;
+    __shared__ dfloat tab[64];
+    __shared__ ulonglong2 part[kPickThreads / 32];
+    __shared__ int last;
+    pdl_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long units = (long long)*a.n_flagged * a.refine_segs;
+    if (blockIdx.x >= units) return;
+    fill_exp_table(tab);
+    __syncthreads();
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int f = (int)(u / a.refine_segs), seg = (int)(u - (long long)f * a.refine_segs);
+        const int row_no = a.flagged[f], item = row_no / a.beams;
+        const float m = a.row_max[row_no];
+        const Row<DT> row(a, item, row_no - item * a.beams);
+        unsigned long long sum = 0ull;                    // of up to 8 terms: below 2^62
+#pragma unroll 2
+        for (int k = 0; k < kRefineElems / kPickThreads; ++k) {
+            const float l = row.elem(seg * kRefineElems + k * kPickThreads + tid);
+            const float d = fmaxf(l, -FLT_MAX);           // -inf and what lies outside the row
+            if (l > -INFINITY) sum += fix_df(exp_df(df_two_sum(d, -m), tab), 0x1p58f);
+        }
+        const unsigned long long high = warp_sum_u64(sum >> 32), low = warp_sum_u64(sum & 0xFFFFFFFFull);
+        __syncthreads();
+        if (lane == 0) part[warp] = make_ulonglong2(high, low);
+        __syncthreads();
+        if (tid == 0) {
+            ulonglong2 all = part[0];
+            for (int w = 1; w < kPickThreads / 32; ++w) {
+                all.x += part[w].x;
+                all.y += part[w].y;
+            }
+            a.refined[(size_t)row_no * a.refine_segs + seg] = all;
+            __threadfence();
+            last = atomicAdd(&a.item_done[item], 1) == a.item_units[item] - 1;
+            __threadfence();
+        }
+        __syncthreads();
+        if (!last) continue;
+        // the item's rows are all there
+        if (tid < a.beams) {
+            const int r = item * a.beams + tid;
+            float score;
+            int kind = beam_kind(a, r, &score);
+            double base = a.base[r];
+            if (a.item_mask[item * 4 + (tid >> 5)] >> (tid & 31) & 1u) {
+                unsigned long long high = 0ull, low = 0ull;
+                for (int i = 0; i < a.refine_segs; ++i) {
+                    const ulonglong2 x = __ldcg(&a.refined[(size_t)r * a.refine_segs + i]);
+                    high += x.x;
+                    low += x.y;
+                }
+                base = (double)score - log((double)high * 0x1p-26 + (double)low * 0x1p-58);
+            } else if (kind == kLive && base == INFINITY) {
+                kind = kDead;
+            }
+            sh.kind[tid] = kind;
+            sh.base[tid] = base;
+            sh.top[tid] = a.row_max[r];
+        }
+        __syncthreads();
+        const Entries e{sh.key, sh.flat, sh.logit};
+        int n = a.item_list[item];
+        if (n >= 0) {
+            for (int i = tid; i < n; i += kPickThreads) {
+                const uint32_t p = (uint32_t)a.list_flat[(size_t)item * kListCap + i];
+                sh.flat[i] = p;
+                sh.logit[i] = a.list_logit[(size_t)item * kListCap + i];
+                sh.key[i] = score_key(sh, (int)(p / (uint32_t)a.vocab), sh.logit[i]);
+            }
+            sort_entries(e, n);
+        } else {
+            n = pick_by_turns<DT>(a, item, sh);
+        }
+        write_item<DT>(a, item, e, n, sh.kind, sh.scratch);
+        __syncthreads();
+    }
+}
+
+struct BeamLayout {
+    size_t head, item_units, item_done, item_list, item_mask, flagged, row_max, base, sums, group_max, list_logit,
+        list_flat, refined, total;
+};
+
+// Sizes for either element type (fp32 rows have the more chunks).
+BeamLayout beam_layout(int n, int beams, int vocab)
+{
+    const size_t rows = (size_t)n * beams, chunks = ((size_t)vocab + 7 + Elem<1>::kChunk - 1) / Elem<1>::kChunk;
+    BeamLayout L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align256(off + bytes);
+        return at;
+    };
+    L.head = take(256);
+    L.item_units = take(4 * (size_t)n);
+    L.item_done = take(4 * (size_t)n);
+    L.item_list = take(4 * (size_t)n);
+    L.item_mask = take(16 * (size_t)n);
+    L.flagged = take(4 * rows);
+    L.row_max = take(4 * rows);
+    L.base = take(8 * rows);
+    L.sums = take(8 * rows * chunks);
+    L.group_max = take(4 * rows * chunks * kVecs);
+    L.list_logit = take(4 * (size_t)n * kListCap);
+    L.list_flat = take(4 * (size_t)n * kListCap);
+    L.refined = take(16 * rows * (((size_t)vocab + kRefineElems - 1) / kRefineElems));
+    L.total = off;
+    return L;
+}
+
+template <int DT>
+cudaError_t launch_select(BeamArgs a, cudaStream_t s)
+{
+    using E = Elem<DT>;
+    const int sms = sm_count();
+    const long long rows = (long long)a.n * a.beams;
+    a.chunks = (a.vocab + E::kPerVec - 1 + E::kChunk - 1) / E::kChunk;
+    a.groups = a.chunks * kVecs;
+    const long long warps = (long long)sms * 4 * (kScanThreads / 32);
+    long long per = rows * a.chunks / (4 * warps);
+    a.seg_chunks = (int)(per < 1 ? 1 : per > kMaxSegChunks ? kMaxSegChunks : per);
+    a.segs = (a.chunks + a.seg_chunks - 1) / a.seg_chunks;
+    a.refine_segs = (a.vocab + kRefineElems - 1) / kRefineElems;
+    const long long units = rows * a.segs;
+    long long grid = (units + kScanThreads / 32 - 1) / (kScanThreads / 32);
+    if (grid > 4LL * sms) grid = 4LL * sms;
+    cudaError_t e = launch_pdl(scan_kernel<DT>, dim3((unsigned)grid), dim3(kScanThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(pick_kernel<DT>, dim3(a.n), dim3(kPickThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(refine_kernel<DT>, dim3(2 * sms), dim3(kPickThreads), 0, s, a);
+}
+
+bool beam_sizes_ok(int n, int beams, int vocab, int n_out)
+{
+    return n >= 1 && n <= (1 << 20) && beams >= 1 && beams <= kMaxBeams && vocab >= 1 && vocab <= kBeamMaxVocab &&
+           n_out >= 1 && n_out <= kMaxOut && n_out <= (long long)beams * vocab &&
+           (long long)n * beams <= (1 << 22);
+}
+
+// ---------------------------------------------------------------------------
+// State rows follow their parents.
+// ---------------------------------------------------------------------------
+constexpr int kReorderThreads = 256;
+
+struct ReorderArgs {
+    const char* src;
+    char* dst;
+    int64_t src_item, src_beam, dst_item, dst_beam;   // bytes
+    int64_t units;                                    // of a row
+    int beams_in, beams_out, in_place;
+    const int32_t* parents;
+    int32_t* status;
+};
+
+// A thread has one unit of every row of its item, so what it reads of the old
+// rows is read before it writes any of them and nobody else does either: in
+// place needs no second copy of the state.
+template <typename R, int ROWS>
+__global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_constant__ ReorderArgs a)
+{
+    extern __shared__ int32_t parent[];
+    pdl_enter();
+    const int64_t item = blockIdx.y;
+    for (int i = threadIdx.x; i < a.beams_out; i += kReorderThreads) {
+        int p = a.parents[item * a.beams_out + i];
+        if (p < 0 || p >= a.beams_in) {
+            if (a.status && blockIdx.x == 0) atomicOr(&a.status[item], kBadLayout);
+            p = -1;
+        } else if (a.in_place && p == i) {
+            p = -1;
+        }
+        parent[i] = p;
+    }
+    __syncthreads();
+    const int64_t u = (int64_t)blockIdx.x * kReorderThreads + threadIdx.x;
+    if (u >= a.units) return;
+    const char* src = a.src + item * a.src_item + u * (int64_t)sizeof(R);
+    char* dst = a.dst + item * a.dst_item + u * (int64_t)sizeof(R);
+    for (int i0 = 0; i0 < a.beams_out; i0 += ROWS) {
+        R x[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (i0 + i < a.beams_out && parent[i0 + i] >= 0)
+                x[i] = *reinterpret_cast<const R*>(src + parent[i0 + i] * a.src_beam);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (i0 + i < a.beams_out && parent[i0 + i] >= 0)
+                *reinterpret_cast<R*>(dst + (i0 + i) * a.dst_beam) = x[i];
+    }
+}
+
+// In place with more rows than a thread's registers hold: they wait in shared memory.
+template <typename R>
+__global__ void __launch_bounds__(kReorderThreads) reorder_shared_kernel(const __grid_constant__ ReorderArgs a)
+{
+    extern __shared__ __align__(16) unsigned char rows_raw[];
+    __shared__ int32_t parent[kMaxBeams];
+    R* rows = reinterpret_cast<R*>(rows_raw);                    // [beams][blockDim.x]
+    pdl_enter();
+    const int64_t item = blockIdx.y;
+    for (int i = threadIdx.x; i < a.beams_out; i += blockDim.x) {
+        int p = a.parents[item * a.beams_out + i];
+        if (p < 0 || p >= a.beams_in) {
+            if (a.status && blockIdx.x == 0) atomicOr(&a.status[item], kBadLayout);
+            p = -1;
+        } else if (p == i) {
+            p = -1;
+        }
+        parent[i] = p;
+    }
+    __syncthreads();
+    const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (u >= a.units) return;
+    const char* src = a.src + item * a.src_item + u * (int64_t)sizeof(R);
+    char* dst = a.dst + item * a.dst_item + u * (int64_t)sizeof(R);
+#pragma unroll 8
+    for (int i = 0; i < a.beams_out; ++i)
+        if (parent[i] >= 0) rows[i * blockDim.x + threadIdx.x] = *reinterpret_cast<const R*>(src + parent[i] * a.src_beam);
+#pragma unroll 8
+    for (int i = 0; i < a.beams_out; ++i)
+        if (parent[i] >= 0) *reinterpret_cast<R*>(dst + i * a.dst_beam) = rows[i * blockDim.x + threadIdx.x];
+}
+
+template <typename R>
+cudaError_t launch_reorder(ReorderArgs a, int n, int64_t row_bytes, cudaStream_t s)
+{
+    a.units = row_bytes / (int64_t)sizeof(R);
+    if (a.in_place && a.beams_out > 32) {
+        const int threads = 64;
+        const size_t smem = sizeof(R) * (size_t)threads * (size_t)a.beams_out;
+        cudaError_t e = cudaFuncSetAttribute(reorder_shared_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(sizeof(R) * threads * kMaxBeams));
+        if (e != cudaSuccess) return e;
+        return launch_pdl(reorder_shared_kernel<R>, dim3((unsigned)((a.units + threads - 1) / threads), n), dim3(threads),
+                          smem, s, a);
+    }
+    const dim3 grid((unsigned)((a.units + kReorderThreads - 1) / kReorderThreads), n);
+    const size_t smem = sizeof(int32_t) * (size_t)a.beams_out;
+    if (a.in_place && a.beams_out > 8) return launch_pdl(reorder_kernel<R, 32>, grid, dim3(kReorderThreads), smem, s, a);
+    return launch_pdl(reorder_kernel<R, 8>, grid, dim3(kReorderThreads), smem, s, a);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t sv_beam_workspace_size(int n, int beams, int vocab, int n_out)
+{
+    return beam_sizes_ok(n, beams, vocab, n_out) ? beam_layout(n, beams, vocab).total : 0;
+}
+
+extern "C" sv_status_t sv_beam_select(const void* logits, sv_dtype_t dt, int64_t stride_item, int64_t stride_beam, int n,
+                                      int beams, int vocab, const float* scores, const uint8_t* finished, int end_token,
+                                      int n_out, int32_t* out_tokens, int32_t* out_parents, float* out_scores,
+                                      int32_t* status, void* ws, size_t ws_bytes, sv_stream_t stream)
+{
+    if (n < 0 || beams < 1 || vocab < 1 || n_out < 1 || (long long)n_out > (long long)beams * vocab ||
+        (dt != SV_DTYPE_BF16 && dt != SV_DTYPE_F32) || (finished && (end_token < 0 || end_token >= vocab)))
+        return SV_ERR_INVALID_ARG;
+    if (n == 0) return SV_OK;
+    if (!logits || !scores || !out_tokens || !out_parents || !out_scores ||
+        !aligned_to(logits, dt == SV_DTYPE_BF16 ? 2 : 4))
+        return SV_ERR_INVALID_ARG;
+    if (!beam_sizes_ok(n, beams, vocab, n_out)) return SV_ERR_UNSUPPORTED;
+    const BeamLayout L = beam_layout(n, beams, vocab);
+    if (!ws || !aligned_to(ws, 256) || ws_bytes < L.total) return SV_ERR_WORKSPACE;
+    char* w = static_cast<char*>(ws);
+    BeamArgs a{};
+    a.logits = logits;
+    a.stride_item = stride_item;
+    a.stride_beam = stride_beam;
+    a.n = n;
+    a.beams = beams;
+    a.vocab = vocab;
+    a.n_out = n_out;
+    a.end_token = end_token;
+    a.scores = scores;
+    a.finished = finished;
+    a.out_tokens = out_tokens;
+    a.out_parents = out_parents;
+    a.out_scores = out_scores;
+    a.status = status;
+    a.n_flagged = reinterpret_cast<int32_t*>(w + L.head);
+    a.item_units = reinterpret_cast<int32_t*>(w + L.item_units);
+    a.item_done = reinterpret_cast<int32_t*>(w + L.item_done);
+    a.item_list = reinterpret_cast<int32_t*>(w + L.item_list);
+    a.item_mask = reinterpret_cast<uint32_t*>(w + L.item_mask);
+    a.flagged = reinterpret_cast<int32_t*>(w + L.flagged);
+    a.row_max = reinterpret_cast<float*>(w + L.row_max);
+    a.base = reinterpret_cast<double*>(w + L.base);
+    a.sums = reinterpret_cast<float2*>(w + L.sums);
+    a.group_max = reinterpret_cast<float*>(w + L.group_max);
+    a.list_logit = reinterpret_cast<float*>(w + L.list_logit);
+    a.list_flat = reinterpret_cast<int32_t*>(w + L.list_flat);
+    a.refined = reinterpret_cast<ulonglong2*>(w + L.refined);
+    const cudaError_t e = dt == SV_DTYPE_BF16 ? launch_select<0>(a, stream) : launch_select<1>(a, stream);
+    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+extern "C" sv_status_t sv_beam_reorder(const void* src, int64_t src_stride_item, int64_t src_stride_beam, void* dst,
+                                       int64_t dst_stride_item, int64_t dst_stride_beam, int64_t row_bytes, int n,
+                                       int beams_in, int beams_out, const int32_t* parents, int32_t* status,
+                                       sv_stream_t stream)
+{
+    const bool in_place = src == dst;
+    if (n < 0 || beams_in < 1 || beams_out < 1 || row_bytes < 0 ||
+        (in_place && (beams_in != beams_out || src_stride_item != dst_stride_item || src_stride_beam != dst_stride_beam)))
+        return SV_ERR_INVALID_ARG;
+    if (n == 0 || row_bytes == 0) return SV_OK;
+    if (!src || !dst || !parents) return SV_ERR_INVALID_ARG;
+    if (n > 65535 || beams_in > kMaxBeams || beams_out > kMaxBeams || row_bytes > (1LL << 36)) return SV_ERR_UNSUPPORTED;
+    ReorderArgs a{};
+    a.src = static_cast<const char*>(src);
+    a.dst = static_cast<char*>(dst);
+    a.src_item = src_stride_item;
+    a.src_beam = src_stride_beam;
+    a.dst_item = dst_stride_item;
+    a.dst_beam = dst_stride_beam;
+    a.beams_in = beams_in;
+    a.beams_out = beams_out;
+    a.in_place = in_place;
+    a.parents = parents;
+    a.status = status;
+    // the widest access that every row allows
+    const uint64_t all = (uint64_t)(uintptr_t)src | (uint64_t)(uintptr_t)dst | (uint64_t)src_stride_item |
+                         (uint64_t)src_stride_beam | (uint64_t)dst_stride_item | (uint64_t)dst_stride_beam |
+                         (uint64_t)row_bytes;
+    cudaError_t e;
+    if (all % 16 == 0) e = launch_reorder<uint4>(a, n, row_bytes, stream);
+    else if (all % 8 == 0) e = launch_reorder<uint2>(a, n, row_bytes, stream);
+    else if (all % 4 == 0) e = launch_reorder<uint32_t>(a, n, row_bytes, stream);
+    else if (all % 2 == 0) e = launch_reorder<uint16_t>(a, n, row_bytes, stream);
+    else e = launch_reorder<uint8_t>(a, n, row_bytes, stream);
+    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}

@@ -1,0 +1,694 @@
+// sv_pages.cu -- the pages of a paged cache: who holds them, copies of them,
+// and tokens that move together.
+//
+// sv_kv_fork keeps counts, not lists: a page is free when nobody holds it, and
+// new pages are the lowest free numbers, so the only state is the table and the
+// counts, and the result does not depend on timing.  Its steps need one another's
+// results from the whole batch:
+//   1  holders: every request gives back what it does not keep and takes what it
+//      does not hold; what changes of a table row is set aside;
+//   2  the rows set aside are written, begun pages count their writers, the pool's
+//      free pages are counted by tiles;
+//   3  each request's new pages get their place in the line of free pages;
+//   4  the free pages go to their places.
+// They are four kernels for large batches and pools, and one CTA with barriers
+// between them for small ones, where launches are what counts.
+//
+// The copies are HBM-bound; see the kernels.
+#include "sv_attn.cuh"
+#include "sv_internal.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kForkThreads = 1024;
+constexpr int kTileCols = 256;        // columns of a table row a warp takes
+constexpr int kTileWords = kTileCols / 32;
+constexpr int kTilePages = 4 * kForkThreads;   // pages of the pool a CTA takes
+constexpr int kForkMaxReq = 1 << 16;
+
+struct ForkArgs {
+    sv_page_pool_t pool;
+    const int32_t* parent;
+    int group;
+    const int32_t* keep_len;
+    const int32_t* new_len;
+    int32_t* copies;
+    int32_t* status;
+    // workspace
+    int32_t* kept;         // [n_req] columns kept
+    int32_t* want;         // [n_req] columns to hold, -1: the count is not a count and stays
+    int32_t* begun;        // [n_req] page that the request would write on, -1 for none
+    int32_t* first;        // [n_req] place in the line of free pages
+    int32_t* how;          // [n_req] kCopy | kServed
+    int32_t* staged;       // [n_req][max_pages] new entries
+    uint32_t* changed;     // [n_req][words] which of them
+    int32_t* writers;      // [n_pages], of begun pages only
+    unsigned long long* best;   // [n_pages], of begun pages only
+    int32_t* tile_free;    // [tiles] free pages of a tile, then of the tiles before it
+    int32_t* line;         // [1] length of the line
+    int col_tiles, words, page_tiles;
+};
+enum { kCopy = 1, kServed = 2 };
+
+struct Plan {
+    int from, kept, want, held;
+    bool bad, lost;
+};
+
+__device__ __forceinline__ Plan plan_of(const ForkArgs& a, int r)
+{
+    const int n = a.pool.n_req;
+    const long long page = a.pool.page_size;
+    Plan p;
+    p.from = r;
+    p.held = a.pool.held[r];
+    p.bad = p.lost = p.held < 0 || p.held > a.pool.max_pages;
+    if (p.lost) p.held = 0;
+    p.kept = p.want = p.held;
+    long long from = r;
+    if (a.parent) {
+        const long long low = a.group > 0 ? (long long)(r / a.group) * a.group : 0;
+        const int q = a.parent[r];
+        if (q < 0 || (a.group > 0 && q >= a.group)) p.bad = true;
+        from = low + q;
+        if (from >= n) p.bad = true;
+    }
+    const long long keep = a.keep_len[r], room = a.new_len[r];
+    if (p.bad) return p;
+    const int avail = a.pool.held[from];
+    if (avail < 0 || avail > a.pool.max_pages || keep < 0 || keep > avail * page || room < keep ||
+        room > a.pool.max_pages * page) {
+        p.bad = true;
+        return p;
+    }
+    p.from = (int)from;
+    p.kept = (int)((keep + page - 1) / page);
+    p.want = (int)((room + page - 1) / page);
+    return p;
+}
+
+__device__ __forceinline__ bool in_pool(const ForkArgs& a, int page) { return page >= 0 && page < a.pool.n_pages; }
+
+// Step 1, a warp a tile of a request's columns.
+__device__ __forceinline__ void fork_holders(const ForkArgs& a, int warp, int warps)
+{
+    const int lane = threadIdx.x & 31;
+    const long long units = (long long)a.pool.n_req * a.col_tiles;
+    for (long long u = warp; u < units; u += warps) {
+        const int r = (int)(u / a.col_tiles), c0 = (int)(u - (long long)r * a.col_tiles) * kTileCols;
+        const Plan p = plan_of(a, r);
+        const int32_t* mine = a.pool.page_table + (int64_t)r * a.pool.ld_table;
+        const int32_t* theirs = a.pool.page_table + (int64_t)p.from * a.pool.ld_table;
+        bool bad = p.bad;
+        if (c0 == 0 && lane == 0) {
+            int begun = -1;
+            if (!p.bad && a.keep_len[r] % a.pool.page_size != 0 && a.new_len[r] > a.keep_len[r]) {
+                begun = theirs[p.kept - 1];
+                if (!in_pool(a, begun)) begun = -1;
+            }
+            a.kept[r] = p.kept;
+            a.want[r] = p.lost ? -1 : p.want;
+            a.begun[r] = begun;
+            if (begun >= 0) {
+                a.writers[begun] = 0;
+                a.best[begun] = 0ull;
+            }
+        }
+        if (p.bad) {
+            // keeps what it holds
+        } else if (p.from == r) {
+            for (int c = max(c0, p.kept) + lane; c < min(c0 + kTileCols, p.held); c += 32) {
+                if (in_pool(a, mine[c])) atomicSub(&a.pool.ref_count[mine[c]], 1);
+                else bad = true;
+            }
+        } else {
+            const int end = max(p.kept, p.held);
+            int had[kTileWords], now[kTileWords];
+#pragma unroll
+            for (int w = 0; w < kTileWords; ++w) {
+                const int c = c0 + w * 32 + lane;
+                had[w] = c < p.held ? mine[c] : -1;
+                now[w] = c < p.kept ? theirs[c] : -1;
+            }
+#pragma unroll
+            for (int w = 0; w < kTileWords; ++w) {
+                const int c = c0 + w * 32 + lane;
+                if (c0 + w * 32 >= end) break;
+                const bool has = c < p.held, keeps = c < p.kept, same = has && keeps && had[w] == now[w];
+                if (has && !same) {
+                    if (in_pool(a, had[w])) atomicSub(&a.pool.ref_count[had[w]], 1);
+                    else bad = true;
+                }
+                const bool differs = keeps && !same;
+                if (differs) {
+                    if (in_pool(a, now[w])) atomicAdd(&a.pool.ref_count[now[w]], 1);
+                    else bad = true;
+                    a.staged[(int64_t)r * a.pool.max_pages + c] = now[w];
+                }
+                const uint32_t bits = __ballot_sync(0xFFFFFFFFu, differs);
+                if (lane == 0) a.changed[(int64_t)r * a.words + (c0 >> 5) + w] = bits;
+            }
+        }
+        if (a.status && __any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(&a.status[r], kBadLayout);
+    }
+}
+
+// Step 2: rows, writers, free pages of every tile of the pool.
+__device__ __forceinline__ void fork_rows(const ForkArgs& a, int warp, int warps)
+{
+    const int lane = threadIdx.x & 31;
+    const long long units = (long long)a.pool.n_req * a.col_tiles;
+    for (long long u = warp; u < units; u += warps) {
+        const int r = (int)(u / a.col_tiles), c0 = (int)(u - (long long)r * a.col_tiles) * kTileCols;
+        if (c0 == 0 && lane == 0) {
+            const int p = __ldcg(&a.begun[r]);
+            if (p >= 0) {
+                atomicAdd(&a.writers[p], 1);
+                atomicMax(&a.best[p], (unsigned long long)(uint32_t)a.keep_len[r] << 32 | (uint32_t)(kForkMaxReq - r));
+            }
+        }
+        if (!a.parent) continue;
+        const Plan p = plan_of(a, r);
+        if (p.from == r) continue;
+        uint32_t bits[kTileWords];
+#pragma unroll
+        for (int w = 0; w < kTileWords; ++w)
+            bits[w] = c0 + w * 32 < p.kept ? __ldcg(&a.changed[(int64_t)r * a.words + (c0 >> 5) + w]) : 0u;
+#pragma unroll
+        for (int w = 0; w < kTileWords; ++w) {
+            const int c = c0 + w * 32 + lane;
+            if (bits[w] >> lane & 1u)
+                a.pool.page_table[(int64_t)r * a.pool.ld_table + c] = __ldcg(&a.staged[(int64_t)r * a.pool.max_pages + c]);
+        }
+    }
+}
+
+// Which of a thread's four pages of a tile are free.
+__device__ __forceinline__ uint32_t free_of(const ForkArgs& a, int tile)
+{
+    const int p0 = tile * kTilePages + (int)threadIdx.x * 4;
+    uint32_t bits = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (p0 + i < a.pool.n_pages && __ldcg(&a.pool.ref_count[p0 + i]) == 0) bits |= 1u << i;
+    return bits;
+}
+
+// Sum over the block of the values of the threads before this one, and of all.
+__device__ __forceinline__ int block_before(int x, int* total, int* s_warp)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int sum = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        int w = lane < (int)(blockDim.x >> 5) ? s_warp[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= o) w += y;
+        }
+        s_warp[lane] = w;
+    }
+    __syncthreads();
+    *total = s_warp[31];
+    return sum - x + (warp ? s_warp[warp - 1] : 0);
+}
+
+__device__ __forceinline__ void fork_count(const ForkArgs& a, int block, int blocks, int* s_warp)
+{
+    for (int tile = block; tile < a.page_tiles; tile += blocks) {
+        int total;
+        block_before(__popc(free_of(a, tile)), &total, s_warp);
+        if (threadIdx.x == 0) a.tile_free[tile] = total;
+    }
+}
+
+// Step 3, one CTA: who copies, the line of new pages, who is served.
+__device__ __forceinline__ void fork_line(const ForkArgs& a, int* s_warp)
+{
+    const int tid = threadIdx.x;
+    int n_free = 0, line = 0, total;
+    for (int t0 = 0; t0 < a.page_tiles; t0 += kForkThreads) {
+        const int t = t0 + tid;
+        const int x = t < a.page_tiles ? __ldcg(&a.tile_free[t]) : 0;
+        const int before = block_before(x, &total, s_warp);
+        if (t < a.page_tiles) a.tile_free[t] = n_free + before;
+        n_free += total;
+    }
+    for (int r0 = 0; r0 < a.pool.n_req; r0 += kForkThreads) {
+        const int r = r0 + tid;
+        int need = 0, how = 0, begun = -1, kept = 0, want = 0, keep = 0;
+        bool lost = false;
+        if (r < a.pool.n_req) {
+            begun = __ldcg(&a.begun[r]);
+            kept = __ldcg(&a.kept[r]);
+            want = __ldcg(&a.want[r]);
+            lost = want < 0;
+            if (lost) want = kept;
+            keep = a.keep_len[r];
+            if (begun >= 0) {
+                const bool only_writers = __ldcg(&a.writers[begun]) == __ldcg(&a.pool.ref_count[begun]);
+                const unsigned long long rank = (unsigned long long)(uint32_t)keep << 32 | (uint32_t)(kForkMaxReq - r);
+                if (!only_writers || __ldcg(&a.best[begun]) != rank) how = kCopy;
+            }
+            need = want - kept + (how & kCopy);
+        }
+        const int first = line + block_before(need, &total, s_warp);
+        line += total;
+        if (r < a.pool.n_req) {
+            if (need == 0 || first + need <= n_free) how |= kServed;
+            const bool served = how & kServed, copy = how == (kCopy | kServed);
+            a.first[r] = first;
+            a.how[r] = how;
+            if (!lost) a.pool.held[r] = served ? want : kept;
+            a.copies[3 * r] = copy ? begun : -1;
+            a.copies[3 * r + 1] = -1;
+            a.copies[3 * r + 2] = copy ? keep % a.pool.page_size : -1;
+            if (!served && a.status) atomicOr(&a.status[r], SV_ROW_NO_PAGES);
+        }
+    }
+    if (tid == 0) *a.line = line;
+}
+
+// Step 4: the j-th free page goes to the request whose part of the line holds j.
+__device__ __forceinline__ void fork_assign(const ForkArgs& a, int block, int blocks, int* s_warp)
+{
+    const int line = __ldcg(a.line);
+    for (int tile = block; tile < a.page_tiles; tile += blocks) {
+        const int before = __ldcg(&a.tile_free[tile]);
+        if (before >= line) return;                             // the tiles after it begin further on
+        const uint32_t bits = free_of(a, tile);
+        int total, j = before + block_before(__popc(bits), &total, s_warp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!(bits >> i & 1u)) continue;
+            if (j >= line) break;
+            int lo = 0, hi = a.pool.n_req;                      // the last request whose part begins at or before j
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (__ldcg(&a.first[mid]) <= j) lo = mid;
+                else hi = mid;
+            }
+            const int how = __ldcg(&a.how[lo]);
+            if (how & kServed) {
+                const int page = tile * kTilePages + (int)threadIdx.x * 4 + i;
+                const int k = j - __ldcg(&a.first[lo]) - (how & kCopy);
+                const int kept = __ldcg(&a.kept[lo]);
+                if (k < 0) {
+                    a.copies[3 * lo + 1] = page;
+                    atomicSub(&a.pool.ref_count[__ldcg(&a.begun[lo])], 1);   // it has other holders: never a free page
+                }
+                a.pool.page_table[(int64_t)lo * a.pool.ld_table + kept + k] = page;
+                a.pool.ref_count[page] = 1;
+            }
+            ++j;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_holders_kernel(const __grid_constant__ ForkArgs a)
+{
+    pdl_enter();
+    fork_holders(a, blockIdx.x * (kForkThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kForkThreads / 32));
+}
+__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const __grid_constant__ ForkArgs a)
+{
+    __shared__ int s_warp[32];
+    pdl_enter();
+    fork_rows(a, blockIdx.x * (kForkThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kForkThreads / 32));
+    fork_count(a, blockIdx.x, gridDim.x, s_warp);
+}
+__global__ void __launch_bounds__(kForkThreads) fork_line_kernel(const __grid_constant__ ForkArgs a)
+{
+    __shared__ int s_warp[32];
+    pdl_enter();
+    fork_line(a, s_warp);
+}
+__global__ void __launch_bounds__(kForkThreads) fork_assign_kernel(const __grid_constant__ ForkArgs a)
+{
+    __shared__ int s_warp[32];
+    pdl_enter();
+    fork_assign(a, blockIdx.x, gridDim.x, s_warp);
+}
+__global__ void __launch_bounds__(kForkThreads) fork_small_kernel(const __grid_constant__ ForkArgs a)
+{
+    __shared__ int s_warp[32];
+    pdl_enter();
+    fork_holders(a, threadIdx.x >> 5, kForkThreads / 32);
+    __syncthreads();
+    fork_rows(a, threadIdx.x >> 5, kForkThreads / 32);
+    fork_count(a, 0, 1, s_warp);
+    __syncthreads();
+    fork_line(a, s_warp);
+    __syncthreads();
+    fork_assign(a, 0, 1, s_warp);
+}
+
+struct ForkLayout {
+    size_t kept, want, begun, first, how, staged, changed, writers, best, tile_free, line, total;
+    int words, page_tiles;
+};
+
+ForkLayout fork_layout(int n_req, int max_pages, int n_pages)
+{
+    ForkLayout L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align256(off + bytes);
+        return at;
+    };
+    const size_t n = (size_t)n_req;
+    L.words = (max_pages + kTileCols - 1) / kTileCols * kTileWords;
+    L.page_tiles = (n_pages + kTilePages - 1) / kTilePages;
+    L.kept = take(4 * n);
+    L.want = take(4 * n);
+    L.begun = take(4 * n);
+    L.first = take(4 * n);
+    L.how = take(4 * n);
+    L.staged = take(4 * n * (size_t)max_pages);
+    L.changed = take(4 * n * (size_t)L.words);
+    L.writers = take(4 * (size_t)n_pages);
+    L.best = take(8 * (size_t)n_pages);
+    L.tile_free = take(4 * (size_t)L.page_tiles);
+    L.line = take(4);
+    L.total = off;
+    return L;
+}
+
+bool fork_sizes_ok(int n_req, int max_pages, int n_pages)
+{
+    return n_req >= 1 && n_req <= kForkMaxReq && max_pages >= 0 && n_pages >= 0 && n_pages <= (1 << 30) &&
+           (long long)n_req * max_pages <= (1LL << 30);
+}
+
+cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s)
+{
+    const long long units = (long long)a.pool.n_req * a.col_tiles;
+    if (units <= 1024 && a.page_tiles <= 8)
+        return launch_pdl(fork_small_kernel, dim3(1), dim3(kForkThreads), 0, s, a);
+    const int sms = sm_count();
+    auto grid = [&](long long blocks) { return dim3((unsigned)(blocks < 1 ? 1 : blocks > 2LL * sms ? 2LL * sms : blocks)); };
+    const long long by_rows = (units + kForkThreads / 32 - 1) / (kForkThreads / 32);
+    cudaError_t e = launch_pdl(fork_holders_kernel, grid(by_rows), dim3(kForkThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(fork_rows_kernel, grid(by_rows > a.page_tiles ? by_rows : a.page_tiles), dim3(kForkThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(fork_line_kernel, dim3(1), dim3(kForkThreads), 0, s, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(fork_assign_kernel, grid(a.page_tiles), dim3(kForkThreads), 0, s, a);
+}
+
+// ---------------------------------------------------------------------------
+// Copies of pages, and tokens that move together.
+// ---------------------------------------------------------------------------
+constexpr int kMoveThreads = 256;
+constexpr int kCopyUnits = 8;      // units a thread has in flight
+constexpr int kMoveUnits = 4;
+
+struct MoveArgs {
+    sv_paged_kv_t cache;           // strides in units of R
+    int64_t layer_k, layer_v;
+    const int32_t* copies;
+    const int32_t* first;
+    const int32_t* keep;
+    const int32_t* n_keep;
+    int32_t* status;
+    int n, ld_keep, max_keep;
+    int per_head;                  // units of a head
+    int strip;                     // sv_kv_compact: units of a token a CTA takes
+    int strips;
+};
+
+template <typename R>
+__device__ __forceinline__ R* layer_of(const MoveArgs& a, int y, int64_t* page, int64_t* token, int64_t* head)
+{
+    const bool is_v = y & 1;
+    const sv_heads_t& h = is_v ? a.cache.v : a.cache.k;
+    *page = is_v ? a.cache.stride_page_v : a.cache.stride_page_k;
+    *token = h.stride_token;
+    *head = h.stride_head;
+    return static_cast<R*>(h.data) + (y >> 1) * (is_v ? a.layer_v : a.layer_k);
+}
+
+// A CTA copies a part of one page of one layer's keys or values; units go in
+// the order they lie in memory, heads inside tokens or tokens inside heads.
+template <typename R>
+__global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constant__ MoveArgs a)
+{
+    pdl_enter();
+    const int src = a.copies[3 * (int64_t)blockIdx.x], dst = a.copies[3 * (int64_t)blockIdx.x + 1],
+              tokens = a.copies[3 * (int64_t)blockIdx.x + 2];
+    if (src < 0 || dst < 0) return;
+    if (src >= a.cache.n_pages || dst >= a.cache.n_pages || tokens < 0 || tokens > a.cache.page_size) {
+        if (a.status && threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) atomicOr(a.status, kBadLayout);
+        return;
+    }
+    int64_t page, token, head;
+    R* base = layer_of<R>(a, blockIdx.y, &page, &token, &head);
+    const R* from = base + src * page;
+    R* to = base + dst * page;
+    const int heads = a.cache.k.heads;
+    const bool tokens_inside = token < head;
+    const uint32_t units = (uint32_t)tokens * (uint32_t)heads * (uint32_t)a.per_head;
+    const uint32_t inner = tokens_inside ? (uint32_t)tokens : (uint32_t)heads;
+    const uint32_t step = gridDim.z * kMoveThreads * kCopyUnits;
+    for (uint32_t u0 = blockIdx.z * kMoveThreads * kCopyUnits + threadIdx.x; u0 < units; u0 += step) {
+        R x[kCopyUnits];
+        int64_t at[kCopyUnits];
+#pragma unroll
+        for (int i = 0; i < kCopyUnits; ++i) {
+            const uint32_t u = u0 + i * kMoveThreads;
+            if (u >= units) continue;
+            const uint32_t m = u / (uint32_t)a.per_head, o = m / inner, k = m - o * inner;
+            at[i] = (u - m * (uint32_t)a.per_head) + (tokens_inside ? k * token + o * head : o * token + k * head);
+            x[i] = from[at[i]];
+        }
+#pragma unroll
+        for (int i = 0; i < kCopyUnits; ++i)
+            if (u0 + i * kMoveThreads < units) to[at[i]] = x[i];
+    }
+}
+
+// A CTA has a strip of every token of a request, in one layer's keys or values,
+// and goes over the kept tokens in order, some at a time: read, barrier, write.
+// A kept token never moves back, so what a turn writes has been read by it or
+// by an earlier one, and CTAs have different strips.
+template <typename R>
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ MoveArgs a)
+{
+    pdl_enter();
+    const int r = blockIdx.x / a.strips, strip = blockIdx.x - r * a.strips;
+    const int n = a.n_keep[r];
+    const long long first = a.first ? a.first[r] : 0;
+    const bool report = a.status && strip == 0 && blockIdx.y == 0;
+    if (n < 0 || n > a.max_keep || first < 0) {
+        if (report && threadIdx.x == 0) atomicOr(&a.status[r], kBadLayout);
+        return;
+    }
+    int64_t page, token, head;
+    R* base = layer_of<R>(a, blockIdx.y, &page, &token, &head);
+    const int lane = (int)threadIdx.x % a.strip, row = (int)threadIdx.x / a.strip, rows = kMoveThreads / a.strip;
+    const int s = strip * a.strip + lane;
+    const bool mine = s < a.per_head * a.cache.k.heads;
+    const int h = s / a.per_head;
+    base += h * head + (s - h * a.per_head);
+    const int32_t* keep = a.keep + (int64_t)r * a.ld_keep;
+    const int32_t* table = a.cache.page_table + (int64_t)r * a.cache.ld_table;
+    const long long limit = (long long)a.cache.max_pages * a.cache.page_size;
+    auto place = [&](long long p, int64_t* at) {
+        if (p >= limit) return false;
+        const int col = (int)(p / a.cache.page_size), slot = (int)(p - (long long)col * a.cache.page_size);
+        const int pg = table[col];
+        *at = pg * page + slot * token;
+        return pg >= 0 && pg < a.cache.n_pages;
+    };
+    for (int j0 = 0; j0 < n; j0 += rows * kMoveUnits) {
+        R x[kMoveUnits];
+        int64_t to[kMoveUnits];
+        bool moves[kMoveUnits];
+#pragma unroll
+        for (int i = 0; i < kMoveUnits; ++i) {
+            const int j = j0 + i * rows + row;
+            moves[i] = false;
+            if (j >= n) continue;
+            const int k = keep[j];
+            bool fine = k >= j && (j == 0 || keep[j - 1] < k);
+            if (fine && k != j) {
+                int64_t from;
+                fine = place(first + k, &from) && place(first + j, &to[i]);
+                moves[i] = fine && mine;
+                if (moves[i]) x[i] = base[from];
+            }
+            if (!fine && report) atomicOr(&a.status[r], kBadLayout);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kMoveUnits; ++i)
+            if (moves[i]) base[to[i]] = x[i];
+    }
+}
+
+// The cache's strides in units of `n` elements, if every head of it is made of such units.
+bool in_units(MoveArgs& a, int n, int size, int head_dim)
+{
+    const sv_paged_kv_t& c = a.cache;
+    if (head_dim % n || !heads_aligned(c.k, n, size) || !heads_aligned(c.v, n, size) || c.stride_page_k % n ||
+        c.stride_page_v % n || a.layer_k % n || a.layer_v % n)
+        return false;
+    a.cache.k.stride_token /= n;
+    a.cache.k.stride_head /= n;
+    a.cache.v.stride_token /= n;
+    a.cache.v.stride_head /= n;
+    a.cache.stride_page_k /= n;
+    a.cache.stride_page_v /= n;
+    a.layer_k /= n;
+    a.layer_v /= n;
+    a.per_head = head_dim / n;
+    return true;
+}
+
+template <typename R>
+cudaError_t launch_move(MoveArgs a, int layers, cudaStream_t s)
+{
+    const long long token = (long long)a.per_head * a.cache.k.heads;
+    if (a.copies) {
+        long long parts = (token * a.cache.page_size + kMoveThreads * kCopyUnits - 1) / (kMoveThreads * kCopyUnits);
+        if (parts > 64) parts = 64;
+        return launch_pdl(copy_kernel<R>, dim3(a.n, 2 * layers, (unsigned)parts), dim3(kMoveThreads), 0, s, a);
+    }
+    const int least = 64 / (int)sizeof(R);                      // a strip of 64 bytes at least
+    a.strip = kMoveThreads / 8;
+    while (a.strip > least && (long long)a.n * 2 * layers * ((token + a.strip - 1) / a.strip) < 8LL * sm_count()) a.strip /= 2;
+    a.strips = (int)((token + a.strip - 1) / a.strip);
+    return launch_pdl(compact_kernel<R>, dim3((unsigned)a.n * a.strips, 2 * layers), dim3(kMoveThreads), 0, s, a);
+}
+
+sv_status_t run_move(MoveArgs a, sv_dtype_t dt, int head_dim, int layers, cudaStream_t s)
+{
+    const int size = dt == SV_DTYPE_F32 ? 4 : 2;
+    cudaError_t e;
+    if (in_units(a, 16 / size, size, head_dim)) e = launch_move<uint4>(a, layers, s);
+    else if (in_units(a, 8 / size, size, head_dim)) e = launch_move<uint2>(a, layers, s);
+    else if (in_units(a, 4 / size, size, head_dim)) e = launch_move<uint32_t>(a, layers, s);
+    else {
+        in_units(a, 1, size, head_dim);
+        e = launch_move<uint16_t>(a, layers, s);
+    }
+    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+sv_status_t check_cache(const sv_paged_kv_t& c, sv_dtype_t dt, int head_dim, int layers)
+{
+    if (head_dim < 1 || layers < 0 || c.k.heads < 1 || c.v.heads != c.k.heads || c.page_size < 1 || c.n_pages < 0 ||
+        (dt != SV_DTYPE_BF16 && dt != SV_DTYPE_F16 && dt != SV_DTYPE_F32))
+        return SV_ERR_INVALID_ARG;
+    const int size = dt == SV_DTYPE_F32 ? 4 : 2;
+    if (layers > 32767 || (long long)c.k.heads * head_dim > (1LL << 19) ||
+        (long long)c.page_size * c.k.heads * head_dim > (1LL << 30))
+        return SV_ERR_UNSUPPORTED;
+    if (layers > 0 && (!c.k.data || !c.v.data || !aligned_to(c.k.data, size) || !aligned_to(c.v.data, size)))
+        return SV_ERR_INVALID_ARG;
+    return SV_OK;
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t sv_kv_fork_workspace_size(int n_req, int max_pages, int n_pages)
+{
+    return fork_sizes_ok(n_req, max_pages, n_pages) ? fork_layout(n_req, max_pages, n_pages).total : 0;
+}
+
+extern "C" sv_status_t sv_kv_fork(sv_page_pool_t pool, const int32_t* parent, int group, const int32_t* keep_len,
+                                  const int32_t* new_len, int32_t* copies, int32_t* status, void* ws, size_t ws_bytes,
+                                  sv_stream_t stream)
+{
+    if (pool.n_req < 0 || pool.max_pages < 0 || pool.ld_table < pool.max_pages || pool.n_pages < 0 ||
+        pool.page_size < 1 || group < 0)
+        return SV_ERR_INVALID_ARG;
+    if (pool.n_req == 0) return SV_OK;
+    if (!pool.page_table || !pool.held || !pool.ref_count || !keep_len || !new_len || !copies) return SV_ERR_INVALID_ARG;
+    if (!fork_sizes_ok(pool.n_req, pool.max_pages, pool.n_pages)) return SV_ERR_UNSUPPORTED;
+    const ForkLayout L = fork_layout(pool.n_req, pool.max_pages, pool.n_pages);
+    if (!ws || !aligned_to(ws, 256) || ws_bytes < L.total) return SV_ERR_WORKSPACE;
+    char* w = static_cast<char*>(ws);
+    ForkArgs a{};
+    a.pool = pool;
+    a.parent = parent;
+    a.group = group;
+    a.keep_len = keep_len;
+    a.new_len = new_len;
+    a.copies = copies;
+    a.status = status;
+    a.kept = reinterpret_cast<int32_t*>(w + L.kept);
+    a.want = reinterpret_cast<int32_t*>(w + L.want);
+    a.begun = reinterpret_cast<int32_t*>(w + L.begun);
+    a.first = reinterpret_cast<int32_t*>(w + L.first);
+    a.how = reinterpret_cast<int32_t*>(w + L.how);
+    a.staged = reinterpret_cast<int32_t*>(w + L.staged);
+    a.changed = reinterpret_cast<uint32_t*>(w + L.changed);
+    a.writers = reinterpret_cast<int32_t*>(w + L.writers);
+    a.best = reinterpret_cast<unsigned long long*>(w + L.best);
+    a.tile_free = reinterpret_cast<int32_t*>(w + L.tile_free);
+    a.line = reinterpret_cast<int32_t*>(w + L.line);
+    a.words = L.words;
+    a.page_tiles = L.page_tiles;
+    a.col_tiles = pool.max_pages > 0 ? L.words / kTileWords : 1;
+    return launch_fork(a, stream) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+extern "C" sv_status_t sv_kv_copy(sv_paged_kv_t cache, sv_dtype_t dt, int head_dim, int layers, int64_t stride_layer_k,
+                                  int64_t stride_layer_v, const int32_t* copies, int n_copies, int32_t* status,
+                                  sv_stream_t stream)
+{
+    const sv_status_t st = check_cache(cache, dt, head_dim, layers);
+    if (st != SV_OK) return st;
+    if (n_copies < 0) return SV_ERR_INVALID_ARG;
+    if (n_copies == 0 || layers == 0) return SV_OK;
+    if (!copies) return SV_ERR_INVALID_ARG;
+    MoveArgs a{};
+    a.cache = cache;
+    a.layer_k = stride_layer_k;
+    a.layer_v = stride_layer_v;
+    a.copies = copies;
+    a.n = n_copies;
+    a.status = status;
+    return run_move(a, dt, head_dim, layers, stream);
+}
+
+extern "C" sv_status_t sv_kv_compact(sv_paged_kv_t cache, sv_dtype_t dt, int head_dim, int layers, int64_t stride_layer_k,
+                                     int64_t stride_layer_v, int n_req, const int32_t* first, const int32_t* keep,
+                                     int ld_keep, int max_keep, const int32_t* n_keep, int32_t* status,
+                                     sv_stream_t stream)
+{
+    const sv_status_t st = check_cache(cache, dt, head_dim, layers);
+    if (st != SV_OK) return st;
+    if (n_req < 0 || max_keep < 0 || ld_keep < max_keep || cache.max_pages < 0 || cache.ld_table < cache.max_pages)
+        return SV_ERR_INVALID_ARG;
+    if (n_req == 0 || layers == 0) return SV_OK;
+    if (!n_keep || (max_keep > 0 && !keep) || (cache.max_pages > 0 && !cache.page_table)) return SV_ERR_INVALID_ARG;
+    if (n_req > (1 << 16)) return SV_ERR_UNSUPPORTED;
+    MoveArgs a{};
+    a.cache = cache;
+    a.layer_k = stride_layer_k;
+    a.layer_v = stride_layer_v;
+    a.first = first;
+    a.keep = keep;
+    a.n_keep = n_keep;
+    a.n = n_req;
+    a.ld_keep = ld_keep;
+    a.max_keep = max_keep;
+    a.status = status;
+    return run_move(a, dt, head_dim, layers, stream);
+}

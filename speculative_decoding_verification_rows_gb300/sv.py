@@ -21,10 +21,10 @@ from . import build as _build
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_WORKSPACE, SV_ERR_CUDA, SV_ERR_UNSUPPORTED = 0, 1, 2, 3, 4
 # per-position status bits (SV_ROW_* in sv.h)
 SV_ROW_NONFINITE, SV_ROW_EMPTY, SV_ROW_BAD_TOKEN, SV_ROW_BAD_PARAM, SV_ROW_BAD_LAYOUT = 1, 2, 4, 8, 16
-SV_ROW_Q_ZERO, SV_ROW_RESID_ZERO, SV_ROW_UNSUPPORTED, SV_ROW_TIMEOUT = 32, 64, 128, 256
+SV_ROW_Q_ZERO, SV_ROW_RESID_ZERO, SV_ROW_UNSUPPORTED, SV_ROW_TIMEOUT, SV_ROW_NO_PAGES = 32, 64, 128, 256, 512
 DTYPE_BF16, DTYPE_F32, DTYPE_F16 = 0, 1, 2
 ROW_NONFINITE, ROW_EMPTY, ROW_BAD_TOKEN, ROW_BAD_PARAM, ROW_BAD_LAYOUT = 1, 2, 4, 8, 16
-ROW_Q_ZERO, ROW_RESID_ZERO, ROW_UNSUPPORTED, ROW_TIMEOUT = 32, 64, 128, 256
+ROW_Q_ZERO, ROW_RESID_ZERO, ROW_UNSUPPORTED, ROW_TIMEOUT, ROW_NO_PAGES = 32, 64, 128, 256, 512
 ROW_ERROR_MASK = (ROW_NONFINITE | ROW_EMPTY | ROW_BAD_TOKEN | ROW_BAD_PARAM | ROW_BAD_LAYOUT | ROW_UNSUPPORTED
                   | ROW_TIMEOUT)
 
@@ -34,7 +34,9 @@ EXPORTED = ("sv_workspace_size", "sv_workspace_size_block", "sv_status_string", 
             "sv_verify_block", "sv_estimator_state_bytes", "sv_estimator_init", "sv_estimator_predict",
             "sv_estimator_observe", "sv_shard_record_bytes", "sv_verify_chain_shard_rows",
             "sv_verify_chain_shard_merge", "sv_q_rows_bytes", "sv_estimator_predict_q", "sv_verify_chain_q",
-            "sv_rotary", "sv_kv_append", "sv_attention_workspace_size", "sv_paged_attention")
+            "sv_rotary", "sv_kv_append", "sv_attention_workspace_size", "sv_paged_attention",
+            "sv_beam_workspace_size", "sv_beam_select", "sv_beam_reorder", "sv_kv_fork_workspace_size", "sv_kv_fork",
+            "sv_kv_copy", "sv_kv_compact")
 
 
 class SVError(RuntimeError):
@@ -66,6 +68,12 @@ class Heads(ctypes.Structure):
 class PagedKV(ctypes.Structure):
     _fields_ = [("k", Heads), ("v", Heads), ("stride_page_k", ctypes.c_int64), ("stride_page_v", ctypes.c_int64),
                 ("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("held", ctypes.c_void_p), ("ref_count", ctypes.c_void_p),
+                ("ld_table", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_req", ctypes.c_int32),
                 ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
@@ -149,6 +157,20 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     L.sv_attention_workspace_size.restype = SZ
     L.sv_paged_attention.argtypes = [Heads, PagedKV, I, I, I, I, P, P, I, ctypes.c_float, I, I, Heads, P, P, P, SZ, P]
     L.sv_paged_attention.restype = I
+    L.sv_beam_workspace_size.argtypes = [I, I, I, I]
+    L.sv_beam_workspace_size.restype = SZ
+    L.sv_beam_select.argtypes = [P, I, I64, I64, I, I, I, P, P, I, I, P, P, P, P, P, SZ, P]
+    L.sv_beam_select.restype = I
+    L.sv_beam_reorder.argtypes = [P, I64, I64, P, I64, I64, I64, I, I, I, P, P, P]
+    L.sv_beam_reorder.restype = I
+    L.sv_kv_fork_workspace_size.argtypes = [I, I, I]
+    L.sv_kv_fork_workspace_size.restype = SZ
+    L.sv_kv_fork.argtypes = [PagePool, P, I, P, P, P, P, P, SZ, P]
+    L.sv_kv_fork.restype = I
+    L.sv_kv_copy.argtypes = [PagedKV, I, I, I, I64, I64, P, I, P, P]
+    L.sv_kv_copy.restype = I
+    L.sv_kv_compact.argtypes = [PagedKV, I, I, I, I64, I64, I, P, P, I, I, P, P, P]
+    L.sv_kv_compact.restype = I
     _lib = L
     return L
 
@@ -823,3 +845,226 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         None if norm is None else norm.data_ptr(), None if status is None else _vector(status, n, device, "status"),
         scratch, nbytes, _stream_handle(device))
     return AttentionOut(out, norm)
+
+
+# ---------------------------------------------------------------------------
+# Beam search, and the pages of a paged cache
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=256)
+def beam_workspace_size(n: int, beams: int, vocab: int, n_out: int) -> int:
+    size = load().sv_beam_workspace_size(n, beams, vocab, n_out)
+    if size == 0:
+        raise SVError("sizes beyond what the library supports")
+    return size
+
+
+@functools.lru_cache(maxsize=256)
+def kv_fork_workspace_size(n_req: int, max_pages: int, n_pages: int) -> int:
+    size = load().sv_kv_fork_workspace_size(n_req, max_pages, n_pages)
+    if size == 0:
+        raise SVError("sizes beyond what the library supports")
+    return size
+
+
+def _scratch(ws: Optional[Workspace], nbytes: int, device: int):
+    """(a workspace to keep alive over the launch, its address) for a call on cuda:device."""
+    if ws is None:
+        ws = Workspace(torch.device("cuda", device))
+    at = ws.address(nbytes)
+    if ws.buf.get_device() != device:
+        raise SVError(f"the workspace must live on cuda:{device}")
+    return ws, at
+
+
+def _matrix(t: torch.Tensor, rows: int, device: int, what: str):
+    """(address, row stride, columns) of an int32 [rows, columns] tensor with contiguous rows."""
+    if t.get_device() != device:
+        raise _not_on_gpu() if not t.is_cuda else SVError(f"{what} must live on cuda:{device}")
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != rows:
+        raise SVError(f"{what} must be int32 [{rows}, columns]")
+    ld, one = t.stride()
+    cols = t.shape[1]
+    if one != 1 and cols > 1:
+        raise SVError(f"the rows of {what} must be contiguous")
+    return t.data_ptr(), ld if rows > 1 else max(ld, cols), cols
+
+
+@dataclass
+class BeamOut:
+    tokens: torch.Tensor         # [n, n_out] int32, best first
+    parents: torch.Tensor        # [n, n_out] int32: the beam that each continues
+    scores: torch.Tensor         # [n, n_out] fp32
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int, finished: Optional[torch.Tensor] = None,
+                end_token: int = 0, out: Optional[BeamOut] = None, status: Optional[torch.Tensor] = None,
+                ws: Optional[Workspace] = None) -> BeamOut:
+    """sv_beam_select: the n_out best continuations of every request over its beams' logits [n, beams, vocab] (bf16 or
+    fp32, rows contiguous) and scores fp32 [n, beams] (-inf: a dead beam).  A beam marked in finished (bool or uint8
+    [n, beams]) has one, end_token with its score unchanged.  Equal scores go by beam, then token.  Autograd records
+    nothing of it."""
+    device = logits.get_device()
+    if device < 0:
+        raise _not_on_gpu()
+    if logits.dim() != 3:
+        raise SVError(f"expected logits [n, beams, vocab], got {tuple(logits.shape)}")
+    dt = _dtype_code(logits)
+    n, beams, vocab = logits.shape
+    s_item, s_beam, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise SVError("logits must be contiguous along the vocabulary")
+    if (scores.get_device() != device or scores.dtype is not torch.float32 or scores.shape != (n, beams) or
+            not scores.is_contiguous()):
+        raise SVError(f"scores must be a contiguous fp32 [{n}, {beams}] on cuda:{device}")
+    marks = None
+    if finished is not None:
+        if (finished.get_device() != device or finished.dtype not in (torch.bool, torch.uint8) or
+                finished.shape != (n, beams) or not finished.is_contiguous()):
+            raise SVError(f"finished must be a contiguous bool or uint8 [{n}, {beams}] on cuda:{device}")
+        marks = finished.data_ptr()
+    if out is None:
+        if n_out < 1:
+            raise SVError("n_out must be positive")
+        out = BeamOut(torch.empty((n, n_out), dtype=torch.int32, device=logits.device),
+                      torch.empty((n, n_out), dtype=torch.int32, device=logits.device),
+                      torch.empty((n, n_out), dtype=torch.float32, device=logits.device))
+    else:
+        for t, kind in ((out.tokens, torch.int32), (out.parents, torch.int32), (out.scores, torch.float32)):
+            if t.get_device() != device or t.dtype is not kind or t.shape != (n, n_out) or not t.is_contiguous():
+                raise SVError(f"out must hold contiguous int32, int32 and fp32 [{n}, {n_out}] on cuda:{device}")
+    if n == 0:
+        return out
+    nbytes = beam_workspace_size(n, beams, vocab, n_out)
+    ws, at = _scratch(ws, nbytes, device)
+    _launch(device, (_lib or load()).sv_beam_select, logits.data_ptr(), dt, s_item, s_beam, n, beams, vocab,
+            scores.data_ptr(), marks, end_token, n_out, out.tokens.data_ptr(), out.parents.data_ptr(),
+            out.scores.data_ptr(), None if status is None else _vector(status, n, device, "status"), at, nbytes,
+            _stream_handle(device))
+    return out
+
+
+def _state_rows(t: torch.Tensor, device: int, what: str):
+    """(item stride, beam stride, row bytes), in bytes, of [n, beams, ...] whose rows are contiguous."""
+    if t.get_device() != device:
+        raise _not_on_gpu() if not t.is_cuda else SVError(f"{what} must live on cuda:{device}")
+    if t.dim() < 2:
+        raise SVError(f"{what} must be [n, beams, ...]")
+    size, row = t.element_size(), 1
+    shape, strides = t.shape, t.stride()
+    for d in range(t.dim() - 1, 1, -1):
+        if shape[d] != 1 and strides[d] != row:
+            raise SVError(f"the rows of {what} must be contiguous")
+        row *= shape[d]
+    return strides[0] * size, strides[1] * size, row * size
+
+
+def beam_reorder(state: torch.Tensor, parents: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """sv_beam_reorder: out[i, j] = state[i, parents[i, j]] for state [n, beams, ...] of any type and parents int32
+    [n, beams_out].  out may be state itself: the rows then move in place.  A parent outside its range leaves the row
+    of out as it is (and sets ROW_BAD_LAYOUT in status int32 [n]).  Autograd records nothing of it."""
+    device = state.get_device()
+    if device < 0:
+        raise _not_on_gpu()
+    src_item, src_beam, row = _state_rows(state, device, "state")
+    n, beams = state.shape[:2]
+    if (parents.get_device() != device or parents.dtype is not torch.int32 or parents.dim() != 2 or
+            parents.shape[0] != n or not parents.is_contiguous()):
+        raise SVError(f"parents must be a contiguous int32 [{n}, beams] on cuda:{device}")
+    beams_out = parents.shape[1]
+    if out is None:
+        out = torch.empty((n, beams_out, *state.shape[2:]), dtype=state.dtype, device=state.device)
+    elif out.dtype is not state.dtype or out.shape != (n, beams_out, *state.shape[2:]):
+        raise SVError(f"out must be {state.dtype} {(n, beams_out, *state.shape[2:])}")
+    dst_item, dst_beam, _ = _state_rows(out, device, "out")
+    if n == 1:                                                   # strides of an axis of one say nothing
+        dst_item = src_item = 0
+    if beams == 1 and beams_out == 1:
+        dst_beam = src_beam = 0
+    if beams_out == 0:
+        return out
+    _launch(device, (_lib or load()).sv_beam_reorder, state.data_ptr(), src_item, src_beam, out.data_ptr(), dst_item,
+            dst_beam, row, n, beams, beams_out, parents.data_ptr(),
+            None if status is None else _vector(status, n, device, "status"), _stream_handle(device))
+    return out
+
+
+def kv_fork(page_table: torch.Tensor, held: torch.Tensor, ref_count: torch.Tensor, page_size: int,
+            keep_len: torch.Tensor, new_len: torch.Tensor, parent: Optional[torch.Tensor] = None, group: int = 0,
+            copies: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+            ws: Optional[Workspace] = None) -> torch.Tensor:
+    """sv_kv_fork: every request takes the pages of the first keep_len tokens of its parent (its own, without parent)
+    and gets room for new_len tokens; page_table int32 [n, max_pages], held int32 [n] and ref_count int32 [n_pages] are
+    updated in place.  With group, parent numbers requests within groups of so many.  Returns copies int32 [n, 3]
+    (page, new page, tokens; -1: none), which kv_copy carries out before anything is appended."""
+    device = page_table.get_device()
+    if device < 0:
+        raise _not_on_gpu()
+    if held.dim() != 1 or ref_count.dim() != 1:
+        raise SVError("held must be int32 [n], ref_count int32 [n_pages]")
+    n, n_pages = held.numel(), ref_count.numel()
+    table, ld, cols = _matrix(page_table, n, device, "page_table")
+    pool = PagePool(table, _vector(held, n, device, "held"), _vector(ref_count, n_pages, device, "ref_count"), ld, cols, n,
+                    n_pages, page_size)
+    if copies is None:
+        copies = torch.empty((n, 3), dtype=torch.int32, device=page_table.device)
+    elif copies.shape != (n, 3):
+        raise SVError(f"copies must be int32 [{n}, 3]")
+    if n == 0:
+        return copies
+    nbytes = kv_fork_workspace_size(n, cols, n_pages)
+    ws, at = _scratch(ws, nbytes, device)
+    _launch(device, (_lib or load()).sv_kv_fork, pool, None if parent is None else _vector(parent, n, device, "parent"),
+            group, _vector(keep_len, n, device, "keep_len"), _vector(new_len, n, device, "new_len"),
+            _vector(copies, 3 * n, device, "copies"), None if status is None else _vector(status, n, device, "status"), at,
+            nbytes, _stream_handle(device))
+    return copies
+
+
+def _layers(k_pages: torch.Tensor, v_pages: torch.Tensor):
+    """(cache without its table, layers, strides of a layer, type, head_dim, device) of pages [n_pages, page_size, heads,
+    head_dim] or [layers, n_pages, ...]."""
+    device = k_pages.get_device()
+    if device < 0:
+        raise _not_on_gpu()
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if len(shape) not in (4, 5) or v_pages.shape != shape:
+        raise SVError("k_pages and v_pages must both be [n_pages, page_size, heads, head_dim], or so with layers first")
+    if v_pages.dtype is not dtype or v_pages.get_device() != device:
+        raise SVError(f"v_pages must be {dtype} on cuda:{device}")
+    ks, vs = k_pages.stride(), v_pages.stride()
+    layers, kl, vl = (shape[0], ks[0], vs[0]) if len(shape) == 5 else (1, 0, 0)
+    if layers == 1:
+        kl = vl = 0
+    n_pages, page, heads, d = shape[-4:]
+    if (ks[-1] != 1 or vs[-1] != 1) and d != 1:
+        raise SVError("the elements of a head must be contiguous")
+    cache = PagedKV(Heads(k_pages.data_ptr(), ks[-3], ks[-2], heads), Heads(v_pages.data_ptr(), vs[-3], vs[-2], heads),
+                    ks[-4], vs[-4], None, 0, 0, n_pages, page)
+    return cache, layers, kl, vl, _attn_dtype(dtype), d, device
+
+
+def kv_copy(k_pages: torch.Tensor, v_pages: torch.Tensor, copies: torch.Tensor, status: Optional[torch.Tensor] = None):
+    """sv_kv_copy: copies int32 [m, 3] (page, page copied to, tokens; negative pages: none) of a cache's pages
+    [n_pages, page_size, heads, head_dim], or of all its layers' at once [layers, n_pages, ...]."""
+    cache, layers, kl, vl, dt, d, device = _layers(k_pages, v_pages)
+    if copies.dim() != 2 or copies.shape[1] != 3:
+        raise SVError("copies must be int32 [entries, 3]")
+    m = copies.shape[0]
+    _launch(device, (_lib or load()).sv_kv_copy, cache, dt, d, layers, kl, vl, _vector(copies, 3 * m, device, "copies"), m,
+            None if status is None else _vector(status, 1, device, "status"), _stream_handle(device))
+
+
+def kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, keep: torch.Tensor,
+               n_keep: torch.Tensor, first: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """sv_kv_compact: token first + keep[r, j] of request r moves to first + j, j < n_keep[r], in place, in a cache's
+    pages [n_pages, page_size, heads, head_dim] or in all layers' at once [layers, n_pages, ...]; keep int32 [n, columns]
+    ascends in each row."""
+    cache, layers, kl, vl, dt, d, device = _layers(k_pages, v_pages)
+    n = n_keep.numel()
+    cache.page_table, cache.ld_table, cache.max_pages = _matrix(page_table, n, device, "page_table")
+    keep_at, ld, cols = _matrix(keep, n, device, "keep")
+    _launch(device, (_lib or load()).sv_kv_compact, cache, dt, d, layers, kl, vl, n,
+            None if first is None else _vector(first, n, device, "first"), keep_at, ld, cols,
+            _vector(n_keep, n, device, "n_keep"), None if status is None else _vector(status, n, device, "status"),
+            _stream_handle(device))
