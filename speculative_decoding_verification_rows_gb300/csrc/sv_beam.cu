@@ -5,12 +5,11 @@
 // base_b = c_b - ln sum exp(l - m_b).  What a call has to read is every live row
 // once; the rest is small.  So one kernel streams the rows (scan_kernel): a warp takes 4 KB
 // chunks, sums exp(l - ref) in fp32 against a running reference and leaves the
-// maximum of every 512-byte group.  The n_out best candidates lie in the n_out
-// best groups: a group that n_out others stand before (by maximum, then by
-// place) has n_out elements before each of its own.  A second kernel
-// (pick_kernel, a CTA an item) bounds the n_out-th best group's score from
-// below, reads again the few groups that reach the bound and sorts the
-// elements that do.
+// chunk's maximum.  The n_out best candidates lie in the n_out best chunks: a
+// chunk that n_out others stand before (by maximum, then by place) has n_out
+// elements before each of its own.  A second kernel (pick_kernel, a CTA an item)
+// bounds the n_out-th best chunk's score from below, reads again the few chunks
+// that reach the bound and sorts the elements that do.
 //
 // Order.  Within a beam it is the logits' and exact.  Between beams it hangs on
 // the difference of two normalisers, and fp32 sums are off by up to kSumEps
@@ -34,10 +33,12 @@ constexpr int kMaxBeams = 128;
 constexpr int kMaxOut = 256;
 constexpr int kBeamMaxVocab = 1 << 19;
 constexpr int kScanThreads = 256;
-constexpr int kVecs = 8;                     // 16-byte vectors a lane takes of a chunk: a group each
+constexpr int kVecs = 8;                     // 16-byte vectors a lane takes of a chunk
 constexpr int kMaxSegChunks = 8;             // chunks a warp sums up before it leaves a partial sum
-constexpr int kPickThreads = 512;
-constexpr int kListCap = 2048;               // groups, and elements, that an item may have at its bound
+constexpr int kPickThreads = 1024;
+constexpr int kListCap = 2048;               // elements that an item may have at its bound
+constexpr int kChunkCap = 1024;              // and chunks
+constexpr int kPickHeld = 4;                 // chunk maxima a thread keeps in registers
 constexpr int kRefineElems = 4096;           // elements of a row a CTA of refine_kernel sums
 
 // |ln sum exp(l - m) - computed| of one row, V <= 2^19.  With p the row's probabilities, sum
@@ -50,6 +51,13 @@ constexpr int kRefineElems = 4096;           // elements of a row a CTA of refin
 constexpr double kSumEps = 8e-6;
 
 enum { kDead = 0, kLive = 1, kFinished = 2 };
+
+// What an item's CTA knows of a beam, read in one piece.
+struct __align__(16) BeamRec {
+    float base, top;    // base in fp32; the row's maximum (0 of a finished beam)
+    float least;        // l - top of a logit that may reach the bound
+    int kind;
+};
 
 struct BeamArgs {
     const void* logits;
@@ -68,14 +76,14 @@ struct BeamArgs {
     int32_t* item_list;      // candidates saved, or -1: more than a list holds
     uint32_t* item_mask;     // [n][4] beams that are summed again
     int32_t* flagged;        // [rows]
-    float* row_max;          // [rows]
+    BeamRec* rec;            // [rows], of items that are sorted again
     double* base;            // [rows]
     float2* sums;            // [rows][segs] reference, sum
-    float* group_max;        // [rows][groups]
+    float* chunk_max;        // [rows][chunks]
     float* list_logit;       // [n][kListCap]
     int32_t* list_flat;
     ulonglong2* refined;     // [rows][refine segments] sums in units of 2^-26 and of 2^-58
-    int chunks, seg_chunks, segs, groups, refine_segs;
+    int chunks, seg_chunks, segs, refine_segs;
 };
 
 // What the rows' element type says about their layout in 16-byte vectors.
@@ -83,8 +91,7 @@ template <int DT>
 struct Elem {
     static constexpr int kSize = DT == 0 ? 2 : 4;
     static constexpr int kPerVec = 16 / kSize;
-    static constexpr int kGroup = 32 * kPerVec;
-    static constexpr int kChunk = kVecs * kGroup;
+    static constexpr int kChunk = kVecs * 32 * kPerVec;
 };
 
 // A row as vectors that start on 16-byte boundaries: element e is slot e + off.
@@ -125,6 +132,22 @@ struct Row {
                               bits(e0 + 4) | bits(e0 + 5) << 16, bits(e0 + 6) | bits(e0 + 7) << 16);
         return make_uint4(bits(e0), bits(e0 + 1), bits(e0 + 2), bits(e0 + 3));
     }
+    // A lane's vectors of chunk c; vector i holds elements from vec_first(c, i) on.
+    __device__ __forceinline__ void chunk(int c, uint4 (&v)[kVecs]) const
+    {
+        const int v0 = c * (kVecs * 32) + (int)(threadIdx.x & 31);
+        if (c * Elem<DT>::kChunk - off >= 0 && (c + 1) * Elem<DT>::kChunk - off <= vocab) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) v[i] = whole(v0 + i * 32);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) v[i] = vec(v0 + i * 32);
+        }
+    }
+    __device__ __forceinline__ int vec_first(int c, int i) const
+    {
+        return ((c * kVecs + i) * 32 + (int)(threadIdx.x & 31)) * Elem<DT>::kPerVec - off;
+    }
     __device__ __forceinline__ float elem(int e) const
     {
         return __uint_as_float(DT == 0 ? bits(e) << 16 : bits(e));
@@ -151,6 +174,12 @@ __device__ __forceinline__ float max_nan(float a, float b)
 {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float warp_max(float x)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ float warp_max_nan(float x)
@@ -221,49 +250,40 @@ __device__ __forceinline__ pair_t vec_exp_sum(const uint4& v, pair_t minus_ref)
 
 __device__ __forceinline__ int beam_kind(const BeamArgs& a, int row, float* score)
 {
+    const uint8_t finished = a.finished ? a.finished[row] : 0;
     *score = a.scores[row];
-    if (*score == -INFINITY) return kDead;
-    return a.finished && a.finished[row] ? kFinished : kLive;
+    return *score == -INFINITY ? kDead : finished ? kFinished : kLive;
+}
+__device__ __forceinline__ bool is_live(const BeamArgs& a, int row)
+{
+    float score;
+    return beam_kind(a, row, &score) == kLive;
 }
 
-// Rows as streams: the unit is a segment of a row, a warp each.
+// A warp's share of rows row0 .. row0 + rows - 1: the unit is a segment of a row.
 template <int DT>
-__global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_constant__ BeamArgs a)
+__device__ __forceinline__ void scan_rows(const BeamArgs& a, int row0, int rows, int warp, int warps)
 {
-    using E = Elem<DT>;
-    pdl_enter();
     const int lane = threadIdx.x & 31;
-    if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) *a.n_flagged = 0;
-        for (int i = threadIdx.x; i < a.n; i += kScanThreads) a.item_done[i] = 0;
-    }
-    const long long units = (long long)a.n * a.beams * a.segs;
-    const long long warps = (long long)gridDim.x * (kScanThreads / 32);
-    for (long long u = (long long)blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
-        const int row_no = (int)(u / a.segs), seg = (int)(u - (long long)row_no * a.segs);
-        float score;
-        if (beam_kind(a, row_no, &score) != kLive) continue;
+    const long long units = (long long)rows * a.segs;
+    long long u = warp;
+    if (u >= units) return;
+    bool live = is_live(a, row0 + (int)(u / a.segs)), next_live;
+    for (; u < units; u += warps, live = next_live) {
+        const int at = (int)(u / a.segs), row_no = row0 + at, seg = (int)(u - (long long)at * a.segs);
+        next_live = u + warps < units && is_live(a, row0 + (int)((u + warps) / a.segs));   // while this one's data is on its way
+        if (!live) continue;
         const Row<DT> row(a, row_no / a.beams, row_no % a.beams);
         const int c1 = min((seg + 1) * a.seg_chunks, a.chunks);
         float ref = -FLT_MAX, s_hi = 0.f, s_lo = 0.f;
         for (int c = seg * a.seg_chunks; c < c1; ++c) {
             uint4 v[kVecs];
-            const int v0 = c * (kVecs * 32) + lane;
-            if (c * E::kChunk - row.off >= 0 && (c + 1) * E::kChunk - row.off <= a.vocab) {
+            row.chunk(c, v);
+            float top = vec_max<DT>(v[0]);
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) v[i] = row.whole(v0 + i * 32);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i) v[i] = row.vec(v0 + i * 32);
-            }
-            float top = -INFINITY, mine = 0.f;
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const float m = warp_max_nan(vec_max<DT>(v[i]));
-                top = max_nan(top, m);
-                if (lane == i) mine = m;
-            }
-            if (lane < kVecs) a.group_max[(size_t)row_no * a.groups + c * kVecs + lane] = mine;
+            for (int i = 1; i < kVecs; ++i) top = max_nan(top, vec_max<DT>(v[i]));
+            top = warp_max_nan(top);
+            if (lane == 0) a.chunk_max[(size_t)row_no * a.chunks + c] = top;
             if (top > ref) {
                 const float f = exp2_approx((ref - top) * kLog2e);
                 s_hi *= f;
@@ -290,6 +310,24 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_cons
     }
 }
 
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kScanThreads, 4) scan_kernel(const __grid_constant__ BeamArgs a)
+{
+    pdl_enter();
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *a.n_flagged = 0;
+        for (int i = threadIdx.x; i < a.n; i += kScanThreads) a.item_done[i] = 0;
+    }
+    scan_rows<DT>(a, 0, a.n * a.beams, blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5),
+                  gridDim.x * (kScanThreads / 32));
+}
+
 // The order of scores in 64 bits as that of unsigned numbers; -0 and +0 are one.
 __device__ __forceinline__ unsigned long long key_of_f64(double x)
 {
@@ -306,17 +344,38 @@ struct Entries {
     unsigned long long* key;
     uint32_t* flat;     // beam * vocab + token
     float* logit;
+    uint8_t* beam;
 };
 
-// Descending by score, ascending by place among equals (bitonic; the places are distinct).
-__device__ void sort_entries(const Entries& e, int n)
+// order[i] becomes the i-th candidate: descending by score, ascending by place
+// among equals (the places are distinct).  Up to 256 candidates find their places
+// by counting those before them, a few threads each: two barriers, where the
+// sorting network has one a stage.  More are sorted (bitonic).
+__device__ void sort_entries(const Entries& e, int n, uint16_t* order)
 {
     int p = 1;
     while (p < n) p <<= 1;
+    if (p <= kPickThreads / 2) {
+        __syncthreads();
+        const int share = min(32, kPickThreads / p), i = threadIdx.x / share;
+        int before = 0;
+        if (i < n) {
+            const unsigned long long k = e.key[i];
+            const uint32_t f = e.flat[i];
+            for (int j = threadIdx.x % share; j < n; j += share)
+                before += e.key[j] > k || (e.key[j] == k && e.flat[j] < f);
+        }
+        for (int o = share >> 1; o; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+        if (i < n && threadIdx.x % share == 0) order[before] = (uint16_t)i;
+        __syncthreads();
+        return;
+    }
+    for (int i = threadIdx.x; i < n; i += blockDim.x) order[i] = (uint16_t)i;
     for (int i = n + threadIdx.x; i < p; i += blockDim.x) {
         e.key[i] = 0ull;
         e.flat[i] = 0xFFFFFFFFu;
         e.logit[i] = -INFINITY;
+        e.beam[i] = 0;
     }
     __syncthreads();
     for (int size = 2; size <= p; size <<= 1) {
@@ -329,12 +388,15 @@ __device__ void sort_entries(const Entries& e, int n)
                 const bool before = ki > kj || (ki == kj && fi < fj);   // i stands before j
                 if (before != down) {
                     const float li = e.logit[i];
+                    const uint8_t bi = e.beam[i];
                     e.key[i] = kj;
                     e.key[j] = ki;
                     e.flat[i] = fj;
                     e.flat[j] = fi;
                     e.logit[i] = e.logit[j];
                     e.logit[j] = li;
+                    e.beam[i] = e.beam[j];
+                    e.beam[j] = bi;
                 }
             }
             __syncthreads();
@@ -342,34 +404,72 @@ __device__ void sort_entries(const Entries& e, int n)
     }
 }
 
+struct PickShared {
+    unsigned long long key[kListCap];
+    uint32_t flat[kListCap];
+    float logit[kListCap];
+    BeamRec rec[kMaxBeams];
+    double base[kMaxBeams];
+    union {
+        int chunk[kChunkCap];
+        int bins[kPickThreads];
+        int scratch[kMaxOut];
+    };
+    uint16_t order[kListCap];
+    uint8_t beam[kListCap];
+    uint32_t mask[4];
+    float warp_best[32];
+    int warp_count[32];
+    float bound;
+    int bound_found;
+    int n_chunks, n_elems, bad, flag_at;
+
+    __device__ Entries entries() { return Entries{key, flat, logit, beam}; }
+};
+
+// A score in fp32 (a finite one stays finite), and how far it may be from the
+// one in 64 bits with the row's true sum.
+__device__ __forceinline__ float score32(const BeamRec& b, float l)
+{
+    return l == -INFINITY ? l : fmaxf(b.base + (l - b.top), -FLT_MAX);
+}
+__device__ __forceinline__ float slack32(const BeamRec& b, float l)
+{
+    return (float)kSumEps + 0x1p-22f * (fabsf(b.base) + fabsf(l - b.top));
+}
+__device__ __forceinline__ unsigned long long score_key(const PickShared& sh, int b, float l)
+{
+    return key_of_f64(sh.base[b] + ((double)l - (double)sh.rec[b].top));
+}
+
 // The item's outputs from its sorted finite candidates.  Where they are fewer
 // than n_out, the places of score -inf follow from the lowest on; they are
 // among the first n_out places, since fewer than n_out are not -inf.
 template <int DT>
-__device__ void write_item(const BeamArgs& a, int item, const Entries& e, int n, const int* kind, int* scratch)
+__device__ void write_item(const BeamArgs& a, int item, const Entries& e, int n, PickShared& sh)
 {
     const int tid = threadIdx.x;
     if (tid < a.n_out && tid < n) {
         const size_t o = (size_t)item * a.n_out + tid;
-        const int b = (int)(e.flat[tid] / (uint32_t)a.vocab);
-        a.out_tokens[o] = (int)(e.flat[tid] - (uint32_t)b * (uint32_t)a.vocab);
+        const int i = sh.order[tid], b = e.beam[i];
+        a.out_tokens[o] = (int)(e.flat[i] - (uint32_t)b * (uint32_t)a.vocab);
         a.out_parents[o] = b;
-        a.out_scores[o] = (float)f64_of_key(e.key[tid]);
+        a.out_scores[o] = (float)f64_of_key(e.key[i]);
     }
     if (n >= a.n_out) return;
     int empty = 0, b = 0, t = 0;
     if (tid < a.n_out) {
         b = tid / a.vocab;
         t = tid - b * a.vocab;
-        if (kind[b] == kDead) empty = 1;
-        else if (kind[b] == kFinished) empty = t != a.end_token;
+        if (sh.rec[b].kind == kDead) empty = 1;
+        else if (sh.rec[b].kind == kFinished) empty = t != a.end_token;
         else empty = Row<DT>(a, item, b).elem(t) == -INFINITY;
-        scratch[tid] = empty;
+        sh.scratch[tid] = empty;
     }
     __syncthreads();
     if (empty) {
         int at = n;
-        for (int i = 0; i < tid; ++i) at += scratch[i];
+        for (int i = 0; i < tid; ++i) at += sh.scratch[i];
         if (at < a.n_out) {
             const size_t o = (size_t)item * a.n_out + at;
             a.out_tokens[o] = t;
@@ -379,47 +479,73 @@ __device__ void write_item(const BeamArgs& a, int item, const Entries& e, int n,
     }
 }
 
-struct PickShared {
-    unsigned long long key[kListCap];
-    uint32_t flat[kListCap];
-    float logit[kListCap];
-    int group[kListCap];
-    double base[kMaxBeams];
-    float base32[kMaxBeams];
-    float top[kMaxBeams];
-    int kind[kMaxBeams];
-    int scratch[kMaxOut];
-    uint32_t mask[4];
-    int n_groups, n_elems, bad, flag_at;
-};
-
-// A score in fp32 (a finite one stays finite), and how far it may be from the
-// one in 64 bits with the row's true sum.
-__device__ __forceinline__ float score32(const PickShared& sh, int b, float l)
+// A lower bound on the n_out-th largest of the threads' values: counted in bins
+// of 1/32 below the largest (four barriers), or, where they lie further apart
+// than the bins reach, by bisection (20 barriers).
+__device__ float nth_bound(float best, int n_out, PickShared& sh)
 {
-    return l == -INFINITY ? l : fmaxf(sh.base32[b] + (l - sh.top[b]), -FLT_MAX);
-}
-__device__ __forceinline__ float slack32(const PickShared& sh, int b, float l)
-{
-    return (float)kSumEps + 0x1p-22f * (fabsf(sh.base32[b]) + fabsf(l - sh.top[b]));
-}
-__device__ __forceinline__ unsigned long long score_key(const PickShared& sh, int b, float l)
-{
-    return key_of_f64(sh.base[b] + ((double)l - (double)sh.top[b]));
-}
-
-template <int DT>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ BeamArgs a)
-{
-    __shared__ PickShared sh;
-    pdl_enter();
+    constexpr float kPerUnit = 32.f;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int item = blockIdx.x, row0 = item * a.beams;
-    if (tid == 0) sh.n_groups = sh.n_elems = sh.bad = 0;
+    sh.bins[tid] = 0;
+    if (tid == 0) sh.bound_found = 0;
+    const float w = warp_max(best);
+    if (lane == 0) sh.warp_best[warp] = w;
+    __syncthreads();
+    const float most = warp_max(sh.warp_best[lane]);
+    const float down = (most - best) * kPerUnit;
+    if (best > -INFINITY && down < (float)kPickThreads) atomicAdd(&sh.bins[(int)down], 1);
+    __syncthreads();
+    const int here = sh.bins[tid];
+    int upto = here;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) sh.warp_count[warp] = upto;
+    __syncthreads();
+    int before = lane < warp ? sh.warp_count[lane] : 0;
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    upto += before;
+    if (upto >= n_out && upto - here < n_out) {                   // (the bin's edge, and what rounding may have moved across it)
+        sh.bound = most - ((float)tid + 1.01f) / kPerUnit - 0x1p-22f * fabsf(most);
+        sh.bound_found = 1;
+    }
+    __syncthreads();
+    if (sh.bound_found) return sh.bound;
+    const uint32_t mine = key_of_f32_bits(__float_as_uint(best));
+    uint32_t bound_key = 0u;
+    for (int bit = 31; bit >= 12; --bit) {
+        const uint32_t tv = bound_key | (1u << bit);
+        if (__syncthreads_count(mine >= tv) >= n_out) bound_key = tv;
+    }
+    return bound_key <= key_of_f32_bits(0xFF800000u) ? -FLT_MAX : f32_of_key(bound_key);
+}
+
+// An item's outputs from its rows' sums and chunk maxima, by one CTA.  Returns 0,
+// or the number of rows (sh.mask) to be summed again first: the candidates stay
+// in shared memory, sh.n_elems of them, or -1 for more than a list holds.
+template <int DT>
+__device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row0 = item * a.beams;
+    const float* chunk_max = a.chunk_max + (size_t)row0 * a.chunks;
+    const int total = a.beams * a.chunks;
+    // The chunks' maxima set out at once, rows that were not read among them (what lies there is not looked at).
+    float held[kPickHeld];
+#pragma unroll
+    for (int k = 0; k < kPickHeld; ++k) {
+        const int i = tid + k * kPickThreads;
+        held[k] = i < total ? __ldcg(&chunk_max[i]) : 0.f;
+    }
+    if (tid == 0) sh.n_chunks = sh.n_elems = sh.bad = 0;
     if (tid < 4) sh.mask[tid] = 0u;
     __syncthreads();
     // normalisers, a warp a beam
     for (int b = warp; b < a.beams; b += kPickThreads / 32) {
+        const float2* sums = a.sums + (size_t)(row0 + b) * a.segs;
+        const float2 part = lane < a.segs ? __ldcg(&sums[lane]) : make_float2(-FLT_MAX, 0.f);
         float score;
         int kind = beam_kind(a, row0 + b, &score);
         double base = (double)score;
@@ -429,13 +555,14 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
             kind = kDead;
         }
         if (kind == kLive) {
-            const float2* sums = a.sums + (size_t)(row0 + b) * a.segs;
-            float m = -FLT_MAX;
-            for (int i = lane; i < a.segs; i += 32) m = fmaxf(m, sums[i].x);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            float s = 0.f;
-            for (int i = lane; i < a.segs; i += 32) s += sums[i].y * exp2_approx((sums[i].x - m) * kLog2e);
+            float m = part.x;
+            for (int i = lane + 32; i < a.segs; i += 32) m = fmaxf(m, __ldcg(&sums[i]).x);
+            m = warp_max(m);
+            float s = part.y * exp2_approx((part.x - m) * kLog2e);
+            for (int i = lane + 32; i < a.segs; i += 32) {
+                const float2 x = __ldcg(&sums[i]);
+                s += x.y * exp2_approx((x.x - m) * kLog2e);
+            }
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             if (s == 0.f) kind = kDead;                           // nothing but -inf: every score is -inf
@@ -443,34 +570,30 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
             top = m;
         }
         if (lane == 0) {
-            sh.kind[b] = kind;
+            sh.rec[b] = BeamRec{(float)base, top, 0.f, kind};
             sh.base[b] = base;
-            sh.base32[b] = (float)base;
-            sh.top[b] = top;
-            a.base[row0 + b] = base;
-            a.row_max[row0 + b] = top;
         }
     }
     __syncthreads();
-    // A lower bound on the n_out-th best group's score: the n_out-th largest of the threads' best.
+    // A lower bound on the n_out-th best chunk's score: on the n_out-th largest of the threads' best.
+    const float per_beam = 1.f / (float)a.chunks;
+    auto beam_of = [&](int i) { return (int)(((float)i + 0.5f) * per_beam); };   // i / chunks: off by 128 3 2^-24 < 0.5 / 513 at most
     float best = -INFINITY;
-    const int total = a.beams * a.groups;
-    for (int i = tid; i < total; i += kPickThreads) {
-        const int b = i / a.groups;
-        if (sh.kind[b] != kLive) continue;
-        const float m = a.group_max[(size_t)row0 * a.groups + i];
+    auto rate = [&](int i, float m) {                             // the most a chunk's best may have, -inf for nothing
+        if (i >= total) return -INFINITY;
+        const BeamRec b = sh.rec[beam_of(i)];
+        if (b.kind != kLive) return -INFINITY;
         if (!(m < INFINITY)) atomicOr(&sh.bad, kNonfinite);
-        const float s = score32(sh, b, m);
-        if (s > -INFINITY) best = fmaxf(best, s - slack32(sh, b, m));
-    }
-    if (tid < a.beams && sh.kind[tid] == kFinished) best = fmaxf(best, sh.base32[tid]);
-    const uint32_t mine = key_of_f32_bits(__float_as_uint(best));
-    uint32_t bound_key = 0u;
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t tv = bound_key | (1u << bit);
-        if (__syncthreads_count(mine >= tv) >= a.n_out) bound_key = tv;
-    }
-    const float bound = bound_key <= key_of_f32_bits(0xFF800000u) ? -FLT_MAX : f32_of_key(bound_key);
+        const float s = score32(b, m), slack = slack32(b, m);
+        if (s == -INFINITY) return s;
+        best = fmaxf(best, s - slack);
+        return s + slack;
+    };
+#pragma unroll
+    for (int k = 0; k < kPickHeld; ++k) held[k] = rate(tid + k * kPickThreads, held[k]);
+    for (int i = tid + kPickHeld * kPickThreads; i < total; i += kPickThreads) rate(i, __ldcg(&chunk_max[i]));
+    if (tid < a.beams && sh.rec[tid].kind == kFinished) best = fmaxf(best, sh.rec[tid].base);
+    const float bound = nth_bound(best, a.n_out, sh);
     if (sh.bad) {                                                 // (its last write is before the barriers above)
         if (tid < a.n_out) {
             const size_t o = (size_t)item * a.n_out + tid;
@@ -478,41 +601,50 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
             a.out_scores[o] = __int_as_float(0x7FC00000);
         }
         if (tid == 0 && a.status) atomicOr(&a.status[item], sh.bad);
-        return;
+        return 0;
     }
-    // the groups that may reach it
-    for (int i = tid; i < total; i += kPickThreads) {
-        const int b = i / a.groups;
-        if (sh.kind[b] != kLive) continue;
-        const float m = a.group_max[(size_t)row0 * a.groups + i];
-        const float s = score32(sh, b, m);
-        if (s > -INFINITY && s + slack32(sh, b, m) >= bound) {
-            const int at = atomicAdd(&sh.n_groups, 1);
-            if (at < kListCap) sh.group[at] = i;
-        }
+    // Where l - m is near bound - base, score and slack are off by 2^-22 (|base| + |bound - base|).
+    if (tid < a.beams && sh.rec[tid].kind == kLive) {
+        const float base = sh.rec[tid].base, at = bound - base;
+        sh.rec[tid].least = fmaxf(at - (2.f * (float)kSumEps + 0x1p-20f * (fabsf(base) + fabsf(at))), -FLT_MAX);
     }
-    if (tid < a.beams && sh.kind[tid] == kFinished && sh.base32[tid] >= bound) {   // one candidate: base alone
+    // the chunks that may reach it
+    auto keep = [&](int i, float most) {
+        if (!(most >= bound)) return;
+        const int at = atomicAdd(&sh.n_chunks, 1);
+        if (at < kChunkCap) sh.chunk[at] = i;
+    };
+#pragma unroll
+    for (int k = 0; k < kPickHeld; ++k) keep(tid + k * kPickThreads, held[k]);
+    for (int i = tid + kPickHeld * kPickThreads; i < total; i += kPickThreads) keep(i, rate(i, __ldcg(&chunk_max[i])));
+    if (tid < a.beams && sh.rec[tid].kind == kFinished && sh.rec[tid].base >= bound) {   // one candidate: base alone
         const int at = atomicAdd(&sh.n_elems, 1);
         sh.flat[at] = (uint32_t)tid * (uint32_t)a.vocab + (uint32_t)a.end_token;
         sh.logit[at] = 0.f;
+        sh.beam[at] = (uint8_t)tid;
     }
     __syncthreads();
-    bool hard = sh.n_groups > kListCap;
+    bool hard = sh.n_chunks > kChunkCap;
     if (!hard) {
-        for (int g = warp; g < sh.n_groups; g += kPickThreads / 32) {
-            const int b = sh.group[g] / a.groups, vec = (sh.group[g] - b * a.groups) * 32 + lane;
+        for (int k = warp; k < sh.n_chunks; k += kPickThreads / 32) {   // a warp a chunk
+            const int i = sh.chunk[k], b = beam_of(i), c = i - b * a.chunks;
             const Row<DT> row(a, item, b);
-            const uint4 v = row.vec(vec);
+            uint4 v[kVecs];
+            row.chunk(c, v);
+            const float top = sh.rec[b].top, least = sh.rec[b].least;
+            auto reaches = [&](float l) { return fmaxf(l - top, -FLT_MAX) >= least; };   // (-inf too, where the bound is none)
 #pragma unroll
-            for (int q = 0; q < Elem<DT>::kPerVec; ++q) {
-                const float l = vec_at<DT>(v, q);
-                const float s = score32(sh, b, l);
-                if (s > -INFINITY && s + slack32(sh, b, l) >= bound) {
+            for (int g = 0; g < kVecs; ++g) {
+                if (!reaches(vec_max<DT>(v[g]))) continue;
+#pragma unroll
+                for (int q = 0; q < Elem<DT>::kPerVec; ++q) {
+                    const float l = vec_at<DT>(v[g], q);
+                    if (!reaches(l) || l == -INFINITY) continue;
                     const int at = atomicAdd(&sh.n_elems, 1);
-                    if (at < kListCap) {
-                        sh.flat[at] = (uint32_t)b * (uint32_t)a.vocab + (uint32_t)(vec * Elem<DT>::kPerVec + q - row.off);
-                        sh.logit[at] = l;
-                    }
+                    if (at >= kListCap) continue;
+                    sh.flat[at] = (uint32_t)b * (uint32_t)a.vocab + (uint32_t)(row.vec_first(c, g) + q);
+                    sh.logit[at] = l;
+                    sh.beam[at] = (uint8_t)b;
                 }
             }
         }
@@ -520,41 +652,58 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     __syncthreads();
     const int n = sh.n_elems;
     hard = hard || n > kListCap;
-    const Entries e{sh.key, sh.flat, sh.logit};
+    const Entries e = sh.entries();
     if (!hard) {
-        for (int i = tid; i < n; i += kPickThreads)
-            sh.key[i] = score_key(sh, (int)(sh.flat[i] / (uint32_t)a.vocab), sh.logit[i]);
-        sort_entries(e, n);
+        for (int i = tid; i < n; i += kPickThreads) sh.key[i] = score_key(sh, sh.beam[i], sh.logit[i]);
+        sort_entries(e, n, sh.order);
         // neighbours of two beams that the normalisers' errors may have put the wrong way round
-        for (int i = tid; i + 1 < n && i < a.n_out; i += kPickThreads) {
-            const int b0 = (int)(sh.flat[i] / (uint32_t)a.vocab), b1 = (int)(sh.flat[i + 1] / (uint32_t)a.vocab);
+        for (int k = tid; k + 1 < n && k < a.n_out; k += kPickThreads) {
+            const int i0 = sh.order[k], i1 = sh.order[k + 1];
+            const double s0 = f64_of_key(sh.key[i0]), s1 = f64_of_key(sh.key[i1]);
+            if (s0 - s1 > 4.0 * kSumEps + 0x1p-50 * fabs(s1)) continue;
+            const int b0 = sh.beam[i0], b1 = sh.beam[i1];
             if (b0 == b1) continue;
-            const double e0 = sh.kind[b0] == kLive ? kSumEps : 0.0, e1 = sh.kind[b1] == kLive ? kSumEps : 0.0;
-            const double l0 = (double)sh.logit[i] - (double)sh.top[b0], l1 = (double)sh.logit[i + 1] - (double)sh.top[b1];
+            const bool live0 = sh.rec[b0].kind == kLive, live1 = sh.rec[b1].kind == kLive;
+            const double e0 = live0 ? kSumEps : 0.0, e1 = live1 ? kSumEps : 0.0;
+            const double l0 = (double)sh.logit[i0] - (double)sh.rec[b0].top, l1 = (double)sh.logit[i1] - (double)sh.rec[b1].top;
             const double lo0 = (sh.base[b0] - e0) + l0, hi0 = (sh.base[b0] + e0) + l0;
             const double lo1 = (sh.base[b1] - e1) + l1, hi1 = (sh.base[b1] + e1) + l1;
             if (hi1 < lo0 || (lo0 == hi0 && lo1 == hi1)) continue;
-            if (sh.kind[b0] == kLive) atomicOr(&sh.mask[b0 >> 5], 1u << (b0 & 31));
-            if (sh.kind[b1] == kLive) atomicOr(&sh.mask[b1 >> 5], 1u << (b1 & 31));
+            if (live0) atomicOr(&sh.mask[b0 >> 5], 1u << (b0 & 31));
+            if (live1) atomicOr(&sh.mask[b1 >> 5], 1u << (b1 & 31));
         }
-    } else if (tid < a.beams && sh.kind[tid] == kLive) {
+    } else if (tid < a.beams && sh.rec[tid].kind == kLive) {
         atomicOr(&sh.mask[tid >> 5], 1u << (tid & 31));
     }
     __syncthreads();
     const int again = __popc(sh.mask[0]) + __popc(sh.mask[1]) + __popc(sh.mask[2]) + __popc(sh.mask[3]);
-    if (again == 0) {
-        write_item<DT>(a, item, e, n, sh.kind, sh.scratch);
-        return;
-    }
+    if (again == 0) write_item<DT>(a, item, e, n, sh);
+    else if (tid == 0 && hard) sh.n_elems = -1;
+    return again;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ BeamArgs a)
+{
+    __shared__ PickShared sh;
+    pdl_enter();
+    const int tid = threadIdx.x, item = blockIdx.x, row0 = item * a.beams;
+    const int again = pick_item<DT>(a, item, sh);
+    if (again == 0) return;
     // refine_kernel finishes the item
-    if (!hard)
-        for (int i = tid; i < n; i += kPickThreads) {
-            a.list_flat[(size_t)item * kListCap + i] = (int32_t)sh.flat[i];
-            a.list_logit[(size_t)item * kListCap + i] = sh.logit[i];
-        }
+    __syncthreads();
+    const int n = sh.n_elems;
+    for (int i = tid; i < n; i += kPickThreads) {
+        a.list_flat[(size_t)item * kListCap + i] = (int32_t)sh.flat[i];
+        a.list_logit[(size_t)item * kListCap + i] = sh.logit[i];
+    }
+    if (tid < a.beams) {
+        a.rec[row0 + tid] = sh.rec[tid];
+        a.base[row0 + tid] = sh.base[tid];
+    }
     if (tid < 4) a.item_mask[item * 4 + tid] = sh.mask[tid];
     if (tid == 0) {
-        a.item_list[item] = hard ? -1 : n;
+        a.item_list[item] = n;
         a.item_units[item] = again * a.refine_segs;
         sh.flag_at = atomicAdd(a.n_flagged, again);
     }
@@ -593,7 +742,7 @@ __device__ void block_best(unsigned long long& key, uint32_t& place, unsigned lo
 }
 
 // An item with more candidates at its bound than a list holds (rows of few
-// distinct values): its n_out best groups one after the other, then the n_out
+// distinct values): its n_out best chunks one after the other, then the n_out
 // best of their elements.  Returns how many there are.
 template <int DT>
 __device__ int pick_by_turns(const BeamArgs& a, int item, PickShared& sh)
@@ -603,16 +752,16 @@ __device__ int pick_by_turns(const BeamArgs& a, int item, PickShared& sh)
     const int tid = threadIdx.x, row0 = item * a.beams;
     unsigned long long last_key = ~0ull;
     uint32_t last = 0u;
-    int n_groups = 0;
-    const int total = a.beams * a.groups;
-    for (; n_groups < a.n_out; ++n_groups) {
+    int n_chunks = 0;
+    const int total = a.beams * a.chunks;
+    for (; n_chunks < a.n_out; ++n_chunks) {
         unsigned long long key = 0ull;
         uint32_t place = 0xFFFFFFFFu;
         for (int i = tid; i < total; i += kPickThreads) {
-            const int b = i / a.groups;
+            const int b = i / a.chunks;
             float m;
-            if (sh.kind[b] == kLive) m = a.group_max[(size_t)row0 * a.groups + i];
-            else if (sh.kind[b] == kFinished && i == b * a.groups) m = 0.f;
+            if (sh.rec[b].kind == kLive) m = a.chunk_max[(size_t)row0 * a.chunks + i];
+            else if (sh.rec[b].kind == kFinished && i == b * a.chunks) m = 0.f;
             else continue;
             if (m == -INFINITY) continue;
             const unsigned long long k = score_key(sh, b, m);
@@ -624,7 +773,7 @@ __device__ int pick_by_turns(const BeamArgs& a, int item, PickShared& sh)
         }
         block_best(key, place, s_key, s_place);
         if (place == 0xFFFFFFFFu) break;
-        if (tid == 0) sh.group[n_groups] = (int)place;
+        if (tid == 0) sh.chunk[n_chunks] = (int)place;
         last_key = key;
         last = place;
     }
@@ -635,33 +784,37 @@ __device__ int pick_by_turns(const BeamArgs& a, int item, PickShared& sh)
     for (; n < a.n_out; ++n) {
         unsigned long long key = 0ull;
         uint32_t place = 0xFFFFFFFFu;
-        for (int i = tid; i < n_groups * 32; i += kPickThreads) {
-            const int b = sh.group[i >> 5] / a.groups;
-            const int vec = (sh.group[i >> 5] - b * a.groups) * 32 + (i & 31);
+        for (int k = tid >> 5; k < n_chunks; k += kPickThreads / 32) {
+            const int b = sh.chunk[k] / a.chunks, c = sh.chunk[k] - b * a.chunks;
             auto look = [&](float l, int token) {
                 if (l == -INFINITY) return;
-                const unsigned long long k = score_key(sh, b, l);
+                const unsigned long long x = score_key(sh, b, l);
                 const uint32_t p = (uint32_t)b * (uint32_t)a.vocab + (uint32_t)token;
-                if (!(k < last_key || (k == last_key && p > last))) return;
-                if (k > key || (k == key && p < place)) {
-                    key = k;
+                if (!(x < last_key || (x == last_key && p > last))) return;
+                if (x > key || (x == key && p < place)) {
+                    key = x;
                     place = p;
                 }
             };
-            if (sh.kind[b] == kFinished) {
-                if ((i & 31) == 0) look(0.f, a.end_token);
+            if (sh.rec[b].kind == kFinished) {
+                look(0.f, a.end_token);
                 continue;
             }
             const Row<DT> row(a, item, b);
-            const uint4 v = row.vec(vec);
+            uint4 v[kVecs];
+            row.chunk(c, v);
 #pragma unroll
-            for (int q = 0; q < Elem<DT>::kPerVec; ++q) look(vec_at<DT>(v, q), vec * Elem<DT>::kPerVec + q - row.off);
+            for (int g = 0; g < kVecs; ++g)
+#pragma unroll
+                for (int q = 0; q < Elem<DT>::kPerVec; ++q) look(vec_at<DT>(v[g], q), row.vec_first(c, g) + q);
         }
         block_best(key, place, s_key, s_place);
         if (place == 0xFFFFFFFFu) break;
         if (tid == 0) {
             sh.key[n] = key;
             sh.flat[n] = place;
+            sh.beam[n] = (uint8_t)(place / (uint32_t)a.vocab);
+            sh.order[n] = (uint16_t)n;
         }
         last_key = key;
         last = place;
@@ -670,9 +823,63 @@ __device__ int pick_by_turns(const BeamArgs& a, int item, PickShared& sh)
     return n;
 }
 
-// Normalisers of the flagged rows again, then their items' order.  A term is a
-// double-float (2^-46 of itself) cut to units of 2^-58, so the sum of 2^19 is
-// good to 2^-39 of itself, and scores to 2e-12.
+// The sum of a segment of a row again, by one CTA: a term is a double-float
+// (2^-46 of itself) cut to units of 2^-58, so the sum of 2^19 is good to 2^-39
+// of itself, and scores to 2e-12.
+template <int DT>
+__device__ void refine_segment(const BeamArgs& a, int row_no, int seg, float top, const dfloat* tab, ulonglong2* part)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Row<DT> row(a, row_no / a.beams, row_no % a.beams);
+    unsigned long long sum = 0ull;                    // of up to 8 terms: below 2^62
+#pragma unroll 2
+    for (int k = 0; k < kRefineElems / kPickThreads; ++k) {
+        const float l = row.elem(seg * kRefineElems + k * kPickThreads + tid);
+        if (l > -INFINITY) sum += fix_df(exp_df(df_two_sum(l, -top), tab), 0x1p58f);   // (what lies outside the row is -inf)
+    }
+    const unsigned long long high = warp_sum_u64(sum >> 32), low = warp_sum_u64(sum & 0xFFFFFFFFull);
+    __syncthreads();
+    if (lane == 0) part[warp] = make_ulonglong2(high, low);
+    __syncthreads();
+    if (tid == 0) {
+        ulonglong2 all = part[0];
+        for (int w = 1; w < kPickThreads / 32; ++w) {
+            all.x += part[w].x;
+            all.y += part[w].y;
+        }
+        a.refined[(size_t)row_no * a.refine_segs + seg] = all;
+    }
+}
+
+// An item's outputs once its rows are summed again; its records and candidates (n, or -1) are in shared memory.
+template <int DT>
+__device__ void finish_item(const BeamArgs& a, int item, int n, PickShared& sh)
+{
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid < a.beams && (sh.mask[tid >> 5] >> (tid & 31) & 1u)) {
+        const int r = item * a.beams + tid;
+        unsigned long long high = 0ull, low = 0ull;
+        for (int i = 0; i < a.refine_segs; ++i) {
+            const ulonglong2 x = __ldcg(&a.refined[(size_t)r * a.refine_segs + i]);
+            high += x.x;
+            low += x.y;
+        }
+        sh.base[tid] = (double)a.scores[r] - log((double)high * 0x1p-26 + (double)low * 0x1p-58);
+    }
+    __syncthreads();
+    const Entries e = sh.entries();
+    if (n >= 0) {
+        for (int i = tid; i < n; i += kPickThreads) sh.key[i] = score_key(sh, sh.beam[i], sh.logit[i]);
+        sort_entries(e, n, sh.order);
+    } else {
+        n = pick_by_turns<DT>(a, item, sh);
+    }
+    write_item<DT>(a, item, e, n, sh);
+    __syncthreads();
+}
+
+// The flagged rows of all items; the CTA that sums an item's last segment finishes the item.
 template <int DT>
 __global__ void __launch_bounds__(kPickThreads) refine_kernel(const __grid_constant__ BeamArgs a)
 {
@@ -681,82 +888,82 @@ __global__ void __launch_bounds__(kPickThreads) refine_kernel(const __grid_const
     __shared__ ulonglong2 part[kPickThreads / 32];
     __shared__ int last;
     pdl_enter();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const long long units = (long long)*a.n_flagged * a.refine_segs;
     if (blockIdx.x >= units) return;
     fill_exp_table(tab);
     __syncthreads();
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const int f = (int)(u / a.refine_segs), seg = (int)(u - (long long)f * a.refine_segs);
-        const int row_no = a.flagged[f], item = row_no / a.beams;
-        const float m = a.row_max[row_no];
-        const Row<DT> row(a, item, row_no - item * a.beams);
-        unsigned long long sum = 0ull;                    // of up to 8 terms: below 2^62
-#pragma unroll 2
-        for (int k = 0; k < kRefineElems / kPickThreads; ++k) {
-            const float l = row.elem(seg * kRefineElems + k * kPickThreads + tid);
-            const float d = fmaxf(l, -FLT_MAX);           // -inf and what lies outside the row
-            if (l > -INFINITY) sum += fix_df(exp_df(df_two_sum(d, -m), tab), 0x1p58f);
-        }
-        const unsigned long long high = warp_sum_u64(sum >> 32), low = warp_sum_u64(sum & 0xFFFFFFFFull);
-        __syncthreads();
-        if (lane == 0) part[warp] = make_ulonglong2(high, low);
-        __syncthreads();
+        const int row_no = a.flagged[f], item = row_no / a.beams, row0 = item * a.beams;
+        refine_segment<DT>(a, row_no, seg, a.rec[row_no].top, tab, part);
         if (tid == 0) {
-            ulonglong2 all = part[0];
-            for (int w = 1; w < kPickThreads / 32; ++w) {
-                all.x += part[w].x;
-                all.y += part[w].y;
-            }
-            a.refined[(size_t)row_no * a.refine_segs + seg] = all;
             __threadfence();
             last = atomicAdd(&a.item_done[item], 1) == a.item_units[item] - 1;
             __threadfence();
         }
         __syncthreads();
         if (!last) continue;
-        // the item's rows are all there
+        const int n = a.item_list[item];
+        for (int i = tid; i < n; i += kPickThreads) {
+            const uint32_t p = (uint32_t)a.list_flat[(size_t)item * kListCap + i];
+            sh.flat[i] = p;
+            sh.logit[i] = a.list_logit[(size_t)item * kListCap + i];
+            sh.beam[i] = (uint8_t)(p / (uint32_t)a.vocab);
+        }
         if (tid < a.beams) {
-            const int r = item * a.beams + tid;
-            float score;
-            int kind = beam_kind(a, r, &score);
-            double base = a.base[r];
-            if (a.item_mask[item * 4 + (tid >> 5)] >> (tid & 31) & 1u) {
-                unsigned long long high = 0ull, low = 0ull;
-                for (int i = 0; i < a.refine_segs; ++i) {
-                    const ulonglong2 x = __ldcg(&a.refined[(size_t)r * a.refine_segs + i]);
-                    high += x.x;
-                    low += x.y;
-                }
-                base = (double)score - log((double)high * 0x1p-26 + (double)low * 0x1p-58);
-            } else if (kind == kLive && base == INFINITY) {
-                kind = kDead;
-            }
-            sh.kind[tid] = kind;
-            sh.base[tid] = base;
-            sh.top[tid] = a.row_max[r];
+            sh.rec[tid] = a.rec[row0 + tid];
+            sh.base[tid] = a.base[row0 + tid];
         }
-        __syncthreads();
-        const Entries e{sh.key, sh.flat, sh.logit};
-        int n = a.item_list[item];
-        if (n >= 0) {
-            for (int i = tid; i < n; i += kPickThreads) {
-                const uint32_t p = (uint32_t)a.list_flat[(size_t)item * kListCap + i];
-                sh.flat[i] = p;
-                sh.logit[i] = a.list_logit[(size_t)item * kListCap + i];
-                sh.key[i] = score_key(sh, (int)(p / (uint32_t)a.vocab), sh.logit[i]);
-            }
-            sort_entries(e, n);
-        } else {
-            n = pick_by_turns<DT>(a, item, sh);
-        }
-        write_item<DT>(a, item, e, n, sh.kind, sh.scratch);
-        __syncthreads();
+        if (tid < 4) sh.mask[tid] = a.item_mask[item * 4 + tid];
+        finish_item<DT>(a, item, n, sh);
     }
 }
 
+// All of it in one launch, a cluster an item: its CTAs scan the item's rows, the
+// first of them picks, and all sum rows again where that is needed.
+template <int DT>
+__global__ void __launch_bounds__(kPickThreads) select_kernel(const __grid_constant__ BeamArgs a)
+{
+    __shared__ PickShared sh;
+    __shared__ dfloat tab[64];
+    __shared__ ulonglong2 part[kPickThreads / 32];
+    pdl_enter();
+    const int tid = threadIdx.x;
+    uint32_t rank, size;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+    const int item = blockIdx.x / size, row0 = item * a.beams;
+    scan_rows<DT>(a, row0, a.beams, (int)rank * (kPickThreads / 32) + (tid >> 5), (int)size * (kPickThreads / 32));
+    cluster_sync();
+    int again = 0;
+    if (rank == 0) {
+        again = pick_item<DT>(a, item, sh);
+        if (tid == 0) a.item_units[item] = again;
+        if (again) {
+            if (tid < 4) a.item_mask[item * 4 + tid] = sh.mask[tid];
+            if (tid < a.beams) a.rec[row0 + tid] = sh.rec[tid];
+        }
+    }
+    cluster_sync();
+    again = __ldcg(&a.item_units[item]);
+    if (again == 0) return;
+    fill_exp_table(tab);
+    __syncthreads();
+    const int units = again * a.refine_segs;
+    for (int u = (int)rank; u < units; u += (int)size) {
+        int f = u / a.refine_segs, b = 0;
+        const int seg = u - f * a.refine_segs;
+        for (;; ++b)                                   // the f-th flagged beam
+            if ((__ldcg(&a.item_mask[item * 4 + (b >> 5)]) >> (b & 31) & 1u) && f-- == 0) break;
+        refine_segment<DT>(a, row0 + b, seg, __ldcg(&a.rec[row0 + b].top), tab, part);
+    }
+    cluster_sync();
+    if (rank == 0) finish_item<DT>(a, item, sh.n_elems, sh);
+}
+
 struct BeamLayout {
-    size_t head, item_units, item_done, item_list, item_mask, flagged, row_max, base, sums, group_max, list_logit,
+    size_t head, item_units, item_done, item_list, item_mask, flagged, rec, base, sums, chunk_max, list_logit,
         list_flat, refined, total;
 };
 
@@ -777,15 +984,32 @@ BeamLayout beam_layout(int n, int beams, int vocab)
     L.item_list = take(4 * (size_t)n);
     L.item_mask = take(16 * (size_t)n);
     L.flagged = take(4 * rows);
-    L.row_max = take(4 * rows);
+    L.rec = take(sizeof(BeamRec) * rows);
     L.base = take(8 * rows);
     L.sums = take(8 * rows * chunks);
-    L.group_max = take(4 * rows * chunks * kVecs);
+    L.chunk_max = take(4 * rows * chunks);
     L.list_logit = take(4 * (size_t)n * kListCap);
     L.list_flat = take(4 * (size_t)n * kListCap);
     L.refined = take(16 * rows * (((size_t)vocab + kRefineElems - 1) / kRefineElems));
     L.total = off;
     return L;
+}
+
+cudaError_t launch_cluster(void (*kernel)(BeamArgs), int grid, int cluster, cudaStream_t s, const BeamArgs& a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    pdl_attr(at[0]);
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int DT>
@@ -795,12 +1019,21 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
     const int sms = sm_count();
     const long long rows = (long long)a.n * a.beams;
     a.chunks = (a.vocab + E::kPerVec - 1 + E::kChunk - 1) / E::kChunk;
-    a.groups = a.chunks * kVecs;
-    const long long warps = (long long)sms * 4 * (kScanThreads / 32);
-    long long per = rows * a.chunks / (4 * warps);
-    a.seg_chunks = (int)(per < 1 ? 1 : per > kMaxSegChunks ? kMaxSegChunks : per);
-    a.segs = (a.chunks + a.seg_chunks - 1) / a.seg_chunks;
     a.refine_segs = (a.vocab + kRefineElems - 1) / kRefineElems;
+    auto segments = [&](long long chunks_a_warp) {
+        a.seg_chunks = (int)(chunks_a_warp < 1 ? 1 : chunks_a_warp > kMaxSegChunks ? kMaxSegChunks : chunks_a_warp);
+        a.segs = (a.chunks + a.seg_chunks - 1) / a.seg_chunks;
+    };
+    // Items that fit the GPU at once, and whose clusters read them in little time
+    const int cluster = a.n * 8 <= sms ? 8 : 4;
+    const int item_warps = cluster * (kPickThreads / 32);
+    const long long item_chunks = (long long)a.beams * a.chunks;
+    if (a.n * cluster <= sms && item_chunks <= 8LL * item_warps) {
+        segments(item_chunks / item_warps);
+        return launch_cluster(select_kernel<DT>, a.n * cluster, cluster, s, a);
+    }
+    const long long warps = (long long)sms * 4 * (kScanThreads / 32);
+    segments(rows * a.chunks / (4 * warps));
     const long long units = rows * a.segs;
     long long grid = (units + kScanThreads / 32 - 1) / (kScanThreads / 32);
     if (grid > 4LL * sms) grid = 4LL * sms;
@@ -808,7 +1041,7 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     e = launch_pdl(pick_kernel<DT>, dim3(a.n), dim3(kPickThreads), 0, s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(refine_kernel<DT>, dim3(2 * sms), dim3(kPickThreads), 0, s, a);
+    return launch_pdl(refine_kernel<DT>, dim3(sms), dim3(kPickThreads), 0, s, a);
 }
 
 bool beam_sizes_ok(int n, int beams, int vocab, int n_out)
@@ -968,10 +1201,10 @@ extern "C" sv_status_t sv_beam_select(const void* logits, sv_dtype_t dt, int64_t
     a.item_list = reinterpret_cast<int32_t*>(w + L.item_list);
     a.item_mask = reinterpret_cast<uint32_t*>(w + L.item_mask);
     a.flagged = reinterpret_cast<int32_t*>(w + L.flagged);
-    a.row_max = reinterpret_cast<float*>(w + L.row_max);
+    a.rec = reinterpret_cast<BeamRec*>(w + L.rec);
     a.base = reinterpret_cast<double*>(w + L.base);
     a.sums = reinterpret_cast<float2*>(w + L.sums);
-    a.group_max = reinterpret_cast<float*>(w + L.group_max);
+    a.chunk_max = reinterpret_cast<float*>(w + L.chunk_max);
     a.list_logit = reinterpret_cast<float*>(w + L.list_logit);
     a.list_flat = reinterpret_cast<int32_t*>(w + L.list_flat);
     a.refined = reinterpret_cast<ulonglong2*>(w + L.refined);
