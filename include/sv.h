@@ -716,7 +716,7 @@ size_t sv_kv_fork_workspace_size(int n_req, int max_pages, int n_pages);
  *   holds are left as they are), held, ref_count, copies (device) int32
  *   [n_req][3]; status (device) int32 [n_req] or NULL, bits OR-ed in.
  *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes; SV_ERR_UNSUPPORTED for
- *   n_req > 65,536, n_pages or n_req * max_pages > 2^30.  Workspace:
+ *   n_req > 16,384, n_pages > 2^30 or n_req * max_pages > 2^28.  Workspace:
  *   sv_kv_fork_workspace_size(...).
  */
 sv_status_t sv_kv_fork(sv_page_pool_t pool, const int32_t* parent, int group, const int32_t* keep_len,

@@ -9,10 +9,10 @@
 //      does not hold; what changes of a table row is set aside;
 //   2  the rows set aside are written, begun pages count their writers, the pool's
 //      free pages are counted by tiles;
-//   3  each request's new pages get their place in the line of free pages;
-//   4  the free pages go to their places.
-// They are four kernels for large batches and pools, and one CTA with barriers
-// between them for small ones, where launches are what counts.
+//   3  each request's new pages get their place in the line of free pages (every
+//      CTA works out the whole line), and the free pages go to their places.
+// They are three kernels for large batches and pools, and one cluster with its
+// barriers between them for others, where latencies and launches are what counts.
 //
 // The copies are HBM-bound; see the kernels.
 #include "sv_attn.cuh"
@@ -25,7 +25,16 @@ constexpr int kForkThreads = 1024;
 constexpr int kTileCols = 256;        // columns of a table row a warp takes
 constexpr int kTileWords = kTileCols / 32;
 constexpr int kTilePages = 4 * kForkThreads;   // pages of the pool a CTA takes
-constexpr int kForkMaxReq = 1 << 16;
+constexpr int kForkMaxReq = 1 << 14;  // their places in the line fit shared memory
+constexpr int kForkCluster = 16;
+
+// What step 1 and 2 know of a request.
+struct __align__(16) Need {
+    int begun;      // page that it would write on, -1 for none
+    int kept;       // columns kept
+    int want;       // columns to hold, -1: its count of pages is not one and stays
+    int holders;    // of the begun page
+};
 
 struct ForkArgs {
     sv_page_pool_t pool;
@@ -36,21 +45,15 @@ struct ForkArgs {
     int32_t* copies;
     int32_t* status;
     // workspace
-    int32_t* kept;         // [n_req] columns kept
-    int32_t* want;         // [n_req] columns to hold, -1: the count is not a count and stays
-    int32_t* begun;        // [n_req] page that the request would write on, -1 for none
-    int32_t* first;        // [n_req] place in the line of free pages
-    int32_t* how;          // [n_req] kCopy | kServed
+    Need* need;            // [n_req]
     int32_t* staged;       // [n_req][max_pages] new entries
     uint32_t* changed;     // [n_req][words] which of them
     int32_t* writers;      // [n_pages], of begun pages only
     unsigned long long* best;   // [n_pages], of begun pages only
-    int32_t* tile_free;    // [tiles] free pages of a tile, then of the tiles before it
-    int32_t* line;         // [1] length of the line
+    int32_t* tile_free;    // [tiles] free pages of a tile
+    int32_t* tile_before;  // [tiles] free pages of the tiles before it
     int col_tiles, words, page_tiles;
 };
-enum { kCopy = 1, kServed = 2 };
-
 struct Plan {
     int from, kept, want, held;
     bool bad, lost;
@@ -59,7 +62,7 @@ struct Plan {
 __device__ __forceinline__ Plan plan_of(const ForkArgs& a, int r)
 {
     const int n = a.pool.n_req;
-    const long long page = a.pool.page_size;
+    const uint32_t page = (uint32_t)a.pool.page_size;
     Plan p;
     p.from = r;
     p.held = a.pool.held[r];
@@ -74,18 +77,24 @@ __device__ __forceinline__ Plan plan_of(const ForkArgs& a, int r)
         from = low + q;
         if (from >= n) p.bad = true;
     }
-    const long long keep = a.keep_len[r], room = a.new_len[r];
+    const int keep = a.keep_len[r], room = a.new_len[r];
     if (p.bad) return p;
     const int avail = a.pool.held[from];
-    if (avail < 0 || avail > a.pool.max_pages || keep < 0 || keep > avail * page || room < keep ||
-        room > a.pool.max_pages * page) {
+    if (avail < 0 || avail > a.pool.max_pages || keep < 0 || keep > (long long)avail * page || room < keep ||
+        room > (long long)a.pool.max_pages * page) {
         p.bad = true;
         return p;
     }
     p.from = (int)from;
-    p.kept = (int)((keep + page - 1) / page);
-    p.want = (int)((room + page - 1) / page);
+    p.kept = (int)(((uint32_t)keep + page - 1u) / page);          // (both below 2^31)
+    p.want = (int)(((uint32_t)room + page - 1u) / page);
     return p;
+}
+
+__device__ __forceinline__ Need load_need(const ForkArgs& a, int r)
+{
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(&a.need[r]));
+    return Need{x.x, x.y, x.z, x.w};
 }
 
 __device__ __forceinline__ bool in_pool(const ForkArgs& a, int page) { return page >= 0 && page < a.pool.n_pages; }
@@ -107,9 +116,7 @@ __device__ __forceinline__ void fork_holders(const ForkArgs& a, int warp, int wa
                 begun = theirs[p.kept - 1];
                 if (!in_pool(a, begun)) begun = -1;
             }
-            a.kept[r] = p.kept;
-            a.want[r] = p.lost ? -1 : p.want;
-            a.begun[r] = begun;
+            a.need[r] = Need{begun, p.kept, p.lost ? -1 : p.want, 0};
             if (begun >= 0) {
                 a.writers[begun] = 0;
                 a.best[begun] = 0ull;
@@ -162,8 +169,9 @@ __device__ __forceinline__ void fork_rows(const ForkArgs& a, int warp, int warps
     for (long long u = warp; u < units; u += warps) {
         const int r = (int)(u / a.col_tiles), c0 = (int)(u - (long long)r * a.col_tiles) * kTileCols;
         if (c0 == 0 && lane == 0) {
-            const int p = __ldcg(&a.begun[r]);
+            const int p = __ldcg(&a.need[r].begun);
             if (p >= 0) {
+                a.need[r].holders = __ldcg(&a.pool.ref_count[p]);   // step 3 changes the count itself
                 atomicAdd(&a.writers[p], 1);
                 atomicMax(&a.best[p], (unsigned long long)(uint32_t)a.keep_len[r] << 32 | (uint32_t)(kForkMaxReq - r));
             }
@@ -231,86 +239,77 @@ __device__ __forceinline__ void fork_count(const ForkArgs& a, int block, int blo
     }
 }
 
-// Step 3, one CTA: who copies, the line of new pages, who is served.
-__device__ __forceinline__ void fork_line(const ForkArgs& a, int* s_warp)
+// Step 3: who copies, the line of new pages, who is served; then the j-th free page
+// goes to the request whose part of the line holds j.
+__device__ void fork_assign(const ForkArgs& a, int block, int blocks, int* s_warp, int* s_list, int* s_first)
 {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, n = a.pool.n_req;
     int n_free = 0, line = 0, total;
     for (int t0 = 0; t0 < a.page_tiles; t0 += kForkThreads) {
         const int t = t0 + tid;
-        const int x = t < a.page_tiles ? __ldcg(&a.tile_free[t]) : 0;
-        const int before = block_before(x, &total, s_warp);
-        if (t < a.page_tiles) a.tile_free[t] = n_free + before;
+        const int before = block_before(t < a.page_tiles ? __ldcg(&a.tile_free[t]) : 0, &total, s_warp);
+        if (t < a.page_tiles) a.tile_before[t] = n_free + before;  // every CTA writes the same and reads its own
         n_free += total;
     }
-    for (int r0 = 0; r0 < a.pool.n_req; r0 += kForkThreads) {
+    for (int r0 = 0; r0 < n; r0 += kForkThreads) {
         const int r = r0 + tid;
-        int need = 0, how = 0, begun = -1, kept = 0, want = 0, keep = 0;
-        bool lost = false;
-        if (r < a.pool.n_req) {
-            begun = __ldcg(&a.begun[r]);
-            kept = __ldcg(&a.kept[r]);
-            want = __ldcg(&a.want[r]);
-            lost = want < 0;
-            if (lost) want = kept;
+        int need = 0, copy = 0, keep = 0;
+        Need m{-1, 0, 0, 0};
+        if (r < n) {
+            m = load_need(a, r);
             keep = a.keep_len[r];
-            if (begun >= 0) {
-                const bool only_writers = __ldcg(&a.writers[begun]) == __ldcg(&a.pool.ref_count[begun]);
+            if (m.begun >= 0) {
                 const unsigned long long rank = (unsigned long long)(uint32_t)keep << 32 | (uint32_t)(kForkMaxReq - r);
-                if (!only_writers || __ldcg(&a.best[begun]) != rank) how = kCopy;
+                copy = __ldcg(&a.writers[m.begun]) != m.holders || __ldcg(&a.best[m.begun]) != rank;
             }
-            need = want - kept + (how & kCopy);
+            need = max(m.want, m.kept) - m.kept + copy;
         }
         const int first = line + block_before(need, &total, s_warp);
         line += total;
-        if (r < a.pool.n_req) {
-            if (need == 0 || first + need <= n_free) how |= kServed;
-            const bool served = how & kServed, copy = how == (kCopy | kServed);
-            a.first[r] = first;
-            a.how[r] = how;
-            if (!lost) a.pool.held[r] = served ? want : kept;
-            a.copies[3 * r] = copy ? begun : -1;
-            a.copies[3 * r + 1] = -1;
-            a.copies[3 * r + 2] = copy ? keep % a.pool.page_size : -1;
-            if (!served && a.status) atomicOr(&a.status[r], SV_ROW_NO_PAGES);
+        if (r < n) {
+            // the place, the copy's bit, and the one of a request that the free pages do not reach to
+            const bool served = need == 0 || first + need <= n_free;
+            s_first[r] = first << 2 | copy << 1 | (served ? 0 : 1);
+            if (block == 0) {
+                if (m.want >= 0) a.pool.held[r] = served ? m.want : m.kept;
+                const bool copies = copy && served;
+                a.copies[3 * r] = copies ? m.begun : -1;
+                if (!copies) a.copies[3 * r + 1] = -1;
+                a.copies[3 * r + 2] = copies ? keep % a.pool.page_size : -1;
+                if (!served && a.status) atomicOr(&a.status[r], SV_ROW_NO_PAGES);
+            }
         }
     }
-    if (tid == 0) *a.line = line;
-}
-
-// Step 4: the j-th free page goes to the request whose part of the line holds j.
-__device__ __forceinline__ void fork_assign(const ForkArgs& a, int block, int blocks, int* s_warp)
-{
-    const int line = __ldcg(a.line);
+    __syncthreads();
     for (int tile = block; tile < a.page_tiles; tile += blocks) {
-        const int before = __ldcg(&a.tile_free[tile]);
+        const int before = a.tile_before[tile];
         if (before >= line) return;                             // the tiles after it begin further on
         const uint32_t bits = free_of(a, tile);
-        int total, j = before + block_before(__popc(bits), &total, s_warp);
+        int at = block_before(__popc(bits), &total, s_warp);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!(bits >> i & 1u)) continue;
-            if (j >= line) break;
-            int lo = 0, hi = a.pool.n_req;                      // the last request whose part begins at or before j
+        for (int i = 0; i < 4; ++i)
+            if (bits >> i & 1u) s_list[at++] = tile * kTilePages + tid * 4 + i;
+        __syncthreads();
+        for (int i = tid; i < total && before + i < line; i += kForkThreads) {
+            const int j = before + i;
+            int lo = 0, hi = n;                                 // the last request whose part begins at or before j
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (__ldcg(&a.first[mid]) <= j) lo = mid;
+                if (s_first[mid] >> 2 <= j) lo = mid;
                 else hi = mid;
             }
-            const int how = __ldcg(&a.how[lo]);
-            if (how & kServed) {
-                const int page = tile * kTilePages + (int)threadIdx.x * 4 + i;
-                const int k = j - __ldcg(&a.first[lo]) - (how & kCopy);
-                const int kept = __ldcg(&a.kept[lo]);
-                if (k < 0) {
-                    a.copies[3 * lo + 1] = page;
-                    atomicSub(&a.pool.ref_count[__ldcg(&a.begun[lo])], 1);   // it has other holders: never a free page
-                }
-                a.pool.page_table[(int64_t)lo * a.pool.ld_table + kept + k] = page;
-                a.pool.ref_count[page] = 1;
+            const int f = s_first[lo], copy = f >> 1 & 1;
+            if (f & 1) continue;
+            const Need m = load_need(a, lo);
+            const int page = s_list[i], k = j - (f >> 2) - copy;
+            if (k < 0) {
+                a.copies[3 * lo + 1] = page;
+                atomicSub(&a.pool.ref_count[m.begun], 1);       // it has other holders: never a free page
             }
-            ++j;
+            a.pool.page_table[(int64_t)lo * a.pool.ld_table + m.kept + k] = page;
+            a.pool.ref_count[page] = 1;
         }
+        __syncthreads();
     }
 }
 
@@ -326,34 +325,38 @@ __global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const __grid_co
     fork_rows(a, blockIdx.x * (kForkThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kForkThreads / 32));
     fork_count(a, blockIdx.x, gridDim.x, s_warp);
 }
-__global__ void __launch_bounds__(kForkThreads) fork_line_kernel(const __grid_constant__ ForkArgs a)
-{
-    __shared__ int s_warp[32];
-    pdl_enter();
-    fork_line(a, s_warp);
-}
 __global__ void __launch_bounds__(kForkThreads) fork_assign_kernel(const __grid_constant__ ForkArgs a)
 {
-    __shared__ int s_warp[32];
+    extern __shared__ int s_first[];                             // [n_req]
+    __shared__ int s_warp[32], s_list[kTilePages];
     pdl_enter();
-    fork_assign(a, blockIdx.x, gridDim.x, s_warp);
+    fork_assign(a, blockIdx.x, gridDim.x, s_warp, s_list, s_first);
 }
-__global__ void __launch_bounds__(kForkThreads) fork_small_kernel(const __grid_constant__ ForkArgs a)
+
+__device__ __forceinline__ void cluster_sync()
 {
-    __shared__ int s_warp[32];
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// All steps in one cluster.
+__global__ void __launch_bounds__(kForkThreads) fork_cluster_kernel(const __grid_constant__ ForkArgs a)
+{
+    extern __shared__ int s_first[];
+    __shared__ int s_warp[32], s_list[kTilePages];
     pdl_enter();
-    fork_holders(a, threadIdx.x >> 5, kForkThreads / 32);
-    __syncthreads();
-    fork_rows(a, threadIdx.x >> 5, kForkThreads / 32);
-    fork_count(a, 0, 1, s_warp);
-    __syncthreads();
-    fork_line(a, s_warp);
-    __syncthreads();
-    fork_assign(a, 0, 1, s_warp);
+    const int block = blockIdx.x, blocks = gridDim.x;             // one cluster
+    const int warp = (threadIdx.x >> 5) * blocks + block, warps = blocks * (kForkThreads / 32);
+    fork_holders(a, warp, warps);
+    cluster_sync();
+    fork_rows(a, warp, warps);
+    fork_count(a, block, blocks, s_warp);
+    cluster_sync();
+    fork_assign(a, block, blocks, s_warp, s_list, s_first);
 }
 
 struct ForkLayout {
-    size_t kept, want, begun, first, how, staged, changed, writers, best, tile_free, line, total;
+    size_t need, staged, changed, writers, best, tile_free, tile_before, total;
     int words, page_tiles;
 };
 
@@ -369,17 +372,13 @@ ForkLayout fork_layout(int n_req, int max_pages, int n_pages)
     const size_t n = (size_t)n_req;
     L.words = (max_pages + kTileCols - 1) / kTileCols * kTileWords;
     L.page_tiles = (n_pages + kTilePages - 1) / kTilePages;
-    L.kept = take(4 * n);
-    L.want = take(4 * n);
-    L.begun = take(4 * n);
-    L.first = take(4 * n);
-    L.how = take(4 * n);
+    L.need = take(sizeof(Need) * n);
     L.staged = take(4 * n * (size_t)max_pages);
     L.changed = take(4 * n * (size_t)L.words);
     L.writers = take(4 * (size_t)n_pages);
     L.best = take(8 * (size_t)n_pages);
     L.tile_free = take(4 * (size_t)L.page_tiles);
-    L.line = take(4);
+    L.tile_before = take(4 * (size_t)L.page_tiles);
     L.total = off;
     return L;
 }
@@ -387,24 +386,57 @@ ForkLayout fork_layout(int n_req, int max_pages, int n_pages)
 bool fork_sizes_ok(int n_req, int max_pages, int n_pages)
 {
     return n_req >= 1 && n_req <= kForkMaxReq && max_pages >= 0 && n_pages >= 0 && n_pages <= (1 << 30) &&
-           (long long)n_req * max_pages <= (1LL << 30);
+           (long long)n_req * max_pages <= (1LL << 28);   // (a place in the line is kept in 29 bits)
+}
+
+// What the runtime has to be told of the two kernels, once a device.
+cudaError_t prepare_fork()
+{
+    static bool done[128] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev >= 0 && dev < 128 && done[dev])) return e;
+    constexpr int kSmem = 4 * kForkMaxReq;
+    e = cudaFuncSetAttribute(fork_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fork_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fork_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess && dev >= 0 && dev < 128) done[dev] = true;
+    return e;
 }
 
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s)
 {
+    constexpr int kWarps = kForkThreads / 32;
     const long long units = (long long)a.pool.n_req * a.col_tiles;
-    if (units <= 1024 && a.page_tiles <= 8)
-        return launch_pdl(fork_small_kernel, dim3(1), dim3(kForkThreads), 0, s, a);
+    const size_t smem = 4 * (size_t)a.pool.n_req;
+    cudaError_t e = prepare_fork();
+    if (e != cudaSuccess) return e;
+    if (units <= 2LL * kForkCluster * kWarps && a.page_tiles <= 4 * kForkCluster) {
+        int blocks = 1;
+        while (blocks < kForkCluster && (units > (long long)blocks * kWarps || a.page_tiles > blocks)) blocks *= 2;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(blocks);
+        cfg.blockDim = dim3(kForkThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute at[2];
+        pdl_attr(at[0]);
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = blocks;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, fork_cluster_kernel, a);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
     const int sms = sm_count();
     auto grid = [&](long long blocks) { return dim3((unsigned)(blocks < 1 ? 1 : blocks > 2LL * sms ? 2LL * sms : blocks)); };
-    const long long by_rows = (units + kForkThreads / 32 - 1) / (kForkThreads / 32);
-    cudaError_t e = launch_pdl(fork_holders_kernel, grid(by_rows), dim3(kForkThreads), 0, s, a);
+    const long long by_rows = (units + kWarps - 1) / kWarps;
+    e = launch_pdl(fork_holders_kernel, grid(by_rows), dim3(kForkThreads), 0, s, a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(fork_rows_kernel, grid(by_rows > a.page_tiles ? by_rows : a.page_tiles), dim3(kForkThreads), 0, s, a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(fork_line_kernel, dim3(1), dim3(kForkThreads), 0, s, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(fork_assign_kernel, grid(a.page_tiles), dim3(kForkThreads), 0, s, a);
+    return launch_pdl(fork_assign_kernel, grid(a.page_tiles), dim3(kForkThreads), smem, s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -631,17 +663,13 @@ extern "C" sv_status_t sv_kv_fork(sv_page_pool_t pool, const int32_t* parent, in
     a.new_len = new_len;
     a.copies = copies;
     a.status = status;
-    a.kept = reinterpret_cast<int32_t*>(w + L.kept);
-    a.want = reinterpret_cast<int32_t*>(w + L.want);
-    a.begun = reinterpret_cast<int32_t*>(w + L.begun);
-    a.first = reinterpret_cast<int32_t*>(w + L.first);
-    a.how = reinterpret_cast<int32_t*>(w + L.how);
+    a.need = reinterpret_cast<Need*>(w + L.need);
     a.staged = reinterpret_cast<int32_t*>(w + L.staged);
     a.changed = reinterpret_cast<uint32_t*>(w + L.changed);
     a.writers = reinterpret_cast<int32_t*>(w + L.writers);
     a.best = reinterpret_cast<unsigned long long*>(w + L.best);
     a.tile_free = reinterpret_cast<int32_t*>(w + L.tile_free);
-    a.line = reinterpret_cast<int32_t*>(w + L.line);
+    a.tile_before = reinterpret_cast<int32_t*>(w + L.tile_before);
     a.words = L.words;
     a.page_tiles = L.page_tiles;
     a.col_tiles = pool.max_pages > 0 ? L.words / kTileWords : 1;

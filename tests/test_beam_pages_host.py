@@ -65,12 +65,12 @@ def test_forking_refuses(lib):
     for change in (dict(table=NONE), dict(held=NONE), dict(ref=NONE), dict(keep=NONE), dict(room=NONE), dict(copies=NONE),
                    dict(ld=9), dict(cols=-1), dict(n=-1), dict(pages=-1), dict(page=0), dict(group=-1)):
         assert fork(**change) == BAD, change
-    for change in (dict(n=65537), dict(pages=(1 << 30) + 1), dict(n=65536, cols=16385, ld=16385)):
+    for change in (dict(n=16385), dict(pages=(1 << 30) + 1), dict(n=16384, cols=16385, ld=16385)):
         assert fork(**change) == UNSUPPORTED, change
     for change in (dict(ws=NONE), dict(ws=ODD), dict(size=100)):
         assert fork(**change) == WS, change
     assert fork(n=0, table=NONE) == OK
-    assert lib.sv_kv_fork_workspace_size(4, 10, 100) > 0 and lib.sv_kv_fork_workspace_size(65537, 10, 100) == 0
+    assert lib.sv_kv_fork_workspace_size(4, 10, 100) > 0 and lib.sv_kv_fork_workspace_size(16385, 10, 100) == 0
 
 
 def test_copies_and_moves_refuse(lib):
