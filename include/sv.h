@@ -753,7 +753,8 @@ sv_status_t sv_kv_copy(sv_paged_kv_t cache, sv_dtype_t dt, int head_dim, int lay
  *   status (device) int32 [n_req] or NULL: SV_ROW_BAD_LAYOUT for n_keep outside
  *   [0, max_keep], a first below 0, an order that does not ascend, a token past
  *   the page table, a page outside the cache.
- *   Errors: as sv_kv_copy; SV_ERR_UNSUPPORTED for n_req > 65,536 too.
+ *   Errors: as sv_kv_copy; SV_ERR_UNSUPPORTED for n_req > 65,536 or max_keep >
+ *   2^30 too.
  */
 sv_status_t sv_kv_compact(sv_paged_kv_t cache, sv_dtype_t dt, int head_dim, int layers, int64_t stride_layer_k,
                           int64_t stride_layer_v, int n_req, const int32_t* first, const int32_t* keep, int ld_keep,

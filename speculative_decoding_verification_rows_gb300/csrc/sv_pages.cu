@@ -511,24 +511,29 @@ __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constan
 }
 
 // A CTA has a strip of every token of a request, in one layer's keys or values,
-// and goes over the kept tokens in order, some at a time: read, barrier, write.
-// A kept token never moves back, so what a turn writes has been read by it or
-// by an earlier one, and CTAs have different strips.
-template <typename R>
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ MoveArgs a)
+// and goes over the kept tokens in order, some at a turn.  A kept token never
+// moves back and tokens keep their order, so what turn t writes has been read by
+// turn t or before, and lies before all that turn t + 1 reads.  So while a turn
+// is written, the next one's units are on their way, the places of the one after
+// that are looked up (once a token, into a ring of three turns) and the list is
+// read another turn ahead; one barrier a turn.  CTAs have different strips.
+template <typename R, int THREADS>
+__global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant__ MoveArgs a)
 {
+    __shared__ int64_t s_from[3][THREADS], s_to[3][THREADS];     // a token's old and new place; from -1: it does not move
     pdl_enter();
-    const int r = blockIdx.x / a.strips, strip = blockIdx.x - r * a.strips;
+    const int r = blockIdx.x / a.strips, strip = blockIdx.x - r * a.strips, tid = threadIdx.x;
     const int n = a.n_keep[r];
     const long long first = a.first ? a.first[r] : 0;
     const bool report = a.status && strip == 0 && blockIdx.y == 0;
     if (n < 0 || n > a.max_keep || first < 0) {
-        if (report && threadIdx.x == 0) atomicOr(&a.status[r], kBadLayout);
+        if (report && tid == 0) atomicOr(&a.status[r], kBadLayout);
         return;
     }
     int64_t page, token, head;
     R* base = layer_of<R>(a, blockIdx.y, &page, &token, &head);
-    const int lane = (int)threadIdx.x % a.strip, row = (int)threadIdx.x / a.strip, rows = kMoveThreads / a.strip;
+    const int lane = tid % a.strip, row = tid / a.strip, rows = THREADS / a.strip;
+    const int turn = rows * kMoveUnits;                           // tokens; at most THREADS, as a strip has kMoveUnits units or more
     const int s = strip * a.strip + lane;
     const bool mine = s < a.per_head * a.cache.k.heads;
     const int h = s / a.per_head;
@@ -536,36 +541,71 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_cons
     const int32_t* keep = a.keep + (int64_t)r * a.ld_keep;
     const int32_t* table = a.cache.page_table + (int64_t)r * a.cache.ld_table;
     const long long limit = (long long)a.cache.max_pages * a.cache.page_size;
-    auto place = [&](long long p, int64_t* at) {
-        if (p >= limit) return false;
-        const int col = (int)(p / a.cache.page_size), slot = (int)(p - (long long)col * a.cache.page_size);
-        const int pg = table[col];
-        *at = pg * page + slot * token;
-        return pg >= 0 && pg < a.cache.n_pages;
+    const uint32_t page_size = (uint32_t)a.cache.page_size;
+    // The thread's token of turn t: entries of the list, then its places.
+    int k = 0, k_before = -1;
+    auto list = [&](int t) {
+        const int j = t * turn + tid;
+        if (tid >= turn || j >= n) return;
+        k = keep[j];
+        k_before = j ? keep[j - 1] : -1;
     };
-    for (int j0 = 0; j0 < n; j0 += rows * kMoveUnits) {
-        R x[kMoveUnits];
-        int64_t to[kMoveUnits];
-        bool moves[kMoveUnits];
-#pragma unroll
-        for (int i = 0; i < kMoveUnits; ++i) {
-            const int j = j0 + i * rows + row;
-            moves[i] = false;
-            if (j >= n) continue;
-            const int k = keep[j];
-            bool fine = k >= j && (j == 0 || keep[j - 1] < k);
+    auto look_up = [&](int t) {
+        const int j = t * turn + tid;
+        if (tid >= turn) return;
+        int64_t from = -1, to = 0;
+        if (j < n) {
+            bool fine = k >= j && k_before < k && first + k < limit;
             if (fine && k != j) {
-                int64_t from;
-                fine = place(first + k, &from) && place(first + j, &to[i]);
-                moves[i] = fine && mine;
-                if (moves[i]) x[i] = base[from];
+                const uint32_t p = (uint32_t)(first + k), q = (uint32_t)(first + j);   // sums of two int32
+                const uint32_t c0 = p / page_size, c1 = q / page_size;
+                const int p0 = table[c0], p1 = table[c1];
+                fine = p0 >= 0 && p0 < a.cache.n_pages && p1 >= 0 && p1 < a.cache.n_pages;
+                if (fine) {
+                    from = p0 * page + (p - c0 * page_size) * token;
+                    to = p1 * page + (q - c1 * page_size) * token;
+                }
             }
             if (!fine && report) atomicOr(&a.status[r], kBadLayout);
         }
-        __syncthreads();
+        s_from[t % 3][tid] = from;
+        s_to[t % 3][tid] = to;
+    };
+    R x[kMoveUnits], next[kMoveUnits];
+    uint32_t moves = 0u;
+    auto read = [&](int t, R (&v)[kMoveUnits]) {                  // which of the units move
+        uint32_t m = 0u;
+        if (!mine) return m;
+#pragma unroll
+        for (int i = 0; i < kMoveUnits; ++i) {
+            const int64_t from = s_from[t % 3][i * rows + row];
+            if (from < 0) continue;
+            v[i] = base[from];
+            m |= 1u << i;
+        }
+        return m;
+    };
+    list(0);
+    look_up(0);
+    list(1);
+    look_up(1);
+    list(2);
+    __syncthreads();
+    moves = read(0, x);
+    __syncthreads();
+    for (int t = 0; t * turn < n; ++t) {
+        const uint32_t next_moves = (t + 1) * turn < n ? read(t + 1, next) : 0u;
 #pragma unroll
         for (int i = 0; i < kMoveUnits; ++i)
-            if (moves[i]) base[to[i]] = x[i];
+            if (moves >> i & 1u) base[s_to[t % 3][i * rows + row]] = x[i];
+        if ((t + 2) * turn < n) {
+            look_up(t + 2);
+            list(t + 3);
+        }
+        __syncthreads();
+        moves = next_moves;
+#pragma unroll
+        for (int i = 0; i < kMoveUnits; ++i) x[i] = next[i];
     }
 }
 
@@ -598,10 +638,13 @@ cudaError_t launch_move(MoveArgs a, int layers, cudaStream_t s)
         return launch_pdl(copy_kernel<R>, dim3(a.n, 2 * layers, (unsigned)parts), dim3(kMoveThreads), 0, s, a);
     }
     const int least = 64 / (int)sizeof(R);                      // a strip of 64 bytes at least
-    a.strip = kMoveThreads / 8;
+    a.strip = 32;
     while (a.strip > least && (long long)a.n * 2 * layers * ((token + a.strip - 1) / a.strip) < 8LL * sm_count()) a.strip /= 2;
     a.strips = (int)((token + a.strip - 1) / a.strip);
-    return launch_pdl(compact_kernel<R>, dim3((unsigned)a.n * a.strips, 2 * layers), dim3(kMoveThreads), 0, s, a);
+    const dim3 grid((unsigned)a.n * a.strips, 2 * layers);
+    // Accepted paths take many small CTAs (8 us, 18 with 512 threads), long lists few large ones.
+    if (a.max_keep <= 64) return launch_pdl(compact_kernel<R, 128>, grid, dim3(128), 0, s, a);
+    return launch_pdl(compact_kernel<R, 512>, grid, dim3(512), 0, s, a);
 }
 
 sv_status_t run_move(MoveArgs a, sv_dtype_t dt, int head_dim, int layers, cudaStream_t s)
@@ -706,7 +749,7 @@ extern "C" sv_status_t sv_kv_compact(sv_paged_kv_t cache, sv_dtype_t dt, int hea
         return SV_ERR_INVALID_ARG;
     if (n_req == 0 || layers == 0) return SV_OK;
     if (!n_keep || (max_keep > 0 && !keep) || (cache.max_pages > 0 && !cache.page_table)) return SV_ERR_INVALID_ARG;
-    if (n_req > (1 << 16)) return SV_ERR_UNSUPPORTED;
+    if (n_req > (1 << 16) || max_keep > (1 << 30)) return SV_ERR_UNSUPPORTED;
     MoveArgs a{};
     a.cache = cache;
     a.layer_k = stride_layer_k;

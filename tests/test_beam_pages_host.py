@@ -98,6 +98,7 @@ def test_copies_and_moves_refuse(lib):
                    dict(cols=-1)):
         assert compact(**change) == BAD, change
     assert compact(n=65537) == UNSUPPORTED and compact(n=0) == OK
+    assert compact(max_keep=(1 << 30) + 1, ld_keep=(1 << 30) + 1) == UNSUPPORTED
 
 
 def test_host_tensors_are_refused():
