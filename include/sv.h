@@ -643,7 +643,7 @@ size_t sv_beam_workspace_size(int n, int beams, int vocab, int n_out);
  *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, n_out > beams * vocab,
  *   an end_token outside the vocabulary where finished is given;
  *   SV_ERR_UNSUPPORTED for more than 128 beams, n_out > 256, a vocabulary above
- *   524,288, more than 2^22 rows.  Workspace: sv_beam_workspace_size(...).
+ *   524,288, more than 2^22 rows or 2^41 logits.  Workspace: sv_beam_workspace_size(...).
  */
 sv_status_t sv_beam_select(const void* logits, sv_dtype_t dt, int64_t stride_item, int64_t stride_beam, int n, int beams,
                            int vocab, const float* scores, const uint8_t* finished, int end_token, int n_out,

@@ -44,10 +44,11 @@ constexpr int kRefineElems = 4096;           // elements of a row a CTA of refin
 // |ln sum exp(l - m) - computed| of one row, V <= 2^19.  With p the row's probabilities, sum
 // p |l - m| = H - ln Z <= ln V <= 13.2, so an argument's relative error r costs
 // 13.2 r.  Differences to the reference and their product with log2 e: 2^-24 +
-// 2^-24 + 2^-26 -> 1.8e-6; ex2.approx 2^-22 for the term, for up to kMaxSegChunks
-// moves of the reference and for joining the partial sums: 10 (2^-22 + 2^-24) ->
-// 3.0e-6; sums by trees of 8 levels in a chunk, 8 chunks, 5 shuffles, 8 + 5
-// levels of partial sums: 34 2^-24 -> 2.0e-6; logf: an ulp of 13.2, 9.6e-7.
+// 2^-24 + 2^-26 (less where the reference is near) -> 1.8e-6; ex2.approx 2^-22 for
+// the term and its reference's scale, for up to kMaxSegChunks moves of the
+// reference and for joining the partial sums: 11 (2^-22 + 2^-24) -> 3.3e-6; sums
+// by trees of 8 levels in a chunk, 8 chunks, 5 shuffles, 5 + 5 levels of partial
+// sums: 31 2^-24 -> 1.9e-6; logf: an ulp of 13.2, 9.6e-7.
 constexpr double kSumEps = 8e-6;
 
 enum { kDead = 0, kLive = 1, kFinished = 2 };
@@ -216,6 +217,12 @@ __device__ __forceinline__ pair_t add2(pair_t a, pair_t b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c)
+{
+    pair_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 __device__ __forceinline__ pair_t mul2(pair_t a, pair_t b)
 {
     pair_t r;
@@ -230,22 +237,54 @@ __device__ __forceinline__ float exp2_approx(float x)
 }
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// exp(x - ref) of two elements.
-__device__ __forceinline__ pair_t exp_pair(float x0, float x1, pair_t minus_ref)
+// What a running reference is to a row's sums.  Near: 2^(x L - c) with one packed
+// fma, L = log2 e and c = ref L in fp32; the product is exact in it, so what c is
+// off by, ref L - c, is off for all x alike and is put right by `scale`.  A
+// reference past 2^20 has too coarse a c: 2^((x - ref) L) then.
+struct Ref {
+    float at = -FLT_MAX, c = 0.f, scale = 1.f;
+    bool near = false;
+
+    __device__ __forceinline__ void move(float top)
+    {
+        at = top;
+        near = fabsf(top) < 0x1p20f;
+        c = top * kLog2e;
+        scale = near ? exp2_approx(-fmaf(top, kLog2e, -c)) : 1.f;
+    }
+};
+template <bool NEAR>
+__device__ __forceinline__ pair_t exp_pair(float x0, float x1, pair_t k)
 {
-    const pair_t y = mul2(add2(pack(x0, x1), minus_ref), pack(kLog2e, kLog2e));
+    const pair_t x = pack(x0, x1), l = pack(kLog2e, kLog2e);
+    const pair_t y = NEAR ? fma2(x, l, k) : mul2(add2(x, k), l);
     float y0, y1;
     unpack(y, y0, y1);
     return pack(exp2_approx(y0), exp2_approx(y1));
 }
-template <int DT>
-__device__ __forceinline__ pair_t vec_exp_sum(const uint4& v, pair_t minus_ref)
+template <int DT, bool NEAR>
+__device__ __forceinline__ pair_t vec_exp_sum(const uint4& v, pair_t k)
 {
-    const pair_t s = add2(exp_pair(vec_at<DT>(v, 0), vec_at<DT>(v, 1), minus_ref),
-                          exp_pair(vec_at<DT>(v, 2), vec_at<DT>(v, 3), minus_ref));
+    const pair_t s = add2(exp_pair<NEAR>(vec_at<DT>(v, 0), vec_at<DT>(v, 1), k),
+                          exp_pair<NEAR>(vec_at<DT>(v, 2), vec_at<DT>(v, 3), k));
     if (DT != 0) return s;
-    return add2(s, add2(exp_pair(vec_at<DT>(v, 4 % Elem<DT>::kPerVec), vec_at<DT>(v, 5 % Elem<DT>::kPerVec), minus_ref),
-                        exp_pair(vec_at<DT>(v, 6 % Elem<DT>::kPerVec), vec_at<DT>(v, 7 % Elem<DT>::kPerVec), minus_ref)));
+    constexpr int kLast = Elem<DT>::kPerVec - 1;
+    return add2(s, add2(exp_pair<NEAR>(vec_at<DT>(v, 4 & kLast), vec_at<DT>(v, 5 & kLast), k),
+                        exp_pair<NEAR>(vec_at<DT>(v, 6 & kLast), vec_at<DT>(v, 7 & kLast), k)));
+}
+template <int DT, bool NEAR>
+__device__ __forceinline__ float chunk_exp_sum(const uint4 (&v)[kVecs], float minus)
+{
+    const pair_t k = pack(minus, minus);
+    pair_t t0 = vec_exp_sum<DT, NEAR>(v[0], k), t1 = vec_exp_sum<DT, NEAR>(v[1], k);
+#pragma unroll
+    for (int i = 2; i < kVecs; i += 2) {
+        t0 = add2(t0, vec_exp_sum<DT, NEAR>(v[i], k));
+        t1 = add2(t1, vec_exp_sum<DT, NEAR>(v[i + 1], k));
+    }
+    float x0, x1;
+    unpack(add2(t0, t1), x0, x1);
+    return x0 + x1;
 }
 
 __device__ __forceinline__ int beam_kind(const BeamArgs& a, int row, float* score)
@@ -265,17 +304,25 @@ template <int DT>
 __device__ __forceinline__ void scan_rows(const BeamArgs& a, int row0, int rows, int warp, int warps)
 {
     const int lane = threadIdx.x & 31;
-    const long long units = (long long)rows * a.segs;
-    long long u = warp;
-    if (u >= units) return;
-    bool live = is_live(a, row0 + (int)(u / a.segs)), next_live;
-    for (; u < units; u += warps, live = next_live) {
-        const int at = (int)(u / a.segs), row_no = row0 + at, seg = (int)(u - (long long)at * a.segs);
-        next_live = u + warps < units && is_live(a, row0 + (int)((u + warps) / a.segs));   // while this one's data is on its way
+    // units in turns of `warps`, their rows and segments without a division each
+    const int more_rows = warps / a.segs, more_segs = warps - more_rows * a.segs;
+    int at = warp / a.segs, seg = warp - at * a.segs;
+    if (at >= rows) return;
+    bool live = is_live(a, row0 + at), next_live;
+    for (int next, next_seg; at < rows; at = next, seg = next_seg, live = next_live) {
+        next = at + more_rows;
+        next_seg = seg + more_segs;
+        if (next_seg >= a.segs) {
+            next_seg -= a.segs;
+            ++next;
+        }
+        next_live = next < rows && is_live(a, row0 + next);       // while this one's data is on its way
         if (!live) continue;
+        const int row_no = row0 + at;
         const Row<DT> row(a, row_no / a.beams, row_no % a.beams);
         const int c1 = min((seg + 1) * a.seg_chunks, a.chunks);
-        float ref = -FLT_MAX, s_hi = 0.f, s_lo = 0.f;
+        float s_hi = 0.f, s_lo = 0.f;
+        Ref ref;
         for (int c = seg * a.seg_chunks; c < c1; ++c) {
             uint4 v[kVecs];
             row.chunk(c, v);
@@ -284,29 +331,21 @@ __device__ __forceinline__ void scan_rows(const BeamArgs& a, int row0, int rows,
             for (int i = 1; i < kVecs; ++i) top = max_nan(top, vec_max<DT>(v[i]));
             top = warp_max_nan(top);
             if (lane == 0) a.chunk_max[(size_t)row_no * a.chunks + c] = top;
-            if (top > ref) {
-                const float f = exp2_approx((ref - top) * kLog2e);
+            if (top > ref.at) {
+                const float f = exp2_approx((ref.at - top) * kLog2e);
                 s_hi *= f;
                 s_lo *= f;
-                ref = top;
+                ref.move(top);
             }
-            const pair_t minus_ref = pack(-ref, -ref);
-            pair_t t0 = vec_exp_sum<DT>(v[0], minus_ref), t1 = vec_exp_sum<DT>(v[1], minus_ref);
-#pragma unroll
-            for (int i = 2; i < kVecs; i += 2) {
-                t0 = add2(t0, vec_exp_sum<DT>(v[i], minus_ref));
-                t1 = add2(t1, vec_exp_sum<DT>(v[i + 1], minus_ref));
-            }
-            float x0, x1;
-            unpack(add2(t0, t1), x0, x1);
-            const dfloat s = df_two_sum(s_hi, x0 + x1);
+            const float x = (ref.near ? chunk_exp_sum<DT, true>(v, -ref.c) : chunk_exp_sum<DT, false>(v, -ref.at)) * ref.scale;
+            const dfloat s = df_two_sum(s_hi, x);
             s_hi = s.hi;
             s_lo += s.lo;
         }
         float s = s_hi + s_lo;
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (lane == 0) a.sums[(size_t)row_no * a.segs + seg] = make_float2(ref, s);
+        if (lane == 0) a.sums[(size_t)row_no * a.segs + seg] = make_float2(ref.at, s);
     }
 }
 
@@ -1020,21 +1059,30 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
     const long long rows = (long long)a.n * a.beams;
     a.chunks = (a.vocab + E::kPerVec - 1 + E::kChunk - 1) / E::kChunk;
     a.refine_segs = (a.vocab + kRefineElems - 1) / kRefineElems;
-    auto segments = [&](long long chunks_a_warp) {
-        a.seg_chunks = (int)(chunks_a_warp < 1 ? 1 : chunks_a_warp > kMaxSegChunks ? kMaxSegChunks : chunks_a_warp);
-        a.segs = (a.chunks + a.seg_chunks - 1) / a.seg_chunks;
+    // Segments such that the warp with the most of them has the least to do: its chunks, and a third of a chunk's
+    // time for every segment (32 x 8 x 151,936: segments of 4 chunks, two for some warps, took 26,000 clocks, 1 chunk 16,000).
+    auto segments = [&](long long of_rows, long long warps) {
+        double least = 0.0;
+        for (int n = 1; n <= kMaxSegChunks; ++n) {
+            const long long segs = (a.chunks + n - 1) / n, turns = (of_rows * segs + warps - 1) / warps;
+            const double cost = (double)turns * (n + 0.33);
+            if (n > 1 && cost >= least) continue;
+            least = cost;
+            a.seg_chunks = n;
+            a.segs = (int)segs;
+        }
     };
     // Items that fit the GPU at once, and whose clusters read them in little time
     const int cluster = a.n * 8 <= sms ? 8 : 4;
     const int item_warps = cluster * (kPickThreads / 32);
     const long long item_chunks = (long long)a.beams * a.chunks;
     if (a.n * cluster <= sms && item_chunks <= 8LL * item_warps) {
-        segments(item_chunks / item_warps);
+        segments(a.beams, item_warps);
         return launch_cluster(select_kernel<DT>, a.n * cluster, cluster, s, a);
     }
     const long long warps = (long long)sms * 4 * (kScanThreads / 32);
-    segments(rows * a.chunks / (4 * warps));
-    const long long units = rows * a.segs;
+    segments(rows, warps);
+    const long long units = rows * a.segs;                        // below 2^31
     long long grid = (units + kScanThreads / 32 - 1) / (kScanThreads / 32);
     if (grid > 4LL * sms) grid = 4LL * sms;
     cudaError_t e = launch_pdl(scan_kernel<DT>, dim3((unsigned)grid), dim3(kScanThreads), 0, s, a);
@@ -1048,7 +1096,7 @@ bool beam_sizes_ok(int n, int beams, int vocab, int n_out)
 {
     return n >= 1 && n <= (1 << 20) && beams >= 1 && beams <= kMaxBeams && vocab >= 1 && vocab <= kBeamMaxVocab &&
            n_out >= 1 && n_out <= kMaxOut && n_out <= (long long)beams * vocab &&
-           (long long)n * beams <= (1 << 22);
+           (long long)n * beams <= (1 << 22) && (long long)n * beams * ((long long)vocab / Elem<1>::kChunk + 2) < (1LL << 31);
 }
 
 // ---------------------------------------------------------------------------
