@@ -397,15 +397,17 @@ __device__ void sort_entries(const Entries& e, int n, uint16_t* order)
     if (p <= kPickThreads / 2) {
         __syncthreads();
         const int share = min(32, kPickThreads / p), i = threadIdx.x / share;
-        int before = 0;
-        if (i < n) {
-            const unsigned long long k = e.key[i];
-            const uint32_t f = e.flat[i];
-            for (int j = threadIdx.x % share; j < n; j += share)
-                before += e.key[j] > k || (e.key[j] == k && e.flat[j] < f);
+        if ((int)(threadIdx.x & ~31u) / share < n) {              // (for whole warps)
+            int before = 0;
+            if (i < n) {
+                const unsigned long long k = e.key[i];
+                const uint32_t f = e.flat[i];
+                for (int j = threadIdx.x % share; j < n; j += share)
+                    before += e.key[j] > k || (e.key[j] == k && e.flat[j] < f);
+            }
+            for (int o = share >> 1; o; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+            if (i < n && threadIdx.x % share == 0) order[before] = (uint16_t)i;
         }
-        for (int o = share >> 1; o; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-        if (i < n && threadIdx.x % share == 0) order[before] = (uint16_t)i;
         __syncthreads();
         return;
     }
@@ -628,8 +630,10 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
         best = fmaxf(best, s - slack);
         return s + slack;
     };
+    const int mine = total - warp * 32;                           // of the chunks a warp's turns begin at
 #pragma unroll
-    for (int k = 0; k < kPickHeld; ++k) held[k] = rate(tid + k * kPickThreads, held[k]);
+    for (int k = 0; k < kPickHeld; ++k)
+        if (k * kPickThreads < mine) held[k] = rate(tid + k * kPickThreads, held[k]);
     for (int i = tid + kPickHeld * kPickThreads; i < total; i += kPickThreads) rate(i, __ldcg(&chunk_max[i]));
     if (tid < a.beams && sh.rec[tid].kind == kFinished) best = fmaxf(best, sh.rec[tid].base);
     const float bound = nth_bound(best, a.n_out, sh);
@@ -654,7 +658,8 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
         if (at < kChunkCap) sh.chunk[at] = i;
     };
 #pragma unroll
-    for (int k = 0; k < kPickHeld; ++k) keep(tid + k * kPickThreads, held[k]);
+    for (int k = 0; k < kPickHeld; ++k)
+        if (k * kPickThreads < mine) keep(tid + k * kPickThreads, held[k]);
     for (int i = tid + kPickHeld * kPickThreads; i < total; i += kPickThreads) keep(i, rate(i, __ldcg(&chunk_max[i])));
     if (tid < a.beams && sh.rec[tid].kind == kFinished && sh.rec[tid].base >= bound) {   // one candidate: base alone
         const int at = atomicAdd(&sh.n_elems, 1);
@@ -695,6 +700,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     if (!hard) {
         for (int i = tid; i < n; i += kPickThreads) sh.key[i] = score_key(sh, sh.beam[i], sh.logit[i]);
         sort_entries(e, n, sh.order);
+        write_item<DT>(a, item, e, n, sh);                        // to be written again where the order may be another
         // neighbours of two beams that the normalisers' errors may have put the wrong way round
         for (int k = tid; k + 1 < n && k < a.n_out; k += kPickThreads) {
             const int i0 = sh.order[k], i1 = sh.order[k + 1];
@@ -716,8 +722,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     }
     __syncthreads();
     const int again = __popc(sh.mask[0]) + __popc(sh.mask[1]) + __popc(sh.mask[2]) + __popc(sh.mask[3]);
-    if (again == 0) write_item<DT>(a, item, e, n, sh);
-    else if (tid == 0 && hard) sh.n_elems = -1;
+    if (tid == 0 && hard) sh.n_elems = -1;
     return again;
 }
 
@@ -967,6 +972,7 @@ __global__ void __launch_bounds__(kPickThreads) select_kernel(const __grid_const
     __shared__ PickShared sh;
     __shared__ dfloat tab[64];
     __shared__ ulonglong2 part[kPickThreads / 32];
+    __shared__ int s_again;
     pdl_enter();
     const int tid = threadIdx.x;
     uint32_t rank, size;
@@ -978,14 +984,18 @@ __global__ void __launch_bounds__(kPickThreads) select_kernel(const __grid_const
     int again = 0;
     if (rank == 0) {
         again = pick_item<DT>(a, item, sh);
-        if (tid == 0) a.item_units[item] = again;
         if (again) {
             if (tid < 4) a.item_mask[item * 4 + tid] = sh.mask[tid];
             if (tid < a.beams) a.rec[row0 + tid] = sh.rec[tid];
         }
+        if (tid < (int)size) {                         // into every CTA's own memory
+            uint32_t there;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_u32(&s_again)), "r"(tid));
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(again) : "memory");
+        }
     }
     cluster_sync();
-    again = __ldcg(&a.item_units[item]);
+    again = s_again;
     if (again == 0) return;
     fill_exp_table(tab);
     __syncthreads();
