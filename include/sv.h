@@ -731,7 +731,8 @@ sv_status_t sv_kv_fork(sv_page_pool_t pool, const int32_t* parent, int group, co
  * used.  Layer y of the cache lies y * stride_layer elements after the first.
  *   status (device) int32 [1] or NULL: SV_ROW_BAD_LAYOUT where an entry has a
  *   page outside the cache, or tokens outside [0, page_size] (nothing is copied
- *   for it).
+ *   for it).  Here and in sv_kv_compact the values may be the keys' tensor itself
+ *   (the same strides); otherwise the two must not overlap.
  *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, head counts that
  *   differ; SV_ERR_UNSUPPORTED for more than 32,767 layers, tokens of more than
  *   2^19 elements or pages of more than 2^30.

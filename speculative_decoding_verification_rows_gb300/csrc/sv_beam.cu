@@ -112,7 +112,7 @@ struct Row {
     __device__ __forceinline__ uint4 whole(int vec) const
     {
         uint4 r;
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                      : "l"(base + (size_t)vec * 16));
         return r;

@@ -456,6 +456,7 @@ struct MoveArgs {
     int32_t* status;
     int n, ld_keep, max_keep;
     int per_head;                  // units of a head
+    int one;                       // keys and values are one tensor
     int strip;                     // sv_kv_compact: units of a token a CTA takes
     int strips;
 };
@@ -463,12 +464,12 @@ struct MoveArgs {
 template <typename R>
 __device__ __forceinline__ R* layer_of(const MoveArgs& a, int y, int64_t* page, int64_t* token, int64_t* head)
 {
-    const bool is_v = y & 1;
+    const bool is_v = !a.one && (y & 1);
     const sv_heads_t& h = is_v ? a.cache.v : a.cache.k;
     *page = is_v ? a.cache.stride_page_v : a.cache.stride_page_k;
     *token = h.stride_token;
     *head = h.stride_head;
-    return static_cast<R*>(h.data) + (y >> 1) * (is_v ? a.layer_v : a.layer_k);
+    return static_cast<R*>(h.data) + (a.one ? y : y >> 1) * (is_v ? a.layer_v : a.layer_k);
 }
 
 // A CTA copies a part of one page of one layer's keys or values; units go in
@@ -632,16 +633,17 @@ template <typename R>
 cudaError_t launch_move(MoveArgs a, int layers, cudaStream_t s)
 {
     const long long token = (long long)a.per_head * a.cache.k.heads;
+    const int tensors = a.one ? layers : 2 * layers;
     if (a.copies) {
         long long parts = (token * a.cache.page_size + kMoveThreads * kCopyUnits - 1) / (kMoveThreads * kCopyUnits);
         if (parts > 64) parts = 64;
-        return launch_pdl(copy_kernel<R>, dim3(a.n, 2 * layers, (unsigned)parts), dim3(kMoveThreads), 0, s, a);
+        return launch_pdl(copy_kernel<R>, dim3(a.n, tensors, (unsigned)parts), dim3(kMoveThreads), 0, s, a);
     }
     const int least = 64 / (int)sizeof(R);                      // a strip of 64 bytes at least
     a.strip = 32;
-    while (a.strip > least && (long long)a.n * 2 * layers * ((token + a.strip - 1) / a.strip) < 8LL * sm_count()) a.strip /= 2;
+    while (a.strip > least && (long long)a.n * tensors * ((token + a.strip - 1) / a.strip) < 8LL * sm_count()) a.strip /= 2;
     a.strips = (int)((token + a.strip - 1) / a.strip);
-    const dim3 grid((unsigned)a.n * a.strips, 2 * layers);
+    const dim3 grid((unsigned)a.n * a.strips, tensors);
     // Accepted paths take many small CTAs (8 us, 18 with 512 threads), long lists few large ones.
     if (a.max_keep <= 64) return launch_pdl(compact_kernel<R, 128>, grid, dim3(128), 0, s, a);
     return launch_pdl(compact_kernel<R, 512>, grid, dim3(512), 0, s, a);
@@ -650,6 +652,9 @@ cudaError_t launch_move(MoveArgs a, int layers, cudaStream_t s)
 sv_status_t run_move(MoveArgs a, sv_dtype_t dt, int head_dim, int layers, cudaStream_t s)
 {
     const int size = dt == SV_DTYPE_F32 ? 4 : 2;
+    const sv_heads_t &k = a.cache.k, &v = a.cache.v;
+    a.one = k.data == v.data && k.stride_token == v.stride_token && k.stride_head == v.stride_head &&
+            a.cache.stride_page_k == a.cache.stride_page_v && a.layer_k == a.layer_v;   // moved twice it would be lost
     cudaError_t e;
     if (in_units(a, 16 / size, size, head_dim)) e = launch_move<uint4>(a, layers, s);
     else if (in_units(a, 8 / size, size, head_dim)) e = launch_move<uint2>(a, layers, s);

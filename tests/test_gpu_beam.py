@@ -123,6 +123,16 @@ def test_rows_of_few_values(ws, dtype, values):
     check(logits[:, :, :3], scores, 9, ws)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,beams,vocab,n_out", [(50, 2, 9001, 5), (1, 64, 70001, 70), (45, 30, 40001, 3)])
+def test_rows_of_one_value_in_large_calls(ws, dtype, n, beams, vocab, n_out):
+    logits = torch.full((n, beams, vocab), 1.25, dtype=dtype)
+    logits[n // 2, beams // 2, vocab // 2] = 1.5
+    scores = torch.full((n, beams), -0.5)
+    scores[0, beams - 1] = -0.25
+    check(logits, scores, n_out, ws)
+
+
 def test_equal_beams_go_by_their_number(ws):
     logits, scores, _ = make(3, 1, 5003, F32, 11)
     logits = logits.expand(3, 6, 5003).contiguous()
@@ -140,10 +150,10 @@ def test_equal_beams_go_by_their_number(ws):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("vocab", [4000, 50001])
-@pytest.mark.parametrize("seed", [0, 1, 2])
-def test_beams_nearer_than_fp32_tells(ws, dtype, vocab, seed):
+@pytest.mark.parametrize("seed,n", [(0, 8), (1, 8), (2, 8), (3, 60)])       # one launch, and three
+def test_beams_nearer_than_fp32_tells(ws, dtype, vocab, seed, n):
     # one row for all beams but for tokens of little mass: the sums differ by 1e-6 to 1e-9 of themselves
-    n, beams = 8, 6
+    beams = 6
     logits, _, g = make(n, 1, vocab, F32, seed, scale=2.0)
     logits = logits.expand(n, beams, vocab).clone()
     for i in range(n):
@@ -179,8 +189,9 @@ def test_what_is_refused_is_refused_by_item(ws, dtype):
     assert sv.beam_select(bad_l.cuda(), bad_s.cuda(), 6).tokens[1].tolist() == [-1] * 6      # without a status too
 
 
-def test_the_same_call_gives_the_same_bits_and_is_captured():
-    logits, scores, g = make(5, 4, 20001, BF16, 23)
+@pytest.mark.parametrize("n", [5, 44])                              # one launch, and three
+def test_the_same_call_gives_the_same_bits_and_is_captured(n):
+    logits, scores, g = make(n, 4, 20001, BF16, 23)
     logits[1, 1], scores[1, 1] = logits[1, 0], scores[1, 0]              # an item that is ordered again
     logits[2] = 1.0                                                     # and one that is picked by turns
     x, c, ws = logits.cuda(), scores.cuda(), sv.Workspace("cuda")
@@ -198,14 +209,14 @@ def test_the_same_call_gives_the_same_bits_and_is_captured():
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
         sv.beam_select(x, c, 8, out=out, ws=ws)
-    logits2, scores2, _ = make(5, 4, 20001, BF16, 24)
+    logits2, scores2, _ = make(n, 4, 20001, BF16, 24)
     for _ in range(2):
         x.copy_(logits2)
         c.copy_(scores2)
         graph.replay()
         tokens, parents, _ = select64(logits2, scores2, 8)
         assert torch.equal(out.tokens.cpu(), tokens) and torch.equal(out.parents.cpu(), parents)
-        logits2, scores2, _ = make(5, 4, 20001, BF16, 25)
+        logits2, scores2, _ = make(n, 4, 20001, BF16, 25)
 
 
 def test_nothing_else_is_written():

@@ -383,3 +383,17 @@ def test_a_long_cache_has_offsets_past_32_bits():
     assert (k[last, :4] == 1).all() and (k[last, 5] == 3).all() and (k[last, 4] == 0).all()
     sv.kv_compact(k, k, ints([[last, 0]]).cuda(), ints([[5]]).cuda(), ints([1]).cuda())
     assert (k[last, 0] == 3).all() and (k[last, 1] == 1).all()
+
+
+@pytest.mark.parametrize("layers", [0, 2])
+def test_one_tensor_for_keys_and_values(layers):
+    # moved once: twice would take the second time what the first has put there
+    page, n_keep = 16, 900
+    k, _ = cache_of(layers, 130, page, 2, 64, BF16, "tokens")
+    table, keep = [list(range(120, 0, -1))], [[2 * j + 1 for j in range(n_keep)]]
+    want = compacted(k, table, [0], keep, [n_keep], page)
+    sv.kv_compact(k, k, ints(table).cuda(), ints(keep).cuda(), ints([n_keep]).cuda())
+    assert torch.equal(k, want)
+    want[..., 125, :9, :, :] = want[..., 3, :9, :, :]
+    sv.kv_copy(k, k, ints([[3, 125, 9]]).cuda())
+    assert torch.equal(k, want)
