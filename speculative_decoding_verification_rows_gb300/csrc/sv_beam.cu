@@ -402,8 +402,11 @@ __device__ void sort_entries(const Entries& e, int n, uint16_t* order)
             if (i < n) {
                 const unsigned long long k = e.key[i];
                 const uint32_t f = e.flat[i];
-                for (int j = threadIdx.x % share; j < n; j += share)
-                    before += e.key[j] > k || (e.key[j] == k && e.flat[j] < f);
+                for (int j = threadIdx.x % share; j < n; j += share) {
+                    const unsigned long long other = e.key[j];
+                    before += other > k;
+                    if (other == k && e.flat[j] < f) ++before;
+                }
             }
             for (int o = share >> 1; o; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
             if (i < n && threadIdx.x % share == 0) order[before] = (uint16_t)i;
@@ -451,12 +454,12 @@ struct PickShared {
     float logit[kListCap];
     BeamRec rec[kMaxBeams];
     double base[kMaxBeams];
+    int chunk[kChunkCap];
     union {
-        int chunk[kChunkCap];
+        uint16_t order[kListCap];
         int bins[kPickThreads];
-        int scratch[kMaxOut];
     };
-    uint16_t order[kListCap];
+    int scratch[kMaxOut];
     uint8_t beam[kListCap];
     uint32_t mask[4];
     float warp_best[32];
@@ -636,7 +639,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
         if (k * kPickThreads < mine) held[k] = rate(tid + k * kPickThreads, held[k]);
     for (int i = tid + kPickHeld * kPickThreads; i < total; i += kPickThreads) rate(i, __ldcg(&chunk_max[i]));
     if (tid < a.beams && sh.rec[tid].kind == kFinished) best = fmaxf(best, sh.rec[tid].base);
-    const float bound = nth_bound(best, a.n_out, sh);
+    float bound = nth_bound(best, a.n_out, sh);
     if (sh.bad) {                                                 // (its last write is before the barriers above)
         if (tid < a.n_out) {
             const size_t o = (size_t)item * a.n_out + tid;
@@ -645,11 +648,6 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
         }
         if (tid == 0 && a.status) atomicOr(&a.status[item], sh.bad);
         return 0;
-    }
-    // Where l - m is near bound - base, score and slack are off by 2^-22 (|base| + |bound - base|).
-    if (tid < a.beams && sh.rec[tid].kind == kLive) {
-        const float base = sh.rec[tid].base, at = bound - base;
-        sh.rec[tid].least = fmaxf(at - (2.f * (float)kSumEps + 0x1p-20f * (fabsf(base) + fabsf(at))), -FLT_MAX);
     }
     // the chunks that may reach it
     auto keep = [&](int i, float most) {
@@ -661,15 +659,41 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     for (int k = 0; k < kPickHeld; ++k)
         if (k * kPickThreads < mine) keep(tid + k * kPickThreads, held[k]);
     for (int i = tid + kPickHeld * kPickThreads; i < total; i += kPickThreads) keep(i, rate(i, __ldcg(&chunk_max[i])));
-    if (tid < a.beams && sh.rec[tid].kind == kFinished && sh.rec[tid].base >= bound) {   // one candidate: base alone
-        const int at = atomicAdd(&sh.n_elems, 1);
-        sh.flat[at] = (uint32_t)tid * (uint32_t)a.vocab + (uint32_t)a.end_token;
-        sh.logit[at] = 0.f;
-        sh.beam[at] = (uint8_t)tid;
-    }
     __syncthreads();
+    constexpr int kPer = Elem<DT>::kPerVec;
     bool hard = sh.n_chunks > kChunkCap;
-    if (!hard) {
+    // Few chunks for n_out (one live beam, a small vocabulary, beams far apart) bound it loosely or not at all; then the
+    // lanes' best of the listed chunks give another bound.  32,003 tokens of one beam for n_out = 64 took 190 us without
+    // it (more elements than a list holds), XX with it.
+    const int enough = a.n_out + 32;
+    for (bool fine = bound == -FLT_MAX || total < 4 * a.n_out; !hard; fine = true) {
+        if (fine) {
+            best = tid < a.beams && sh.rec[tid].kind == kFinished ? sh.rec[tid].base : -INFINITY;
+            for (int k = warp; k < sh.n_chunks; k += kPickThreads / 32) {
+                const int i = sh.chunk[k], b = beam_of(i);
+                uint4 v[kVecs];
+                Row<DT>(a, item, b).chunk(i - b * a.chunks, v);
+                float l = vec_max<DT>(v[0]);
+#pragma unroll
+                for (int g = 1; g < kVecs; ++g) l = fmaxf(l, vec_max<DT>(v[g]));
+                const float s = score32(sh.rec[b], l);
+                if (s > -INFINITY) best = fmaxf(best, s - slack32(sh.rec[b], l));
+            }
+            bound = fmaxf(bound, nth_bound(best, a.n_out, sh));
+        }
+        // Where l - m is near bound - base, score and slack are off by 2^-22 (|base| + |bound - base|).
+        if (tid < a.beams && sh.rec[tid].kind == kLive) {
+            const float base = sh.rec[tid].base, at = bound - base;
+            sh.rec[tid].least = fmaxf(at - (2.f * (float)kSumEps + 0x1p-20f * (fabsf(base) + fabsf(at))), -FLT_MAX);
+        }
+        __syncthreads();
+        if (tid < a.beams && sh.rec[tid].kind == kFinished && sh.rec[tid].base >= bound) {   // one candidate: base alone
+            const int at = atomicAdd(&sh.n_elems, 1);
+            sh.flat[at] = (uint32_t)tid * (uint32_t)a.vocab + (uint32_t)a.end_token;
+            sh.logit[at] = 0.f;
+            sh.beam[at] = (uint8_t)tid;
+        }
+        __syncthreads();                                          // (they find room)
         for (int k = warp; k < sh.n_chunks; k += kPickThreads / 32) {   // a warp a chunk
             const int i = sh.chunk[k], b = beam_of(i), c = i - b * a.chunks;
             const Row<DT> row(a, item, b);
@@ -677,23 +701,47 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             row.chunk(c, v);
             const float top = sh.rec[b].top, least = sh.rec[b].least;
             auto reaches = [&](float l) { return fmaxf(l - top, -FLT_MAX) >= least; };   // (-inf too, where the bound is none)
+            // a lane's elements that reach the bound, then room for the warp's at once
+            unsigned long long in = 0ull;
 #pragma unroll
             for (int g = 0; g < kVecs; ++g) {
                 if (!reaches(vec_max<DT>(v[g]))) continue;
 #pragma unroll
-                for (int q = 0; q < Elem<DT>::kPerVec; ++q) {
+                for (int q = 0; q < kPer; ++q) {
                     const float l = vec_at<DT>(v[g], q);
-                    if (!reaches(l) || l == -INFINITY) continue;
-                    const int at = atomicAdd(&sh.n_elems, 1);
-                    if (at >= kListCap) continue;
+                    if (reaches(l) && l > -INFINITY) in |= 1ull << (g * kPer + q);
+                }
+            }
+            const int own = __popcll(in);
+            if (!__any_sync(0xFFFFFFFFu, own != 0)) continue;
+            int upto = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            int at = 0;
+            if (lane == 31) at = atomicAdd(&sh.n_elems, upto);
+            at = __shfl_sync(0xFFFFFFFFu, at, 31) + upto - own;
+            if (!fine && at > enough) continue;                   // to be done again, with another bound
+#pragma unroll
+            for (int g = 0; g < kVecs; ++g) {
+                if (!(in >> (g * kPer) & ((1u << kPer) - 1u))) continue;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) {
+                    if (!(in >> (g * kPer + q) & 1u) || at >= kListCap) continue;
                     sh.flat[at] = (uint32_t)b * (uint32_t)a.vocab + (uint32_t)(row.vec_first(c, g) + q);
-                    sh.logit[at] = l;
+                    sh.logit[at] = vec_at<DT>(v[g], q);
                     sh.beam[at] = (uint8_t)b;
+                    ++at;
                 }
             }
         }
+        __syncthreads();
+        if (sh.n_elems <= enough || fine) break;
+        __syncthreads();
+        if (tid == 0) sh.n_elems = 0;
     }
-    __syncthreads();
     const int n = sh.n_elems;
     hard = hard || n > kListCap;
     const Entries e = sh.entries();
@@ -973,6 +1021,7 @@ __global__ void __launch_bounds__(kPickThreads) select_kernel(const __grid_const
     __shared__ dfloat tab[64];
     __shared__ ulonglong2 part[kPickThreads / 32];
     __shared__ int s_again;
+    __shared__ uint32_t s_mask[4];
     pdl_enter();
     const int tid = threadIdx.x;
     uint32_t rank, size;
@@ -997,6 +1046,7 @@ __global__ void __launch_bounds__(kPickThreads) select_kernel(const __grid_const
     cluster_sync();
     again = s_again;
     if (again == 0) return;
+    if (tid < 4) s_mask[tid] = __ldcg(&a.item_mask[item * 4 + tid]);
     fill_exp_table(tab);
     __syncthreads();
     const int units = again * a.refine_segs;
@@ -1004,7 +1054,7 @@ __global__ void __launch_bounds__(kPickThreads) select_kernel(const __grid_const
         int f = u / a.refine_segs, b = 0;
         const int seg = u - f * a.refine_segs;
         for (;; ++b)                                   // the f-th flagged beam
-            if ((__ldcg(&a.item_mask[item * 4 + (b >> 5)]) >> (b & 31) & 1u) && f-- == 0) break;
+            if ((s_mask[b >> 5] >> (b & 31) & 1u) && f-- == 0) break;
         refine_segment<DT>(a, row0 + b, seg, __ldcg(&a.rec[row0 + b].top), tab, part);
     }
     cluster_sync();

@@ -133,6 +133,18 @@ def test_rows_of_one_value_in_large_calls(ws, dtype, n, beams, vocab, n_out):
     check(logits, scores, n_out, ws)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("beams,vocab,n_out", [(1, 32003, 64), (1, 4000, 8), (2, 30000, 256), (8, 9000, 250), (32, 2100, 40)])
+@pytest.mark.parametrize("spread", [0.0, 40.0])
+def test_few_rows_for_what_is_asked(ws, dtype, beams, vocab, n_out, spread):
+    # fewer chunks than continuations, and beams so far apart that the bound of the best is none for them
+    logits, scores, _ = make(3, beams, vocab, dtype, beams + n_out)
+    scores -= spread * torch.arange(beams)
+    scores[2, 1:] = -math.inf                       # the first step
+    check(logits, scores, n_out, ws)
+    check(logits * 40.0, scores, n_out, ws)
+
+
 def test_equal_beams_go_by_their_number(ws):
     logits, scores, _ = make(3, 1, 5003, F32, 11)
     logits = logits.expand(3, 6, 5003).contiguous()
