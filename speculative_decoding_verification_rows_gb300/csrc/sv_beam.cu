@@ -664,7 +664,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     bool hard = sh.n_chunks > kChunkCap;
     // Few chunks for n_out (one live beam, a small vocabulary, beams far apart) bound it loosely or not at all; then the
     // lanes' best of the listed chunks give another bound.  32,003 tokens of one beam for n_out = 64 took 190 us without
-    // it (more elements than a list holds), XX with it.
+    // it (more elements than a list holds), 14 with it.
     const int enough = a.n_out + 32;
     for (bool fine = bound == -FLT_MAX || total < 4 * a.n_out; !hard; fine = true) {
         if (fine) {
@@ -1094,21 +1094,49 @@ BeamLayout beam_layout(int n, int beams, int vocab)
     return L;
 }
 
-cudaError_t launch_cluster(void (*kernel)(BeamArgs), int grid, int cluster, cudaStream_t s, const BeamArgs& a)
+cudaLaunchConfig_t cluster_config(int clusters, int size, cudaLaunchAttribute (&at)[2], cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(clusters * size);
     cfg.blockDim = dim3(kPickThreads);
     cfg.stream = s;
-    cudaLaunchAttribute at[2];
     pdl_attr(at[0]);
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.x = size;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return cfg;
+}
+
+// The largest cluster of which n run at once, 0 for none.  (On a GB300 15 of eight CTAs do, 36 of four, 76 of two, 152
+// of one; a second wave costs as much as the first.)
+template <int DT>
+cudaError_t cluster_for(int n, int* size)
+{
+    constexpr int kSizes[4] = {8, 4, 2, 1};
+    static int active[128][4];                         // + 1, once a device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < 4; ++i) {
+        int many = dev >= 0 && dev < 128 ? active[dev][i] - 1 : -1;
+        if (many < 0) {
+            cudaLaunchAttribute at[2];
+            cudaLaunchConfig_t cfg = cluster_config(1, kSizes[i], at, nullptr);
+            cfg.attrs = at + 1;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&many, select_kernel<DT>, &cfg);
+            if (e != cudaSuccess) return e;
+            if (dev >= 0 && dev < 128) active[dev][i] = many + 1;
+        }
+        if (n <= many) {
+            *size = kSizes[i];
+            return cudaSuccess;
+        }
+    }
+    *size = 0;
+    return cudaSuccess;
 }
 
 template <int DT>
@@ -1132,20 +1160,27 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
             a.segs = (int)segs;
         }
     };
-    // Items that fit the GPU at once, and whose clusters read them in little time
-    const int cluster = a.n * 8 <= sms ? 8 : 4;
+    // One launch of clusters saves two launches (5 us of the host, 2 of the GPU), but an item has its cluster's warps
+    // alone: taken where they get no more than two chunks beyond what the whole GPU's would (us on the GPU in one launch
+    // and in three: 32 x 8 x 32,000 12.6 and 17.3, 32 x 8 x 151,936 18.6 and 19.0, 1 x 16 x 151,936 19.1 and 14.6).
+    int cluster = 0;
+    cudaError_t e = cluster_for<DT>(a.n, &cluster);
+    if (e != cudaSuccess) return e;
+    const double item_chunks = (double)a.beams * a.chunks;
     const int item_warps = cluster * (kPickThreads / 32);
-    const long long item_chunks = (long long)a.beams * a.chunks;
-    if (a.n * cluster <= sms && item_chunks <= 8LL * item_warps) {
+    if (cluster && item_chunks / item_warps <= a.n * item_chunks / (32.0 * sms) + 2.0) {
         segments(a.beams, item_warps);
-        return launch_cluster(select_kernel<DT>, a.n * cluster, cluster, s, a);
+        cudaLaunchAttribute at[2];
+        const cudaLaunchConfig_t cfg = cluster_config(a.n, cluster, at, s);
+        e = cudaLaunchKernelEx(&cfg, select_kernel<DT>, a);
+        return e != cudaSuccess ? e : cudaGetLastError();
     }
     const long long warps = (long long)sms * 4 * (kScanThreads / 32);
     segments(rows, warps);
     const long long units = rows * a.segs;                        // below 2^31
     long long grid = (units + kScanThreads / 32 - 1) / (kScanThreads / 32);
     if (grid > 4LL * sms) grid = 4LL * sms;
-    cudaError_t e = launch_pdl(scan_kernel<DT>, dim3((unsigned)grid), dim3(kScanThreads), 0, s, a);
+    e = launch_pdl(scan_kernel<DT>, dim3((unsigned)grid), dim3(kScanThreads), 0, s, a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(pick_kernel<DT>, dim3(a.n), dim3(kPickThreads), 0, s, a);
     if (e != cudaSuccess) return e;
