@@ -40,16 +40,18 @@ constexpr int kListCap = 2048;               // elements that an item may have a
 constexpr int kChunkCap = 1024;              // and chunks
 constexpr int kPickHeld = 4;                 // chunk maxima a thread keeps in registers
 constexpr int kRefineElems = 4096;           // elements of a row a CTA of refine_kernel sums
+constexpr int kRefineTurns = 32;             // elements a thread sums at most: 32 2^58 < 2^64
 
-// |ln sum exp(l - m) - computed| of one row, V <= 2^19.  With p the row's probabilities, sum
-// p |l - m| = H - ln Z <= ln V <= 13.2, so an argument's relative error r costs
-// 13.2 r.  Differences to the reference and their product with log2 e: 2^-24 +
-// 2^-24 + 2^-26 (less where the reference is near) -> 1.8e-6; ex2.approx 2^-22 for
-// the term and its reference's scale, for up to kMaxSegChunks moves of the
-// reference and for joining the partial sums: 11 (2^-22 + 2^-24) -> 3.3e-6; sums
-// by trees of 8 levels in a chunk, 8 chunks, 5 shuffles, 5 + 5 levels of partial
-// sums: 31 2^-24 -> 1.9e-6; logf: an ulp of 13.2, 9.6e-7.
-constexpr double kSumEps = 8e-6;
+// |ln sum exp(l - m) - computed| of one row, V <= 2^19.  With p the row's probabilities,
+// sum p |l - m| = H - ln Z <= ln V <= 13.2, so an argument's relative error r costs 13.2 r.
+// Near zero (references of whole powers of two, see Ref): the argument's rounding and
+// log2 e, 13.2 (2^-24 + 2^-26) -> 1.0e-6; ex2.approx 2^-22 -> 2.4e-7; sums by trees of 8
+// levels in a chunk, 5 shuffles, 5 of the segments', 2 joins of parts: 20 2^-24 -> 1.2e-6;
+// logf, an ulp of 13.2 -> 9.6e-7: 3.4e-6 in all.  Elsewhere: difference and product
+// 2^-24 each, up to kMaxSegChunks moves of the reference and the segments' join,
+// 9 (2^-22 + 2^-24) -> 2.7e-6: 6.9e-6.
+constexpr double kSumEps = 8e-6, kNearEps = 4e-6;
+constexpr float kNear = 0x1p20f;
 
 enum { kDead = 0, kLive = 1, kFinished = 2 };
 
@@ -84,7 +86,7 @@ struct BeamArgs {
     float* list_logit;       // [n][kListCap]
     int32_t* list_flat;
     ulonglong2* refined;     // [rows][refine segments] sums in units of 2^-26 and of 2^-58
-    int chunks, seg_chunks, segs, refine_segs;
+    int chunks, seg_chunks, segs, refine_elems, refine_segs;
 };
 
 // What the rows' element type says about their layout in 16-byte vectors.
@@ -237,22 +239,32 @@ __device__ __forceinline__ float exp2_approx(float x)
 }
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// What a running reference is to a row's sums.  Near: 2^(x L - c) with one packed
-// fma, L = log2 e and c = ref L in fp32; the product is exact in it, so what c is
-// off by, ref L - c, is off for all x alike and is put right by `scale`.  A
-// reference past 2^20 has too coarse a c: 2^((x - ref) L) then.
+// What a segment's reference, its maximum so far, is to its sum.  Near zero: terms are
+// 2^(x L - c), one packed fma each, L = log2 e in fp32 and c the whole number next to
+// ref L, so that moves of the reference and joins of segments are exact, and what the
+// sum is off by, 2^(c - m L), is known.  Elsewhere 2^((x - ref) L).
 struct Ref {
-    float at = -FLT_MAX, c = 0.f, scale = 1.f;
+    float at = -FLT_MAX, c = 0.f;
     bool near = false;
 
     __device__ __forceinline__ void move(float top)
     {
         at = top;
-        near = fabsf(top) < 0x1p20f;
-        c = top * kLog2e;
-        scale = near ? exp2_approx(-fmaf(top, kLog2e, -c)) : 1.f;
+        near = fabsf(top) < kNear;
+        c = near ? rintf(top * kLog2e) : 0.f;
     }
 };
+__device__ __forceinline__ float whole_exp2(float e)               // of a whole number up to 0
+{
+    return e < -126.f ? 0.f : __int_as_float(((int)e + 127) << 23);
+}
+// By what a sum over reference `from` counts in one over `to`, from.at <= to.at.
+__device__ __forceinline__ float ref_weight(const Ref& from, const Ref& to)
+{
+    if (from.near && to.near) return whole_exp2(from.c - to.c);
+    if (from.near == to.near) return exp2_approx((from.at - to.at) * kLog2e);
+    return from.near ? exp2_approx(fmaf(-to.at, kLog2e, from.c)) : exp2_approx(fmaf(from.at, kLog2e, -to.c));
+}
 template <bool NEAR>
 __device__ __forceinline__ pair_t exp_pair(float x0, float x1, pair_t k)
 {
@@ -332,12 +344,14 @@ __device__ __forceinline__ void scan_rows(const BeamArgs& a, int row0, int rows,
             top = warp_max_nan(top);
             if (lane == 0) a.chunk_max[(size_t)row_no * a.chunks + c] = top;
             if (top > ref.at) {
-                const float f = exp2_approx((ref.at - top) * kLog2e);
+                Ref to;
+                to.move(top);
+                const float f = ref_weight(ref, to);
                 s_hi *= f;
                 s_lo *= f;
-                ref.move(top);
+                ref = to;
             }
-            const float x = (ref.near ? chunk_exp_sum<DT, true>(v, -ref.c) : chunk_exp_sum<DT, false>(v, -ref.at)) * ref.scale;
+            const float x = ref.near ? chunk_exp_sum<DT, true>(v, -ref.c) : chunk_exp_sum<DT, false>(v, -ref.at);
             const dfloat s = df_two_sum(s_hi, x);
             s_hi = s.hi;
             s_lo += s.lo;
@@ -477,6 +491,10 @@ __device__ __forceinline__ float score32(const BeamRec& b, float l)
 {
     return l == -INFINITY ? l : fmaxf(b.base + (l - b.top), -FLT_MAX);
 }
+__device__ __forceinline__ double eps_of(const BeamRec& b)
+{
+    return b.kind != kLive ? 0.0 : fabsf(b.top) < 0.5f * kNear ? kNearEps : kSumEps;   // (segments that are not near count nothing then)
+}
 __device__ __forceinline__ float slack32(const BeamRec& b, float l)
 {
     return (float)kSumEps + 0x1p-22f * (fabsf(b.base) + fabsf(l - b.top));
@@ -602,15 +620,21 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             float m = part.x;
             for (int i = lane + 32; i < a.segs; i += 32) m = fmaxf(m, __ldcg(&sums[i]).x);
             m = warp_max(m);
-            float s = part.y * exp2_approx((part.x - m) * kLog2e);
+            Ref all, one;
+            all.move(m);
+            one.move(part.x);
+            dfloat sum{part.y * ref_weight(one, all), 0.f};
             for (int i = lane + 32; i < a.segs; i += 32) {
                 const float2 x = __ldcg(&sums[i]);
-                s += x.y * exp2_approx((x.x - m) * kLog2e);
+                one.move(x.x);
+                sum = df_add_f(sum, x.y * ref_weight(one, all));
             }
+            float s = sum.hi + sum.lo;
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             if (s == 0.f) kind = kDead;                           // nothing but -inf: every score is -inf
             base = (double)score - (double)logf(s);
+            if (all.near) base -= ((double)all.c - (double)m * (double)kLog2e) * kLn2;
             top = m;
         }
         if (lane == 0) {
@@ -753,17 +777,16 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
         for (int k = tid; k + 1 < n && k < a.n_out; k += kPickThreads) {
             const int i0 = sh.order[k], i1 = sh.order[k + 1];
             const double s0 = f64_of_key(sh.key[i0]), s1 = f64_of_key(sh.key[i1]);
-            if (s0 - s1 > 4.0 * kSumEps + 0x1p-50 * fabs(s1)) continue;
+            if (s0 - s1 > 2.0 * kSumEps + 0x1p-50 * fabs(s1)) continue;
             const int b0 = sh.beam[i0], b1 = sh.beam[i1];
             if (b0 == b1) continue;
-            const bool live0 = sh.rec[b0].kind == kLive, live1 = sh.rec[b1].kind == kLive;
-            const double e0 = live0 ? kSumEps : 0.0, e1 = live1 ? kSumEps : 0.0;
+            const double e0 = eps_of(sh.rec[b0]), e1 = eps_of(sh.rec[b1]);
             const double l0 = (double)sh.logit[i0] - (double)sh.rec[b0].top, l1 = (double)sh.logit[i1] - (double)sh.rec[b1].top;
             const double lo0 = (sh.base[b0] - e0) + l0, hi0 = (sh.base[b0] + e0) + l0;
             const double lo1 = (sh.base[b1] - e1) + l1, hi1 = (sh.base[b1] + e1) + l1;
             if (hi1 < lo0 || (lo0 == hi0 && lo1 == hi1)) continue;
-            if (live0) atomicOr(&sh.mask[b0 >> 5], 1u << (b0 & 31));
-            if (live1) atomicOr(&sh.mask[b1 >> 5], 1u << (b1 & 31));
+            if (e0 != 0.0) atomicOr(&sh.mask[b0 >> 5], 1u << (b0 & 31));
+            if (e1 != 0.0) atomicOr(&sh.mask[b1 >> 5], 1u << (b1 & 31));
         }
     } else if (tid < a.beams && sh.rec[tid].kind == kLive) {
         atomicOr(&sh.mask[tid >> 5], 1u << (tid & 31));
@@ -923,23 +946,29 @@ __device__ void refine_segment(const BeamArgs& a, int row_no, int seg, float top
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Row<DT> row(a, row_no / a.beams, row_no % a.beams);
-    unsigned long long sum = 0ull;                    // of up to 8 terms: below 2^62
-#pragma unroll 2
-    for (int k = 0; k < kRefineElems / kPickThreads; ++k) {
-        const float l = row.elem(seg * kRefineElems + k * kPickThreads + tid);
-        if (l > -INFINITY) sum += fix_df(exp_df(df_two_sum(l, -top), tab), 0x1p58f);   // (what lies outside the row is -inf)
-    }
-    const unsigned long long high = warp_sum_u64(sum >> 32), low = warp_sum_u64(sum & 0xFFFFFFFFull);
-    __syncthreads();
-    if (lane == 0) part[warp] = make_ulonglong2(high, low);
-    __syncthreads();
-    if (tid == 0) {
-        ulonglong2 all = part[0];
-        for (int w = 1; w < kPickThreads / 32; ++w) {
-            all.x += part[w].x;
-            all.y += part[w].y;
+    const int e1 = min((seg + 1) * a.refine_elems, a.vocab);
+    unsigned long long sum = 0ull;                    // of up to kRefineTurns terms
+    for (int e0 = seg * a.refine_elems; e0 < e1; e0 += 4 * kPickThreads) {
+        float l[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int e = e0 + k * kPickThreads + tid;
+            l[k] = row.elem(min(e, a.vocab - 1));
+            if (e >= e1) l[k] = -INFINITY;
         }
-        a.refined[(size_t)row_no * a.refine_segs + seg] = all;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (l[k] > -INFINITY) sum += fix_df(exp_df(df_two_sum(l[k], -top), tab), 0x1p58f);
+    }
+    ulonglong2 all = make_ulonglong2(warp_sum_u64(sum >> 32), warp_sum_u64(sum & 0xFFFFFFFFull));
+    __syncthreads();
+    if (lane == 0) part[warp] = all;
+    __syncthreads();
+    if (warp == 0) {
+        all = part[lane];
+        all.x = warp_sum_u64(all.x);
+        all.y = warp_sum_u64(all.y);
+        if (lane == 0) a.refined[(size_t)row_no * a.refine_segs + seg] = all;
     }
 }
 
@@ -1146,7 +1175,6 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
     const int sms = sm_count();
     const long long rows = (long long)a.n * a.beams;
     a.chunks = (a.vocab + E::kPerVec - 1 + E::kChunk - 1) / E::kChunk;
-    a.refine_segs = (a.vocab + kRefineElems - 1) / kRefineElems;
     // Segments such that the warp with the most of them has the least to do: its chunks, and a third of a chunk's
     // time for every segment (32 x 8 x 151,936: segments of 4 chunks, two for some warps, took 26,000 clocks, 1 chunk 16,000).
     auto segments = [&](long long of_rows, long long warps) {
@@ -1160,6 +1188,11 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
             a.segs = (int)segs;
         }
     };
+    auto refined_by = [&](int elems) {
+        const int turns = (elems + kPickThreads - 1) / kPickThreads;
+        a.refine_elems = kPickThreads * (turns < 4 ? 4 : turns > kRefineTurns ? kRefineTurns : turns);
+        a.refine_segs = (a.vocab + a.refine_elems - 1) / a.refine_elems;
+    };
     // One launch of clusters saves two launches (5 us of the host, 2 of the GPU), but an item has its cluster's warps
     // alone: taken where they get no more than two chunks beyond what the whole GPU's would (us on the GPU in one launch
     // and in three: 32 x 8 x 32,000 12.6 and 17.3, 32 x 8 x 151,936 18.6 and 19.0, 1 x 16 x 151,936 19.1 and 14.6).
@@ -1170,6 +1203,7 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
     const int item_warps = cluster * (kPickThreads / 32);
     if (cluster && item_chunks / item_warps <= a.n * item_chunks / (32.0 * sms) + 2.0) {
         segments(a.beams, item_warps);
+        refined_by((a.vocab + cluster - 1) / cluster);            // a CTA sums its part of every row
         cudaLaunchAttribute at[2];
         const cudaLaunchConfig_t cfg = cluster_config(a.n, cluster, at, s);
         e = cudaLaunchKernelEx(&cfg, select_kernel<DT>, a);
@@ -1177,6 +1211,7 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
     }
     const long long warps = (long long)sms * 4 * (kScanThreads / 32);
     segments(rows, warps);
+    refined_by(kRefineElems);
     const long long units = rows * a.segs;                        // below 2^31
     long long grid = (units + kScanThreads / 32 - 1) / (kScanThreads / 32);
     if (grid > 4LL * sms) grid = 4LL * sms;
