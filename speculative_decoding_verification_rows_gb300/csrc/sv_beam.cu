@@ -50,6 +50,7 @@ constexpr int kScanThreads = 256;
 constexpr int kVecs = 8;                     // 16-byte vectors a lane takes of a chunk
 constexpr int kMaxSegChunks = 8;             // chunks a warp sums up before it leaves a partial sum
 constexpr int kPickThreads = 1024;
+constexpr int kSmallPick = 256;              // threads of an item's CTA where items are many; kMaxOut at least
 constexpr int kListCap = 2048;               // elements that an item may have at its bound
 constexpr int kChunkCap = 1024;              // and chunks
 constexpr int kPickHeld = 4;                 // chunk maxima a thread keeps in registers
@@ -418,13 +419,14 @@ struct Entries {
 // among equals (the places are distinct).  Up to 256 candidates find their places
 // by counting those before them, a few threads each: two barriers, where the
 // sorting network has one a stage.  More are sorted (bitonic).
+template <int T>
 __device__ void sort_entries(const Entries& e, int n, uint16_t* order)
 {
     int p = 1;
     while (p < n) p <<= 1;
-    if (p <= kPickThreads / 2) {
+    if (p <= T / 2) {
         __syncthreads();
-        const int share = min(32, kPickThreads / p), i = threadIdx.x / share;
+        const int share = min(32, T / p), i = threadIdx.x / share;
         if ((int)(threadIdx.x & ~31u) / share < n) {              // (for whole warps)
             int before = 0;
             if (i < n) {
@@ -442,8 +444,8 @@ __device__ void sort_entries(const Entries& e, int n, uint16_t* order)
         __syncthreads();
         return;
     }
-    for (int i = threadIdx.x; i < n; i += blockDim.x) order[i] = (uint16_t)i;
-    for (int i = n + threadIdx.x; i < p; i += blockDim.x) {
+    for (int i = threadIdx.x; i < n; i += T) order[i] = (uint16_t)i;
+    for (int i = n + threadIdx.x; i < p; i += T) {
         e.key[i] = 0ull;
         e.flat[i] = 0xFFFFFFFFu;
         e.logit[i] = -INFINITY;
@@ -452,7 +454,7 @@ __device__ void sort_entries(const Entries& e, int n, uint16_t* order)
     __syncthreads();
     for (int size = 2; size <= p; size <<= 1) {
         for (int stride = size >> 1; stride; stride >>= 1) {
-            for (int t = threadIdx.x; t < (p >> 1); t += blockDim.x) {
+            for (int t = threadIdx.x; t < (p >> 1); t += T) {
                 const int i = 2 * t - (t & (stride - 1)), j = i + stride;
                 const bool down = (i & size) == 0;
                 const unsigned long long ki = e.key[i], kj = e.key[j];
@@ -558,9 +560,10 @@ __device__ void write_item(const BeamArgs& a, int item, const Entries& e, int n,
 // A lower bound on the n_out-th largest of the threads' values: counted in bins
 // of 1/32 below the largest (four barriers), or, where they lie further apart
 // than the bins reach, by bisection (20 barriers).
+template <int T>
 __device__ float nth_bound(float best, int n_out, PickShared& sh)
 {
-    constexpr float kPerUnit = 32.f;
+    constexpr float kPerUnit = (float)(T / 32);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     sh.bins[tid] = 0;
     if (tid == 0) sh.bound_found = 0;
@@ -569,7 +572,7 @@ __device__ float nth_bound(float best, int n_out, PickShared& sh)
     __syncthreads();
     const float most = warp_max(sh.warp_best[lane]);
     const float down = (most - best) * kPerUnit;
-    if (best > -INFINITY && down < (float)kPickThreads) atomicAdd(&sh.bins[(int)down], 1);
+    if (best > -INFINITY && down < (float)T) atomicAdd(&sh.bins[(int)down], 1);
     __syncthreads();
     const int here = sh.bins[tid];
     int upto = here;
@@ -601,7 +604,7 @@ __device__ float nth_bound(float best, int n_out, PickShared& sh)
 // An item's outputs from its rows' sums and chunk maxima, by one CTA.  Returns 0,
 // or the number of rows (sh.mask) to be summed again first: the candidates stay
 // in shared memory, sh.n_elems of them, or -1 for more than a list holds.
-template <int DT>
+template <int DT, int T>
 __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -612,14 +615,14 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     float held[kPickHeld];
 #pragma unroll
     for (int k = 0; k < kPickHeld; ++k) {
-        const int i = tid + k * kPickThreads;
+        const int i = tid + k * T;
         held[k] = i < total ? __ldcg(&chunk_max[i]) : 0.f;
     }
     if (tid == 0) sh.n_chunks = sh.n_elems = sh.bad = 0;
     if (tid < 4) sh.mask[tid] = 0u;
     __syncthreads();
     // normalisers, a warp a beam
-    for (int b = warp; b < a.beams; b += kPickThreads / 32) {
+    for (int b = warp; b < a.beams; b += T / 32) {
         const float2* sums = a.sums + (size_t)(row0 + b) * a.segs;
         const float2 part = lane < a.segs ? __ldcg(&sums[lane]) : make_float2(-FLT_MAX, 0.f);
         float score;
@@ -674,10 +677,10 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     const int mine = total - warp * 32;                           // of the chunks a warp's turns begin at
 #pragma unroll
     for (int k = 0; k < kPickHeld; ++k)
-        if (k * kPickThreads < mine) held[k] = rate(tid + k * kPickThreads, held[k]);
-    for (int i = tid + kPickHeld * kPickThreads; i < total; i += kPickThreads) rate(i, __ldcg(&chunk_max[i]));
+        if (k * T < mine) held[k] = rate(tid + k * T, held[k]);
+    for (int i = tid + kPickHeld * T; i < total; i += T) rate(i, __ldcg(&chunk_max[i]));
     if (tid < a.beams && sh.rec[tid].kind == kFinished) best = fmaxf(best, sh.rec[tid].base);
-    float bound = nth_bound(best, a.n_out, sh);
+    float bound = nth_bound<T>(best, a.n_out, sh);
     if (sh.bad) {                                                 // (its last write is before the barriers above)
         if (tid < a.n_out) {
             const size_t o = (size_t)item * a.n_out + tid;
@@ -695,8 +698,8 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     };
 #pragma unroll
     for (int k = 0; k < kPickHeld; ++k)
-        if (k * kPickThreads < mine) keep(tid + k * kPickThreads, held[k]);
-    for (int i = tid + kPickHeld * kPickThreads; i < total; i += kPickThreads) keep(i, rate(i, __ldcg(&chunk_max[i])));
+        if (k * T < mine) keep(tid + k * T, held[k]);
+    for (int i = tid + kPickHeld * T; i < total; i += T) keep(i, rate(i, __ldcg(&chunk_max[i])));
     __syncthreads();
     constexpr int kPer = Elem<DT>::kPerVec;
     bool hard = sh.n_chunks > kChunkCap;
@@ -707,7 +710,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     for (bool fine = bound == -FLT_MAX || total < 4 * a.n_out; !hard; fine = true) {
         if (fine) {
             best = tid < a.beams && sh.rec[tid].kind == kFinished ? sh.rec[tid].base : -INFINITY;
-            for (int k = warp; k < sh.n_chunks; k += kPickThreads / 32) {
+            for (int k = warp; k < sh.n_chunks; k += T / 32) {
                 const int i = sh.chunk[k], b = beam_of(i);
                 uint4 v[kVecs];
                 Row<DT>(a, item, b).chunk(i - b * a.chunks, v);
@@ -717,7 +720,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
                 const float s = score32(sh.rec[b], l);
                 if (s > -INFINITY) best = fmaxf(best, s - slack32(sh.rec[b], l));
             }
-            bound = fmaxf(bound, nth_bound(best, a.n_out, sh));
+            bound = fmaxf(bound, nth_bound<T>(best, a.n_out, sh));
         }
         // Where l - m is near bound - base, score and slack are off by 2^-22 (|base| + |bound - base|).
         if (tid < a.beams && sh.rec[tid].kind == kLive) {
@@ -732,7 +735,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             sh.beam[at] = (uint8_t)tid;
         }
         __syncthreads();                                          // (they find room)
-        for (int k = warp; k < sh.n_chunks; k += kPickThreads / 32) {   // a warp a chunk
+        for (int k = warp; k < sh.n_chunks; k += T / 32) {   // a warp a chunk
             const int i = sh.chunk[k], b = beam_of(i), c = i - b * a.chunks;
             const Row<DT> row(a, item, b);
             uint4 v[kVecs];
@@ -784,11 +787,11 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     hard = hard || n > kListCap;
     const Entries e = sh.entries();
     if (!hard) {
-        for (int i = tid; i < n; i += kPickThreads) sh.key[i] = score_key(sh, sh.beam[i], sh.logit[i]);
-        sort_entries(e, n, sh.order);
+        for (int i = tid; i < n; i += T) sh.key[i] = score_key(sh, sh.beam[i], sh.logit[i]);
+        sort_entries<T>(e, n, sh.order);
         write_item<DT>(a, item, e, n, sh);                        // to be written again where the order may be another
         // neighbours of two beams that the normalisers' errors may have put the wrong way round
-        for (int k = tid; k + 1 < n && k < a.n_out; k += kPickThreads) {
+        for (int k = tid; k + 1 < n && k < a.n_out; k += T) {
             const int i0 = sh.order[k], i1 = sh.order[k + 1];
             const double s0 = f64_of_key(sh.key[i0]), s1 = f64_of_key(sh.key[i1]);
             if (s0 - s1 > 2.0 * kSumEps + 0x1p-50 * fabs(s1)) continue;
@@ -811,18 +814,18 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
     return again;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ BeamArgs a)
+template <int DT, int T>
+__global__ void __launch_bounds__(T) pick_kernel(const __grid_constant__ BeamArgs a)
 {
     __shared__ PickShared sh;
     pdl_enter();
     const int tid = threadIdx.x, item = blockIdx.x, row0 = item * a.beams;
-    const int again = pick_item<DT>(a, item, sh);
+    const int again = pick_item<DT, T>(a, item, sh);
     if (again == 0) return;
     // refine_kernel finishes the item
     __syncthreads();
     const int n = sh.n_elems;
-    for (int i = tid; i < n; i += kPickThreads) {
+    for (int i = tid; i < n; i += T) {
         a.list_flat[(size_t)item * kListCap + i] = (int32_t)sh.flat[i];
         a.list_logit[(size_t)item * kListCap + i] = sh.logit[i];
     }
@@ -1006,7 +1009,7 @@ __device__ void finish_item(const BeamArgs& a, int item, int n, PickShared& sh)
     const Entries e = sh.entries();
     if (n >= 0) {
         for (int i = tid; i < n; i += kPickThreads) sh.key[i] = score_key(sh, sh.beam[i], sh.logit[i]);
-        sort_entries(e, n, sh.order);
+        sort_entries<kPickThreads>(e, n, sh.order);
     } else {
         n = pick_by_turns<DT>(a, item, sh);
     }
@@ -1075,7 +1078,7 @@ __global__ void __launch_bounds__(kPickThreads) select_kernel(const __grid_const
     cluster_sync();
     int again = 0;
     if (rank == 0) {
-        again = pick_item<DT>(a, item, sh);
+        again = pick_item<DT, kPickThreads>(a, item, sh);
         if (again) {
             if (tid < 4) a.item_mask[item * 4 + tid] = sh.mask[tid];
             if (tid < a.beams) a.rec[row0 + tid] = sh.rec[tid];
@@ -1231,7 +1234,11 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
     if (grid > 4LL * sms) grid = 4LL * sms;
     e = launch_pdl(scan_kernel<DT>, dim3((unsigned)grid), dim3(kScanThreads), 0, s, a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(pick_kernel<DT>, dim3(a.n), dim3(kPickThreads), 0, s, a);
+    // More items than SMs: four small CTAs an SM, where an item has few chunks to read again or there are many waves
+    // (n x beams x vocabulary, n_out; us with large and small CTAs: 1,024 x 4 x 1,000, 8: 69 and 23; 160 x 4 x 32,000, 8:
+    // 22.7 and 17.8; 300 x 16 x 32,000, 32: 78 and 83; 200 x 8 x 151,936, 16: 88 and 94).
+    e = a.n > sms && (a.n_out <= 8 || a.n > 4 * sms) ? launch_pdl(pick_kernel<DT, kSmallPick>, dim3(a.n), dim3(kSmallPick), 0, s, a)
+            : launch_pdl(pick_kernel<DT, kPickThreads>, dim3(a.n), dim3(kPickThreads), 0, s, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(refine_kernel<DT>, dim3(sms), dim3(kPickThreads), 0, s, a);
 }

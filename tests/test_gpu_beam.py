@@ -145,6 +145,18 @@ def test_few_rows_for_what_is_asked(ws, dtype, beams, vocab, n_out, spread):
     check(logits * 40.0, scores, n_out, ws)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,beams,vocab,n_out", [(160, 3, 4099, 8), (700, 2, 1001, 17), (620, 3, 300, 256), (900, 1, 40, 3)])
+def test_more_items_than_run_at_once(ws, dtype, n, beams, vocab, n_out):
+    logits, scores, g = make(n, beams, vocab, dtype, n)
+    logits[n // 2] = logits[n // 2, :1]              # equal rows, equal scores: ordered again
+    scores[n // 2] = -1.0
+    logits[n // 3] = -0.5                            # one value
+    logits[n // 4, 0] = -math.inf
+    finished = torch.rand((n, beams), generator=g) < 0.2
+    check(logits, scores, n_out, ws, finished, end_token=7)
+
+
 def test_equal_beams_go_by_their_number(ws):
     logits, scores, _ = make(3, 1, 5003, F32, 11)
     logits = logits.expand(3, 6, 5003).contiguous()
