@@ -1265,18 +1265,20 @@ struct ReorderArgs {
     int32_t* status;
 };
 
-// A thread has one unit of every row of its item, so what it reads of the old
-// rows is read before it writes any of them and nobody else does either: in
-// place needs no second copy of the state.  HBM bounds it: 16 x 8 rows of 1 MB,
-// half of them moving, in 20.5 us (6.2 TB/s of rows moved, 91% of the copy
-// bandwidth); 32 x 8 histories of 4 KB in 2.3 us of the GPU, 7.7 with the host.
+// A CTA has some units of every row of its item, so what it reads of the old rows
+// is read before it writes any of them and nobody else does either: in place needs
+// no second copy of the state.  A thread has a unit of up to ROWS rows in registers
+// (with more rows, blockDim.y threads share a unit's, and a barrier stands between
+// their reads and writes).  HBM bounds it: 16 x 8 rows of 1 MB, half of them moving,
+// in 20.5 us (6.2 TB/s of rows moved, 91% of the copy bandwidth); 32 x 8 histories
+// of 4 KB in 2.3 us of the GPU, 7.7 with the host.
 template <typename R, int ROWS>
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_constant__ ReorderArgs a)
 {
-    extern __shared__ int32_t parent[];
+    __shared__ int32_t parent[kMaxBeams];
     pdl_enter();
     const int64_t item = blockIdx.y;
-    for (int i = threadIdx.x; i < a.beams_out; i += kReorderThreads) {
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < a.beams_out; i += kReorderThreads) {
         int p = a.parents[item * a.beams_out + i];
         if (p < 0 || p >= a.beams_in) {
             if (a.status && blockIdx.x == 0) atomicOr(&a.status[item], kBadLayout);
@@ -1287,72 +1289,38 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_c
         parent[i] = p;
     }
     __syncthreads();
-    const int64_t u = (int64_t)blockIdx.x * kReorderThreads + threadIdx.x;
-    if (u >= a.units) return;
+    const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const char* src = a.src + item * a.src_item + u * (int64_t)sizeof(R);
     char* dst = a.dst + item * a.dst_item + u * (int64_t)sizeof(R);
-    for (int i0 = 0; i0 < a.beams_out; i0 += ROWS) {
+    const int rows = u < a.units ? a.beams_out : 0;
+    const int turns = a.in_place ? 1 : (a.beams_out + ROWS - 1) / ROWS;   // in place all rows go at once
+    for (int turn = 0; turn < turns; ++turn) {
+        const int i0 = (turn + (int)threadIdx.y) * ROWS;
         R x[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
-            if (i0 + i < a.beams_out && parent[i0 + i] >= 0)
-                x[i] = *reinterpret_cast<const R*>(src + parent[i0 + i] * a.src_beam);
+            if (i0 + i < rows && parent[i0 + i] >= 0) x[i] = *reinterpret_cast<const R*>(src + parent[i0 + i] * a.src_beam);
+        if (blockDim.y > 1) __syncthreads();
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
-            if (i0 + i < a.beams_out && parent[i0 + i] >= 0)
-                *reinterpret_cast<R*>(dst + (i0 + i) * a.dst_beam) = x[i];
+            if (i0 + i < rows && parent[i0 + i] >= 0) *reinterpret_cast<R*>(dst + (i0 + i) * a.dst_beam) = x[i];
     }
 }
 
-// In place with more rows than a thread's registers hold: they wait in shared memory.
-template <typename R>
-__global__ void __launch_bounds__(kReorderThreads) reorder_shared_kernel(const __grid_constant__ ReorderArgs a)
-{
-    extern __shared__ __align__(16) unsigned char rows_raw[];
-    __shared__ int32_t parent[kMaxBeams];
-    R* rows = reinterpret_cast<R*>(rows_raw);                    // [beams][blockDim.x]
-    pdl_enter();
-    const int64_t item = blockIdx.y;
-    for (int i = threadIdx.x; i < a.beams_out; i += blockDim.x) {
-        int p = a.parents[item * a.beams_out + i];
-        if (p < 0 || p >= a.beams_in) {
-            if (a.status && blockIdx.x == 0) atomicOr(&a.status[item], kBadLayout);
-            p = -1;
-        } else if (p == i) {
-            p = -1;
-        }
-        parent[i] = p;
-    }
-    __syncthreads();
-    const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (u >= a.units) return;
-    const char* src = a.src + item * a.src_item + u * (int64_t)sizeof(R);
-    char* dst = a.dst + item * a.dst_item + u * (int64_t)sizeof(R);
-#pragma unroll 8
-    for (int i = 0; i < a.beams_out; ++i)
-        if (parent[i] >= 0) rows[i * blockDim.x + threadIdx.x] = *reinterpret_cast<const R*>(src + parent[i] * a.src_beam);
-#pragma unroll 8
-    for (int i = 0; i < a.beams_out; ++i)
-        if (parent[i] >= 0) *reinterpret_cast<R*>(dst + i * a.dst_beam) = rows[i * blockDim.x + threadIdx.x];
-}
-
-template <typename R>
-cudaError_t launch_reorder(ReorderArgs a, int n, int64_t row_bytes, cudaStream_t s)
+template <typename R, int ROWS>
+cudaError_t launch_reorder(ReorderArgs a, int n, int64_t row_bytes, int share, cudaStream_t s)
 {
     a.units = row_bytes / (int64_t)sizeof(R);
-    if (a.in_place && a.beams_out > 32) {
-        const int threads = 64;
-        const size_t smem = sizeof(R) * (size_t)threads * (size_t)a.beams_out;
-        cudaError_t e = cudaFuncSetAttribute(reorder_shared_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)(sizeof(R) * threads * kMaxBeams));
-        if (e != cudaSuccess) return e;
-        return launch_pdl(reorder_shared_kernel<R>, dim3((unsigned)((a.units + threads - 1) / threads), n), dim3(threads),
-                          smem, s, a);
-    }
-    const dim3 grid((unsigned)((a.units + kReorderThreads - 1) / kReorderThreads), n);
-    const size_t smem = sizeof(int32_t) * (size_t)a.beams_out;
-    if (a.in_place && a.beams_out > 8) return launch_pdl(reorder_kernel<R, 32>, grid, dim3(kReorderThreads), smem, s, a);
-    return launch_pdl(reorder_kernel<R, 8>, grid, dim3(kReorderThreads), smem, s, a);
+    const int wide = kReorderThreads / share;
+    return launch_pdl(reorder_kernel<R, ROWS>, dim3((unsigned)((a.units + wide - 1) / wide), n), dim3(wide, share), 0, s, a);
+}
+template <typename R>
+cudaError_t launch_reorder_rows(const ReorderArgs& a, int n, int64_t row_bytes, cudaStream_t s)
+{
+    if (!a.in_place || a.beams_out <= 8) return launch_reorder<R, 8>(a, n, row_bytes, 1, s);
+    int share = 1;
+    while (share * 16 < a.beams_out) share *= 2;
+    return launch_reorder<R, 16>(a, n, row_bytes, share, s);
 }
 
 }  // namespace
@@ -1442,10 +1410,10 @@ extern "C" sv_status_t sv_beam_reorder(const void* src, int64_t src_stride_item,
                          (uint64_t)src_stride_beam | (uint64_t)dst_stride_item | (uint64_t)dst_stride_beam |
                          (uint64_t)row_bytes;
     cudaError_t e;
-    if (all % 16 == 0) e = launch_reorder<uint4>(a, n, row_bytes, stream);
-    else if (all % 8 == 0) e = launch_reorder<uint2>(a, n, row_bytes, stream);
-    else if (all % 4 == 0) e = launch_reorder<uint32_t>(a, n, row_bytes, stream);
-    else if (all % 2 == 0) e = launch_reorder<uint16_t>(a, n, row_bytes, stream);
-    else e = launch_reorder<uint8_t>(a, n, row_bytes, stream);
+    if (all % 16 == 0) e = launch_reorder_rows<uint4>(a, n, row_bytes, stream);
+    else if (all % 8 == 0) e = launch_reorder_rows<uint2>(a, n, row_bytes, stream);
+    else if (all % 4 == 0) e = launch_reorder_rows<uint32_t>(a, n, row_bytes, stream);
+    else if (all % 2 == 0) e = launch_reorder_rows<uint16_t>(a, n, row_bytes, stream);
+    else e = launch_reorder_rows<uint8_t>(a, n, row_bytes, stream);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

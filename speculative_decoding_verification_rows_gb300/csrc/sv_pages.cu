@@ -25,6 +25,27 @@
 namespace sv {
 namespace {
 
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+cudaLaunchConfig_t cluster_config(dim3 grid, int threads, int size, size_t smem, cudaLaunchAttribute (&at)[2], cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    pdl_attr(at[0]);
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = size;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
 constexpr int kForkThreads = 1024;
 constexpr int kTileCols = 256;        // columns of a table row a warp takes
 constexpr int kTileWords = kTileCols / 32;
@@ -337,12 +358,6 @@ __global__ void __launch_bounds__(kForkThreads) fork_assign_kernel(const __grid_
     fork_assign(a, blockIdx.x, gridDim.x, s_warp, s_list, s_first);
 }
 
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // All steps in one cluster.
 __global__ void __launch_bounds__(kForkThreads) fork_cluster_kernel(const __grid_constant__ ForkArgs a)
 {
@@ -418,18 +433,8 @@ cudaError_t launch_fork(const ForkArgs& a, cudaStream_t s)
     if (units <= 2LL * kForkCluster * kWarps && a.page_tiles <= 4 * kForkCluster) {
         int blocks = 1;
         while (blocks < kForkCluster && (units > (long long)blocks * kWarps || a.page_tiles > blocks)) blocks *= 2;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(blocks);
-        cfg.blockDim = dim3(kForkThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = s;
         cudaLaunchAttribute at[2];
-        pdl_attr(at[0]);
-        at[1].id = cudaLaunchAttributeClusterDimension;
-        at[1].val.clusterDim.x = blocks;
-        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 2;
+        const cudaLaunchConfig_t cfg = cluster_config(dim3(blocks), kForkThreads, blocks, smem, at, s);
         e = cudaLaunchKernelEx(&cfg, fork_cluster_kernel, a);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
@@ -461,6 +466,7 @@ struct MoveArgs {
     int n, ld_keep, max_keep;
     int per_head;                  // units of a head
     int one;                       // keys and values are one tensor
+    int tensors;                   // keys and values of all layers
     int strip;                     // sv_kv_compact: units of a token a CTA takes
     int strips;
 };
@@ -526,27 +532,37 @@ __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constan
 // read another turn ahead; one barrier a turn.  CTAs have different strips.  Half
 // of 4 x 16,383 tokens (8 heads of 128, strips of 64 bytes) in 50 us (5.4 TB/s, 79%
 // of the copy bandwidth); 157 when a turn waited for its own lookups and reads.
+//
+// A cluster shares a strip's turns where strips alone are too few CTAs.  A list
+// of one turn keeps its places for all the layers that its CTA takes, the next
+// layer's units on their way while one is written.
 template <typename R, int THREADS>
-__global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant__ MoveArgs a)
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 2 : 9) compact_kernel(const __grid_constant__ MoveArgs a)
 {
     __shared__ int64_t s_from[3][THREADS], s_to[3][THREADS];     // a token's old and new place; from -1: it does not move
     pdl_enter();
-    const int r = blockIdx.x / a.strips, strip = blockIdx.x - r * a.strips, tid = threadIdx.x;
+    uint32_t rank, size;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+    const int tid = threadIdx.x, work = blockIdx.x / size, r = work / a.strips, strip = work - r * a.strips;
     const int n = a.n_keep[r];
     const long long first = a.first ? a.first[r] : 0;
     const bool report = a.status && strip == 0 && blockIdx.y == 0;
     if (n < 0 || n > a.max_keep || first < 0) {
-        if (report && tid == 0) atomicOr(&a.status[r], kBadLayout);
+        if (report && rank == 0 && tid == 0) atomicOr(&a.status[r], kBadLayout);
         return;
     }
-    int64_t page, token, head;
-    R* base = layer_of<R>(a, blockIdx.y, &page, &token, &head);
     const int lane = tid % a.strip, row = tid / a.strip, rows = THREADS / a.strip;
-    const int turn = rows * kMoveUnits;                           // tokens; at most THREADS, as a strip has kMoveUnits units or more
+    const int share = rows * kMoveUnits;                          // tokens of a CTA's turn; at most THREADS, as a strip has kMoveUnits units or more
+    const int turn = share * (int)size, before = share * (int)rank;
     const int s = strip * a.strip + lane;
     const bool mine = s < a.per_head * a.cache.k.heads;
     const int h = s / a.per_head;
-    base += h * head + (s - h * a.per_head);
+    int64_t page, token, head;
+    auto strip_of = [&](int y) {
+        R* base = layer_of<R>(a, y, &page, &token, &head);
+        return base + h * head + (s - h * a.per_head);
+    };
     const int32_t* keep = a.keep + (int64_t)r * a.ld_keep;
     const int32_t* table = a.cache.page_table + (int64_t)r * a.cache.ld_table;
     const long long limit = (long long)a.cache.max_pages * a.cache.page_size;
@@ -554,14 +570,14 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant_
     // The thread's token of turn t: entries of the list, then its places.
     int k = 0, k_before = -1;
     auto list = [&](int t) {
-        const int j = t * turn + tid;
-        if (tid >= turn || j >= n) return;
+        const int j = t * turn + before + tid;
+        if (tid >= share || j >= n) return;
         k = keep[j];
         k_before = j ? keep[j - 1] : -1;
     };
     auto look_up = [&](int t) {
-        const int j = t * turn + tid;
-        if (tid >= turn) return;
+        const int j = t * turn + before + tid;
+        if (tid >= share) return;
         int64_t from = -1, to = 0;
         if (j < n) {
             bool fine = k >= j && k_before < k && first + k < limit;
@@ -581,8 +597,7 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant_
         s_to[t % 3][tid] = to;
     };
     R x[kMoveUnits], next[kMoveUnits];
-    uint32_t moves = 0u;
-    auto read = [&](int t, R (&v)[kMoveUnits]) {                  // which of the units move
+    auto read = [&](const R* base, int t, R (&v)[kMoveUnits]) {   // which of the units move
         uint32_t m = 0u;
         if (!mine) return m;
 #pragma unroll
@@ -594,27 +609,54 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant_
         }
         return m;
     };
-    list(0);
-    look_up(0);
-    list(1);
-    look_up(1);
-    list(2);
-    __syncthreads();
-    moves = read(0, x);
-    __syncthreads();
-    for (int t = 0; t * turn < n; ++t) {
-        const uint32_t next_moves = (t + 1) * turn < n ? read(t + 1, next) : 0u;
+    auto write = [&](R* base, int t, uint32_t moves) {
 #pragma unroll
-        for (int i = 0; i < kMoveUnits; ++i)
+        for (int i = 0; i < kMoveUnits; ++i) {
             if (moves >> i & 1u) base[s_to[t % 3][i * rows + row]] = x[i];
-        if ((t + 2) * turn < n) {
-            look_up(t + 2);
-            list(t + 3);
+            x[i] = next[i];
         }
+    };
+    auto barrier = [&]() {
+        if (size > 1) cluster_sync();
+        else __syncthreads();
+    };
+    if (n <= turn) {
+        R* base = strip_of(blockIdx.y);
+        list(0);
+        look_up(0);
         __syncthreads();
-        moves = next_moves;
-#pragma unroll
-        for (int i = 0; i < kMoveUnits; ++i) x[i] = next[i];
+        uint32_t moves = read(base, 0, x);
+        for (int y = blockIdx.y; y < a.tensors; y += gridDim.y) { // all of them keys, or values: the places are the same
+            const int y1 = y + gridDim.y;
+            R* base1 = y1 < a.tensors ? strip_of(y1) : base;
+            const uint32_t next_moves = y1 < a.tensors ? read(base1, 0, next) : 0u;
+            barrier();
+            write(base, 0, moves);
+            base = base1;
+            moves = next_moves;
+        }
+        return;
+    }
+    for (int y = blockIdx.y; y < a.tensors; y += gridDim.y) {
+        R* base = strip_of(y);
+        list(0);
+        look_up(0);
+        list(1);
+        look_up(1);
+        list(2);
+        __syncthreads();
+        uint32_t moves = read(base, 0, x);
+        barrier();
+        for (int t = 0; t * turn < n; ++t) {
+            const uint32_t next_moves = (t + 1) * turn < n ? read(base, t + 1, next) : 0u;
+            write(base, t, moves);
+            if ((t + 2) * turn < n) {
+                look_up(t + 2);
+                list(t + 3);
+            }
+            barrier();
+            moves = next_moves;
+        }
     }
 }
 
@@ -641,7 +683,7 @@ template <typename R>
 cudaError_t launch_move(MoveArgs a, int layers, cudaStream_t s)
 {
     const long long token = (long long)a.per_head * a.cache.k.heads;
-    const int tensors = a.one ? layers : 2 * layers;
+    const int tensors = a.tensors = a.one ? layers : 2 * layers;
     if (a.copies) {
         long long parts = (token * a.cache.page_size + kMoveThreads * kCopyUnits - 1) / (kMoveThreads * kCopyUnits);
         if (parts > 64) parts = 64;
@@ -651,10 +693,20 @@ cudaError_t launch_move(MoveArgs a, int layers, cudaStream_t s)
     a.strip = 32;
     while (a.strip > least && (long long)a.n * tensors * ((token + a.strip - 1) / a.strip) < 8LL * sm_count()) a.strip /= 2;
     a.strips = (int)((token + a.strip - 1) / a.strip);
-    const dim3 grid((unsigned)a.n * a.strips, tensors);
-    // Accepted paths take many small CTAs (8 us, 18 with 512 threads), long lists few large ones.
-    if (a.max_keep <= 64) return launch_pdl(compact_kernel<R, 128>, grid, dim3(128), 0, s, a);
-    return launch_pdl(compact_kernel<R, 512>, grid, dim3(512), 0, s, a);
+    const long long strips = (long long)a.n * a.strips, sms = sm_count();
+    if (a.max_keep <= 64) {                                     // accepted paths: small CTAs (5 us, 18 with 512 threads), some layers each
+        const int both = a.one ? 1 : 2;
+        const long long groups = (16 * sms + strips * both - 1) / (strips * both);
+        const int y = both * (int)(groups < layers ? groups : layers);
+        return launch_pdl(compact_kernel<R, 128>, dim3((unsigned)strips, y), dim3(128), 0, s, a);
+    }
+    int size = 1;                                               // two CTAs an SM
+    while (size < 8 && 2 * size * strips * tensors <= 2 * sms) size *= 2;
+    if (size == 1) return launch_pdl(compact_kernel<R, 512>, dim3((unsigned)strips, tensors), dim3(512), 0, s, a);
+    cudaLaunchAttribute at[2];
+    const cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)strips * size, tensors), 512, size, 0, at, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, compact_kernel<R, 512>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 sv_status_t run_move(MoveArgs a, sv_dtype_t dt, int head_dim, int layers, cudaStream_t s)

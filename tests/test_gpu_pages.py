@@ -337,6 +337,15 @@ def test_windows_of_all_lengths(n, window, share, page, heads):
     run_compact(k, v, first, table, keep, n_keep, page)
 
 
+@pytest.mark.parametrize("layers,n,window,share", [(40, 6, 30, 0.4), (33, 64, 20, 0.3), (3, 300, 70, 0.5), (5, 1, 5000, 0.7)])
+def test_many_layers_and_long_lists(layers, n, window, share):
+    first, table, keep, n_keep, n_pages = compact_case(n, 16, window, layers, share)
+    keep = [row[:max(n_keep)] for row in keep]                # a short list, whatever the window
+    k, v = cache_of(layers, n_pages, 16, 2, 64, F16, "tokens")
+    v = torch.cat([v, v], -1)[..., 17:81]                     # values in other places than the keys
+    run_compact(k, v, first, table, keep, n_keep, 16)
+
+
 def test_every_second_token_and_no_first():
     # overlapping moves of a page at a time, from the first token of the cache
     page, n_keep = 16, 500
