@@ -1268,17 +1268,18 @@ struct ReorderArgs {
 // A CTA has some units of every row of its item, so what it reads of the old rows
 // is read before it writes any of them and nobody else does either: in place needs
 // no second copy of the state.  A thread has a unit of up to ROWS rows in registers
-// (with more rows, blockDim.y threads share a unit's, and a barrier stands between
-// their reads and writes).  HBM bounds it: 16 x 8 rows of 1 MB, half of them moving,
+// (with more rows SHARE threads share a unit's, and a barrier stands between their
+// reads and writes).  HBM bounds it: 16 x 8 rows of 1 MB, half of them moving,
 // in 20.5 us (6.2 TB/s of rows moved, 91% of the copy bandwidth); 32 x 8 histories
 // of 4 KB in 2.3 us of the GPU, 7.7 with the host.
-template <typename R, int ROWS>
+template <typename R, int ROWS, int SHARE>
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_constant__ ReorderArgs a)
 {
+    constexpr int kWide = kReorderThreads / SHARE;
     __shared__ int32_t parent[kMaxBeams];
     pdl_enter();
     const int64_t item = blockIdx.y;
-    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < a.beams_out; i += kReorderThreads) {
+    for (int i = threadIdx.x; i < a.beams_out; i += kReorderThreads) {
         int p = a.parents[item * a.beams_out + i];
         if (p < 0 || p >= a.beams_in) {
             if (a.status && blockIdx.x == 0) atomicOr(&a.status[item], kBadLayout);
@@ -1289,38 +1290,41 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_c
         parent[i] = p;
     }
     __syncthreads();
-    const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t u = (int64_t)blockIdx.x * kWide + threadIdx.x % kWide;
+    if (SHARE == 1 && u >= a.units) return;
     const char* src = a.src + item * a.src_item + u * (int64_t)sizeof(R);
     char* dst = a.dst + item * a.dst_item + u * (int64_t)sizeof(R);
     const int rows = u < a.units ? a.beams_out : 0;
-    const int turns = a.in_place ? 1 : (a.beams_out + ROWS - 1) / ROWS;   // in place all rows go at once
-    for (int turn = 0; turn < turns; ++turn) {
-        const int i0 = (turn + (int)threadIdx.y) * ROWS;
+    for (int i0 = (int)threadIdx.x / kWide * ROWS; i0 < a.beams_out || SHARE > 1; i0 += ROWS) {   // in place one turn does
         R x[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
             if (i0 + i < rows && parent[i0 + i] >= 0) x[i] = *reinterpret_cast<const R*>(src + parent[i0 + i] * a.src_beam);
-        if (blockDim.y > 1) __syncthreads();
+        if (SHARE > 1) __syncthreads();
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
             if (i0 + i < rows && parent[i0 + i] >= 0) *reinterpret_cast<R*>(dst + (i0 + i) * a.dst_beam) = x[i];
+        if (SHARE > 1) return;
     }
 }
 
-template <typename R, int ROWS>
-cudaError_t launch_reorder(ReorderArgs a, int n, int64_t row_bytes, int share, cudaStream_t s)
+template <typename R, int ROWS, int SHARE>
+cudaError_t launch_reorder(ReorderArgs a, int n, int64_t row_bytes, cudaStream_t s)
 {
     a.units = row_bytes / (int64_t)sizeof(R);
-    const int wide = kReorderThreads / share;
-    return launch_pdl(reorder_kernel<R, ROWS>, dim3((unsigned)((a.units + wide - 1) / wide), n), dim3(wide, share), 0, s, a);
+    constexpr int kWide = kReorderThreads / SHARE;
+    return launch_pdl(reorder_kernel<R, ROWS, SHARE>, dim3((unsigned)((a.units + kWide - 1) / kWide), n), dim3(kReorderThreads),
+                      0, s, a);
 }
 template <typename R>
 cudaError_t launch_reorder_rows(const ReorderArgs& a, int n, int64_t row_bytes, cudaStream_t s)
 {
-    if (!a.in_place || a.beams_out <= 8) return launch_reorder<R, 8>(a, n, row_bytes, 1, s);
-    int share = 1;
-    while (share * 16 < a.beams_out) share *= 2;
-    return launch_reorder<R, 16>(a, n, row_bytes, share, s);
+    const int rows = a.in_place ? a.beams_out : 1;
+    if (rows <= 8) return launch_reorder<R, 8, 1>(a, n, row_bytes, s);
+    if (rows <= 16) return launch_reorder<R, 16, 1>(a, n, row_bytes, s);
+    if (rows <= 32) return launch_reorder<R, 16, 2>(a, n, row_bytes, s);
+    if (rows <= 64) return launch_reorder<R, 16, 4>(a, n, row_bytes, s);
+    return launch_reorder<R, 16, 8>(a, n, row_bytes, s);
 }
 
 }  // namespace
