@@ -689,12 +689,16 @@ cudaError_t launch_move(MoveArgs a, int layers, cudaStream_t s)
         if (parts > 64) parts = 64;
         return launch_pdl(copy_kernel<R>, dim3(a.n, tensors, (unsigned)parts), dim3(kMoveThreads), 0, s, a);
     }
-    const int least = 64 / (int)sizeof(R);                      // a strip of 64 bytes at least
+    // Strips as wide as give three CTAs two SMs, of 64 bytes at least, and of which a token is whole ones if it can be (8 x
+    // 16,384 tokens, half kept: 99 us with 64 bytes, 93 with 128; 4 requests of those 51 and 58).
+    const int least = 64 / (int)sizeof(R);
     a.strip = 32;
-    while (a.strip > least && (long long)a.n * tensors * ((token + a.strip - 1) / a.strip) < 8LL * sm_count()) a.strip /= 2;
+    while (a.strip > least && (token % a.strip || 2LL * a.n * tensors * (token / a.strip) < 3LL * sm_count())) a.strip /= 2;
     a.strips = (int)((token + a.strip - 1) / a.strip);
     const long long strips = (long long)a.n * a.strips, sms = sm_count();
-    if (a.max_keep <= 64) {                                     // accepted paths: small CTAs (5 us, 18 with 512 threads), some layers each
+    // Accepted paths: small CTAs, some layers each (64 x 9 tokens 5 us, 18 with 512 threads; 256 x 80 31 and 41; 64 x 256
+    // 48.7 and 47.9).
+    if (a.max_keep <= 128) {
         const int both = a.one ? 1 : 2;
         const long long groups = (16 * sms + strips * both - 1) / (strips * both);
         const int y = both * (int)(groups < layers ? groups : layers);
