@@ -62,7 +62,7 @@ constexpr int kRefineTurns = 32;             // elements a thread sums at most: 
 // Near zero (references of whole powers of two, see Ref): the argument's rounding and
 // log2 e, 13.2 (2^-24 + 2^-26) -> 1.0e-6; ex2.approx 2^-22 -> 2.4e-7; sums by trees of 8
 // levels in a chunk, 5 shuffles, 5 of the segments', 2 joins of parts: 20 2^-24 -> 1.2e-6;
-// logf, an ulp of 13.2 -> 9.6e-7: 3.4e-6 in all.  Elsewhere: difference and product
+// logf, an ulp of 13.2 -> 9.6e-7; the reference's part 5e-8: 3.5e-6 in all.  Elsewhere: difference and product
 // 2^-24 each, up to kMaxSegChunks moves of the reference and the segments' join,
 // 9 (2^-22 + 2^-24) -> 2.7e-6: 6.9e-6.
 constexpr double kSumEps = 8e-6, kNearEps = 4e-6;
@@ -422,24 +422,24 @@ struct Entries {
 template <int T>
 __device__ void sort_entries(const Entries& e, int n, uint16_t* order)
 {
-    int p = 1;
-    while (p < n) p <<= 1;
+    const int bits = n > 1 ? 32 - __clz(n - 1) : 0, p = 1 << bits;
     if (p <= T / 2) {
         __syncthreads();
-        const int share = min(32, T / p), i = threadIdx.x / share;
-        if ((int)(threadIdx.x & ~31u) / share < n) {              // (for whole warps)
+        const int most = 31 - __clz(T), share_bits = min(5, most - bits), share = 1 << share_bits;
+        const int i = threadIdx.x >> share_bits, j0 = threadIdx.x & (share - 1);
+        if ((int)(threadIdx.x & ~31u) >> share_bits < n) {        // (for whole warps)
             int before = 0;
             if (i < n) {
                 const unsigned long long k = e.key[i];
                 const uint32_t f = e.flat[i];
-                for (int j = threadIdx.x % share; j < n; j += share) {
+                for (int j = j0; j < n; j += share) {
                     const unsigned long long other = e.key[j];
                     before += other > k;
                     if (other == k && e.flat[j] < f) ++before;
                 }
             }
             for (int o = share >> 1; o; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-            if (i < n && threadIdx.x % share == 0) order[before] = (uint16_t)i;
+            if (i < n && j0 == 0) order[before] = (uint16_t)i;
         }
         __syncthreads();
         return;
@@ -639,7 +639,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             m = warp_max(m);
             Ref all, one;
             all.move(m);
-            one.move(part.x);
+            one.move(lane < a.segs ? part.x : m);                 // (no lane of another kind without need)
             dfloat sum{part.y * ref_weight(one, all), 0.f};
             for (int i = lane + 32; i < a.segs; i += 32) {
                 const float2 x = __ldcg(&sums[i]);
@@ -651,7 +651,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             if (s == 0.f) kind = kDead;                           // nothing but -inf: every score is -inf
             base = (double)score - (double)logf(s);
-            if (all.near) base -= ((double)all.c - (double)m * (double)kLog2e) * kLn2;
+            if (all.near) base -= (double)(fmaf(-m, kLog2e, all.c) * (float)kLn2);   // up to 0.35: good to 5e-8
             top = m;
         }
         if (lane == 0) {
