@@ -14,8 +14,8 @@
 // Order.  Within a beam it is the logits' and exact.  Between beams it hangs on
 // the difference of two normalisers, and fp32 sums are off by up to kNearEps
 // (derived below), while candidates of a batch come nearer than that now and
-// then.  Where two neighbours of different beams do, at or before the last
-// selected place, the rows of both are summed again (refine_kernel), terms in
+// then.  Where neighbours of different beams do, up to the last selected place or
+// as near behind it, their beams' rows are summed again (refine_kernel), terms in
 // double-float arithmetic, the sum in whole numbers, and the item's saved
 // candidates are sorted once more: the order is then that of scores in 64 bits,
 // rows of the same values have the same sum in whatever order, and ties go to
@@ -62,9 +62,9 @@ constexpr int kRefineTurns = 32;             // elements a thread sums at most: 
 // Near zero (references of whole powers of two, see Ref): the argument's rounding and
 // log2 e, 13.2 (2^-24 + 2^-26) -> 1.0e-6; ex2.approx 2^-22 -> 2.4e-7; sums by trees of 8
 // levels in a chunk, 5 shuffles, 5 of the segments', 2 joins of parts: 20 2^-24 -> 1.2e-6;
-// logf, an ulp of 13.2 -> 9.6e-7; the reference's part 5e-8: 3.5e-6 in all.  Elsewhere: difference and product
-// 2^-24 each, up to kMaxSegChunks moves of the reference and the segments' join,
-// 9 (2^-22 + 2^-24) -> 2.7e-6: 6.9e-6.
+// logf, an ulp of 13.2 -> 9.6e-7; the reference's part 5e-8: 3.5e-6 in all.
+// Elsewhere: difference and product 2^-24 each, up to kMaxSegChunks moves of the
+// reference and the segments' join, 9 (2^-22 + 2^-24) -> 2.7e-6: 6.9e-6.
 constexpr double kSumEps = 8e-6, kNearEps = 4e-6;
 constexpr float kNear = 0x1p20f;
 
@@ -496,7 +496,7 @@ struct PickShared {
     int warp_count[32];
     float bound;
     int bound_found;
-    int n_chunks, n_elems, bad, flag_at;
+    int n_chunks, n_elems, bad, far, flag_at;
 
     __device__ Entries entries() { return Entries{key, flat, logit, beam}; }
 };
@@ -506,10 +506,6 @@ struct PickShared {
 __device__ __forceinline__ float score32(const BeamRec& b, float l)
 {
     return l == -INFINITY ? l : fmaxf(b.base + (l - b.top), -FLT_MAX);
-}
-__device__ __forceinline__ double eps_of(const BeamRec& b)
-{
-    return b.kind != kLive ? 0.0 : fabsf(b.top) < 0.5f * kNear ? kNearEps : kSumEps;   // (segments that are not near count nothing then)
 }
 __device__ __forceinline__ float slack32(const BeamRec& b, float l)
 {
@@ -618,7 +614,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
         const int i = tid + k * T;
         held[k] = i < total ? __ldcg(&chunk_max[i]) : 0.f;
     }
-    if (tid == 0) sh.n_chunks = sh.n_elems = sh.bad = 0;
+    if (tid == 0) sh.n_chunks = sh.n_elems = sh.bad = sh.far = 0;
     if (tid < 4) sh.mask[tid] = 0u;
     __syncthreads();
     // normalisers, a warp a beam
@@ -653,6 +649,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             base = (double)score - (double)logf(s);
             if (all.near) base -= (double)(fmaf(-m, kLog2e, all.c) * (float)kLn2);   // up to 0.35: good to 5e-8
             top = m;
+            if (lane == 0 && !(fabsf(m) < 0.5f * kNear)) sh.far = 1;   // (nearer ones: segments that are not near count nothing)
         }
         if (lane == 0) {
             sh.rec[b] = BeamRec{(float)base, top, 0.f, kind};
@@ -790,20 +787,18 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
         for (int i = tid; i < n; i += T) sh.key[i] = score_key(sh, sh.beam[i], sh.logit[i]);
         sort_entries<T>(e, n, sh.order);
         write_item<DT>(a, item, e, n, sh);                        // to be written again where the order may be another
-        // neighbours of two beams that the normalisers' errors may have put the wrong way round
-        for (int k = tid; k + 1 < n && k < a.n_out; k += T) {
-            const int i0 = sh.order[k], i1 = sh.order[k + 1];
-            const double s0 = f64_of_key(sh.key[i0]), s1 = f64_of_key(sh.key[i1]);
-            if (s0 - s1 > 2.0 * kSumEps + 0x1p-50 * fabs(s1)) continue;
-            const int b0 = sh.beam[i0], b1 = sh.beam[i1];
+        // What the normalisers' errors, eps at most, may have put the wrong way round: neighbours of two beams within 2 eps,
+        // and behind the last place those within 2 eps of it.  (Candidates without such neighbours between them keep
+        // their order; those further behind have n_out before them in any case.)  One eps for all beams, finished
+        // ones too: between two of larger eps a third must not part them.
+        const double eps = sh.far ? kSumEps : kNearEps;
+        for (int k = tid; k + 1 < n; k += T) {
+            const int i1 = sh.order[k + 1], b0 = sh.beam[sh.order[k]], b1 = sh.beam[i1];
             if (b0 == b1) continue;
-            const double e0 = eps_of(sh.rec[b0]), e1 = eps_of(sh.rec[b1]);
-            const double l0 = (double)sh.logit[i0] - (double)sh.rec[b0].top, l1 = (double)sh.logit[i1] - (double)sh.rec[b1].top;
-            const double lo0 = (sh.base[b0] - e0) + l0, hi0 = (sh.base[b0] + e0) + l0;
-            const double lo1 = (sh.base[b1] - e1) + l1, hi1 = (sh.base[b1] + e1) + l1;
-            if (hi1 < lo0 || (lo0 == hi0 && lo1 == hi1)) continue;
-            if (e0 != 0.0) atomicOr(&sh.mask[b0 >> 5], 1u << (b0 & 31));
-            if (e1 != 0.0) atomicOr(&sh.mask[b1 >> 5], 1u << (b1 & 31));
+            const double s0 = f64_of_key(sh.key[sh.order[min(k, a.n_out - 1)]]), s1 = f64_of_key(sh.key[i1]);
+            if (s0 - s1 > 2.0 * eps + 0x1p-50 * (fabs(s1) + fabs(sh.base[b0]) + fabs(sh.base[b1]))) continue;
+            if (sh.rec[b0].kind == kLive) atomicOr(&sh.mask[b0 >> 5], 1u << (b0 & 31));
+            if (sh.rec[b1].kind == kLive) atomicOr(&sh.mask[b1 >> 5], 1u << (b1 & 31));
         }
     } else if (tid < a.beams && sh.rec[tid].kind == kLive) {
         atomicOr(&sh.mask[tid >> 5], 1u << (tid & 31));

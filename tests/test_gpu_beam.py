@@ -192,6 +192,30 @@ def test_beams_nearer_than_fp32_tells(ws, dtype, vocab, seed, n):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,beams,vocab,n_out", [(16, 52, 6, 78), (126, 52, 6, 100), (10, 40, 3001, 7), (100, 128, 12, 33)])
+@pytest.mark.parametrize("finished", [False, True])
+def test_many_near_beams_at_the_last_place(ws, dtype, n, beams, vocab, n_out, finished):
+    # three equal candidates a beam, all beams' within fp32's rounding of their scores of one another: what belongs
+    # before the last place may stand further behind it than its neighbour
+    g = torch.Generator().manual_seed(vocab + n)
+    logits = -1.0 - torch.rand(n, beams, vocab, generator=g)
+    logits.scatter_(-1, torch.rand(n, beams, vocab, generator=g).argsort(-1)[..., :3], 2.0)
+    logits = logits.to(dtype)
+    x = logits.double()
+    scores = (x.logsumexp(-1) - 2.0 - 4.0).float()
+    ended = None
+    if finished:                                    # theirs among the others' best
+        ended = torch.rand(n, beams, generator=g) < 0.2
+        scores = torch.where(ended, -4.0 + 2.0 ** -22 * torch.randint(-1, 2, (n, beams), generator=g), scores)
+    # items in which no two scores in 64 bits are nearer than those are good to, unless they are one beam's and equal
+    s = select64(logits, scores, beams * vocab, ended, 1)[2]
+    d = s[:, :-1] - s[:, 1:]
+    clear = ~((d > 0) & (d < 5e-12)).any(-1)
+    assert clear.sum() >= n // 2
+    check(logits[clear], scores[clear], n_out, ws, finished=None if ended is None else ended[clear], end_token=1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_what_is_refused_is_refused_by_item(ws, dtype):
     n, beams, vocab = 7, 3, 2500
     logits, scores, _ = make(n, beams, vocab, dtype, 19)
