@@ -632,7 +632,7 @@ size_t sv_beam_workspace_size(int n, int beams, int vocab, int n_out);
  *   A continuation's score is c - ln Z + (l - m), m = max l, Z = sum exp(l - m),
  *   in 64 bits; -inf for tokens at -inf, for dead beams and for rows of nothing
  *   but -inf.  The order is by score, descending, equal scores by beam and then
- *   by token, ascending; it is that of the scores in 64 bits (errors of 1e-12),
+ *   by token, ascending; it is that of the scores in 64 bits (errors of 2e-12),
  *   and does not depend on timing.
  *   out_tokens, out_parents (device) int32 [n, n_out]: the continuations' tokens
  *   and beams, best first; out_scores (device) fp32 [n, n_out].

@@ -145,6 +145,18 @@ def test_few_rows_for_what_is_asked(ws, dtype, beams, vocab, n_out, spread):
     check(logits * 40.0, scores, n_out, ws)
 
 
+@pytest.mark.parametrize("n", [2, 3])
+def test_offsets_past_32_bits(ws, n):
+    # beams 2^30 elements and 3 apart, items 2^32 bytes and more
+    beams, vocab = 2, 5001
+    logits, scores, _ = make(n, beams, vocab, BF16, n)
+    step = 2 ** 30 + 3
+    wide = torch.empty((n * beams - 1) * step + vocab, dtype=BF16, device="cuda")
+    view = wide.as_strided((n, beams, vocab), (2 * step, step, 1))
+    view.copy_(logits)
+    check(logits, scores, 8, ws, view=view)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("n,beams,vocab,n_out", [(160, 3, 4099, 8), (700, 2, 1001, 17), (620, 3, 300, 256), (900, 1, 40, 3)])
 def test_more_items_than_run_at_once(ws, dtype, n, beams, vocab, n_out):
