@@ -635,7 +635,9 @@ size_t sv_beam_workspace_size(int n, int beams, int vocab, int n_out);
  *   by token, ascending; it is that of the scores in 64 bits (errors of 2e-12),
  *   and does not depend on timing.
  *   out_tokens, out_parents (device) int32 [n, n_out]: the continuations' tokens
- *   and beams, best first; out_scores (device) fp32 [n, n_out].
+ *   and beams, best first; out_scores (device) fp32 [n, n_out], which may be
+ *   scores itself where n_out == beams; otherwise outputs and inputs must not
+ *   overlap.
  *   status   (device) int32 [n] or NULL, SV_ROW_* bits OR-ed in (the caller
  *            clears it): SV_ROW_NONFINITE: NaN or +inf logit in a row that is
  *            read; SV_ROW_BAD_PARAM: NaN or +inf score.  Such an item gets
@@ -658,7 +660,7 @@ sv_status_t sv_beam_select(const void* logits, sv_dtype_t dt, int64_t stride_ite
  * overlap.
  *   parents (device) int32 [n, beams_out]; one outside [0, beams_in) leaves its
  *   row of dst as it is and sets SV_ROW_BAD_LAYOUT in status (device) int32 [n]
- *   or NULL.
+ *   or NULL.  dst must not overlap it.
  *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, different strides or
  *   beams in place; SV_ERR_UNSUPPORTED for more than 65,535 items, 128 beams or
  *   rows above 2^36 bytes.
@@ -714,7 +716,8 @@ size_t sv_kv_fork_workspace_size(int n_req, int max_pages, int n_pages);
  *   counted).
  *   Written: page_table (the columns that change; those past what a request
  *   holds are left as they are), held, ref_count, copies (device) int32
- *   [n_req][3]; status (device) int32 [n_req] or NULL, bits OR-ed in.
+ *   [n_req][3]; status (device) int32 [n_req] or NULL, bits OR-ed in.  None of
+ *   them may overlap another or the inputs.
  *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes; SV_ERR_UNSUPPORTED for
  *   n_req > 16,384, n_pages > 2^30 or n_req * max_pages > 2^28.  Workspace:
  *   sv_kv_fork_workspace_size(...).

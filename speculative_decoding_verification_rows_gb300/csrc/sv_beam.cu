@@ -73,7 +73,7 @@ enum { kDead = 0, kLive = 1, kFinished = 2 };
 // What an item's CTA knows of a beam, read in one piece.
 struct __align__(16) BeamRec {
     float base, top;    // base in fp32; the row's maximum (0 of a finished beam)
-    float least;        // l - top of a logit that may reach the bound
+    float score;        // as it was before the call: the outputs may lie where the scores do
     int kind;
 };
 
@@ -489,7 +489,10 @@ struct PickShared {
         uint16_t order[kListCap];
         int bins[kPickThreads];
     };
-    int scratch[kMaxOut];
+    union {
+        int scratch[kMaxOut];
+        float least[kMaxBeams];    // l - top of a logit that may reach the bound
+    };
     uint8_t beam[kListCap];
     uint32_t mask[4];
     float warp_best[32];
@@ -652,7 +655,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             if (lane == 0 && !(fabsf(m) < 0.5f * kNear)) sh.far = 1;   // (nearer ones: segments that are not near count nothing)
         }
         if (lane == 0) {
-            sh.rec[b] = BeamRec{(float)base, top, 0.f, kind};
+            sh.rec[b] = BeamRec{(float)base, top, score, kind};
             sh.base[b] = base;
         }
     }
@@ -722,7 +725,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
         // Where l - m is near bound - base, score and slack are off by 2^-22 (|base| + |bound - base|).
         if (tid < a.beams && sh.rec[tid].kind == kLive) {
             const float base = sh.rec[tid].base, at = bound - base;
-            sh.rec[tid].least = fmaxf(at - (2.f * (float)kSumEps + 0x1p-20f * (fabsf(base) + fabsf(at))), -FLT_MAX);
+            sh.least[tid] = fmaxf(at - (2.f * (float)kSumEps + 0x1p-20f * (fabsf(base) + fabsf(at))), -FLT_MAX);
         }
         __syncthreads();
         if (tid < a.beams && sh.rec[tid].kind == kFinished && sh.rec[tid].base >= bound) {   // one candidate: base alone
@@ -737,7 +740,7 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             const Row<DT> row(a, item, b);
             uint4 v[kVecs];
             row.chunk(c, v);
-            const float top = sh.rec[b].top, least = sh.rec[b].least;
+            const float top = sh.rec[b].top, least = sh.least[b];
             auto reaches = [&](float l) { return fmaxf(l - top, -FLT_MAX) >= least; };   // (-inf too, where the bound is none)
             // a lane's elements that reach the bound, then room for the warp's at once
             unsigned long long in = 0ull;
@@ -998,7 +1001,7 @@ __device__ void finish_item(const BeamArgs& a, int item, int n, PickShared& sh)
             high += x.x;
             low += x.y;
         }
-        sh.base[tid] = (double)a.scores[r] - log((double)high * 0x1p-26 + (double)low * 0x1p-58);
+        sh.base[tid] = (double)sh.rec[tid].score - log((double)high * 0x1p-26 + (double)low * 0x1p-58);
     }
     __syncthreads();
     const Entries e = sh.entries();

@@ -901,8 +901,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int, finished
                 ws: Optional[Workspace] = None) -> BeamOut:
     """sv_beam_select: the n_out best continuations of every request over its beams' logits [n, beams, vocab] (bf16 or
     fp32, rows contiguous) and scores fp32 [n, beams] (-inf: a dead beam).  A beam marked in finished (bool or uint8
-    [n, beams]) has one, end_token with its score unchanged.  Equal scores go by beam, then token.  Autograd records
-    nothing of it."""
+    [n, beams]) has one, end_token with its score unchanged.  Equal scores go by beam, then token.  out.scores may be
+    scores itself.  Autograd records nothing of it."""
     device = logits.get_device()
     if device < 0:
         raise _not_on_gpu()

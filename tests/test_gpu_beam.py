@@ -145,6 +145,34 @@ def test_few_rows_for_what_is_asked(ws, dtype, beams, vocab, n_out, spread):
     check(logits * 40.0, scores, n_out, ws)
 
 
+@pytest.mark.parametrize("n", [6, 90])                              # one launch, and three
+@pytest.mark.parametrize("near", [False, True])
+def test_scores_are_replaced_in_place(ws, n, near):
+    # (near: every beam summed again, from the score that it had)
+    beams, vocab = 6, 3001
+    logits, scores, g = make(n, beams, vocab, F32, n)
+    if near:
+        logits[:] = logits[:, :1].clone()
+        scores[:] = scores[:, :1] + 2.0 ** -20 * torch.rand(n, beams, generator=g).argsort(-1)
+    tokens, parents, want = select64(logits, scores, beams)
+    mine = scores.cuda()
+    out = sv.BeamOut(torch.empty(n, beams, dtype=torch.int32, device="cuda"),
+                     torch.empty(n, beams, dtype=torch.int32, device="cuda"), mine)
+    sv.beam_select(logits.cuda(), mine, beams, out=out, ws=ws)
+    assert torch.equal(out.tokens.cpu(), tokens) and torch.equal(out.parents.cpu(), parents)
+    assert ((mine.double().cpu() - want).abs() <= score_tolerance(want)).all()
+
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_one_row_for_all_beams(ws, n):
+    # a search's first step: one row for all beams, all but one of them dead, or all of them alive
+    logits, scores, _ = make(n, 1, 5003, BF16, n)
+    first = torch.full((n, 4), -math.inf)
+    first[:, 0] = 0.0
+    for s in (first, -torch.arange(4.0).expand(n, 4).contiguous()):
+        check(logits.expand(n, 4, 5003).contiguous(), s, 8, ws, view=logits.cuda().expand(n, 4, 5003))
+
+
 @pytest.mark.parametrize("n", [2, 3])
 def test_offsets_past_32_bits(ws, n):
     # beams 2^30 elements and 3 apart, items 2^32 bytes and more
