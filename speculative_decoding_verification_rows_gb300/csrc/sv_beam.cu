@@ -558,7 +558,9 @@ __device__ void write_item(const BeamArgs& a, int item, const Entries& e, int n,
 
 // A lower bound on the n_out-th largest of the threads' values: counted in bins
 // of 1/32 below the largest (four barriers), or, where they lie further apart
-// than the bins reach, by bisection (20 barriers).
+// than the bins reach, by bisection (20 barriers).  -FLT_MAX at least: -inf is what
+// is not a value (rows that are not read, what lies past the last chunk), and none
+// of it may reach the bound.
 template <int T>
 __device__ float nth_bound(float best, int n_out, PickShared& sh)
 {
@@ -590,7 +592,7 @@ __device__ float nth_bound(float best, int n_out, PickShared& sh)
         sh.bound_found = 1;
     }
     __syncthreads();
-    if (sh.bound_found) return sh.bound;
+    if (sh.bound_found) return fmaxf(sh.bound, -FLT_MAX);         // (a step below the lowest finite number is -inf)
     const uint32_t mine = key_of_f32_bits(__float_as_uint(best));
     uint32_t bound_key = 0u;
     for (int bit = 31; bit >= 12; --bit) {
