@@ -724,10 +724,12 @@ __device__ int pick_item(const BeamArgs& a, int item, PickShared& sh)
             }
             bound = fmaxf(bound, nth_bound<T>(best, a.n_out, sh));
         }
-        // Where l - m is near bound - base, score and slack are off by 2^-22 (|base| + |bound - base|).
+        // Where l - m is near bound - base, score and slack are off by 2^-22 (|base| + |bound - base|).  A bound of -FLT_MAX
+        // is none: scores in 64 bits go below it (the lowest score with a token at the lowest value), and every token counts.
         if (tid < a.beams && sh.rec[tid].kind == kLive) {
             const float base = sh.rec[tid].base, at = bound - base;
-            sh.least[tid] = fmaxf(at - (2.f * (float)kSumEps + 0x1p-20f * (fabsf(base) + fabsf(at))), -FLT_MAX);
+            const float least = at - (2.f * (float)kSumEps + 0x1p-20f * (fabsf(base) + fabsf(at)));
+            sh.least[tid] = bound == -FLT_MAX ? -FLT_MAX : fmaxf(least, -FLT_MAX);
         }
         __syncthreads();
         if (tid < a.beams && sh.rec[tid].kind == kFinished && sh.rec[tid].base >= bound) {   // one candidate: base alone
