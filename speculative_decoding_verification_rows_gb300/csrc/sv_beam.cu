@@ -416,7 +416,7 @@ struct Entries {
 };
 
 // order[i] becomes the i-th candidate: descending by score, ascending by place
-// among equals (the places are distinct).  Up to 256 candidates find their places
+// among equals (the places are distinct).  Up to T / 2 candidates find their places
 // by counting those before them, a few threads each: two barriers, where the
 // sorting network has one a stage.  More are sorted (bitonic).
 template <int T>
@@ -557,8 +557,8 @@ __device__ void write_item(const BeamArgs& a, int item, const Entries& e, int n,
 }
 
 // A lower bound on the n_out-th largest of the threads' values: counted in bins
-// of 1/32 below the largest (four barriers), or, where they lie further apart
-// than the bins reach, by bisection (20 barriers).  -FLT_MAX at least: -inf is what
+// of 32 / T below the largest (four barriers), or, where they lie further apart
+// than the T bins reach, by bisection (20 barriers).  -FLT_MAX at least: -inf is what
 // is not a value (rows that are not read, what lies past the last chunk), and none
 // of it may reach the bound.
 template <int T>
@@ -571,7 +571,7 @@ __device__ float nth_bound(float best, int n_out, PickShared& sh)
     const float w = warp_max(best);
     if (lane == 0) sh.warp_best[warp] = w;
     __syncthreads();
-    const float most = warp_max(sh.warp_best[lane]);
+    const float most = warp_max(lane < T / 32 ? sh.warp_best[lane] : -INFINITY);
     const float down = (most - best) * kPerUnit;
     if (best > -INFINITY && down < (float)T) atomicAdd(&sh.bins[(int)down], 1);
     __syncthreads();

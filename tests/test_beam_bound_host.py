@@ -204,3 +204,16 @@ def test_a_bound_is_reached_by_as_many_as_asked(bounds, threads):
         else:                                       # a bin of 32 / threads, or what a bisection of 20 bits leaves
             nth, most = float(finite[n - 1]), float(finite[0])
             assert float(bound) >= nth - max(33.0 / threads + 2.0 ** -22 * abs(most), 2.0 ** -10 * abs(nth))
+
+
+@pytest.mark.parametrize("threads", [256, 1024])
+def test_what_lay_in_shared_memory_has_no_part_in_a_bound(bounds, threads):
+    rng = np.random.default_rng(threads + 1)
+    rows = [(4, padded(threads, rng.standard_normal(100) * 3 - 100)), (8, padded(threads, rng.standard_normal(200) * 3)),
+            (3, np.full(threads, LOWEST)), (5, padded(threads, [-7.0] * 4))]
+    stale = [-INF, 0.0, INF, float("nan"), 1e30, -104.0, -2.0]
+    cases = [(n, s, values) for n, values in rows for s in stale]
+    got = bounds(threads, cases)
+    check(threads, cases, got)
+    got = got.reshape(len(rows), len(stale))
+    assert (got == got[:, :1]).all()
