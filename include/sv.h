@@ -97,10 +97,10 @@ enum {
     SV_ROW_TIMEOUT = 256,     /* a bounded wait on a bulk copy gave up: rows of the
                                  call were not processed (never seen in practice);
                                  of sv_paged_attention: results are right or NaN  */
-    SV_ROW_NO_PAGES = 512     /* sv_kv_fork: the pool has no pages for the request     */
+    SV_ROW_NO_PAGES = 512     /* sv_kv_fork: the pool has no pages for the request */
 };
 #define SV_ROW_ERROR_MASK (SV_ROW_NONFINITE | SV_ROW_EMPTY | SV_ROW_BAD_TOKEN | SV_ROW_BAD_PARAM | \
-                           SV_ROW_BAD_LAYOUT | SV_ROW_UNSUPPORTED | SV_ROW_TIMEOUT)
+                           SV_ROW_BAD_LAYOUT | SV_ROW_UNSUPPORTED | SV_ROW_TIMEOUT | SV_ROW_NO_PAGES)
 
 /* Host-side promises about a batch's sampling parameters (sv_sampling_t.flags).
  *   SV_SAMPLING_SMALL_TOPK  every request is greedy (T == 0) or keeps at most
@@ -707,7 +707,9 @@ size_t sv_kv_fork_workspace_size(int n_req, int max_pages, int n_pages);
  *   copy's first); pages given back by the call are free for it.  A request
  *   whose pages, counted after those of all requests before it, exceed the free
  *   ones gets none: it holds the pages of keep_len tokens, nothing is copied for
- *   it, and status gets SV_ROW_NO_PAGES.
+ *   it, and status gets SV_ROW_NO_PAGES.  Nothing may be appended to it past
+ *   keep_len: what its row of the table says further on may be another's page by
+ *   now, and its begun page may be written on by another.
  *   A request with keep_len outside [0, held[parent] * page_size], new_len
  *   outside [keep_len, max_pages * page_size], a parent outside its range or a
  *   held count outside [0, max_pages] keeps what it holds and gets

@@ -26,7 +26,7 @@ DTYPE_BF16, DTYPE_F32, DTYPE_F16 = 0, 1, 2
 ROW_NONFINITE, ROW_EMPTY, ROW_BAD_TOKEN, ROW_BAD_PARAM, ROW_BAD_LAYOUT = 1, 2, 4, 8, 16
 ROW_Q_ZERO, ROW_RESID_ZERO, ROW_UNSUPPORTED, ROW_TIMEOUT, ROW_NO_PAGES = 32, 64, 128, 256, 512
 ROW_ERROR_MASK = (ROW_NONFINITE | ROW_EMPTY | ROW_BAD_TOKEN | ROW_BAD_PARAM | ROW_BAD_LAYOUT | ROW_UNSUPPORTED
-                  | ROW_TIMEOUT)
+                  | ROW_TIMEOUT | ROW_NO_PAGES)
 
 EXPORTED = ("sv_workspace_size", "sv_workspace_size_block", "sv_status_string", "sv_plan_budget",
             "sv_build_target_probs", "sv_verify_chain", "sv_verify_ragged", "sv_set_timing_events",
@@ -996,7 +996,8 @@ def kv_fork(page_table: torch.Tensor, held: torch.Tensor, ref_count: torch.Tenso
     """sv_kv_fork: every request takes the pages of the first keep_len tokens of its parent (its own, without parent)
     and gets room for new_len tokens; page_table int32 [n, max_pages], held int32 [n] and ref_count int32 [n_pages] are
     updated in place.  With group, parent numbers requests within groups of so many.  Returns copies int32 [n, 3]
-    (page, new page, tokens; -1: none), which kv_copy carries out before anything is appended."""
+    (page, new page, tokens; -1: none), which kv_copy carries out before anything is appended.  A request that status int32
+    [n] has an error for holds no room for new tokens: nothing may be appended to it."""
     device = page_table.get_device()
     if device < 0:
         raise _not_on_gpu()
