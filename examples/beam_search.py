@@ -8,8 +8,8 @@ A step of a batch of requests with some beams each:
   pages   -> sv.kv_fork                   beams share what they have in common, and get room for a token
           -> sv.kv_copy                   begun pages that several beams would write on
 
-A finished beam gives its pages back and stays among the beams with its score.  Weights are random, so the text means
-nothing.  Run: python examples/beam_search.py [--requests 16] [--beams 4] [--steps 32]
+A finished beam gives its pages back and stays among the beams with its score.  So does one that the pool has no pages
+for: its text ends there, and nothing is appended to it.  Weights are random, so the text means nothing.  Run: python examples/beam_search.py [--requests 16] [--beams 4] [--steps 32]
 """
 from __future__ import annotations
 
@@ -34,7 +34,8 @@ class BeamSearch:
         self.held = torch.zeros(rows, dtype=torch.int32, device=device)
         self.ref = torch.zeros(target.k_pages.shape[0], dtype=torch.int32, device=device)
         self.copies = torch.empty((rows, 3), dtype=torch.int32, device=device)
-        self.status = torch.zeros(rows, dtype=torch.int32, device=device)
+        self.status = torch.zeros(rows, dtype=torch.int32, device=device)                 # of the last fork
+        self.refusals = torch.zeros((), dtype=torch.int64, device=device)
         self.scores = torch.zeros((n, beams), device=device)
         self.finished = torch.zeros((n, beams), dtype=torch.bool, device=device)
         self.tokens = torch.zeros((n, beams), dtype=torch.int32, device=device)           # not yet in the cache
@@ -43,9 +44,14 @@ class BeamSearch:
         self.done = torch.zeros((), dtype=torch.int64, device=device)                     # steps taken
 
     def room(self, parent, group, keep, length):
+        self.status.zero_()
         sv.kv_fork(self.t.table, self.held, self.ref, self.t.page, keep, length, parent=parent, group=group,
                    copies=self.copies, status=self.status, ws=self.t.ws)
         sv.kv_copy(self.t.k_pages, self.t.v_pages, self.copies)
+        refused = (self.status & sv.ROW_ERROR_MASK) != 0       # no room for another token: these beams end here
+        self.finished |= refused.view(self.n, self.beams)
+        self.length.masked_fill_(refused, 0)                   # (their pages go back with the next fork)
+        self.refusals += refused.sum()
 
     def start(self, prompts: torch.Tensor):
         """Prompts [n, length] into the first beam of every request, and its best continuations into all of them."""
@@ -53,6 +59,8 @@ class BeamSearch:
         first = torch.arange(n * beams, device=prompts.device) % beams == 0
         self.length.copy_(first * p)
         self.room(None, 0, torch.zeros_like(self.length), self.length)
+        if int(self.refusals):
+            raise RuntimeError("the pool has no pages for the prompts")
         qo = torch.zeros(n * beams + 1, dtype=torch.int32, device=prompts.device)
         qo[1:] = self.length.cumsum(0)
         logits = self.t.forward(prompts.reshape(-1), qo, self.length, p)
@@ -110,7 +118,8 @@ def main():
         search.step()
     stop.record()
     torch.cuda.synchronize()
-    assert int(search.status.max()) == 0, "a request was refused"
+    if int(search.refusals):
+        print(f"{int(search.refusals)} beams ended for want of pages")
     pages = int((search.ref > 0).sum())
     print(f"{a.requests} requests x {a.beams} beams, {a.steps} tokens: best score {float(search.scores.max()):.3f}, "
           f"{pages} pages for {int(search.held.sum())} held, {start.elapsed_time(stop) / max(a.steps - 2, 1):.3f} ms a step")
