@@ -9,7 +9,8 @@ A step of a batch of requests with some beams each:
           -> sv.kv_copy                   begun pages that several beams would write on
 
 A finished beam gives its pages back and stays among the beams with its score.  So does one that the pool has no pages
-for: its text ends there, and nothing is appended to it.  Weights are random, so the text means nothing.  Run: python examples/beam_search.py [--requests 16] [--beams 4] [--steps 32]
+for, and the beams of a request whose logits are NaN: their text ends there, and nothing is appended to them.  Weights
+are random, so the text means nothing.  Run: python examples/beam_search.py [--requests 16] [--beams 4] [--steps 32]
 """
 from __future__ import annotations
 
@@ -41,6 +42,7 @@ class BeamSearch:
         self.tokens = torch.zeros((n, beams), dtype=torch.int32, device=device)           # not yet in the cache
         self.history = torch.full((n, beams, steps), end_token, dtype=torch.int32, device=device)
         self.length = torch.zeros(rows, dtype=torch.int32, device=device)                 # cached tokens of a beam
+        self.place = torch.arange(beams, dtype=torch.int32, device=device).expand(n, beams)
         self.done = torch.zeros((), dtype=torch.int64, device=device)                     # steps taken
 
     def room(self, parent, group, keep, length):
@@ -71,17 +73,19 @@ class BeamSearch:
 
     def follow(self, out):
         """The selected continuations become the beams."""
-        self.finished.copy_(sv.beam_reorder(self.finished, out.parents))
-        sv.beam_reorder(self.history, out.parents, out=self.history)
-        self.history.scatter_(2, self.done.expand(self.n, self.beams, 1), out.tokens[..., None])
-        self.scores.copy_(out.scores)
-        self.tokens.copy_(out.tokens)
-        self.finished |= out.tokens == self.end
+        refused = out.parents < 0                              # a request whose selection was: its beams end as they are
+        parents = torch.where(refused, self.place, out.parents)
+        self.tokens.copy_(out.tokens.masked_fill(refused, self.end))
+        self.scores.copy_(torch.where(refused, self.scores, out.scores))
+        self.finished.copy_(sv.beam_reorder(self.finished, parents))
+        sv.beam_reorder(self.history, parents, out=self.history)
+        self.history.scatter_(2, self.done.expand(self.n, self.beams, 1), self.tokens[..., None])
+        self.finished |= self.tokens == self.end
         self.done += 1
         over = self.finished.view(-1)
-        keep = sv.beam_reorder(self.length.view(self.n, self.beams), out.parents).view(-1).masked_fill(over, 0)
+        keep = sv.beam_reorder(self.length.view(self.n, self.beams), parents).view(-1).masked_fill(over, 0)
         self.length.copy_((keep + 1).masked_fill(over, 0))
-        self.room(out.parents.view(-1), self.beams, keep, self.length)
+        self.room(parents.view(-1), self.beams, keep, self.length)
 
     def step(self):
         """Append the beams' tokens, score and select.  Returns (logits [n, beams, vocab], selection)."""

@@ -88,3 +88,18 @@ def test_prompts_without_pages_are_refused():
     search.ref[:3] = 0
     with pytest.raises(RuntimeError, match="pages"):
         search.start(prompts)
+
+
+def test_a_request_of_nan_logits_ends():
+    end = 3
+    t, search, prompts = searching(end)
+    prompts[1, 4] = end                             # (nobody feeds it back: a beam that has it is finished)
+    t.embed[end] = float("nan")
+    search.start(prompts)
+    assert search.finished[1].all() and not search.finished[0].all()
+    for s in range(1, STEPS):
+        step_on_the_dense_layer(t, search, prompts, s)
+        assert search.finished[1].all() and (search.length.view(N, BEAMS)[1] == 0).all()
+        assert (search.held.view(N, BEAMS)[1] == 0).all() and search.scores.isfinite().all()
+        assert (search.history[1, :, :s + 1] == end).all()
+        assert torch.equal(search.ref.cpu(), counted(search, torch.zeros_like(search.ref).cpu()))
