@@ -2,6 +2,8 @@
 // workspace carving and the launch sequence of each entry point.
 #include <stdint.h>
 
+#include <atomic>
+
 #include "sv_attn.cuh"
 #include "sv_internal.cuh"
 
@@ -9,15 +11,15 @@ using namespace sv;
 
 int sv::sm_count()
 {
-    static int cached[128] = {0};
+    static std::atomic<int> cached[128];               // (callers may be several threads)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 1;
-    if (!cached[dev]) {
-        int n = 0;
+    int n = cached[dev];
+    if (!n) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 1;
         cached[dev] = n;
     }
-    return cached[dev];
+    return n;
 }
 
 namespace {

@@ -37,6 +37,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "sv_attn.cuh"
 #include "sv_internal.cuh"
 
@@ -1163,7 +1165,7 @@ template <int DT>
 cudaError_t cluster_for(int n, int* size)
 {
     constexpr int kSizes[4] = {8, 4, 2, 1};
-    static int active[128][4];                         // + 1, once a device
+    static std::atomic<int> active[128][4];            // + 1, once a device (callers may be several threads)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

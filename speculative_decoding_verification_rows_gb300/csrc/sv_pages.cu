@@ -19,6 +19,8 @@
 // us by three kernels, 38 by one cluster.
 //
 // The copies are HBM-bound; see the kernels.
+#include <atomic>
+
 #include "sv_attn.cuh"
 #include "sv_internal.cuh"
 
@@ -411,7 +413,7 @@ bool fork_sizes_ok(int n_req, int max_pages, int n_pages)
 // What the runtime has to be told of the two kernels, once a device.
 cudaError_t prepare_fork()
 {
-    static bool done[128] = {false};
+    static std::atomic<bool> done[128];               // (callers may be several threads)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || (dev >= 0 && dev < 128 && done[dev])) return e;
