@@ -850,8 +850,17 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
 # ---------------------------------------------------------------------------
 # Beam search, and the pages of a paged cache
 # ---------------------------------------------------------------------------
+_INT_MAX = 0x7FFFFFFF        # ctypes cuts an int down to its 32 bits without a word
+
+
+def _too_large():
+    return SVError("sizes beyond what the library supports")
+
+
 @functools.lru_cache(maxsize=256)
 def beam_workspace_size(n: int, beams: int, vocab: int, n_out: int) -> int:
+    if max(n, beams, vocab, n_out) > _INT_MAX:
+        raise _too_large()
     size = load().sv_beam_workspace_size(n, beams, vocab, n_out)
     if size == 0:
         raise SVError("sizes beyond what the library supports")
@@ -860,6 +869,8 @@ def beam_workspace_size(n: int, beams: int, vocab: int, n_out: int) -> int:
 
 @functools.lru_cache(maxsize=256)
 def kv_fork_workspace_size(n_req: int, max_pages: int, n_pages: int) -> int:
+    if max(n_req, max_pages, n_pages) > _INT_MAX:
+        raise _too_large()
     size = load().sv_kv_fork_workspace_size(n_req, max_pages, n_pages)
     if size == 0:
         raise SVError("sizes beyond what the library supports")
@@ -886,7 +897,11 @@ def _matrix(t: torch.Tensor, rows: int, device: int, what: str):
     cols = t.shape[1]
     if one != 1 and cols > 1:
         raise SVError(f"the rows of {what} must be contiguous")
-    return t.data_ptr(), ld if rows > 1 else max(ld, cols), cols
+    if rows <= 1:                                                # the stride of an axis of one says nothing
+        ld = cols
+    if (ld | cols) > _INT_MAX:
+        raise _too_large()
+    return t.data_ptr(), ld, cols
 
 
 @dataclass
@@ -921,6 +936,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int, finished
         if (finished.get_device() != device or finished.dtype not in (torch.bool, torch.uint8) or
                 finished.shape != (n, beams) or not finished.is_contiguous()):
             raise SVError(f"finished must be a contiguous bool or uint8 [{n}, {beams}] on cuda:{device}")
+        if not 0 <= end_token < vocab:
+            raise SVError(f"end_token must be one of {vocab} tokens")
         marks = finished.data_ptr()
     if out is None:
         if n_out < 1:
@@ -937,7 +954,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int, finished
     nbytes = beam_workspace_size(n, beams, vocab, n_out)
     ws, at = _scratch(ws, nbytes, device)
     _launch(device, (_lib or load()).sv_beam_select, logits.data_ptr(), dt, s_item, s_beam, n, beams, vocab,
-            scores.data_ptr(), marks, end_token, n_out, out.tokens.data_ptr(), out.parents.data_ptr(),
+            scores.data_ptr(), marks, end_token if marks else 0, n_out, out.tokens.data_ptr(), out.parents.data_ptr(),
             out.scores.data_ptr(), None if status is None else _vector(status, n, device, "status"), at, nbytes,
             _stream_handle(device))
     return out
@@ -972,6 +989,8 @@ def beam_reorder(state: torch.Tensor, parents: torch.Tensor, out: Optional[torch
             parents.shape[0] != n or not parents.is_contiguous()):
         raise SVError(f"parents must be a contiguous int32 [{n}, beams] on cuda:{device}")
     beams_out = parents.shape[1]
+    if (n | beams | beams_out) > _INT_MAX:
+        raise _too_large()
     if out is None:
         out = torch.empty((n, beams_out, *state.shape[2:]), dtype=state.dtype, device=state.device)
     elif out.dtype is not state.dtype or out.shape != (n, beams_out, *state.shape[2:]):
@@ -1003,6 +1022,8 @@ def kv_fork(page_table: torch.Tensor, held: torch.Tensor, ref_count: torch.Tenso
         raise _not_on_gpu()
     if held.dim() != 1 or ref_count.dim() != 1:
         raise SVError("held must be int32 [n], ref_count int32 [n_pages]")
+    if not (0 < page_size <= _INT_MAX and 0 <= group <= _INT_MAX):
+        raise SVError("page_size must be positive, group a number of requests")
     n, n_pages = held.numel(), ref_count.numel()
     table, ld, cols = _matrix(page_table, n, device, "page_table")
     pool = PagePool(table, _vector(held, n, device, "held"), _vector(ref_count, n_pages, device, "ref_count"), ld, cols, n,
@@ -1038,6 +1059,8 @@ def _layers(k_pages: torch.Tensor, v_pages: torch.Tensor):
     if layers == 1:
         kl = vl = 0
     n_pages, page, heads, d = shape[-4:]
+    if (layers | n_pages | page | heads | d) > _INT_MAX:
+        raise _too_large()
     if (ks[-1] != 1 or vs[-1] != 1) and d != 1:
         raise SVError("the elements of a head must be contiguous")
     cache = PagedKV(Heads(k_pages.data_ptr(), ks[-3], ks[-2], heads), Heads(v_pages.data_ptr(), vs[-3], vs[-2], heads),
@@ -1052,6 +1075,8 @@ def kv_copy(k_pages: torch.Tensor, v_pages: torch.Tensor, copies: torch.Tensor, 
     if copies.dim() != 2 or copies.shape[1] != 3:
         raise SVError("copies must be int32 [entries, 3]")
     m = copies.shape[0]
+    if m > _INT_MAX:
+        raise _too_large()
     _launch(device, (_lib or load()).sv_kv_copy, cache, dt, d, layers, kl, vl, _vector(copies, 3 * m, device, "copies"), m,
             None if status is None else _vector(status, 1, device, "status"), _stream_handle(device))
 
@@ -1063,6 +1088,8 @@ def kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.T
     ascends in each row."""
     cache, layers, kl, vl, dt, d, device = _layers(k_pages, v_pages)
     n = n_keep.numel()
+    if n > _INT_MAX:
+        raise _too_large()
     cache.page_table, cache.ld_table, cache.max_pages = _matrix(page_table, n, device, "page_table")
     keep_at, ld, cols = _matrix(keep, n, device, "keep")
     _launch(device, (_lib or load()).sv_kv_compact, cache, dt, d, layers, kl, vl, n,
