@@ -632,12 +632,15 @@ size_t sv_beam_workspace_size(int n, int beams, int vocab, int n_out);
  *   A continuation's score is c - ln Z + (l - m), m = max l, Z = sum exp(l - m),
  *   in 64 bits; -inf for tokens at -inf, for dead beams and for rows of nothing
  *   but -inf.  The order is by score, descending, equal scores by beam and then
- *   by token, ascending; it is that of the scores in 64 bits (errors of 2e-12),
- *   and does not depend on timing.
+ *   by token, ascending; it is that of the scores in 64 bits (errors of 2e-12
+ *   and of their rounding), and does not depend on timing.
  *   out_tokens, out_parents (device) int32 [n, n_out]: the continuations' tokens
  *   and beams, best first; out_scores (device) fp32 [n, n_out], which may be
  *   scores itself where n_out == beams; otherwise outputs and inputs must not
- *   overlap.
+ *   overlap.  What out_scores gives is a score with ln Z summed in fp32, off by up
+ *   to 4e-6 (8e-6 in an item with a row whose maximum is 2^19 or further from
+ *   zero), or by 2e-12 where the order needed more and the row was summed again;
+ *   then rounded to fp32, -inf where that does not reach so low.
  *   status   (device) int32 [n] or NULL, SV_ROW_* bits OR-ed in (the caller
  *            clears it): SV_ROW_NONFINITE: NaN or +inf logit in a row that is
  *            read; SV_ROW_BAD_PARAM: NaN or +inf score.  Such an item gets
@@ -658,9 +661,10 @@ sv_status_t sv_beam_select(const void* logits, sv_dtype_t dt, int64_t stride_ite
  * be src itself (the same strides, beams_in == beams_out): every row then
  * becomes its parent's as it was before the call; otherwise the two must not
  * overlap.
- *   parents (device) int32 [n, beams_out]; one outside [0, beams_in) leaves its
- *   row of dst as it is and sets SV_ROW_BAD_LAYOUT in status (device) int32 [n]
- *   or NULL.  dst must not overlap it.
+ *   parents (device) int32 [n, beams_out]; one outside [0, beams_in) (that of a
+ *   refused selection is -1) leaves its row of dst as it is and sets
+ *   SV_ROW_BAD_LAYOUT in status (device) int32 [n] or NULL.  dst must not overlap
+ *   parents.
  *   Errors: SV_ERR_INVALID_ARG for null pointers, sizes, different strides or
  *   beams in place; SV_ERR_UNSUPPORTED for more than 65,535 items, 128 beams or
  *   rows above 2^36 bytes.

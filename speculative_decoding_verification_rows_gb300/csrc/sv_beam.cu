@@ -25,9 +25,10 @@
 // scan is 78.5 (6.48 TB/s, 95% of the copy bandwidth; 334 warp instructions a
 // chunk of 2,048 elements, 47% of the issue slots); what follows it is a chain of
 // latencies, 12,000 clocks: normalisers 2,900, bound 1,100, chunks read again
-// 2,500, order 1,800 and the steps between them.  32 x 8 x 151,936 in 19 us, one
-// item of 4 x 32,000 in 11 (16 with the host's part).  An item whose order is
-// checked again costs 8 to 12 us more.
+// 2,500, order 1,800 and the steps between them.  64 x 16 x 124,160 fp32 in 84 us
+// (89% of the copy bandwidth), 32 x 8 x 151,936 bf16 in 19, one item of 4 x 32,000
+// in 11 (15 to 20 with the host's part).  An item whose order is checked again costs
+// 8 to 12 us more.
 //
 // Tried and dropped: chunks set out by cp.async to a stage a warp (32 x 8 x
 // 151,936 32 us instead of 22 at the time: more instructions, and those are what
@@ -879,7 +880,11 @@ __device__ void block_best(unsigned long long& key, uint32_t& place, unsigned lo
 
 // An item with more candidates at its bound than a list holds (rows of few
 // distinct values): its n_out best chunks one after the other, then the n_out
-// best of their elements.  Returns how many there are.
+// best of their elements.  Returns how many there are.  Right, not fast: a pass
+// over the chunks and one over the listed ones' elements for every continuation,
+// by one CTA (32 items of 8 x 151,936 of one value: 1.4 ms for 16 continuations, 15
+// for 64; 64 of 16 x 248,320, 32: 246, for in three launches items wait for the CTAs
+// that finish others).
 template <int DT>
 __device__ int pick_by_turns(const BeamArgs& a, int item, PickShared& sh)
 {
@@ -1239,8 +1244,8 @@ cudaError_t launch_select(BeamArgs a, cudaStream_t s)
     e = launch_pdl(scan_kernel<DT>, dim3((unsigned)grid), dim3(kScanThreads), 0, s, a);
     if (e != cudaSuccess) return e;
     // More items than SMs: four small CTAs an SM, where an item has few chunks to read again or there are many waves
-    // (n x beams x vocabulary, n_out; us with large and small CTAs: 1,024 x 4 x 1,000, 8: 69 and 23; 160 x 4 x 32,000, 8:
-    // 22.7 and 17.8; 300 x 16 x 32,000, 32: 78 and 83; 200 x 8 x 151,936, 16: 88 and 94).
+    // (n x beams x vocabulary, n_out; us with large and small CTAs: 1,024 x 4 x 1,000, 8: 76 and 26; 160 x 4 x 32,000, 8:
+    // 22.9 and 18.1; 700 x 8 x 9,000, 16: 67 and 45; 300 x 16 x 32,000, 32: 78 and 82; 200 x 8 x 151,936, 16: 86 and 92).
     e = a.n > sms && (a.n_out <= 8 || a.n > 4 * sms) ? launch_pdl(pick_kernel<DT, kSmallPick>, dim3(a.n), dim3(kSmallPick), 0, s, a)
             : launch_pdl(pick_kernel<DT, kPickThreads>, dim3(a.n), dim3(kPickThreads), 0, s, a);
     if (e != cudaSuccess) return e;
@@ -1274,8 +1279,8 @@ struct ReorderArgs {
 // no second copy of the state.  A thread has a unit of up to ROWS rows in registers
 // (with more rows SHARE threads share a unit's, and a barrier stands between their
 // reads and writes).  HBM bounds it: 16 x 8 rows of 1 MB, half of them moving,
-// in 20.5 us (6.2 TB/s of rows moved, 91% of the copy bandwidth); 32 x 8 histories
-// of 4 KB in 2.3 us of the GPU, 7.7 with the host.
+// in 20.8 to 22.1 us over several boxes (5.7 to 6.1 TB/s of rows moved, 85 to 90% of
+// the copy bandwidth); 32 x 8 histories of 4 KB in 2.3 us of the GPU, 7.9 with the host.
 template <typename R, int ROWS, int SHARE>
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_constant__ ReorderArgs a)
 {

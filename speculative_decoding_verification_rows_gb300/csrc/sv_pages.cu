@@ -14,9 +14,10 @@
 // They are three kernels for large batches and pools, and one cluster with its
 // barriers between them for others, where latencies and launches are what counts.
 // Measured on a GB300: 256 windows resized (28,000 pages) in 10.5 us of the GPU,
-// 57 by one CTA, of which the three steps are 4,000, 4,000 and 8,000 clocks, chains
-// of four to six reads of L2 each; 128 beams of up to 131,072 tokens forked in 12.3
-// us by three kernels, 38 by one cluster.
+// 57 by one CTA, of which the three steps are 4,000, 4,000 and 8,000 clocks: the first
+// two chains of four to six reads of L2, the third three scans over the block (tiles,
+// requests, a tile's pages), three barriers each, one after another in every CTA; 128
+// beams of up to 131,072 tokens forked in 12.3 us by three kernels, 38 by one cluster.
 //
 // The copies are HBM-bound; see the kernels.
 #include <atomic>
@@ -532,8 +533,9 @@ __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constan
 // is written, the next one's units are on their way, the places of the one after
 // that are looked up (once a token, into a ring of three turns) and the list is
 // read another turn ahead; one barrier a turn.  CTAs have different strips.  Half
-// of 4 x 16,383 tokens (8 heads of 128, strips of 64 bytes) in 50 us (5.4 TB/s, 79%
+// of 4 x 16,383 tokens (8 heads of 128, strips of 64 bytes) in 51.6 us (5.1 TB/s, 76%
 // of the copy bandwidth); 157 when a turn waited for its own lookups and reads.
+// With 16-byte units the launch bounds cost spills: 36 bytes with 128 threads, 8 with 512.
 //
 // A cluster shares a strip's turns where strips alone are too few CTAs.  A list
 // of one turn keeps its places for all the layers that its CTA takes, the next

@@ -917,7 +917,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int, finished
     """sv_beam_select: the n_out best continuations of every request over its beams' logits [n, beams, vocab] (bf16 or
     fp32, rows contiguous) and scores fp32 [n, beams] (-inf: a dead beam).  A beam marked in finished (bool or uint8
     [n, beams]) has one, end_token with its score unchanged.  Equal scores go by beam, then token.  out.scores may be
-    scores itself.  Autograd records nothing of it."""
+    scores itself.  The order is that of scores in 64 bits; out.scores are off by up to 4e-6 and an fp32 rounding (8e-6
+    in a request with a row whose maximum is 2^19 or further from zero).  A request that status int32 [n] refuses gets
+    tokens and parents of -1 and scores of NaN.  Autograd records nothing of it."""
     device = logits.get_device()
     if device < 0:
         raise _not_on_gpu()
@@ -979,7 +981,8 @@ def beam_reorder(state: torch.Tensor, parents: torch.Tensor, out: Optional[torch
                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """sv_beam_reorder: out[i, j] = state[i, parents[i, j]] for state [n, beams, ...] of any type and parents int32
     [n, beams_out].  out may be state itself: the rows then move in place.  A parent outside its range leaves the row
-    of out as it is (and sets ROW_BAD_LAYOUT in status int32 [n]).  Autograd records nothing of it."""
+    of out as it is (and sets ROW_BAD_LAYOUT in status int32 [n]); without out that row holds anything.  Autograd
+    records nothing of it."""
     device = state.get_device()
     if device < 0:
         raise _not_on_gpu()
